@@ -1083,3 +1083,245 @@ gs_status gs_mb_atomic(float* records, int64_t n_records, int64_t n_ops, int32_t
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- label learning
+
+namespace {
+
+gs_status check_rows(const char* fn, int64_t n, int64_t dim, int64_t vocab, int32_t dtype) {
+    REQUIRE(n >= 0 && n <= (int64_t)1 << 30, "%s: n must be in [0, 2^30], got %lld", fn, (long long)n);
+    REQUIRE(dim >= 1 && dim <= 65536, "%s: dim must be in [1, 65536], got %lld", fn, (long long)dim);
+    REQUIRE(vocab >= 1 && vocab <= (int64_t)1 << 30, "%s: vocab must be in [1, 2^30], got %lld", fn,
+            (long long)vocab);
+    if (dtype != GS_F32 && dtype != GS_BF16)
+        return fail(GS_ERR_UNSUPPORTED, "%s: dtype must be GS_F32 or GS_BF16, got %d", fn, dtype);
+    return GS_OK;
+}
+
+gs_status check_index(const char* fn, const void* ids, int32_t type, int64_t n) {
+    if (type != GS_I32 && type != GS_I64)
+        return fail(GS_ERR_UNSUPPORTED, "%s: index_type must be GS_I32 or GS_I64, got %d", fn, type);
+    REQUIRE(n == 0 || ids, "%s: the index array must not be NULL", fn);
+    REQUIRE(aligned(ids, type == GS_I64 ? 8 : 4), "%s: misaligned index array", fn);
+    return GS_OK;
+}
+
+// A matrix of `rows` rows: present (unless it has no rows, or may be left out), aligned to its type, rows apart.
+gs_status check_matrix(const char* fn, const char* name, const void* p, int64_t stride, int64_t rows, int64_t dim,
+                       int32_t dtype, bool input, bool optional) {
+    if (!p) {
+        REQUIRE(optional || rows == 0, "%s: %s must not be NULL", fn, name);
+        return GS_OK;
+    }
+    REQUIRE(aligned(p, dtype == GS_F32 ? 4 : 2), "%s: misaligned %s", fn, name);
+    REQUIRE((stride >= dim && stride <= (int64_t)1 << 31) || (input && stride == 0),
+            "%s: %s's row stride must be in [%lld, 2^31]%s, got %lld", fn, name, (long long)dim,
+            input ? " or 0" : "", (long long)stride);
+    return GS_OK;
+}
+
+gs_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t need) {
+    REQUIRE(bytes >= need, "%s: workspace too small: %zu bytes, needs %zu", fn, bytes, need);
+    REQUIRE(need == 0 || ws, "%s: workspace must not be NULL", fn);
+    REQUIRE(aligned(ws, 256), "%s: workspace must be 256-byte aligned", fn);
+    return GS_OK;
+}
+
+bool rows_ok(int64_t n, int64_t dim, int64_t vocab, int32_t dtype) {
+    return n >= 0 && n <= (int64_t)1 << 30 && dim >= 1 && dim <= 65536 && vocab >= 1 && vocab <= (int64_t)1 << 30 &&
+           (dtype == GS_F32 || dtype == GS_BF16);
+}
+
+#define TRY(call)                          \
+    do {                                   \
+        const gs_status st_ = (call);      \
+        if (st_ != GS_OK) return st_;      \
+    } while (0)
+
+}  // namespace
+
+extern "C" {
+
+gs_status gs_embed_fwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, const void* table, int64_t table_stride,
+                       const void* ids, int32_t index_type, float scale, void* out, int64_t out_stride,
+                       void* stream) {
+    try {
+        static const char* fn = "gs_embed_fwd";
+        g_err[0] = 0;
+        TRY(check_rows(fn, n, dim, vocab, dtype));
+        TRY(check_index(fn, ids, index_type, n));
+        TRY(check_matrix(fn, "table", table, table_stride, vocab, dim, dtype, true, false));
+        TRY(check_matrix(fn, "out", out, out_stride, n, dim, dtype, false, false));
+        if (n == 0) return GS_OK;
+        return hip_check(gs::launch_embed_fwd(n, dim, (int)vocab, dtype == GS_BF16, table, table_stride, ids,
+                                              index_type == GS_I64, scale, out, out_stride, (hipStream_t)stream),
+                         fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_embed_fwd: unexpected exception");
+    }
+}
+
+size_t gs_embed_bwd_workspace_size(int64_t n, int32_t dim, int64_t vocab, int32_t dtype) {
+    return rows_ok(n, dim, vocab, dtype) && n > 0 ? gs::embed_bwd_layout(n, dim, (int)vocab).total : 0;
+}
+
+gs_status gs_embed_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, const void* ids, int32_t index_type,
+                       float scale, const void* dout, int64_t dout_stride, void* dtable, int64_t dtable_stride,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    try {
+        static const char* fn = "gs_embed_bwd";
+        g_err[0] = 0;
+        TRY(check_rows(fn, n, dim, vocab, dtype));
+        TRY(check_index(fn, ids, index_type, n));
+        TRY(check_matrix(fn, "dout", dout, dout_stride, n, dim, dtype, true, false));
+        TRY(check_matrix(fn, "dtable", dtable, dtable_stride, vocab, dim, dtype, false, false));
+        TRY(check_workspace(fn, workspace, workspace_bytes, gs_embed_bwd_workspace_size(n, dim, vocab, dtype)));
+        return hip_check(gs::launch_embed_bwd(n, dim, (int)vocab, dtype == GS_BF16, ids, index_type == GS_I64, scale,
+                                              dout, dout_stride, dtable, dtable_stride, (char*)workspace,
+                                              (hipStream_t)stream),
+                         fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_embed_bwd: unexpected exception");
+    }
+}
+
+gs_status gs_layer_norm_fwd(int64_t n, int32_t dim, int32_t dtype, const void* x, int64_t x_stride,
+                            const void* weight, const void* bias, float eps, void* y, int64_t y_stride, float* mean,
+                            float* rstd, void* stream) {
+    try {
+        static const char* fn = "gs_layer_norm_fwd";
+        g_err[0] = 0;
+        TRY(check_rows(fn, n, dim, 1, dtype));
+        REQUIRE(isfinite(eps) && eps >= 0.f, "%s: eps must be finite and >= 0", fn);
+        TRY(check_matrix(fn, "x", x, x_stride, n, dim, dtype, true, false));
+        TRY(check_matrix(fn, "weight", weight, dim, 1, dim, dtype, true, true));
+        TRY(check_matrix(fn, "bias", bias, dim, 1, dim, dtype, true, true));
+        TRY(check_matrix(fn, "y", y, y_stride, n, dim, dtype, false, false));
+        REQUIRE(aligned(mean, 4) && aligned(rstd, 4), "%s: misaligned mean or rstd", fn);
+        if (n == 0) return GS_OK;
+        return hip_check(gs::launch_norm_fwd(n, dim, dtype == GS_BF16, x, x_stride, weight, bias, eps, y, y_stride,
+                                             mean, rstd, (hipStream_t)stream),
+                         fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_layer_norm_fwd: unexpected exception");
+    }
+}
+
+size_t gs_layer_norm_bwd_workspace_size(int64_t n, int32_t dim, int32_t dtype) {
+    return rows_ok(n, dim, 1, dtype) ? gs::norm_bwd_workspace(n, dim) : 0;
+}
+
+gs_status gs_layer_norm_bwd(int64_t n, int32_t dim, int32_t dtype, const void* x, int64_t x_stride,
+                            const void* weight, const float* mean, const float* rstd, const void* dy,
+                            int64_t dy_stride, void* dx, int64_t dx_stride, void* dweight, void* dbias,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    try {
+        static const char* fn = "gs_layer_norm_bwd";
+        g_err[0] = 0;
+        TRY(check_rows(fn, n, dim, 1, dtype));
+        TRY(check_matrix(fn, "x", x, x_stride, n, dim, dtype, true, false));
+        TRY(check_matrix(fn, "weight", weight, dim, 1, dim, dtype, true, true));
+        TRY(check_matrix(fn, "dy", dy, dy_stride, n, dim, dtype, true, false));
+        REQUIRE(n == 0 || (mean && rstd), "%s: mean and rstd must not be NULL", fn);
+        REQUIRE(aligned(mean, 4) && aligned(rstd, 4), "%s: misaligned mean or rstd", fn);
+        TRY(check_matrix(fn, "dx", dx, dx_stride, n, dim, dtype, false, true));
+        TRY(check_matrix(fn, "dweight", dweight, dim, 1, dim, dtype, false, true));
+        TRY(check_matrix(fn, "dbias", dbias, dim, 1, dim, dtype, false, true));
+        if (dweight || dbias)
+            TRY(check_workspace(fn, workspace, workspace_bytes, gs_layer_norm_bwd_workspace_size(n, dim, dtype)));
+        return hip_check(gs::launch_norm_bwd(n, dim, dtype == GS_BF16, x, x_stride, weight, mean, rstd, dy, dy_stride,
+                                             dx, dx_stride, dweight, dbias, (float*)workspace, (hipStream_t)stream),
+                         fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_layer_norm_bwd: unexpected exception");
+    }
+}
+
+size_t gs_label_loss_workspace_size(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, int32_t backward) {
+    return rows_ok(n, dim, vocab, dtype)
+               ? gs::label_loss_workspace(n, dim, (int)vocab, dtype == GS_BF16, backward != 0)
+               : 0;
+}
+
+gs_status gs_label_loss_fwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, const void* x, int64_t x_stride,
+                            const void* w, int64_t w_stride, const void* labels, int32_t index_type, float* loss,
+                            float* lse, float* mean, int32_t* count, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    try {
+        static const char* fn = "gs_label_loss_fwd";
+        g_err[0] = 0;
+        TRY(check_rows(fn, n, dim, vocab, dtype));
+        TRY(check_matrix(fn, "x", x, x_stride, n, dim, dtype, true, false));
+        TRY(check_matrix(fn, "w", w, w_stride, vocab, dim, dtype, true, false));
+        TRY(check_index(fn, labels, index_type, n));
+        REQUIRE(n == 0 || (loss && lse), "%s: loss and lse must not be NULL", fn);
+        REQUIRE(mean && count, "%s: mean and count must not be NULL", fn);
+        REQUIRE(aligned(loss, 4) && aligned(lse, 4) && aligned(mean, 4) && aligned(count, 4),
+                "%s: misaligned loss, lse, mean or count", fn);
+        TRY(check_workspace(fn, workspace, workspace_bytes,
+                            gs_label_loss_workspace_size(n, dim, vocab, dtype, 0)));
+        gs::LabelLossArgs a{};
+        a.n = n;
+        a.dim = dim;
+        a.vocab = (int)vocab;
+        a.half = dtype == GS_BF16;
+        a.wide_labels = index_type == GS_I64;
+        a.x = x;
+        a.w = w;
+        a.labels = labels;
+        a.x_stride = x_stride;
+        a.w_stride = w_stride;
+        a.loss = loss;
+        a.lse = lse;
+        a.mean = mean;
+        a.count = count;
+        return hip_check(gs::launch_label_loss_fwd(a, (char*)workspace, (hipStream_t)stream), fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_label_loss_fwd: unexpected exception");
+    }
+}
+
+gs_status gs_label_loss_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, const void* x, int64_t x_stride,
+                            const void* w, int64_t w_stride, const void* labels, int32_t index_type,
+                            const float* lse, const float* dmean, const float* dloss, void* dx, int64_t dx_stride,
+                            void* dw, int64_t dw_stride, void* workspace, size_t workspace_bytes, void* stream) {
+    try {
+        static const char* fn = "gs_label_loss_bwd";
+        g_err[0] = 0;
+        TRY(check_rows(fn, n, dim, vocab, dtype));
+        TRY(check_matrix(fn, "x", x, x_stride, n, dim, dtype, true, false));
+        TRY(check_matrix(fn, "w", w, w_stride, vocab, dim, dtype, true, false));
+        TRY(check_index(fn, labels, index_type, n));
+        REQUIRE(n == 0 || lse, "%s: lse must not be NULL", fn);
+        REQUIRE(n == 0 || dmean || dloss, "%s: dmean and dloss must not both be NULL", fn);
+        REQUIRE(aligned(lse, 4) && aligned(dmean, 4) && aligned(dloss, 4), "%s: misaligned lse, dmean or dloss", fn);
+        TRY(check_matrix(fn, "dx", dx, dx_stride, n, dim, dtype, false, true));
+        TRY(check_matrix(fn, "dw", dw, dw_stride, vocab, dim, dtype, false, true));
+        TRY(check_workspace(fn, workspace, workspace_bytes,
+                            gs_label_loss_workspace_size(n, dim, vocab, dtype, 1)));
+        if (!dx && !dw) return GS_OK;
+        gs::LabelLossArgs a{};
+        a.n = n;
+        a.dim = dim;
+        a.vocab = (int)vocab;
+        a.half = dtype == GS_BF16;
+        a.wide_labels = index_type == GS_I64;
+        a.x = x;
+        a.w = w;
+        a.labels = labels;
+        a.x_stride = x_stride;
+        a.w_stride = w_stride;
+        a.lse = const_cast<float*>(lse);
+        a.dmean = dmean;
+        a.dloss = dloss;
+        a.dx = dx;
+        a.dx_stride = dx_stride;
+        a.dw = dw;
+        a.dw_stride = dw_stride;
+        return hip_check(gs::launch_label_loss_bwd(a, (char*)workspace, (hipStream_t)stream), fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_label_loss_bwd: unexpected exception");
+    }
+}
+
+}  // extern "C"

@@ -1648,4 +1648,31 @@ hipError_t launch_bin_emit(int n, int P, int P1, int TX, int TY, const float* de
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------- index sort (embed.hip)
+
+static_assert(RADIX_TOTAL_WORDS == 2 * RT * 256, "two digit-total buffers");
+
+size_t radix_sort_scratch(int64_t n) {
+    const size_t nblocks = ((size_t)n + RE - 1) / RE;
+    return align256(((size_t)RADIX_TOTAL_WORDS + 256 * nblocks) * sizeof(uint32_t));
+}
+
+hipError_t launch_radix_sort(int n, uint32_t max_key, uint32_t* const keys[2], uint32_t* const vals[2], char* scratch,
+                             int* sorted_at, hipStream_t s) {
+    uint32_t* rtot = reinterpret_cast<uint32_t*>(scratch);
+    uint32_t* hist = rtot + RADIX_TOTAL_WORDS;
+    int bits = 1;
+    while (bits < 32 && (max_key >> bits) != 0u) ++bits;
+    const int passes = (bits + 7) / 8, per = (bits + passes - 1) / passes;
+    int cur = 0;
+    for (int p = 0; p < passes; ++p, cur ^= 1) {
+        const int b = min(per, bits - p * per);
+        hipError_t e = radix_pass(SrcMem<uint32_t>{keys[cur], vals[cur]}, n, nullptr, p * per, b, hist, rtot, p,
+                                  keys[cur ^ 1], vals[cur ^ 1], s);
+        if (e != hipSuccess) return e;
+    }
+    *sorted_at = cur;
+    return hipSuccess;
+}
+
 }  // namespace gs

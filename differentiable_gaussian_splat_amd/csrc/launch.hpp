@@ -151,4 +151,51 @@ hipError_t launch_adam_step(const AdamLr& lr, float beta1, float beta2, float ep
                             float* const v[5], float* scales, float* opacities, float* grad_norm,
                             hipStream_t stream);
 
+// Stable ascending sort of n < 2^31 - 4096 (key, value) pairs, keys <= max_key, by the binning's
+// radix passes. keys[0], vals[0] hold the input, the sorted pairs end in keys[*sorted_at],
+// vals[*sorted_at]; the other buffers are overwritten. The scratch's first RADIX_TOTAL_WORDS
+// words are zero on entry.
+constexpr int RADIX_TOTAL_WORDS = 4096;
+size_t radix_sort_scratch(int64_t n);
+hipError_t launch_radix_sort(int n, uint32_t max_key, uint32_t* const keys[2], uint32_t* const vals[2], char* scratch,
+                             int* sorted_at, hipStream_t s);
+
+// Label learning (embed.hip, norm.hip, labelloss.hip). `half`: rows are bfloat16, otherwise
+// float32; strides count elements; index arrays are int64 with `wide_ids`, otherwise int32.
+struct EmbedLayout {
+    size_t keys[2], pos[2], sort, part, tail_key, end_block, total;
+};
+EmbedLayout embed_bwd_layout(int64_t n, int dim, int vocab);
+hipError_t launch_embed_fwd(int64_t n, int dim, int vocab, bool half, const void* table, int64_t table_stride,
+                            const void* ids, bool wide_ids, float scale, void* out, int64_t out_stride,
+                            hipStream_t stream);
+hipError_t launch_embed_bwd(int64_t n, int dim, int vocab, bool half, const void* ids, bool wide_ids, float scale,
+                            const void* dout, int64_t dout_stride, void* dtable, int64_t dtable_stride, char* ws,
+                            hipStream_t stream);
+
+size_t norm_bwd_workspace(int64_t n, int dim);
+hipError_t launch_norm_fwd(int64_t n, int dim, bool half, const void* x, int64_t xs, const void* weight,
+                           const void* bias, float eps, void* y, int64_t ys, float* mean, float* rstd,
+                           hipStream_t stream);
+hipError_t launch_norm_bwd(int64_t n, int dim, bool half, const void* x, int64_t xs, const void* weight,
+                           const float* mean, const float* rstd, const void* dy, int64_t dys, void* dx, int64_t dxs,
+                           void* dweight, void* dbias, float* part, hipStream_t stream);
+
+// One call of the vocabulary loss (device pointers; strides in elements). The backward reads
+// lse and writes dx and dw (either may be null); the forward writes loss, lse, mean and count.
+struct LabelLossArgs {
+    int64_t n;
+    int dim, vocab;
+    bool half, wide_labels;
+    const void *x, *w, *labels;
+    int64_t x_stride, w_stride, dx_stride, dw_stride;
+    float *loss, *lse, *mean;
+    int32_t* count;
+    const float *dmean, *dloss;  // either may be null
+    void *dx, *dw;
+};
+size_t label_loss_workspace(int64_t n, int dim, int vocab, bool half, bool backward);
+hipError_t launch_label_loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t stream);
+hipError_t launch_label_loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t stream);
+
 }  // namespace gs

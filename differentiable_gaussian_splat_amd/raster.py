@@ -74,7 +74,10 @@ EXPORTS = ["gs_default_options", "gs_version", "gs_last_error", "gs_release_thre
            "gs_render_fwd_views", "gs_render_bwd_raster_views", "gs_preprocess_bwd_views", "gs_adam_step",
            "gs_mb_render_bwd_naive", "gs_mb_render_bwd_adaptive", "gs_mb_hbm_read", "gs_mb_hbm_copy", "gs_mb_atomic", "gs_render_bwd_noalloc",
            "gs_mb_render_counts", "gs_surfel_preprocess", "gs_surfel_render_fwd", "gs_surfel_render_bwd_raster",
-           "gs_surfel_preprocess_bwd", "gs_surfel_render_bwd_workspace_size", "gs_surfel_render_bwd"]
+           "gs_surfel_preprocess_bwd", "gs_surfel_render_bwd_workspace_size", "gs_surfel_render_bwd",
+           "gs_embed_fwd", "gs_embed_bwd_workspace_size", "gs_embed_bwd", "gs_layer_norm_fwd",
+           "gs_layer_norm_bwd_workspace_size", "gs_layer_norm_bwd", "gs_label_loss_workspace_size",
+           "gs_label_loss_fwd", "gs_label_loss_bwd"]
 SURFEL_GRAD_STRIDE = 16
 NOALLOC_MAX_N = 1 << 20  # GS_NOALLOC_MAX_N
 MAX_VIEWS = 32
@@ -164,6 +167,26 @@ def load_library(path: str = LIB_PATH):
         L.gs_mb_hbm_copy.restype = i32
         L.gs_mb_atomic.argtypes = [P, i64, i64, i32, P]
         L.gs_mb_atomic.restype = i32
+        f32 = C.c_float
+        L.gs_embed_fwd.argtypes = [i64, i32, i64, i32, P, i64, P, i32, f32, P, i64, P]
+        L.gs_embed_fwd.restype = i32
+        L.gs_embed_bwd_workspace_size.argtypes = [i64, i32, i64, i32]
+        L.gs_embed_bwd_workspace_size.restype = sz
+        L.gs_embed_bwd.argtypes = [i64, i32, i64, i32, P, i32, f32, P, i64, P, i64, P, sz, P]
+        L.gs_embed_bwd.restype = i32
+        L.gs_layer_norm_fwd.argtypes = [i64, i32, i32, P, i64, P, P, f32, P, i64, P, P, P]
+        L.gs_layer_norm_fwd.restype = i32
+        L.gs_layer_norm_bwd_workspace_size.argtypes = [i64, i32, i32]
+        L.gs_layer_norm_bwd_workspace_size.restype = sz
+        L.gs_layer_norm_bwd.argtypes = [i64, i32, i32, P, i64, P, P, P, P, i64, P, i64, P, P, P, sz, P]
+        L.gs_layer_norm_bwd.restype = i32
+        L.gs_label_loss_workspace_size.argtypes = [i64, i32, i64, i32, i32]
+        L.gs_label_loss_workspace_size.restype = sz
+        L.gs_label_loss_fwd.argtypes = [i64, i32, i64, i32, P, i64, P, i64, P, i32] + [P] * 4 + [P, sz, P]
+        L.gs_label_loss_fwd.restype = i32
+        L.gs_label_loss_bwd.argtypes = ([i64, i32, i64, i32, P, i64, P, i64, P, i32] + [P] * 3 +
+                                        [P, i64, P, i64, P, sz, P])
+        L.gs_label_loss_bwd.restype = i32
         _lib = L
         return L
 

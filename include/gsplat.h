@@ -591,6 +591,98 @@ gs_status gs_mb_hbm_copy(void *dst, const void *src, size_t bytes, void *stream)
 gs_status gs_mb_atomic(float *records, int64_t n_records, int64_t n_ops, int32_t lanes_per_record,
                        void *stream);
 
+/* ------------------------------------------------------------------ label learning
+ *
+ * Labels of a scene's Gaussians (or of rendered pixels) from learned features:
+ * a feature codebook looked up by each Gaussian's code, layer normalisation,
+ * and the softmax cross entropy of the normalised features against a
+ * vocabulary of label rows, each with its gradients.
+ *
+ * Conventions of these calls, beside the ones above:
+ * - Matrices are row-major with consecutive columns; *_stride is the distance
+ *   of two rows in elements (an input's may be 0: one row for all; otherwise
+ *   at least the columns). They hold `dtype` elements, GS_F32 or GS_BF16, one
+ *   type per call; statistics, losses and lse are float32. Sums and statistics
+ *   are formed in float32 or wider and rounded once.
+ * - Index arrays hold `index_type` elements, GS_I32 or GS_I64. An index
+ *   outside [0, vocab) names nothing: its row takes no part (use -1).
+ * - Results are the same bit for bit from run to run (no atomics), and are
+ *   written, not added. Outputs must not overlap inputs.
+ * - Workspaces are 256-byte aligned, of at least the size the *_workspace_size
+ *   function gives (0 for arguments the call would refuse).
+ * - 0 <= n <= 2^30 rows, 1 <= dim <= 65536, 1 <= vocab <= 2^30. With n = 0 the
+ *   arrays of n rows may be NULL.
+ */
+#define GS_F32 0
+#define GS_BF16 1
+#define GS_I32 0
+#define GS_I64 1
+
+/*
+ * gs_embed_fwd -- out[i] = scale * table[ids[i]], a zero row where ids[i] names
+ * no row. table[vocab, dim], ids[n], out[n, dim].
+ */
+gs_status gs_embed_fwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, const void *table,
+                       int64_t table_stride, const void *ids, int32_t index_type, float scale, void *out,
+                       int64_t out_stride, void *stream);
+
+/*
+ * gs_embed_bwd -- dtable[v] = scale * sum over the rows i with ids[i] = v of
+ * dout[i]; every row of dtable[vocab, dim] is written (zeros where no index
+ * names it).
+ */
+size_t gs_embed_bwd_workspace_size(int64_t n, int32_t dim, int64_t vocab, int32_t dtype);
+gs_status gs_embed_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, const void *ids,
+                       int32_t index_type, float scale, const void *dout, int64_t dout_stride, void *dtable,
+                       int64_t dtable_stride, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gs_layer_norm_fwd -- y = (x - mean) rstd weight + bias per row, with the
+ * row's mean and rstd = 1 / sqrt(variance + eps) (the mean squared deviation),
+ * eps >= 0. x[n, dim], y[n, dim]; weight[dim], bias[dim] nullable (1 and 0);
+ * mean[n], rstd[n] nullable outputs, kept for the backward.
+ */
+gs_status gs_layer_norm_fwd(int64_t n, int32_t dim, int32_t dtype, const void *x, int64_t x_stride,
+                            const void *weight, const void *bias, float eps, void *y, int64_t y_stride,
+                            float *mean, float *rstd, void *stream);
+
+/*
+ * gs_layer_norm_bwd -- gradients of gs_layer_norm_fwd from dy[n, dim] and the
+ * forward's mean and rstd: dx[n, dim], dweight[dim], dbias[dim], each nullable.
+ */
+size_t gs_layer_norm_bwd_workspace_size(int64_t n, int32_t dim, int32_t dtype);
+gs_status gs_layer_norm_bwd(int64_t n, int32_t dim, int32_t dtype, const void *x, int64_t x_stride,
+                            const void *weight, const float *mean, const float *rstd, const void *dy,
+                            int64_t dy_stride, void *dx, int64_t dx_stride, void *dweight, void *dbias,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gs_label_loss_fwd -- softmax cross entropy of x[n, dim] against the label
+ * rows w[vocab, dim]: with z_v = x[i] . w[v],
+ *     lse[i] = log sum_v exp z_v,   loss[i] = lse[i] - z_labels[i],
+ * both 0 where labels[i] names no label (whatever x[i] holds); mean[0] = the
+ * losses' mean over the labelled rows (0 if there is none), count[0] = their
+ * number. The logits are never stored.
+ */
+size_t gs_label_loss_workspace_size(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, int32_t backward);
+gs_status gs_label_loss_fwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, const void *x,
+                            int64_t x_stride, const void *w, int64_t w_stride, const void *labels,
+                            int32_t index_type, float *loss, float *lse, float *mean, int32_t *count,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gs_label_loss_bwd -- gradients from the same inputs and the forward's lse.
+ * The upstream gradient of row i is dloss[i] (dloss[n], of the losses) plus
+ * dmean[0] / labelled rows (dmean[1], of their mean); either may be NULL, not
+ * both. dx[n, dim] (zero rows where there is no label), dw[vocab, dim], each
+ * nullable. Workspace: gs_label_loss_workspace_size with backward = 1.
+ */
+gs_status gs_label_loss_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, const void *x,
+                            int64_t x_stride, const void *w, int64_t w_stride, const void *labels,
+                            int32_t index_type, const float *lse, const float *dmean, const float *dloss,
+                            void *dx, int64_t dx_stride, void *dw, int64_t dw_stride, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

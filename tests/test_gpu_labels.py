@@ -1,0 +1,638 @@
+"""The label-learning operators (codebook lookup, layer normalisation,
+vocabulary loss) against plain forms in 64 bits on the same inputs.
+
+Tolerances are the operators' own error bounds, entry by entry. With u the
+float32 half step (2^-24) and ut the half step of the result's type
+(finfo.eps / 2), a sum of k terms in float32 is off by at most about
+k u sum |terms| (k: the longest chain of additions, which for a tree over lanes
+is the terms per lane plus the levels), a product or quotient by u of itself,
+and the stored result by ut of itself. Errors of intermediate values are
+carried through the formulas by their magnitudes. Where entries of a gradient
+pass through bfloat16 on the way (dz), each is off by 2^-8 of itself at most.
+"""
+import math
+
+import pytest
+import torch
+
+from differentiable_gaussian_splat_amd import labels as L
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+F32, BF16 = torch.float32, torch.bfloat16
+TYPES = [F32, BF16]
+IDS = ["f32", "bf16"]
+DEV = "cuda"
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape, dtype=F32, pad=0, offset=0):
+    """Normal values; with pad (offset) columns of a wider matrix, starting at column offset."""
+    t = torch.randn((shape[0], shape[1] + pad + offset), generator=g, device=DEV).to(dtype)
+    return t[:, offset:offset + shape[1]]
+
+
+def within(name, got, ref, tol):
+    got, ref = got.double(), ref.double()
+    bad = ~((got - ref).abs() <= tol) & ~(got.isnan() & ref.isnan()) & ~(got == ref)
+    if bad.any():
+        i = torch.nonzero(bad)[0].tolist()
+        raise AssertionError(f"{name}: {int(bad.sum())} of {bad.numel()} off, first at {i}: got {got[tuple(i)]}, "
+                             f"expected {ref[tuple(i)]}, tolerance {tol.expand_as(ref)[tuple(i)]}")
+
+
+def empty(*shape, dtype=F32, fill=float("nan")):
+    """An output buffer full of NaN, so that an entry left unwritten shows."""
+    return torch.full(shape, fill, dtype=dtype, device=DEV)
+
+
+def ws_of(size):
+    # full of NaN patterns: a kernel that reads what it has not written shows
+    return torch.full((max(size, 1),), 0xFF, dtype=torch.uint8, device=DEV)
+
+
+# ------------------------------------------------------------------ codebook lookup
+
+def embed_ref(table, ids, scale):
+    ok = (ids >= 0) & (ids < table.shape[0])
+    out = table.double()[ids.long().clamp(0, table.shape[0] - 1)] * scale
+    return torch.where(ok[:, None], out, 0.0)
+
+
+def run_embed(table, ids, dout, scale, out=None, dtable=None):
+    n, dim = dout.shape
+    out = empty(n, dim, dtype=table.dtype) if out is None else out
+    dtable = empty(table.shape[0], dim, dtype=table.dtype) if dtable is None else dtable
+    L.gs_embed_fwd(table, ids, out, scale)
+    ws = ws_of(L.gs_embed_bwd_workspace_size(n, dim, table.shape[0], table.dtype))
+    L.gs_embed_bwd(ids, dout, dtable, ws, scale)
+    return out, dtable
+
+
+def check_embed(table, ids, dout, scale):
+    out, dtable = run_embed(table, ids, dout, scale)
+    s = float(torch.tensor(scale, dtype=F32))
+    ref = embed_ref(table, ids, s)
+    ut = half_step(table.dtype)
+    within("out", out, ref, ref.abs() * (ut + 2 * U))
+    vocab = table.shape[0]
+    ok = (ids >= 0) & (ids < vocab)
+    rows = ids.long()[ok]
+    d = dout.double()[ok]
+    ref = torch.zeros((vocab, dout.shape[1]), dtype=torch.float64, device=DEV).index_add_(0, rows, d * s)
+    mag = torch.zeros_like(ref).index_add_(0, rows, (d * s).abs())
+    # chain: 32 positions of a lane group, up to 32 group sums, the blocks of a run over 128 or fewer groups
+    chain = 32 + 64 + 16 + ids.shape[0] / 128 / 16
+    within("dtable", dtable, ref, mag * chain * U + ref.abs() * (ut + 2 * U))
+    assert (dtable[torch.bincount(rows, minlength=vocab) == 0] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("n,dim,vocab", [(1, 1, 1), (1, 64, 5), (33, 32, 500), (64, 7, 3), (129, 8, 2), (1000, 24, 17),
+                                         (513, 65, 1000), (4097, 128, 255), (2050, 300, 256), (777, 1030, 70_000)])
+def test_embed(n, dim, vocab, dtype):
+    g = gen(n + dim)
+    table, dout = randn(g, vocab, dim, dtype=dtype), randn(g, n, dim, dtype=dtype)
+    ids = torch.randint(-1, vocab, (n,), generator=g, device=DEV)
+    check_embed(table, ids if dim % 2 else ids.int(), dout, 1.7)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_embed_long_runs(dtype):
+    """One code that most rows name, runs that end at block borders, a code per row."""
+    g = gen(3)
+    n, dim, vocab = 20_000, 40, 300
+    table, dout = randn(g, vocab, dim, dtype=dtype), randn(g, n, dim, dtype=dtype)
+    mostly = torch.where(torch.rand(n, generator=g, device=DEV) < 0.8, 7, torch.randint(0, vocab, (n,), generator=g,
+                                                                                       device=DEV))
+    check_embed(table, mostly, dout, 0.5)
+    check_embed(table, torch.zeros_like(mostly), dout, 0.5)
+    check_embed(table, torch.full_like(mostly, vocab - 1), dout, 0.5)
+    for run in (128, 256, 512, 1024, 32, 31):
+        check_embed(table, (torch.arange(n, device=DEV) // run) % vocab, dout, 0.5)
+
+
+def test_embed_indices_that_name_nothing():
+    g = gen(4)
+    table, dout = randn(g, 50, 16), randn(g, 300, 16)
+    dout[::3] = float("nan")
+    ids = torch.randint(0, 50, (300,), generator=g, device=DEV)
+    ids[::3] = torch.tensor([-1, 50, -2 ** 40, 2 ** 33 + 1, 2 ** 62] * 20, device=DEV)
+    check_embed(table, ids, dout, 1.0)
+    out, dtable = run_embed(table, torch.full((300,), -1, device=DEV), dout, 1.0)
+    assert (out == 0).all() and (dtable == 0).all()
+
+
+@pytest.mark.parametrize("pad,offset", [(5, 0), (8, 8), (3, 1)])
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_embed_strided(pad, offset, dtype):
+    g = gen(5)
+    n, dim, vocab = 700, 32, 90
+    table = randn(g, vocab, dim, dtype=dtype, pad=pad, offset=offset)
+    dout = randn(g, n, dim, dtype=dtype, pad=pad, offset=offset)
+    ids = torch.randint(0, vocab, (n,), generator=g, device=DEV, dtype=torch.int32)
+    a = run_embed(table, ids, dout, 1.25)
+    wide_o, wide_t = empty(n, dim + pad + offset, dtype=dtype), empty(vocab, dim + pad + offset, dtype=dtype)
+    cols = slice(offset, offset + dim)
+    run_embed(table, ids, dout, 1.25, wide_o[:, cols], wide_t[:, cols])
+    assert torch.equal(wide_o[:, cols], a[0])
+    # other groupings of the same sums: equal up to their order
+    within("dtable", wide_t[:, cols], a[1], (a[1].double().abs() + 10) * 2 * half_step(dtype))
+    for w in (wide_o, wide_t):  # nothing beside the rows is written
+        assert w[:, :offset].isnan().all() and w[:, offset + dim:].isnan().all()
+    check_embed(table, ids, dout, 1.25)
+    check_embed(table, ids, dout[:1].expand(n, dim), 1.25)  # one gradient row for all
+
+
+def test_embed_offsets_past_32_bits():
+    vocab, dim = 40_000_000, 64  # 2.56e9 elements
+    table = torch.zeros((vocab, dim), dtype=BF16, device=DEV)
+    ids = torch.tensor([vocab - 1, 0, vocab - 2, 33_600_000, vocab - 1], device=DEV)
+    table[ids] = randn(gen(6), 5, dim, dtype=BF16)
+    out = empty(5, dim, dtype=BF16)
+    L.gs_embed_fwd(table, ids, out, 2.0)
+    assert torch.equal(out, table[ids] * 2)
+    dout = randn(gen(7), 5, dim, dtype=BF16)
+    ws = ws_of(L.gs_embed_bwd_workspace_size(5, dim, vocab, BF16))
+    L.gs_embed_bwd(ids, dout, table, ws, 1.0)
+    within("dtable", table[ids[1:]], torch.stack([dout[1], dout[2], dout[3], (dout[0].float() + dout[4].float()).to(BF16)]),
+           torch.zeros((), device=DEV, dtype=torch.float64))
+    table[ids] = 0
+    assert int(torch.count_nonzero(table.view(torch.int32))) == 0
+
+
+# ------------------------------------------------------------------ layer normalisation
+
+def check_norm(x, weight, bias, dy, eps=1e-5):
+    n, dim = x.shape
+    dtype = x.dtype
+    y, dx = empty(n, dim, dtype=dtype), empty(n, dim, dtype=dtype)
+    mean, rstd = empty(n), empty(n)
+    dw, db = (empty(dim, dtype=dtype) if weight is not None else None for _ in range(2))
+    L.gs_layer_norm_fwd(x, weight, bias, y, mean, rstd, eps)
+    ws = ws_of(L.gs_layer_norm_bwd_workspace_size(n, dim, dtype))
+    L.gs_layer_norm_bwd(x, weight, mean, rstd, dy, dx, dw, db, ws)
+    X, G = x.double(), dy.double()
+    W = weight.double() if weight is not None else torch.ones(dim, dtype=torch.float64, device=DEV)
+    B = bias.double() if bias is not None else torch.zeros(dim, dtype=torch.float64, device=DEV)
+    e = float(torch.tensor(eps, dtype=F32))
+    M = X.mean(1, keepdim=True)
+    R = 1 / torch.sqrt(((X - M) ** 2).mean(1, keepdim=True) + e)
+    H = (X - M) * R
+    ut = half_step(dtype)
+    # terms per lane (32 at most in registers, dim / 256 beyond), the levels of the tree, the single steps after it
+    c = (32 + 16 + max(0, dim / 256 - 32)) * U
+    me = c * X.abs().mean(1, keepdim=True)      # of the mean
+    he = 2 * c * H.abs() + R * me + 2 * U * R * X.abs()   # of x hat
+    within("mean", mean, M[:, 0], me[:, 0])
+    within("rstd", rstd, R[:, 0], (R * (2 * c + (R * me) ** 2))[:, 0])
+    Y = H * W + B
+    within("y", y, Y, he * W.abs() + 4 * U * ((H * W).abs() + B.abs()) + ut * Y.abs())
+    A = G * W
+    mg, mx = A.mean(1, keepdim=True), (A * H).mean(1, keepdim=True)
+    ha = H.abs()
+    aa, ax = A.abs().mean(1, keepdim=True), (A.abs() * ha).mean(1, keepdim=True)
+    D = R * (A - mg - H * mx)
+    mxe = (A.abs() * he).mean(1, keepdim=True) + 2 * c * ax
+    tol = R * (2 * c * aa + he * mx.abs() + ha * mxe + he * mxe + 4 * U * (A.abs() + mg.abs() + (H * mx).abs()))
+    within("dx", dx, D, tol + D.abs() * (2 * c + ut))
+    if weight is not None:
+        rows = n / 1024 + 1 + 8 + 4 + 1024 / 64 + 6   # a group's rows, groups of a wave, waves, blocks of a column
+        DW, DB = (G * H).sum(0), G.sum(0)
+        within("dweight", dw, DW, (G.abs() * (he + rows * U * ha)).sum(0) + DW.abs() * ut)
+        within("dbias", db, DB, rows * U * G.abs().sum(0) + DB.abs() * ut)
+    return y, dx
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("n,dim", [(1, 1), (1, 64), (5, 2), (64, 64), (33, 32), (1001, 27), (70, 128), (257, 129),
+                                   (40, 256), (19, 512), (31, 771), (9, 1024), (7, 2048), (3, 2056), (5, 4096),
+                                   (2, 5000), (3, 8192), (4, 8193), (2, 30_000), (5000, 16)])
+def test_norm(n, dim, dtype):
+    g = gen(n * dim)
+    x = (randn(g, n, dim).mul_(1.5).add_(0.7)).to(dtype)
+    w, b = randn(g, 1, dim, dtype=dtype)[0], randn(g, 1, dim, dtype=dtype)[0]
+    check_norm(x, w, b, randn(g, n, dim, dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_norm_without_weights_and_strided(dtype):
+    g = gen(11)
+    check_norm(randn(g, 65, 96, dtype=dtype), None, None, randn(g, 65, 96, dtype=dtype))
+    for pad, offset in ((8, 8), (5, 0), (2, 3)):
+        x = randn(g, 100, 72, dtype=dtype, pad=pad, offset=offset)
+        dy = randn(g, 100, 72, dtype=dtype, pad=pad, offset=offset)
+        w, b = randn(g, 1, 72, dtype=dtype)[0], randn(g, 1, 72, dtype=dtype)[0]
+        check_norm(x, w, b, dy)
+    check_norm(x, w, b, dy[:1].expand(100, 72))
+    # rows and weights that are not 16-byte aligned, though their strides are
+    w2 = torch.zeros(73, dtype=dtype, device=DEV)
+    w2[1:] = w
+    check_norm(randn(g, 100, 72, dtype=dtype), w2[1:], b, randn(g, 100, 72, dtype=dtype))
+
+
+def test_norm_large_offset_keeps_the_variance():
+    """Rows far from zero: the variance is of the deviations, not a difference of squares."""
+    g = gen(12)
+    x = randn(g, 200, 64) + 1000.0
+    w, b = randn(g, 1, 64)[0], randn(g, 1, 64)[0]
+    check_norm(x, w, b, randn(g, 200, 64))
+
+
+def test_norm_constant_rows_and_empty():
+    x = torch.full((3, 40), 2.5, device=DEV)
+    y = empty(3, 40)
+    L.gs_layer_norm_fwd(x, None, None, y, eps=1e-5)
+    assert (y == 0).all()
+    e = torch.empty((0, 40), device=DEV)
+    v = torch.empty(0, device=DEV)
+    dw, db = empty(40), empty(40)
+    L.gs_layer_norm_fwd(e, None, None, e.clone(), v, v.clone())
+    L.gs_layer_norm_bwd(e, None, v, v, e, e.clone(), dw, db, ws_of(256))
+    assert (dw == 0).all() and (db == 0).all()
+
+
+def test_norm_bad_row_stays_in_its_row():
+    g = gen(13)
+    x = randn(g, 20, 48)
+    x[3, 5], x[7, 0] = float("nan"), float("inf")
+    y = empty(20, 48)
+    L.gs_layer_norm_fwd(x, None, None, y)
+    bad = torch.zeros(20, dtype=torch.bool, device=DEV)
+    bad[[3, 7]] = True
+    assert y[bad].isnan().any(1).all() and y[~bad].isfinite().all()
+
+
+# ------------------------------------------------------------------ vocabulary loss
+
+def run_loss(x, w, labels, dmean=None, dloss=None):
+    n, dim = x.shape
+    vocab = w.shape[0]
+    loss, lse, mean, count = empty(n), empty(n), empty(1), torch.full((1,), -7, dtype=torch.int32, device=DEV)
+    ws = ws_of(L.gs_label_loss_workspace_size(n, dim, vocab, x.dtype, True))
+    L.gs_label_loss_fwd(x, w, labels, loss, lse, mean, count, ws)
+    dx, dw = empty(n, dim, dtype=x.dtype), empty(vocab, dim, dtype=x.dtype)
+    ws.fill_(0xFF)
+    L.gs_label_loss_bwd(x, w, labels, lse, dx, dw, ws, dmean, dloss)
+    return loss, lse, mean, count, dx, dw
+
+
+def check_loss(x, w, labels, dmean=None, dloss=None):
+    n, dim = x.shape
+    vocab, dtype = w.shape[0], x.dtype
+    loss, lse, mean, count, dx, dw = run_loss(x, w, labels, dmean, dloss)
+    have = (labels >= 0) & (labels < vocab)
+    X = torch.where(have[:, None], x, 0).double()  # a row without a label may hold anything
+    W = w.double()
+    cnt = int(have.sum())
+    assert int(count) == cnt
+    Z = X @ W.t()
+    # products to float32's own rounding (bfloat16 ones are exact; split float32 ones leave out less than
+    # 3 x 2^-24 of the magnitudes), sums over dim terms in float32 (six sums of parts)
+    ze = (X.abs() @ W.abs().t()) * ((dim + 8) * U)
+    lab = labels.long().clamp(0, vocab - 1)[:, None]
+    S = torch.logsumexp(Z, 1)
+    p = torch.exp(Z - S[:, None])
+    se = (p * ze).sum(1) + (64 + vocab / 256) * U + 4 * U * S.abs()
+    T = torch.where(have, S - Z.gather(1, lab)[:, 0], 0.0)
+    te = torch.where(have, se + ze.gather(1, lab)[:, 0] + 4 * U * (S.abs() + Z.gather(1, lab)[:, 0].abs()), 0.0)
+    within("lse", lse, torch.where(have, S, 0.0), se)
+    within("loss", loss, T, te)
+    within("mean", mean, T.sum().reshape(1) / max(cnt, 1), te.sum().reshape(1) / max(cnt, 1) + T.sum().abs() * U)
+    up = torch.zeros(n, dtype=torch.float64, device=DEV)
+    if dloss is not None:
+        up = up + dloss.double()
+    if dmean is not None:
+        up = up + dmean.double() / max(cnt, 1)
+    up = torch.where(have, up, 0.0)[:, None]
+    dz = p.clone().scatter_add_(1, lab, torch.full_like(up, -1.0)) * up
+    through = 2.0 ** -8 if dtype == BF16 else 4 * U
+    pe = p * (ze + se[:, None] + 8 * U * (1 + Z.abs() + S.abs()[:, None]))
+    dze = up.abs() * pe + dz.abs() * (through + 4 * U) + 2.0 ** -126
+    ut = half_step(dtype)
+    DX, DW = dz @ W, dz.t() @ X
+    within("dx", dx, DX, dze @ W.abs() + (dz.abs() @ W.abs()) * ((vocab + 80) * U) + DX.abs() * ut)
+    within("dw", dw, DW, dze.t() @ X.abs() + (dz.abs().t() @ X.abs()) * ((n + 80) * U) + DW.abs() * ut)
+    # as a whole: independent roundings do not add up
+    for name, got, ref in (("dx", dx, DX), ("dw", dw, DW)):
+        size = float(ref.norm())
+        err = float((got.double() - ref).norm())
+        # dz and the result to bfloat16: half a step each at most; float32: a few units of 2^-24 per product
+        limit = 2 * 2.0 ** -8 if dtype == BF16 else 2e-5
+        assert err <= limit * size + 1e-30, (name, err, size)
+    return loss, lse, mean, count, dx, dw
+
+
+def loss_inputs(seed, n, dim, vocab, dtype, missing=0.2, wide=True):
+    g = gen(seed)
+    w = (randn(g, vocab, dim) / math.sqrt(dim)).to(dtype)
+    labels = torch.randint(0, vocab, (n,), generator=g, device=DEV)
+    x = (randn(g, n, dim) + 2 * w[labels].float()).to(dtype)
+    labels = torch.where(torch.rand(n, generator=g, device=DEV) < missing, -1, labels)
+    return x, w, labels if wide else labels.int(), g
+
+
+ONE = lambda: torch.ones(1, device=DEV)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("n,dim,vocab", [(1, 1, 1), (1, 64, 1000), (2, 8, 2), (48, 32, 1000), (128, 64, 128),
+                                         (129, 65, 129), (300, 129, 2000), (1000, 64, 20), (513, 256, 777),
+                                         (260, 512, 4099), (9000, 16, 130)])
+def test_loss(n, dim, vocab, dtype):
+    x, w, labels, g = loss_inputs(n + vocab, n, dim, vocab, dtype, wide=bool(n % 2))
+    check_loss(x, w, labels, dmean=ONE())
+    check_loss(x, w, labels, dloss=torch.rand(n, generator=g, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_loss_both_upstream_gradients(dtype):
+    x, w, labels, g = loss_inputs(21, 200, 40, 333, dtype)
+    check_loss(x, w, labels, dmean=torch.full((1,), -0.75, device=DEV),
+               dloss=torch.randn(200, generator=g, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_loss_rows_without_label_take_no_part(dtype):
+    x, w, labels, g = loss_inputs(22, 400, 48, 500, dtype, missing=0.5)
+    off = labels < 0
+    ref = check_loss(x, w, labels, dmean=ONE())
+    labels = labels.clone()
+    labels[off] = torch.tensor([-1, 500, -100, 2 ** 40, -2 ** 50], device=DEV).repeat(100)[:int(off.sum())]
+    x = x.clone()
+    x[off] = torch.tensor([float("nan"), float("inf"), -float("inf"), torch.finfo(dtype).min],
+                          device=DEV).repeat(200)[:int(off.sum())].to(dtype)[:, None]
+    got = check_loss(x, w, labels, dmean=ONE())
+    for a, b in zip(ref, got):
+        assert torch.equal(a, b)
+    assert (got[0][off] == 0).all() and (got[4][off] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("n", [0, 1, 130, 9000])
+def test_loss_no_row_with_a_label(n, dtype):
+    g = gen(23)
+    x, w = randn(g, max(n, 1), 33, dtype=dtype)[:n], randn(g, 70, 33, dtype=dtype)
+    x.fill_(float("nan"))
+    labels = torch.full((n,), -1, device=DEV)
+    loss, lse, mean, count, dx, dw = run_loss(x, w, labels, dmean=ONE())
+    assert int(count) == 0 and float(mean) == 0
+    for t in (loss, lse, dx, dw):
+        assert (t == 0).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_loss_one_row_with_a_label(dtype):
+    x, w, labels, _ = loss_inputs(24, 10_000, 24, 300, dtype, missing=2.0)
+    labels[9_999] = 299
+    check_loss(x, w, labels, dmean=ONE())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_loss_vocabulary_rows_masked_by_the_lowest_value(dtype):
+    """A constant feature column with the type's lowest value in some label rows takes those labels out."""
+    x, w, labels, _ = loss_inputs(25, 150, 32, 600, dtype)
+    x[:, 0] = 1.0
+    w[:, 0] = 0.0
+    kept = torch.arange(600, device=DEV) % 3 != 1
+    labels = torch.where(labels >= 0, labels // 3 * 3, labels)
+    w[~kept, 0] = torch.finfo(dtype).min
+    loss, lse, mean, count, dx, dw = run_loss(x, w, labels, dmean=ONE())
+    pos = torch.cumsum(kept, 0) - 1
+    sub = torch.where(labels >= 0, pos[labels.clamp(min=0)], -1)
+    a = run_loss(x, w[kept].contiguous(), sub, dmean=ONE())
+    # the same sums over fewer terms (zeros left out), grouped otherwise
+    within("loss", loss, a[0], (a[0].abs() + 10).double() * 64 * U)
+    assert (dw[~kept] == 0).all() and dx[:, 1:].isfinite().all()
+    within("dw", dw[kept], a[5], a[5].double().abs() * 2 * half_step(dtype) + float(a[5].float().abs().max()) * 2e-3)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_loss_large_logits(dtype):
+    """Logits of a few hundred: exp overflows without the running maximum."""
+    x, w, labels, _ = loss_inputs(26, 100, 64, 400, dtype)
+    check_loss((x.float() * 60).to(dtype), w, labels, dmean=ONE())
+
+
+def test_loss_nan_stays_in_its_row():
+    x, w, labels, _ = loss_inputs(27, 64, 40, 300, F32, missing=0.0)
+    x[5, 3] = float("nan")
+    loss = run_loss(x, w, labels, dmean=ONE())[0]
+    ok = torch.arange(64, device=DEV) != 5
+    assert loss[5].isnan() and loss[ok].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_loss_strided(dtype):
+    g = gen(28)
+    n, dim, vocab = 140, 64, 260
+    labels = torch.randint(-1, vocab, (n,), generator=g, device=DEV)
+    for pad, offset in ((8, 0), (8, 8), (3, 0), (64, 1)):
+        x = randn(g, n, dim, dtype=dtype, pad=pad, offset=offset)
+        w = (randn(g, vocab, dim, pad=pad, offset=offset) / 8).to(dtype)
+        ref = check_loss(x.contiguous(), w.contiguous(), labels, dmean=ONE())
+        got = run_loss(x, w, labels, dmean=ONE())
+        for a, b in zip(ref, got):
+            assert torch.equal(a, b)
+        # a matrix whose last row ends its memory
+        flat = w.new_zeros((vocab - 1) * (dim + pad) + dim)
+        tail = torch.as_strided(flat, (vocab, dim), (dim + pad, 1))
+        tail.copy_(w)
+        for a, b in zip(ref, run_loss(x, tail, labels, dmean=ONE())):
+            assert torch.equal(a, b)
+        # outputs with space between the rows
+        wide_x, wide_w = empty(n, dim + 5, dtype=dtype), empty(vocab, dim + 5, dtype=dtype)
+        ws = ws_of(L.gs_label_loss_workspace_size(n, dim, vocab, dtype, True))
+        L.gs_label_loss_bwd(x, w, labels, ref[1], wide_x[:, :dim], wide_w[:, :dim], ws, dmean=ONE())
+        assert torch.equal(wide_x[:, :dim], ref[4]) and torch.equal(wide_w[:, :dim], ref[5])
+        assert wide_x[:, dim:].isnan().all() and wide_w[:, dim:].isnan().all()
+        for dx, dw in ((wide_x[:, :dim], None), (None, wide_w[:, :dim])):  # either gradient alone
+            L.gs_label_loss_bwd(x, w, labels, ref[1], dx, dw, ws, dmean=ONE())
+        assert torch.equal(wide_x[:, :dim], ref[4]) and torch.equal(wide_w[:, :dim], ref[5])
+    check_loss(x[:1].expand(n, dim), w, labels, dmean=ONE())
+
+
+def test_loss_backward_in_pieces():
+    """A vocabulary of more rows than one piece of the workspace holds."""
+    n, dim, vocab = 3, 8, (1 << 21) + 5
+    assert L.gs_label_loss_workspace_size(n, dim, vocab, BF16, True) < 128 * vocab * 2 + (1 << 30)
+    x, w, labels, _ = loss_inputs(29, n, dim, vocab, BF16, missing=0.0)
+    labels[0], labels[2] = vocab - 1, (1 << 21) - 1
+    check_loss(x, w, labels, dmean=ONE())
+
+
+def test_loss_forward_in_pieces():
+    n, dim, vocab = 16_384, 8, 131_072 + 77
+    x, w, labels, _ = loss_inputs(30, n, dim, vocab, BF16, missing=0.0)
+    labels[:2] = torch.tensor([vocab - 1, 131_071], device=DEV)
+    loss, lse, mean, count = empty(n), empty(n), empty(1), torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = ws_of(L.gs_label_loss_workspace_size(n, dim, vocab, BF16, False))
+    L.gs_label_loss_fwd(x, w, labels, loss, lse, mean, count, ws)
+    r = torch.cat([torch.arange(40, device=DEV), torch.arange(n - 40, n, device=DEV)])
+    Z = x[r].double() @ w.double().t()
+    S = torch.logsumexp(Z, 1)
+    within("lse", lse[r], S, (64 + vocab / 256) * U + 16 * U * S.abs() + 40 * U * Z.abs().max(1).values)
+    T = S - Z.gather(1, labels[r][:, None])[:, 0]
+    within("loss", loss[r], T, (64 + vocab / 256) * U + 16 * U * S.abs() + 40 * U * Z.abs().max(1).values)
+    within("mean", mean, loss.double().mean().reshape(1), loss.double().mean().reshape(1) * 2 * U)
+
+
+# ------------------------------------------------------------------ together
+
+def test_bitwise_repeatable():
+    x, w, labels, g = loss_inputs(31, 700, 96, 1500, BF16)
+    a, b = (run_loss(x, w, labels, dmean=ONE()) for _ in range(2))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    ids = torch.randint(0, 40, (9000,), generator=g, device=DEV)
+    table, dout = randn(g, 40, 24), randn(g, 9000, 24)
+    a, b = (run_embed(table, ids, dout, 1.0) for _ in range(2))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def head_ref(codes, labels, P, scale, eps):
+    """The chain of the three operators in the parameters' own (64-bit) arithmetic; codes and labels may be -1."""
+    f = torch.where((codes >= 0)[:, None], P["codebook"][codes.clamp(min=0)] * scale, 0.0)
+    m = f.mean(1, keepdim=True)
+    h = (f - m) / torch.sqrt(((f - m) ** 2).mean(1, keepdim=True) + eps)
+    z = (h * P["weight"] + P["bias"]) @ P["vocabulary"].t()
+    have = labels >= 0
+    loss = torch.logsumexp(z, 1) - z.gather(1, labels.clamp(min=0)[:, None])[:, 0]
+    return (loss * have).sum() / have.sum()
+
+
+def test_head_gradients_against_differences():
+    """The whole chain's gradients (float32) along random directions, against central differences of the 64-bit
+    form. The difference's own error is h^2 / 6 of a third derivative of order one, 1e-9 here; float32 gradients
+    are good to about 1e-5 of their norm."""
+    torch.manual_seed(5)
+    head = L.LabelHead(60, 48, 200)
+    with torch.no_grad():
+        head.weight.add_(0.1 * torch.randn_like(head.weight))
+        head.bias.add_(0.1 * torch.randn_like(head.bias))
+    g = gen(32)
+    codes = torch.randint(-1, 60, (500,), generator=g, device=DEV)
+    labels = torch.randint(-1, 200, (500,), generator=g, device=DEV)
+    head(codes, labels).backward()
+    P = {k: v.detach().double() for k, v in head.named_parameters()}
+    value = float(head(codes, labels).detach())
+    assert abs(value - float(head_ref(codes, labels, P, head.scale, head.eps))) < 2e-6 * (1 + abs(value))
+    h = 1e-4
+    for k, v in head.named_parameters():
+        d = torch.randn(v.shape, generator=g, device=DEV, dtype=torch.float64)
+        plus, minus = (head_ref(codes, labels, {**P, k: P[k] + s * h * d}, head.scale, head.eps) for s in (1, -1))
+        slope = float((plus - minus) / (2 * h))
+        got = float((v.grad.double() * d).sum())
+        assert abs(got - slope) <= 2e-5 * float(v.grad.double().norm() * d.norm()) + 1e-8, (k, got, slope)
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+def test_autograd_reductions(reduction):
+    x, w, labels, g = loss_inputs(33, 90, 40, 210, F32)
+    x.requires_grad_(True)
+    w.requires_grad_(True)
+    out = L.label_loss(x, w, labels, reduction)
+    up = torch.rand(90, generator=g, device=DEV)
+    (out * up if reduction == "none" else out * 0.5).sum().backward()
+    X, W = x.detach().double().requires_grad_(True), w.detach().double().requires_grad_(True)
+    z = X @ W.t()
+    have = labels >= 0
+    l = (torch.logsumexp(z, 1) - z.gather(1, labels.clamp(min=0)[:, None])[:, 0]) * have
+    ref = dict(mean=lambda: l.sum() / have.sum() * 0.5, sum=lambda: l.sum() * 0.5, none=lambda: (l * up).sum())
+    ref[reduction]().backward()
+    for a, b in ((x.grad, X.grad), (w.grad, W.grad)):
+        assert float((a.double() - b).norm()) <= 2e-5 * float(b.norm())
+
+
+def test_partial_gradients_and_frozen_inputs():
+    x, w, labels, _ = loss_inputs(34, 50, 16, 40, F32)
+    w.requires_grad_(True)
+    L.label_loss(x, w, labels).backward()
+    assert x.grad is None and w.grad.isfinite().all()
+    v = torch.randn((50, 16), device=DEV, requires_grad=True)
+    L.layer_norm(v.t().contiguous().t()).sum().backward()  # columns apart, a broadcast gradient
+    assert v.grad.abs().max() < 1e-5
+
+
+def test_on_a_side_stream():
+    x, w, labels, _ = loss_inputs(35, 300, 64, 900, BF16)
+    ref = run_loss(x, w, labels, dmean=ONE())
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = run_loss(x, w, labels, dmean=ONE())
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+def test_captured_step_replays():
+    """The calls recorded into a graph: replayed on changed inputs, with eager work between the replays."""
+    n, dim, codes, vocab = 1500, 64, 300, 700
+    g = gen(36)
+    table, w = randn(g, codes, dim), randn(g, vocab, dim) / 8
+    lw, lb = randn(g, 1, dim)[0], randn(g, 1, dim)[0]
+    ids = torch.randint(-1, codes, (n,), generator=g, device=DEV)
+    labels = torch.randint(-1, vocab, (n,), generator=g, device=DEV)
+    one = ONE()
+    ws = ws_of(max(L.gs_label_loss_workspace_size(n, dim, vocab, F32, True),
+                   L.gs_embed_bwd_workspace_size(n, dim, codes, F32), L.gs_layer_norm_bwd_workspace_size(n, dim, F32)))
+    B = dict(f=empty(n, dim), y=empty(n, dim), mean=empty(n), rstd=empty(n), loss=empty(n), lse=empty(n), avg=empty(1),
+             count=torch.zeros(1, dtype=torch.int32, device=DEV), dy=empty(n, dim), dw=empty(vocab, dim),
+             df=empty(n, dim), dlw=empty(dim), dlb=empty(dim), dtable=empty(codes, dim))
+
+    def step():
+        L.gs_embed_fwd(table, ids, B["f"], 8.0)
+        L.gs_layer_norm_fwd(B["f"], lw, lb, B["y"], B["mean"], B["rstd"])
+        L.gs_label_loss_fwd(B["y"], w, labels, B["loss"], B["lse"], B["avg"], B["count"], ws)
+        L.gs_label_loss_bwd(B["y"], w, labels, B["lse"], B["dy"], B["dw"], ws, dmean=one)
+        L.gs_layer_norm_bwd(B["f"], lw, B["mean"], B["rstd"], B["dy"], B["df"], B["dlw"], B["dlb"], ws)
+        L.gs_embed_bwd(ids, B["df"], B["dtable"], ws, 8.0)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for k in range(4):
+        ids.copy_(torch.randint(-1, codes, (n,), generator=g, device=DEV))
+        labels.copy_(torch.randint(-1, vocab, (n,), generator=g, device=DEV))
+        if k == 2:
+            labels.fill_(-1)
+        table.copy_(randn(g, codes, dim))
+        step()
+        want = {k_: v.clone() for k_, v in B.items()}
+        for v in B.values():
+            v.fill_(-3)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k_, v in B.items():
+            assert torch.equal(v, want[k_]), (k, k_)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_head_learns(dtype):
+    """A few steps of plain gradient descent on a head lower its loss."""
+    torch.manual_seed(7)
+    head = L.LabelHead(50, 32, 20, dtype=dtype)
+    codes = torch.randint(0, 50, (2000,), device=DEV)
+    labels = torch.where(codes % 7 == 0, -1, codes % 20)
+    first = None
+    for _ in range(40):
+        loss = head(codes, labels)
+        first = float(loss) if first is None else first
+        head.zero_grad()
+        loss.backward()
+        with torch.no_grad():
+            for p in head.parameters():
+                p -= 0.5 * p.grad
+    assert math.isfinite(first) and float(loss) < 0.5 * first
