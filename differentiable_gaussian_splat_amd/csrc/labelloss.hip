@@ -36,12 +36,12 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-#define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int BT = 128;         // tile edge of every product, rows and columns
-constexpr int BK = 64;          // depth of one staged step
-constexpr int GT = 256;         // threads: 2 x 2 waves of 64 x 64
-constexpr int SLAB = 64;        // vocabulary rows one wave sums: one (maximum, sum) pair per row
+constexpr int BN = 128;         // columns of every product's tile (rows of x, or of the vocabulary)
+constexpr int BK = 32;          // depth of one staged step
+constexpr int GT = 256;         // threads: four waves, two blocks to a compute unit
+constexpr int STAGES = 3;       // steps in LDS: one read, two on their way
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
 
@@ -57,7 +57,7 @@ struct Product {
     const int32_t* rows;          // labelled row -> row of the caller's arrays
     const void* labels;
     int wide_labels;
-    int v0, vocab, np, slab0;
+    int v0, vocab, np;
     float2* part;                 // LSE: [slab][np]
     float* target;                // LSE: z at the label
     const float *lse, *dmean, *dloss;
@@ -68,7 +68,7 @@ struct Product {
     int add;
     void* out;                    // DW without splits
     int64_t ldout;
-    int out_dim;
+    int out_dim, out_wide;
 };
 
 __device__ __forceinline__ float up_of(const Product& p, int row, int cnt) {
@@ -77,74 +77,104 @@ __device__ __forceinline__ float up_of(const Product& p, int row, int cnt) {
     return u;
 }
 
-// Stages a BT x BK operand tile into LDS: rows of 64 depth elements (128
-// bytes, 16-byte chunks exchanged by the row's low bits so that the readers of
-// one depth chunk spread over the banks) or, TR, depth rows of BT elements
-// (64-byte segments exchanged by the depth row's low bits).
-template <bool TR>
+// Stages a T x BK operand tile into LDS: rows of 32 depth elements (64 bytes;
+// their 16-byte chunks are exchanged by the row, so that eight rows' chunks of
+// one depth spread over all banks) or, TR, depth rows of T elements (64-byte
+// segments exchanged by the depth row, for the transposing reads).
+template <int T, bool TR>
 struct Stage {
-    uint32_t off[4];  // byte offsets of the lane's chunks from the tile's first element
+    static constexpr int NI = T / 64;  // 16-byte loads per lane
+    uint32_t off[NI];                  // byte offsets of the lane's chunks from the tile's first element
 
     __device__ __forceinline__ Stage(int64_t ld) {
         const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NI; ++i) {
             if (TR) {
-                const int r = (i * 4 + w) * 4 + l / 16;
-                const int seg = ((l % 16) / 4) ^ (r & 3);
+                const int r = (i * 4 + w) * (512 / T) + l / (T / 8);
+                const int seg = ((l % (T / 8)) / 4) ^ (r & (T / 32 - 1) & 3);
                 off[i] = (uint32_t)((r * ld + seg * 32 + (l % 4) * 8) * 2);
             } else {
-                const int r = (i * 4 + w) * 8 + l / 8;
-                off[i] = (uint32_t)((r * ld + ((l % 8) ^ (r & 7)) * 8) * 2);
+                const int r = (i * 4 + w) * 16 + l / 4;
+                off[i] = (uint32_t)((r * ld + ((l % 4) ^ ((r >> 1) & 3)) * 8) * 2);
             }
         }
     }
 
-    // p: first element of the tile; bytes: how far the operand's memory reaches from there (reads beyond give 0)
-    __device__ __forceinline__ void load(const bf16* p, int64_t bytes, bf16* lds) const {
-        const int w = threadIdx.x >> 6;
-        const int lim = bytes > 0x7fffffff ? 0x7fffffff : bytes < 0 ? 0 : (int)bytes;
-        auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16*>(p), 0, lim, 0x00020000);
+    // p: first element of the tile; bytes: how far the operand's memory reaches from there (reads beyond give 0);
+    // lds: byte address of the tile in LDS. The load writes no register, so that nothing of it is the compiler's to
+    // keep: step_barrier waits for its arrival. (As a builtin, every LDS read behind it would wait for it first.)
+    // The wait states are those that a vector write of the descriptor and the write of m0 need before it.
+    __device__ __forceinline__ void load(const bf16* p, int64_t bytes, uint32_t lds) const {
+        const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const uint64_t at = (uint64_t)p;
+        u32x4 r;
+        r[0] = __builtin_amdgcn_readfirstlane((uint32_t)at);
+        r[1] = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) & 0xffffu;
+        r[2] = __builtin_amdgcn_readfirstlane((uint32_t)(bytes > 0x7fffffff ? 0x7fffffff : bytes < 0 ? 0 : bytes));
+        r[3] = 0x00020000u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(lds + (i * 4 + w) * 512), 16, off[i], 0, 0, 0);
+        for (int i = 0; i < NI; ++i)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
+                             lds + (i * 4 + w) * 1024),
+                         "v"(off[i]), "s"(r)
+                         : "memory");
     }
 };
 
-// The 8 depth elements of a lane for one 32-row fragment: row `r0 + lane % 32`, depth 16 kk + 8 (lane / 32).
-template <bool TR>
+// The 8 depth elements of a lane for one 32-row fragment: row r0 + lane % 32, depth 16 kk + 8 (lane / 32).
+template <int T, bool TR>
 __device__ __forceinline__ bf16x8 fragment(const bf16* lds, int r0, int kk) {
     const int l = threadIdx.x & 63;
     if constexpr (TR) {
         const int j = l % 16, k = 16 * kk + 8 * (l / 32) + j / 4;
-        const bf16* q = lds + k * BT + (((r0 / 32) ^ (j / 4)) * 32) + ((l / 16) & 1) * 16 + (j % 4) * 4;
+        const bf16* q = lds + k * T + (((r0 / 32) ^ ((j / 4) & (T / 32 - 1))) * 32) + ((l / 16) & 1) * 16 + (j % 4) * 4;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)q);
         const s16x4 hi =
-            __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(q + 4 * BT));
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(q + 4 * T));
         bf16x8 v;
         __builtin_memcpy(&v, &lo, 8);
         __builtin_memcpy(reinterpret_cast<char*>(&v) + 8, &hi, 8);
         return v;
     } else {
         const int r = r0 + l % 32;
-        return *reinterpret_cast<const bf16x8*>(lds + r * BK + ((2 * kk + l / 32) ^ (r & 7)) * 8);
+        return *reinterpret_cast<const bf16x8*>(lds + r * BK + ((2 * kk + l / 32) ^ ((r >> 1) & 3)) * 8);
     }
 }
 
-// exp(z - ref); the difference first, which is exact where the two are close. Results below 2^-126 are 0.
-__device__ __forceinline__ float exp_diff(float z, float ref) { return __builtin_amdgcn_exp2f((z - ref) * LOG2E); }
+// Waits until all but the last `left` of this wave's loads have arrived and its LDS reads are done, then for the block.
+template <int LEFT>
+__device__ __forceinline__ void step_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
 
-// One product, C[m][n] = sum_k A[m][k] B[n][k], by 128 x 128 tiles; a lane
+// 2^x; results below 2^-126 are 0
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// exp(z - ref); the difference first, which is exact where the two are close
+__device__ __forceinline__ float exp_diff(float z, float ref) { return exp2_fast((z - ref) * LOG2E); }
+
+// One product, C[m][n] = sum_k A[m][k] B[n][k], by BM x 128 tiles; a lane
 // holds, for one n, runs of four consecutive m. PARTS: 1, or 3 for split
 // operands.
-template <int MODE, int PARTS, class T>
+//
+// The loop keeps three steps in LDS: while one is multiplied the next two are
+// loaded straight to LDS, and one barrier a step both publishes the arrived
+// step and frees the one before it. Loads past the last step are made with an
+// empty extent (they bring zeros), which keeps the count of loads in flight
+// the same in every step.
+template <int MODE, int PARTS, int BM, class T>
 __global__ __launch_bounds__(GT, 2) void k_product(Product p) {
     constexpr bool TA = MODE == DX || MODE == DW, TB = MODE == DW;
-    __shared__ __align__(16) bf16 s_a[2][BT * BK];
-    __shared__ __align__(16) bf16 s_b[2][BT * BK];
+    constexpr int WM = BM == 64 ? 64 : BM / 2;       // rows of a wave's part
+    constexpr int WN = BM == 64 ? 32 : 64;           // columns
+    constexpr int MW = BM / WM;                      // waves along m
+    constexpr int TM = WM / 32, TN = WN / 32;
+    constexpr int STEP = (BM + BN) * BK;  // elements of one staged step: the a tile, then the b tile
+    __shared__ __align__(16) bf16 s_tiles[STAGES * STEP];
     const int cnt = *p.count;
     const int nn = MODE == DW ? p.n : cnt;
-    const int mt = (p.m + BT - 1) / BT, nt = (nn + BT - 1) / BT;
+    const int mt = (p.m + BM - 1) / BM, nt = (nn + BN - 1) / BN;
     // consecutive blocks go to the eight dies in turn: each takes a contiguous
     // run of tiles, in groups of 8 columns, so that its cache serves both operands
     const int tiles = mt * nt, per_die = (tiles + 7) / 8;
@@ -152,164 +182,230 @@ __global__ __launch_bounds__(GT, 2) void k_product(Product p) {
     if ((int)(blockIdx.x >> 3) >= per_die || tile >= tiles) return;
     const int grp = tile / (8 * mt), in_grp = tile - grp * 8 * mt;
     const int gw = min(8, nt - grp * 8);
-    const int m0 = in_grp / gw * BT, n0 = (grp * 8 + in_grp % gw) * BT;
+    const int m0 = in_grp / gw * BM, n0 = (grp * 8 + in_grp % gw) * BN;
 
     const int depth = MODE == DW ? cnt : p.k;
     const int nk = (depth + BK - 1) / BK;
     const int share = (nk + p.splits - 1) / p.splits;
     const int k_first = min(nk, (int)blockIdx.y * share), k_end = min(nk, k_first + share);
-    const int steps = (k_end - k_first) * (PARTS == 3 ? 6 : 1);
+    const int per = k_end - k_first;
+    const int steps = per * (PARTS == 3 ? 6 : 1);
 
-    const Stage<TA> sa(p.lda);
-    const Stage<TB> sb(p.ldb);
+    const Stage<BM, TA> sa(p.lda);
+    const Stage<BN, TB> sb(p.ldb);
     const int a_rows = TA ? (MODE == DW ? p.np : p.k) : p.m;  // rows of the operand's memory
     const int b_rows = p.np;
-    auto issue = [&](int t, int buf) {
-        int ia = 0, ib = 0, kt = t;
-        if (PARTS == 3) {
-            const int per = k_end - k_first, pr = t / per;
-            kt = t - pr * per;
-            ia = (0x001012 >> (4 * pr)) & 3;  // 2 1 0 1 0 0
-            ib = (0x010210 >> (4 * pr)) & 3;  // 0 1 2 0 1 0
+    // the next step to load: depth step kt of part pair pr
+    int kt = 0, pr = 0;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_tiles;
+    auto issue = [&](int buf) {
+        const bool live = pr < (PARTS == 3 ? 6 : 1) && per > 0;
+        const int ia = PARTS == 3 ? (0x001012 >> (4 * pr)) & 3 : 0;  // 2 1 0 1 0 0
+        const int ib = PARTS == 3 ? (0x010210 >> (4 * pr)) & 3 : 0;  // 0 1 2 0 1 0
+        const int64_t k0 = live ? (k_first + kt) * BK : 0;
+        const bf16* a = p.a + ia * p.pa + (TA ? k0 * p.lda + m0 : m0 * p.lda + k0);
+        const bf16* b = p.b + ib * p.pb + (TB ? k0 * p.ldb + n0 : n0 * p.ldb + k0);
+        const int64_t ea = TA ? (min((int64_t)BK, a_rows - k0) - 1) * p.lda + p.m - m0
+                              : (int64_t)(min(BM, a_rows - m0) - 1) * p.lda + BK;
+        const int64_t eb = TB ? (min((int64_t)BK, b_rows - k0) - 1) * p.ldb + p.ldb - n0
+                              : (int64_t)(min(BN, b_rows - n0) - 1) * p.ldb + BK;
+        sa.load(a, live ? ea * 2 : 0, lds0 + buf * STEP * 2);
+        sb.load(b, live ? eb * 2 : 0, lds0 + (buf * STEP + BM * BK) * 2);
+        if (++kt >= per) {
+            kt = 0;
+            ++pr;
         }
-        const int k0 = (k_first + kt) * BK;
-        const bf16* a = p.a + ia * p.pa;
-        const bf16* b = p.b + ib * p.pb;
-        if (TA)
-            sa.load(a + k0 * p.lda + m0, ((int64_t)(min(BK, a_rows - k0) - 1) * p.lda + p.m - m0) * 2, s_a[buf]);
-        else
-            sa.load(a + m0 * p.lda + k0, ((int64_t)(min(BT, a_rows - m0) - 1) * p.lda + BK) * 2, s_a[buf]);
-        if (TB)
-            sb.load(b + k0 * p.ldb + n0, ((int64_t)(min(BK, b_rows - k0) - 1) * p.ldb + p.ldb - n0) * 2, s_b[buf]);
-        else
-            sb.load(b + n0 * p.ldb + k0, ((int64_t)(min(BT, b_rows - n0) - 1) * p.ldb + BK) * 2, s_b[buf]);
     };
 
     const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
-    const int wm = (w & 1) * 64, wn = (w >> 1) * 64;
-    f32x16 acc[2][2];
+    const int wm = (w % MW) * WM, wn = (w / MW) * WN;
+    f32x16 acc[TM][TN];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-    if (steps > 0) issue(0, 0);
+    constexpr int LOADS = Stage<BM, TA>::NI + Stage<BN, TB>::NI;  // of one step
+    issue(0);
+    issue(1);
+    int buf = 0;
     for (int t = 0; t < steps; ++t) {
-        const int buf = t & 1;
-        __syncthreads();  // step t has arrived, and the other buffer's readers are done
-        if (t + 1 < steps) issue(t + 1, buf ^ 1);
+        step_barrier<LOADS>();
+        issue(buf == 0 ? STAGES - 1 : buf - 1);
+        const bf16 *la = s_tiles + buf * STEP, *lb = la + BM * BK;
+        buf = buf == STAGES - 1 ? 0 : buf + 1;
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
-            bf16x8 fa[2], fb[2];
+            bf16x8 fa[TM], fb[TN];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) fa[i] = fragment<TA>(s_a[buf], wm + 32 * i, kk);
+            for (int i = 0; i < TM; ++i) fa[i] = fragment<BM, TA>(la, wm + 32 * i, kk);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fb[j] = fragment<TB>(s_b[buf], wn + 32 * j, kk);
+            for (int j = 0; j < TN; ++j) fb[j] = fragment<BN, TB>(lb, wn + 32 * j, kk);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < TN; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
         }
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last step
 
     // element e of acc[i][j]: m = mb + 32 i + 8 (e / 4) + e % 4, n = nb + 32 j
     const int mb = m0 + wm + 4 * (l / 32), nb = n0 + wn + l % 32;
     if constexpr (MODE == LSE || MODE == DZ) {
-        const bool edge = m0 + BT > p.m;
+        const bool edge = m0 + BM > p.m;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < TN; ++j) {
             const int n = nb + 32 * j;
+            int room = p.m - mb;  // elements at or beyond it are past the vocabulary
+            asm volatile("" : "+v"(room));  // compared anew for each j: kept comparisons would not fit the registers
             const int row = n < cnt ? p.rows[n] : -1;
             const int lab = row >= 0 ? row_index(p.labels, p.wide_labels, row, p.vocab) - p.v0 : -1;
-            const bool hit = __any(lab >= m0 + wm && lab < m0 + wm + SLAB);
+            const int at = lab - mb;  // of the label's element among this lane's: 32 i + 8 (e / 4) + e % 4
+            const bool hit = __any(lab >= m0 + wm && lab < m0 + wm + WM);
             if constexpr (MODE == LSE) {
                 if (edge)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < TM; ++i)
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            if (mb + 32 * i + 8 * (e / 4) + e % 4 >= p.m) acc[i][j][e] = -INFINITY;
-                float top = -INFINITY, sum = 0.f;
+                            if (32 * i + 8 * (e / 4) + e % 4 >= room) acc[i][j][e] = -INFINITY;
+                float top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
+                    for (int e = 0; e < 16; e += 2) top = fmaxf(fmaxf(top, acc[i][j][e]), acc[i][j][e + 1]);
                 top = fmaxf(top, __shfl_xor(top, 32));
-                // an infinite maximum: entries equal to it count 1 (+inf) or 0 (-inf), others 0
-                const bool fin = top > -INFINITY && top < INFINITY;
+                const float ref = top * LOG2E;
+                float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float z = acc[i][j][e];
-                        sum += fin ? exp_diff(z, top) : z != z ? z : z == INFINITY ? 1.f : 0.f;
+                    for (int e = 0; e < 16; e += 2) {
+                        s0 += exp2_fast(fmaf(acc[i][j][e], LOG2E, -ref));
+                        s1 += exp2_fast(fmaf(acc[i][j][e + 1], LOG2E, -ref));
                     }
+                float sum = s0 + s1;
+                if (!__all(fabsf(top) < INFINITY)) {
+                    // an infinite maximum: entries equal to +inf count 1, other numbers 0
+                    float c = 0.f;
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float z = acc[i][j][e];
+                            c += z != z ? z : z == INFINITY ? 1.f : 0.f;
+                        }
+                    if (!(fabsf(top) < INFINITY)) sum = c;
+                }
                 sum += __shfl_xor(sum, 32);
                 if (l < 32 && n < cnt)
-                    p.part[(int64_t)(p.slab0 + (m0 + wm) / SLAB) * p.np + n] = make_float2(top, sum);
+                    p.part[(int64_t)((m0 + wm) / WM) * p.np + n] = make_float2(top, sum);
                 if (hit)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < TM; ++i)
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            if (lab >= 0 && mb + 32 * i + 8 * (e / 4) + e % 4 == lab) p.target[n] = acc[i][j][e];
+                            if (at == 32 * i + 8 * (e / 4) + e % 4 && lab >= 0) p.target[n] = acc[i][j][e];
             } else {
-                const float lse = row >= 0 ? p.lse[row] : 0.f;
+                const float ref = row >= 0 ? p.lse[row] * LOG2E : 0.f;
                 const float up = row >= 0 ? up_of(p, row, cnt) : 0.f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const int m = mb + 32 * i + 2 * e;
-                        bf16x4 o[PARTS];
+                    for (int e = 0; e < 16; ++e) acc[i][j][e] = exp2_fast(fmaf(acc[i][j][e], LOG2E, -ref));
+                if (hit)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float g = exp_diff(acc[i][j][e + q], lse);
-                            if (hit && lab == m + q) g -= 1.f;
-                            g *= up;
-                            if (row < 0 || m + q >= p.m) g = 0.f;
-                            o[0][q] = (bf16)g;
-                            if (PARTS == 3) {
-                                const float r1 = g - (float)o[0][q];
-                                o[PARTS / 2][q] = (bf16)r1;
-                                o[PARTS - 1][q] = (bf16)(r1 - (float)o[PARTS / 2][q]);
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            acc[i][j][e] -= at == 32 * i + 8 * (e / 4) + e % 4 ? 1.f : 0.f;
+                // rows past the labelled ones have z = 0 and up = 0
+                if (edge)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (32 * i + 8 * (e / 4) + e % 4 >= room) acc[i][j][e] = 0.f;
+                // a lane and the one 32 further hold runs of four columns in turn: they
+                // exchange runs, so that each stores eight columns at a time
+                const int h = l / 32;
+                bf16* q = p.dz + n * p.lddz + (m0 + wm + 8 * h);
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8) {
+                        float g[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) g[c] = acc[i][j][e + c] * up;
+#pragma unroll
+                        for (int c = 0; c < PARTS; ++c) {
+                            union {
+                                bf16x4 v[2];
+                                uint32_t u[4];
+                            } o;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const bf16 b = (bf16)g[k];
+                                o.v[k / 4][k % 4] = b;
+                                if (c + 1 < PARTS) g[k] -= (float)b;
                             }
+                            auto x0 = __builtin_amdgcn_permlane32_swap(o.u[0], o.u[2], false, false);
+                            auto x1 = __builtin_amdgcn_permlane32_swap(o.u[1], o.u[3], false, false);
+                            *reinterpret_cast<uint4*>(q + c * p.pdz + 32 * i + 2 * e) =
+                                make_uint4(x0[0], x1[0], x0[1], x1[1]);
                         }
-#pragma unroll
-                        for (int c = 0; c < PARTS; ++c)
-                            *reinterpret_cast<bf16x4*>(p.dz + c * p.pdz + n * p.lddz + m) = o[c];
                     }
             }
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < TN; ++j) {
             const int n = nb + 32 * j;
             if (n >= nn) continue;
+            int room = (p.acc ? (int)p.ldacc : p.out_dim) - mb;
+            asm volatile("" : "+v"(room));
+            if (p.acc) {
+                float* q = p.acc + blockIdx.y * p.pacc + n * p.ldacc + mb;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const int m = mb + 32 * i + 2 * e;
-                    if (p.acc) {
-                        if (m >= p.ldacc) continue;
-                        float4* q = reinterpret_cast<float4*>(p.acc + blockIdx.y * p.pacc + n * p.ldacc + m);
+                    for (int e = 0; e < 16; e += 4) {
+                        if (32 * i + 2 * e >= room) continue;
+                        float4* d = reinterpret_cast<float4*>(q + 32 * i + 2 * e);
                         float4 v = make_float4(acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]);
                         if (p.add) {
-                            const float4 o = *q;
+                            const float4 o = *d;
                             v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
                         }
-                        *q = v;
-                    } else {
-                        T* q = static_cast<T*>(p.out) + n * p.ldout + m;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (m + c < p.out_dim) q[c] = (T)acc[i][j][e + c];
+                        *d = v;
                     }
-                }
+            } else {
+                T* q = static_cast<T*>(p.out) + n * p.ldout + mb;
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const int c0 = 32 * i + 2 * e;
+                        if (p.out_wide && c0 + 4 <= room) {
+                            if constexpr (sizeof(T) == 2) {
+                                bf16x4 v;
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) v[c] = (bf16)acc[i][j][e + c];
+                                *reinterpret_cast<bf16x4*>(q + c0) = v;
+                            } else {
+                                *reinterpret_cast<float4*>(q + c0) =
+                                    make_float4(acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (c0 + c < room) q[c0 + c] = (T)acc[i][j][e + c];
+                        }
+                    }
+            }
         }
     }
 }
@@ -392,7 +488,7 @@ __global__ __launch_bounds__(LT) void k_label_rows(int64_t n, int vocab, const v
 }
 
 // Rows into bfloat16 parts of kp columns (a multiple of BK, zero beyond dim).
-// With a list: the listed rows, and zero rows up to the next multiple of BT.
+// With a list: the listed rows, and zero rows up to the next multiple of BN.
 template <class T, int PARTS>
 __global__ __launch_bounds__(256) void k_pack(int64_t rows, int dim, int kp, const T* __restrict__ x, int64_t xs,
                                               bool wide, const int32_t* __restrict__ list,
@@ -402,7 +498,7 @@ __global__ __launch_bounds__(256) void k_pack(int64_t rows, int dim, int kp, con
     int64_t live = rows, padded = rows;
     if (list) {
         live = *count;
-        padded = (live + BT - 1) / BT * BT;
+        padded = (live + BN - 1) / BN * BN;
     }
     const int64_t total = padded * per;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
@@ -532,6 +628,7 @@ __global__ __launch_bounds__(256) void k_join_splits(int64_t rows, int dim, int 
         for (int c = lane; c < dim; c += 64) {
             float a = 0.f;
             if (src >= 0)
+#pragma unroll 8
                 for (int s = 0; s < splits; ++s) a += acc[s * pacc + src * ldacc + c];
             out[r * ldout + c] = (T)a;
         }
@@ -542,37 +639,49 @@ __global__ __launch_bounds__(256) void k_join_splits(int64_t rows, int dim, int 
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-struct LossPlan {
-    int parts, kp;
-    int64_t np;                    // rows of x padded to the tile
-    int64_t piece_f, piece_b;      // vocabulary rows per piece (multiples of BT)
-    int split_dx, split_dw;
-    size_t rows, place, count, block_count, xp, wp, part, target, state, block_sum, dz, dxp, dwp, total;
-};
-
 // Blocks a launch needs to fill the chip; products with fewer tiles split their depth.
 constexpr int FILL = 512;
 
-int splits_for(int64_t tiles, int64_t nk) {
+// Tile rows of a product with m rows and n columns: the largest that still makes
+// enough tiles, and no more than m fills.
+int tile_rows(int64_t m, int64_t n) {
+    if (m > 128 && up(m, 256) / 256 * (up(n, BN) / BN) >= FILL / 2) return 256;
+    return m > 64 ? 128 : 64;
+}
+
+int splits_for(int64_t tiles, int64_t nk, int parts) {
     int64_t s = tiles > 0 ? FILL / tiles : 1;
-    if (s > nk / 4) s = nk / 4;  // at least four steps each
+    const int64_t most = nk * (parts == 3 ? 6 : 1) / 8;  // at least eight steps each
+    if (s > most) s = most;
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
+
+struct LossPlan {
+    int parts, kp;
+    int64_t np;                    // rows of x padded to the tile
+    int64_t piece_f, piece_b;      // vocabulary rows per piece (multiples of 256)
+    int bm_z, bm_dx, bm_dw;        // tile rows: over the vocabulary, over dim
+    int split_dx, split_dw;
+    size_t rows, place, count, block_count, xp, wp, part, target, state, block_sum, dz, dxp, dwp, total;
+};
 
 LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     LossPlan L{};
     L.parts = half ? 1 : 3;
     L.kp = (int)up(dim, BK);
-    L.np = up(n > 0 ? n : 1, BT);
-    const int64_t vp = up(vocab, BT);
+    L.np = up(n > 0 ? n : 1, BN);
+    const int64_t vp = up(vocab, 256);
     auto piece = [&](int64_t budget) {  // vocabulary rows whose per-row cost fits the budget
-        const int64_t v = budget / L.np / BT * BT;
-        return v < BT ? BT : v > vp ? vp : v;
+        const int64_t v = budget / L.np / 256 * 256;
+        return v < 256 ? 256 : v > vp ? vp : v;
     };
     L.piece_f = piece((int64_t)1 << 31);  // 8 bytes per 64 vocabulary rows: 256 MB
     L.piece_b = piece(((int64_t)1 << 28) / L.parts);  // 2 bytes per part: 512 MB
-    L.split_dx = splits_for(up(L.kp, BT) / BT * (L.np / BT), L.piece_b / BK);
-    L.split_dw = splits_for(up(L.kp, BT) / BT * (L.piece_b / BT), L.np / BK);
+    L.bm_z = tile_rows(backward ? L.piece_b : L.piece_f, L.np);
+    L.bm_dx = tile_rows(L.kp, L.np);
+    L.bm_dw = tile_rows(L.kp, L.piece_b);
+    L.split_dx = splits_for(up(L.kp, L.bm_dx) / L.bm_dx * (L.np / BN), L.piece_b / BK, L.parts);
+    L.split_dw = splits_for(up(L.kp, L.bm_dw) / L.bm_dw * (L.piece_b / BN), L.np / BK, L.parts);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -589,15 +698,13 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
         L.dz = take((size_t)L.parts * L.np * L.piece_b * 2);
         L.dxp = take((size_t)L.split_dx * L.np * L.kp * 4);
         L.dwp = L.split_dw > 1 ? take((size_t)L.split_dw * L.piece_b * L.kp * 4) : 0;
+    } else {
+        L.part = take((size_t)(L.piece_f / 64) * L.np * 8);
+        L.target = take((size_t)L.np * 4);
+        L.state = take((size_t)L.np * 8);
+        L.block_sum = take((size_t)(L.np / JR + 1) * 8);
     }
-    const size_t both = o;
-    // the forward's arrays share the backward's space: no call uses both
-    o = L.dz ? L.dz : both;
-    L.part = take((size_t)(L.piece_f / SLAB) * L.np * 8);
-    L.target = take((size_t)L.np * 4);
-    L.state = take((size_t)L.np * 8);
-    L.block_sum = take((size_t)(L.np / JR + 1) * 8);
-    L.total = o > both ? o : both;
+    L.total = o;
     return L;
 }
 
@@ -637,9 +744,16 @@ hipError_t label_rows(const LabelLossArgs& a, const LossPlan& L, char* ws, bool 
     return hipGetLastError();
 }
 
-unsigned tile_grid(int64_t m, int64_t n) {
-    const int64_t t = up(m, BT) / BT * (up(n, BT) / BT);
-    return (unsigned)(t < 8 ? 8 : up(t, 8));
+template <int MODE, int PARTS, class T>
+void launch_product(int bm, const Product& p, int64_t m, int64_t n, hipStream_t s) {
+    const int64_t t = up(m, bm) / bm * (up(n, BN) / BN);
+    const dim3 grid((unsigned)(t < 8 ? 8 : up(t, 8)), p.splits);
+    if (bm == 256)
+        k_product<MODE, PARTS, 256, T><<<grid, GT, 0, s>>>(p);
+    else if (bm == 128)
+        k_product<MODE, PARTS, 128, T><<<grid, GT, 0, s>>>(p);
+    else
+        k_product<MODE, PARTS, 64, T><<<grid, GT, 0, s>>>(p);
 }
 
 template <class T>
@@ -681,9 +795,10 @@ hipError_t loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         p.v0 = (int)v0;
         p.part = part;
         p.target = (float*)(ws + L.target);
-        k_product<LSE, PARTS, T><<<tile_grid(mv, a.n), GT, 0, s>>>(p);
-        // every tile writes its two slabs, so the last may lie beyond the vocabulary (an empty one)
-        k_lse_join<<<(unsigned)(L.np / JR), JT, 0, s>>>((int)(up(mv, BT) / SLAB), (int)L.np, part, p.target, p.rows,
+        launch_product<LSE, PARTS, T>(L.bm_z, p, mv, a.n, s);
+        // every tile writes its slabs, so the last may lie beyond the vocabulary (an empty one)
+        const int slabs = (int)(up(mv, L.bm_z) / (L.bm_z == 256 ? 128 : 64));
+        k_lse_join<<<(unsigned)(L.np / JR), JT, 0, s>>>(slabs, (int)L.np, part, p.target, p.rows,
                                                        p.count, state, v0 == 0, v0 + L.piece_f < a.vocab, a.loss,
                                                        a.lse, bs);
     }
@@ -716,7 +831,7 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         p.dz = dz;
         p.lddz = L.piece_b;
         p.pdz = L.np * L.piece_b;
-        k_product<DZ, PARTS, T><<<tile_grid(mv, a.n), GT, 0, s>>>(p);
+        launch_product<DZ, PARTS, T>(L.bm_z, p, mv, a.n, s);
         if (a.dx) {
             Product q = product_base<T>(a, L, ws);
             q.a = p.a;
@@ -732,7 +847,7 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
             q.ldacc = L.kp;
             q.pacc = L.np * L.kp;
             q.add = v0 > 0;
-            k_product<DX, PARTS, T><<<dim3(tile_grid(L.kp, a.n), q.splits), GT, 0, s>>>(q);
+            launch_product<DX, PARTS, T>(L.bm_dx, q, L.kp, a.n, s);
         }
         if (a.dw) {
             Product q = product_base<T>(a, L, ws);
@@ -754,8 +869,9 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
                 q.out = out;
                 q.ldout = a.dw_stride;
                 q.out_dim = a.dim;
+                q.out_wide = (uintptr_t)a.dw % (4 * sizeof(T)) == 0 && a.dw_stride % 4 == 0;
             }
-            k_product<DW, PARTS, T><<<dim3(tile_grid(L.kp, mv), q.splits), GT, 0, s>>>(q);
+            launch_product<DW, PARTS, T>(L.bm_dw, q, L.kp, mv, s);
             if (L.split_dw > 1)
                 k_join_splits<T><<<(unsigned)(mv < 16384 ? (mv + 3) / 4 : 4096), 256, 0, s>>>(
                     mv, a.dim, L.split_dw, dwp, L.kp, q.pacc, nullptr, out, a.dw_stride);

@@ -19,7 +19,7 @@ from __future__ import annotations
 
 import torch
 
-from .raster import _check, _nbytes, _p, _stream, load_library
+from .raster import _check, _nbytes, _stream, load_library
 
 __all__ = ["gs_embed_fwd", "gs_embed_bwd_workspace_size", "gs_embed_bwd", "gs_layer_norm_fwd",
            "gs_layer_norm_bwd_workspace_size", "gs_layer_norm_bwd", "gs_label_loss_workspace_size",
@@ -30,6 +30,9 @@ _INDEX_TYPES = {torch.int32: 0, torch.int64: 1}
 
 
 # ------------------------------------------------------------------ argument checks
+#
+# The smallest calls are bound by the launch, so each check has a fast way
+# through for a good argument; what fails it is looked at again for the message.
 
 def _dtype(dtype) -> int:
     if dtype not in _DTYPES:
@@ -38,53 +41,60 @@ def _dtype(dtype) -> int:
 
 
 def _matrix(name, t, like=None, rows=None, cols=None):
-    """Checks a matrix of rows and returns its row stride."""
+    """Checks a matrix of rows (of the type and device of `like`, if given) and returns its row stride."""
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+    n, dim = t.shape
+    st = t.stride()
+    if (rows is not None and n != rows) or (cols is not None and dim != cols):
         raise ValueError(f"{name} must have shape ({'*' if rows is None else rows}, {'*' if cols is None else cols}), "
                          f"got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}'s columns must be consecutive, got strides {t.stride()}")
-    _dtype(t.dtype)
-    _same(name, t, like)
+    if dim > 1 and st[1] != 1:
+        raise ValueError(f"{name}'s columns must be consecutive, got strides {st}")
+    if like is not None:
+        if t.dtype != like.dtype or t.get_device() != like.get_device():
+            raise TypeError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    else:
+        _dtype(t.dtype)
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be on the GPU, got {t.device}")
     # one row has no stride of its own; torch may give it any
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
-
-
-def _same(name, t, like):
-    if like is None and t.device.type != "cuda":
-        raise TypeError(f"{name} must be on the GPU, got {t.device}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise TypeError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    return st[0] if n > 1 else max(dim, 1)
 
 
 def _vector(name, t, n, dtype, device):
+    """Checks a contiguous vector of n (device: an index, as get_device() gives it) and returns its address."""
     if t is None:
-        return
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        return None
+    if t.dtype is dtype and t.get_device() == device and t.dim() == 1 and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n}, got shape {tuple(t.shape)}")
-    if t.dtype != dtype or t.device != device:
-        raise TypeError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    raise TypeError(f"{name} must be {dtype} on device {device}, got {t.dtype} on {t.device}")
 
 
 def _index(name, t, n, device) -> int:
+    """Checks an index vector; its address and type."""
     if t.dtype not in _INDEX_TYPES:
         raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
-    _vector(name, t, n, t.dtype, device)
-    return _INDEX_TYPES[t.dtype]
+    return _vector(name, t, n, t.dtype, device), _INDEX_TYPES[t.dtype]
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
 
 
 # ------------------------------------------------------------------ thin C-ABI wrappers
 
 def gs_embed_fwd(table, ids, out, scale=1.0, stream=None):
     """out[i] = scale * table[ids[i]]; zero rows where ids[i] names no row."""
+    ts = _matrix("table", table)
     vocab, dim = table.shape
     n = ids.shape[0]
-    ts, os_ = _matrix("table", table), _matrix("out", out, table, n, dim)
-    it = _index("ids", ids, n, table.device)
-    st = load_library().gs_embed_fwd(n, dim, vocab, _dtype(table.dtype), _p(table), ts, _p(ids), it, float(scale),
-                                     _p(out), os_, _stream(stream))
+    os_ = _matrix("out", out, table, n, dim)
+    ip, it = _index("ids", ids, n, table.get_device())
+    st = load_library().gs_embed_fwd(n, dim, vocab, _DTYPES[table.dtype], table.data_ptr(), ts, ip, it, scale,
+                                     out.data_ptr(), os_, _stream(stream))
     _check(st, "gs_embed_fwd")
 
 
@@ -94,24 +104,25 @@ def gs_embed_bwd_workspace_size(n, dim, vocab, dtype) -> int:
 
 def gs_embed_bwd(ids, dout, dtable, workspace, scale=1.0, stream=None):
     """dtable[v] = scale * sum of dout over the rows whose index is v (every row of dtable is written)."""
+    ds = _matrix("dout", dout)
     n, dim = dout.shape
-    ds, ts = _matrix("dout", dout), _matrix("dtable", dtable, dout, None, dim)
-    it = _index("ids", ids, n, dout.device)
-    st = load_library().gs_embed_bwd(n, dim, dtable.shape[0], _dtype(dout.dtype), _p(ids), it, float(scale), _p(dout),
-                                     ds, _p(dtable), ts, _p(workspace), _nbytes(workspace), _stream(stream))
+    ts = _matrix("dtable", dtable, dout, None, dim)
+    ip, it = _index("ids", ids, n, dout.get_device())
+    st = load_library().gs_embed_bwd(n, dim, dtable.shape[0], _DTYPES[dout.dtype], ip, it, scale, dout.data_ptr(), ds,
+                                     dtable.data_ptr(), ts, _opt(workspace), _nbytes(workspace), _stream(stream))
     _check(st, "gs_embed_bwd")
 
 
 def gs_layer_norm_fwd(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, stream=None):
     """y = (x - mean) * rstd * weight + bias per row; weight and bias may be None."""
+    xs = _matrix("x", x)
     n, dim = x.shape
-    xs, ys = _matrix("x", x), _matrix("y", y, x, n, dim)
-    for name, t in (("weight", weight), ("bias", bias)):
-        _vector(name, t, dim, x.dtype, x.device)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _vector(name, t, n, torch.float32, x.device)
-    st = load_library().gs_layer_norm_fwd(n, dim, _dtype(x.dtype), _p(x), xs, _p(weight), _p(bias), float(eps), _p(y),
-                                          ys, _p(mean), _p(rstd), _stream(stream))
+    ys = _matrix("y", y, x, n, dim)
+    dt, dev = x.dtype, x.get_device()
+    st = load_library().gs_layer_norm_fwd(n, dim, _DTYPES[dt], x.data_ptr(), xs,
+                                          _vector("weight", weight, dim, dt, dev), _vector("bias", bias, dim, dt, dev),
+                                          eps, y.data_ptr(), ys, _vector("mean", mean, n, torch.float32, dev),
+                                          _vector("rstd", rstd, n, torch.float32, dev), _stream(stream))
     _check(st, "gs_layer_norm_fwd")
 
 
@@ -121,16 +132,17 @@ def gs_layer_norm_bwd_workspace_size(n, dim, dtype) -> int:
 
 def gs_layer_norm_bwd(x, weight, mean, rstd, dy, dx, dweight, dbias, workspace, stream=None):
     """Gradients of gs_layer_norm_fwd into dx, dweight and dbias (each may be None)."""
+    xs = _matrix("x", x)
     n, dim = x.shape
-    xs, dys = _matrix("x", x), _matrix("dy", dy, x, n, dim)
+    dys = _matrix("dy", dy, x, n, dim)
     dxs = _matrix("dx", dx, x, n, dim) if dx is not None else dim
-    for name, t in (("weight", weight), ("dweight", dweight), ("dbias", dbias)):
-        _vector(name, t, dim, x.dtype, x.device)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _vector(name, t, n, torch.float32, x.device)
-    st = load_library().gs_layer_norm_bwd(n, dim, _dtype(x.dtype), _p(x), xs, _p(weight), _p(mean), _p(rstd), _p(dy),
-                                          dys, _p(dx), dxs, _p(dweight), _p(dbias), _p(workspace),
-                                          _nbytes(workspace), _stream(stream))
+    dt, dev, f32 = x.dtype, x.get_device(), torch.float32
+    st = load_library().gs_layer_norm_bwd(n, dim, _DTYPES[dt], x.data_ptr(), xs,
+                                          _vector("weight", weight, dim, dt, dev), _vector("mean", mean, n, f32, dev),
+                                          _vector("rstd", rstd, n, f32, dev), dy.data_ptr(), dys, _opt(dx), dxs,
+                                          _vector("dweight", dweight, dim, dt, dev),
+                                          _vector("dbias", dbias, dim, dt, dev), _opt(workspace), _nbytes(workspace),
+                                          _stream(stream))
     _check(st, "gs_layer_norm_bwd")
 
 
@@ -141,31 +153,33 @@ def gs_label_loss_workspace_size(n, dim, vocab, dtype, backward) -> int:
 def gs_label_loss_fwd(x, w, labels, loss, lse, mean, count, workspace, stream=None):
     """Per row lse = log sum_v exp(x . w[v]) and loss = lse - x . w[label] (0 without a label); the mean loss and
     the number of labelled rows."""
+    xs = _matrix("x", x)
     n, dim = x.shape
-    xs, ws = _matrix("x", x), _matrix("w", w, x, None, dim)
-    it = _index("labels", labels, n, x.device)
-    for name, t, k, dt in (("loss", loss, n, torch.float32), ("lse", lse, n, torch.float32),
-                           ("mean", mean, 1, torch.float32), ("count", count, 1, torch.int32)):
-        _vector(name, t, k, dt, x.device)
-    st = load_library().gs_label_loss_fwd(n, dim, w.shape[0], _dtype(x.dtype), _p(x), xs, _p(w), ws, _p(labels), it,
-                                          _p(loss), _p(lse), _p(mean), _p(count), _p(workspace), _nbytes(workspace),
-                                          _stream(stream))
+    ws = _matrix("w", w, x, None, dim)
+    dev, f32 = x.get_device(), torch.float32
+    ip, it = _index("labels", labels, n, dev)
+    st = load_library().gs_label_loss_fwd(n, dim, w.shape[0], _DTYPES[x.dtype], x.data_ptr(), xs, w.data_ptr(), ws, ip,
+                                          it, _vector("loss", loss, n, f32, dev), _vector("lse", lse, n, f32, dev),
+                                          _vector("mean", mean, 1, f32, dev),
+                                          _vector("count", count, 1, torch.int32, dev), _opt(workspace),
+                                          _nbytes(workspace), _stream(stream))
     _check(st, "gs_label_loss_fwd")
 
 
 def gs_label_loss_bwd(x, w, labels, lse, dx, dw, workspace, dmean=None, dloss=None, stream=None):
     """Gradients into dx and dw (each may be None) from the upstream gradients of the mean loss and of the rows'
     losses."""
+    xs = _matrix("x", x)
     n, dim = x.shape
-    xs, ws = _matrix("x", x), _matrix("w", w, x, None, dim)
-    it = _index("labels", labels, n, x.device)
-    for name, t, k in (("lse", lse, n), ("dmean", dmean, 1), ("dloss", dloss, n)):
-        _vector(name, t, k, torch.float32, x.device)
+    ws = _matrix("w", w, x, None, dim)
+    dev, f32 = x.get_device(), torch.float32
+    ip, it = _index("labels", labels, n, dev)
     dxs = _matrix("dx", dx, x, n, dim) if dx is not None else dim
     dws = _matrix("dw", dw, w, w.shape[0], dim) if dw is not None else dim
-    st = load_library().gs_label_loss_bwd(n, dim, w.shape[0], _dtype(x.dtype), _p(x), xs, _p(w), ws, _p(labels), it,
-                                          _p(lse), _p(dmean), _p(dloss), _p(dx), dxs, _p(dw), dws, _p(workspace),
-                                          _nbytes(workspace), _stream(stream))
+    st = load_library().gs_label_loss_bwd(n, dim, w.shape[0], _DTYPES[x.dtype], x.data_ptr(), xs, w.data_ptr(), ws, ip,
+                                          it, _vector("lse", lse, n, f32, dev), _vector("dmean", dmean, 1, f32, dev),
+                                          _vector("dloss", dloss, n, f32, dev), _opt(dx), dxs, _opt(dw), dws,
+                                          _opt(workspace), _nbytes(workspace), _stream(stream))
     _check(st, "gs_label_loss_bwd")
 
 

@@ -142,8 +142,8 @@ def test_binding_refuses_mismatched_shapes():
     with pytest.raises(TypeError):
         L._matrix("out", _t(3, 4), _t(3, 4, dtype=torch.bfloat16), 3, 4)
     with pytest.raises(ValueError):
-        L._vector("weight", _t(3), 4, torch.float32, torch.device("cpu"))
+        L._vector("weight", _t(3), 4, torch.float32, -1)
     with pytest.raises(TypeError):
-        L._index("ids", _i(3, torch.int16), 3, torch.device("cpu"))
+        L._index("ids", _i(3, torch.int16), 3, -1)
     with pytest.raises(ValueError):
-        L._index("ids", _i(4), 3, torch.device("cpu"))
+        L._index("ids", _i(4), 3, -1)
