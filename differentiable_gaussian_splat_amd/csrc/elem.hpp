@@ -16,53 +16,59 @@ typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 template <class T>
 constexpr int WIDE = 16 / (int)sizeof(T);
 
-// V consecutive elements; V is 1 or WIDE<T> (then p is 16-byte aligned).
-template <int V>
-__device__ __forceinline__ void load_row(const float* p, float (&v)[V]) {
-    if constexpr (V == 4) {
-        const float4 t = *reinterpret_cast<const float4*>(p);
-        v[0] = t.x;
-        v[1] = t.y;
-        v[2] = t.z;
-        v[3] = t.w;
+// 16 bytes at an address that is aligned to the element only: gfx950 takes
+// 16-byte global accesses at any address, so rows of odd lengths and strides
+// need no narrower ones.
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef bf16 bf16x8_any __attribute__((ext_vector_type(8), aligned(2)));
+
+// The WIDE<T> elements of a row at p, of which `left` are inside the row (the others read as 0).
+__device__ __forceinline__ void load_row(const float* p, int left, float (&v)[4]) {
+    if (left >= 4) {
+        const f32x4_any t = *reinterpret_cast<const f32x4_any*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = t[i];
     } else {
-        static_assert(V == 1, "");
-        v[0] = *p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < left ? p[i] : 0.f;
     }
 }
 
-template <int V>
-__device__ __forceinline__ void load_row(const bf16* p, float (&v)[V]) {
-    if constexpr (V == 8) {
-        const bf16x8 t = *reinterpret_cast<const bf16x8*>(p);
+__device__ __forceinline__ void load_row(const bf16* p, int left, float (&v)[8]) {
+    if (left >= 8) {
+        const bf16x8_any t = *reinterpret_cast<const bf16x8_any*>(p);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (float)t[i];
     } else {
-        static_assert(V == 1, "");
-        v[0] = (float)*p;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? (float)p[i] : 0.f;
     }
 }
 
-template <int V>
-__device__ __forceinline__ void store_row(float* p, const float (&v)[V]) {
-    if constexpr (V == 4) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+// Stores the first `left` (or all) of WIDE<T> elements.
+__device__ __forceinline__ void store_row(float* p, int left, const float (&v)[4]) {
+    if (left >= 4) {
+        f32x4_any t;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = v[i];
+        *reinterpret_cast<f32x4_any*>(p) = t;
     } else {
-        static_assert(V == 1, "");
-        *p = v[0];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < left) p[i] = v[i];
     }
 }
 
-template <int V>
-__device__ __forceinline__ void store_row(bf16* p, const float (&v)[V]) {
-    if constexpr (V == 8) {
-        bf16x8 t;
+__device__ __forceinline__ void store_row(bf16* p, int left, const float (&v)[8]) {
+    if (left >= 8) {
+        bf16x8_any t;
 #pragma unroll
         for (int i = 0; i < 8; ++i) t[i] = (bf16)v[i];
-        *reinterpret_cast<bf16x8*>(p) = t;
+        *reinterpret_cast<bf16x8_any*>(p) = t;
     } else {
-        static_assert(V == 1, "");
-        *p = (bf16)v[0];
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < left) p[i] = (bf16)v[i];
     }
 }
 
@@ -71,12 +77,6 @@ __device__ __forceinline__ void store_row(bf16* p, const float (&v)[V]) {
 __device__ __forceinline__ int row_index(const void* ids, bool wide, int64_t i, int rows) {
     const int64_t v = wide ? static_cast<const int64_t*>(ids)[i] : (int64_t)static_cast<const int32_t*>(ids)[i];
     return v >= 0 && v < rows ? (int)v : -1;
-}
-
-// Whether rows of `dim` elements at p, `stride` apart, can be read 16 bytes at a time.
-template <class T>
-inline bool wide_rows(const void* p, int64_t stride, int dim) {
-    return p == nullptr || ((uintptr_t)p % 16 == 0 && stride % WIDE<T> == 0 && dim % WIDE<T> == 0);
 }
 
 }  // namespace gs

@@ -23,14 +23,20 @@ namespace {
 constexpr int EB = 256;         // threads per block
 constexpr int RUN_TOKENS = 32;  // sorted positions a row group sums
 constexpr int JOIN_T = 1024;
+constexpr int FEW = 256;        // positions up to which one launch makes the gradient (a multiple of 64)
 
-// LPR lanes per output row, each VEC elements per step over the row.
-template <class T, int VEC, int LPR>
+enum EmbedPass { LOOKUP, FEW_SUMS, RUN_SUMS };
+
+// Threads of a block that sums runs with lpr lanes per row: 32 lane groups (64 of one lane, 4 of a wave).
+constexpr int run_threads(int lpr) { return lpr <= 2 ? 64 : lpr == 4 ? 128 : EB; }
+
+// LPR lanes per output row, 16 bytes each per step over the row.
+template <class T, int LPR>
 __global__ __launch_bounds__(EB) void k_embed(int64_t n, int dim, int vocab, const T* __restrict__ table, int64_t ts,
                                               const void* __restrict__ ids, bool wide, float scale,
                                               T* __restrict__ out, int64_t os) {
     constexpr int U = 4;  // rows in flight per lane group
-    constexpr int G = EB / LPR;
+    constexpr int G = EB / LPR, VEC = WIDE<T>;
     const int l = threadIdx.x % LPR;
     const int64_t r0 = (int64_t)blockIdx.x * G * U + threadIdx.x / LPR;
     int row[U];
@@ -46,7 +52,7 @@ __global__ __launch_bounds__(EB) void k_embed(int64_t n, int dim, int vocab, con
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[u][k] = 0.f;
             if (row[u] >= 0) {
-                load_row<VEC>(table + row[u] * ts + c, v[u]);
+                load_row(table + row[u] * ts + c, dim - c, v[u]);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) v[u][k] *= scale;
             }
@@ -54,7 +60,7 @@ __global__ __launch_bounds__(EB) void k_embed(int64_t n, int dim, int vocab, con
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + u * G;
-            if (r < n) store_row<VEC>(out + r * os + c, v[u]);
+            if (r < n) store_row(out + r * os + c, dim - c, v[u]);
         }
     }
 }
@@ -72,14 +78,64 @@ __global__ __launch_bounds__(EB) void k_embed_keys(int n, int vocab, const void*
     }
 }
 
-template <class T, int VEC>
-__global__ __launch_bounds__(EB) void k_zero_rows(int64_t rows, int dim, T* __restrict__ p, int64_t stride) {
-    const int per = dim / VEC;
-    const int64_t total = rows * per;
-    const float z[VEC] = {};
-    for (int64_t i = (int64_t)blockIdx.x * EB + threadIdx.x; i < total; i += (int64_t)gridDim.x * EB) {
-        const int64_t r = i / per;
-        store_row<VEC>(p + r * stride + (i - r * per) * VEC, z);
+template <class T>
+__global__ __launch_bounds__(EB) void k_zero_rows(int rows, int dim, int lanes, T* __restrict__ p, int64_t stride) {
+    const float z[WIDE<T>] = {};
+    const int l = threadIdx.x % lanes, per = EB / lanes;
+    for (int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / lanes; r < rows; r += (int64_t)gridDim.x * per)
+        for (int c = l * WIDE<T>; c < dim; c += lanes * WIDE<T>) store_row(p + r * stride + c, dim - c, z);
+}
+
+// The gradient of few positions in one launch: a wave takes 64 / LPR rows of
+// the table in turn, and looks through the indices (in LDS) for each.
+template <class T, int LPR>
+__global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, const void* __restrict__ ids, bool wide,
+                                                  float scale, const T* __restrict__ dout, int64_t ds,
+                                                  T* __restrict__ dtable, int64_t ts) {
+    constexpr int VEC = WIDE<T>, U = 4;
+    __shared__ int s_id[FEW];
+    for (int i = threadIdx.x; i < FEW; i += EB) s_id[i] = i < n ? row_index(ids, wide, i, vocab) : -1;
+    __syncthreads();
+    const int lane = threadIdx.x & 63, sub = lane / LPR;
+    const int wave = (int)(blockIdx.x * (EB / 64)) + (int)(threadIdx.x >> 6), waves = (int)gridDim.x * (EB / 64);
+    for (int64_t v0 = (int64_t)wave * (64 / LPR); v0 < vocab; v0 += (int64_t)waves * (64 / LPR)) {
+        const int row = (int)v0 + sub;  // of this lane group
+        // positions of the group's row, 64 at a time
+        for (int c = (lane % LPR) * VEC; c - (lane % LPR) * VEC < dim; c += LPR * VEC) {
+            float acc[VEC];
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+            for (int i0 = 0; i0 < n; i0 += 64) {
+                uint64_t mine = 0;
+                const int id = s_id[i0 + lane];
+                if (!__any(id >= (int)v0 && id < (int)v0 + 64 / LPR)) continue;
+#pragma unroll
+                for (int q = 0; q < 64 / LPR; ++q) {
+                    const uint64_t m = __ballot(id == (int)v0 + q);
+                    mine = q == sub ? m : mine;
+                }
+                while (mine) {
+                    float t[U][VEC];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) t[u][k] = 0.f;
+                        if (mine) {
+                            const int i = i0 + __ffsll((unsigned long long)mine) - 1;
+                            mine &= mine - 1;
+                            if (c < dim) load_row(dout + (int64_t)i * ds + c, dim - c, t[u]);
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) acc[k] += t[u][k];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) acc[k] *= scale;
+            if (row < vocab && c < dim) store_row(dtable + (int64_t)row * ts + c, dim - c, acc);
+        }
     }
 }
 
@@ -89,54 +145,60 @@ __global__ __launch_bounds__(EB) void k_zero_rows(int64_t rows, int dim, T* __re
 // earlier block, and its last run where it goes on in the next (and began in
 // this one). tail_key[b]: that last run's key, or vocab; end_block[key]: the
 // block in which a run that came from an earlier block ends.
-template <class T, int VEC, int LPR>
-__global__ __launch_bounds__(EB) void k_embed_runs(int n, int dim, int vocab, const uint32_t* __restrict__ keys,
-                                                   const uint32_t* __restrict__ pos, const T* __restrict__ dout,
-                                                   int64_t ds, float scale, T* __restrict__ dtable, int64_t ts,
-                                                   float* __restrict__ part, uint32_t* __restrict__ tail_key,
-                                                   uint32_t* __restrict__ end_block) {
-    constexpr int G = EB / LPR;
+template <class T, int LPR>
+__global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
+    int n, int dim, int vocab, const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos,
+    const T* __restrict__ dout, int64_t ds, float scale, T* __restrict__ dtable, int64_t ts,
+    float* __restrict__ part, uint32_t* __restrict__ tail_key, uint32_t* __restrict__ end_block) {
+    constexpr int NT = run_threads(LPR);
+    constexpr int G = NT / LPR;
     constexpr int BT = G * RUN_TOKENS;
-    constexpr int CW = LPR * VEC;
+    constexpr int VEC = WIDE<T>, CW = LPR * VEC;
     constexpr int U = 8;
+    __shared__ uint32_t s_tok[BT], s_pos[BT];
     __shared__ uint32_t s_key[2 * G];  // per group: its first run's key and, if another, its last run's
     __shared__ float s_sum[2 * G][CW];
     const uint32_t none = (uint32_t)vocab;
     const int g = threadIdx.x / LPR, l = threadIdx.x % LPR;
     const int c0 = blockIdx.y * CW, c = c0 + l * VEC;
-    const bool in = c < dim;
     const int b0 = blockIdx.x * BT, b1 = min(n, b0 + BT);
-    const int p0 = b0 + g * RUN_TOKENS, p1 = min(b1, p0 + RUN_TOKENS);
+    for (int i = threadIdx.x; i < BT; i += NT) {
+        s_tok[i] = b0 + i < b1 ? keys[b0 + i] : none;
+        s_pos[i] = b0 + i < b1 ? pos[b0 + i] : 0u;
+    }
+    const uint32_t before = b0 > 0 ? keys[b0 - 1] : none;
+    const uint32_t after = b1 < n ? keys[b1] : none;
+    __syncthreads();
+    const int p0 = g * RUN_TOKENS;
 
     float acc[VEC];
-    uint32_t cur = none, first = none;
+    const uint32_t first = s_tok[p0];
+    uint32_t cur = first;
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
     bool lead = true;  // still in the group's first run
-    for (int p = p0; p < p1; p += U) {
+    for (int p = p0; p < p0 + RUN_TOKENS; p += U) {
+        if (s_tok[p] == none) break;  // sorted last: nothing follows
         uint32_t kk[U];
         float v[U][VEC];
 #pragma unroll
-        for (int u = 0; u < U; ++u) kk[u] = p + u < p1 ? keys[p + u] : none;
-#pragma unroll
         for (int u = 0; u < U; ++u) {
+            kk[u] = s_tok[p + u];
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[u][k] = 0.f;
-            if (kk[u] != none && in) load_row<VEC>(dout + (int64_t)pos[p + u] * ds + c, v[u]);
+            if (kk[u] != none && c < dim) load_row(dout + (int64_t)s_pos[p + u] * ds + c, dim - c, v[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (kk[u] == none) break;  // sorted last: nothing follows
-            if (p + u == p0) first = cur = kk[u];
-            if (kk[u] != cur) {
+            if (kk[u] != none && kk[u] != cur) {
                 if (lead) {
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) s_sum[2 * g][l * VEC + k] = acc[k];
                     lead = false;
-                } else if (in) {  // a run between two others of the group is whole
+                } else if (c < dim) {  // a run between two others of the group is whole
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) acc[k] *= scale;
-                    store_row<VEC>(dtable + (int64_t)cur * ts + c, acc);
+                    store_row(dtable + (int64_t)cur * ts + c, dim - c, acc);
                 }
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
@@ -155,9 +217,7 @@ __global__ __launch_bounds__(EB) void k_embed_runs(int n, int dim, int vocab, co
     __syncthreads();
 
     // the groups' first and last runs in order, one thread per column
-    const uint32_t before = b0 > 0 ? keys[b0 - 1] : none;
-    const uint32_t after = b1 < n ? keys[b1] : none;
-    for (int j = threadIdx.x; j < CW; j += EB) {
+    for (int j = threadIdx.x; j < CW; j += NT) {
         const bool col = c0 + j < dim;
         uint32_t run = none;
         float sum = 0.f;
@@ -178,6 +238,7 @@ __global__ __launch_bounds__(EB) void k_embed_runs(int n, int dim, int vocab, co
         bool any = false;
         for (int e = 0; e < 2 * G; ++e) {
             const uint32_t key = s_key[e];
+            const float x = s_sum[e][j];
             if (key == none) continue;
             if (key != run) {
                 close(false);
@@ -186,7 +247,7 @@ __global__ __launch_bounds__(EB) void k_embed_runs(int n, int dim, int vocab, co
                 run = key;
                 sum = 0.f;
             }
-            sum += s_sum[e][j];
+            sum += x;
         }
         close(run == after);
         if (j == 0 && blockIdx.y == 0) tail_key[blockIdx.x] = has_tail ? run : none;
@@ -196,13 +257,13 @@ __global__ __launch_bounds__(EB) void k_embed_runs(int n, int dim, int vocab, co
 // Rows whose run crosses blocks: the last run of block b, then the first runs
 // of the blocks after it up to the one where it ends, a contiguous share per
 // row group, the groups joined in order.
-template <class T, int VEC, int LPR>
+template <class T, int LPR>
 __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const uint32_t* __restrict__ tail_key,
                                                        const uint32_t* __restrict__ end_block,
                                                        const float* __restrict__ part, float scale,
                                                        T* __restrict__ dtable, int64_t ts) {
-    constexpr int G = JOIN_T / LPR;
-    constexpr int CW = LPR * VEC;
+    constexpr int VEC = WIDE<T>, CW = LPR * VEC;
+    constexpr int G = JOIN_T / LPR < 64 ? JOIN_T / LPR : 64;  // groups that take part
     __shared__ float s_sum[G][CW];
     const uint32_t key = tail_key[blockIdx.x];
     if (key == (uint32_t)vocab) return;
@@ -210,7 +271,7 @@ __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const
     const int c = blockIdx.y * CW + l * VEC;
     const int b = blockIdx.x, cnt = (int)end_block[key] - b + 1;
     const int per = (cnt + G - 1) / G;
-    const int j0 = g * per, j1 = min(cnt, j0 + per);
+    const int j0 = g * per, j1 = g < G ? min(cnt, j0 + per) : 0;
     float acc[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
@@ -219,11 +280,12 @@ __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const
         for (int j = j0; j < j1; ++j) {
             const float* q = part + ((size_t)(b + j) * 2 + (j == 0 ? 1 : 0)) * dim + c;
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) acc[k] += q[k];
+            for (int k = 0; k < VEC; ++k) acc[k] += c + k < dim ? q[k] : 0.f;
         }
     }
+    if (g < G)
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) s_sum[g][l * VEC + k] = acc[k];
+        for (int k = 0; k < VEC; ++k) s_sum[g][l * VEC + k] = acc[k];
     __syncthreads();
     for (int h = G / 2; h > 0; h >>= 1) {
         if (g < h)
@@ -234,7 +296,7 @@ __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const
     if (g == 0 && c < dim) {
 #pragma unroll
         for (int k = 0; k < VEC; ++k) acc[k] = s_sum[0][l * VEC + k] * scale;
-        store_row<VEC>(dtable + (int64_t)key * ts + c, acc);
+        store_row(dtable + (int64_t)key * ts + c, dim - c, acc);
     }
 }
 
@@ -251,58 +313,58 @@ struct EmbedArgs {
     uint32_t *tail_key, *end_block;
 };
 
-template <class T, int VEC, int LPR>
-hipError_t embed_rows(const EmbedArgs& a, bool backward, hipStream_t s) {
-    constexpr int G = EB / LPR;
-    if (!backward) {
+template <class T, int LPR>
+hipError_t embed_rows(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
+    if (pass == LOOKUP) {
+        constexpr int G = EB / LPR;
         const int64_t blocks = (a.n + G * 4 - 1) / (G * 4);
-        k_embed<T, VEC, LPR><<<(unsigned)blocks, EB, 0, s>>>(a.n, a.dim, a.vocab, (const T*)a.src, a.ss, a.ids, a.wide,
-                                                            a.scale, (T*)a.dst, a.ds);
+        k_embed<T, LPR><<<(unsigned)blocks, EB, 0, s>>>(a.n, a.dim, a.vocab, (const T*)a.src, a.ss, a.ids, a.wide,
+                                                       a.scale, (T*)a.dst, a.ds);
         return hipGetLastError();
     }
-    constexpr int BT = G * RUN_TOKENS;
+    if (pass == FEW_SUMS) {
+        const int64_t want = (a.vocab + EB / LPR - 1) / (EB / LPR);
+        k_embed_few<T, LPR><<<(unsigned)(want < 2048 ? want : 2048), EB, 0, s>>>(
+            (int)a.n, a.dim, a.vocab, a.ids, a.wide, a.scale, (const T*)a.src, a.ss, (T*)a.dst, a.ds);
+        return hipGetLastError();
+    }
+    constexpr int BT = run_threads(LPR) / LPR * RUN_TOKENS;
     const int nb = (int)((a.n + BT - 1) / BT);
-    const dim3 grid(nb, (a.dim + LPR * VEC - 1) / (LPR * VEC));
-    k_embed_runs<T, VEC, LPR><<<grid, EB, 0, s>>>((int)a.n, a.dim, a.vocab, a.keys, a.pos, (const T*)a.src, a.ss,
-                                                 a.scale, (T*)a.dst, a.ds, a.part, a.tail_key, a.end_block);
+    const dim3 grid(nb, (a.dim + LPR * WIDE<T> - 1) / (LPR * WIDE<T>));
+    k_embed_runs<T, LPR><<<grid, run_threads(LPR), 0, s>>>((int)a.n, a.dim, a.vocab, a.keys, a.pos, (const T*)a.src,
+                                                          a.ss, a.scale, (T*)a.dst, a.ds, a.part, a.tail_key,
+                                                          a.end_block);
     if (nb > 1)
-        k_embed_join<T, VEC, LPR><<<grid, JOIN_T, 0, s>>>(a.dim, a.vocab, a.tail_key, a.end_block, a.part, a.scale,
-                                                         (T*)a.dst, a.ds);
+        k_embed_join<T, LPR><<<grid, JOIN_T, 0, s>>>(a.dim, a.vocab, a.tail_key, a.end_block, a.part, a.scale,
+                                                    (T*)a.dst, a.ds);
     return hipGetLastError();
 }
 
-template <class T, int VEC>
-hipError_t embed_pick(const EmbedArgs& a, bool backward, hipStream_t s) {
-    const int v = (a.dim + VEC - 1) / VEC;
-    if (v <= 8) return embed_rows<T, VEC, 8>(a, backward, s);
-    if (v <= 16) return embed_rows<T, VEC, 16>(a, backward, s);
-    if (v <= 32) return embed_rows<T, VEC, 32>(a, backward, s);
-    return embed_rows<T, VEC, 64>(a, backward, s);
+// The fewest lanes that hold a row with one 16-byte access each, up to a wave.
+template <class T>
+hipError_t embed_run(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
+    const int v = (a.dim + WIDE<T> - 1) / WIDE<T>;
+    if (v <= 1) return embed_rows<T, 1>(a, pass, s);
+    if (v <= 2) return embed_rows<T, 2>(a, pass, s);
+    if (v <= 4) return embed_rows<T, 4>(a, pass, s);
+    if (v <= 8) return embed_rows<T, 8>(a, pass, s);
+    if (v <= 16) return embed_rows<T, 16>(a, pass, s);
+    if (v <= 32) return embed_rows<T, 32>(a, pass, s);
+    return embed_rows<T, 64>(a, pass, s);
 }
 
 template <class T>
-hipError_t embed_run(const EmbedArgs& a, bool backward, hipStream_t s) {
-    if (wide_rows<T>(a.src, a.ss, a.dim) && wide_rows<T>(a.dst, a.ds, a.dim))
-        return embed_pick<T, WIDE<T>>(a, backward, s);
-    return embed_pick<T, 1>(a, backward, s);
-}
-
-template <class T>
-hipError_t zero_rows(int64_t rows, int dim, void* p, int64_t stride, hipStream_t s) {
-    const bool w = wide_rows<T>(p, stride, dim);
-    const int64_t total = rows * (w ? dim / WIDE<T> : dim);
-    const int64_t want = (total + EB - 1) / EB;
-    const unsigned blocks = (unsigned)(want < 4096 ? want : 4096);
-    if (w)
-        k_zero_rows<T, WIDE<T>><<<blocks, EB, 0, s>>>(rows, dim, (T*)p, stride);
-    else
-        k_zero_rows<T, 1><<<blocks, EB, 0, s>>>(rows, dim, (T*)p, stride);
+hipError_t zero_rows(int rows, int dim, void* p, int64_t stride, hipStream_t s) {
+    int lanes = 1;
+    while (lanes < 64 && lanes * WIDE<T> < dim) lanes *= 2;
+    const int64_t want = ((int64_t)rows * lanes + EB - 1) / EB;
+    k_zero_rows<T><<<(unsigned)(want < 4096 ? want : 4096), EB, 0, s>>>(rows, dim, lanes, (T*)p, stride);
     return hipGetLastError();
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// The shortest run of positions per block (64 lanes per row) bounds the block count.
+// The fewest positions per block (64 lanes per row) bound the block count.
 int64_t max_blocks(int64_t n) { return (n + EB / 64 * RUN_TOKENS - 1) / (EB / 64 * RUN_TOKENS); }
 
 }  // namespace
@@ -341,15 +403,27 @@ hipError_t launch_embed_fwd(int64_t n, int dim, int vocab, bool half, const void
     a.dst = out;
     a.ds = out_stride;
     a.scale = scale;
-    return half ? embed_run<bf16>(a, false, stream) : embed_run<float>(a, false, stream);
+    return half ? embed_run<bf16>(a, LOOKUP, stream) : embed_run<float>(a, LOOKUP, stream);
 }
 
 hipError_t launch_embed_bwd(int64_t n, int dim, int vocab, bool half, const void* ids, bool wide_ids, float scale,
                             const void* dout, int64_t dout_stride, void* dtable, int64_t dtable_stride, char* ws,
                             hipStream_t stream) {
+    EmbedArgs a{};
+    a.n = n;
+    a.dim = dim;
+    a.vocab = vocab;
+    a.wide = wide_ids;
+    a.ids = ids;
+    a.src = dout;
+    a.ss = dout_stride;
+    a.dst = dtable;
+    a.ds = dtable_stride;
+    a.scale = scale;
+    if (n <= FEW) return half ? embed_run<bf16>(a, FEW_SUMS, stream) : embed_run<float>(a, FEW_SUMS, stream);
     hipError_t e = half ? zero_rows<bf16>(vocab, dim, dtable, dtable_stride, stream)
                         : zero_rows<float>(vocab, dim, dtable, dtable_stride, stream);
-    if (e != hipSuccess || n == 0) return e;
+    if (e != hipSuccess) return e;
     const EmbedLayout L = embed_bwd_layout(n, dim, vocab);
     uint32_t* keys[2] = {(uint32_t*)(ws + L.keys[0]), (uint32_t*)(ws + L.keys[1])};
     uint32_t* pos[2] = {(uint32_t*)(ws + L.pos[0]), (uint32_t*)(ws + L.pos[1])};
@@ -360,21 +434,12 @@ hipError_t launch_embed_bwd(int64_t n, int dim, int vocab, bool half, const void
     int at = 0;
     e = launch_radix_sort((int)n, vocab, keys, pos, ws + L.sort, &at, stream);
     if (e != hipSuccess) return e;
-    EmbedArgs a{};
-    a.n = n;
-    a.dim = dim;
-    a.vocab = vocab;
-    a.src = dout;
-    a.ss = dout_stride;
-    a.dst = dtable;
-    a.ds = dtable_stride;
-    a.scale = scale;
     a.keys = keys[at];
     a.pos = pos[at];
     a.part = (float*)(ws + L.part);
     a.tail_key = (uint32_t*)(ws + L.tail_key);
     a.end_block = (uint32_t*)(ws + L.end_block);
-    return half ? embed_run<bf16>(a, true, stream) : embed_run<float>(a, true, stream);
+    return half ? embed_run<bf16>(a, RUN_SUMS, stream) : embed_run<float>(a, RUN_SUMS, stream);
 }
 
 }  // namespace gs

@@ -52,6 +52,7 @@ struct Product {
     int64_t lda, ldb, pa, pb;     // row strides and distance between the parts of a split operand
     int m, n, k;                  // n, k: host bounds where the device count does not give them
     int splits;                   // of the depth
+    int grid;                     // blocks per split
     const int32_t* count;         // labelled rows
     // epilogues
     const int32_t* rows;          // labelled row -> row of the caller's arrays
@@ -164,22 +165,22 @@ __device__ __forceinline__ float exp_diff(float z, float ref) { return exp2_fast
 // empty extent (they bring zeros), which keeps the count of loads in flight
 // the same in every step.
 template <int MODE, int PARTS, int BM, class T>
-__global__ __launch_bounds__(GT, 2) void k_product(Product p) {
+__device__ __forceinline__ void product(const Product& p, int block, bf16* s_tiles) {
     constexpr bool TA = MODE == DX || MODE == DW, TB = MODE == DW;
     constexpr int WM = BM == 64 ? 64 : BM / 2;       // rows of a wave's part
     constexpr int WN = BM == 64 ? 32 : 64;           // columns
     constexpr int MW = BM / WM;                      // waves along m
     constexpr int TM = WM / 32, TN = WN / 32;
     constexpr int STEP = (BM + BN) * BK;  // elements of one staged step: the a tile, then the b tile
-    __shared__ __align__(16) bf16 s_tiles[STAGES * STEP];
     const int cnt = *p.count;
     const int nn = MODE == DW ? p.n : cnt;
     const int mt = (p.m + BM - 1) / BM, nt = (nn + BN - 1) / BN;
     // consecutive blocks go to the eight dies in turn: each takes a contiguous
     // run of tiles, in groups of 8 columns, so that its cache serves both operands
     const int tiles = mt * nt, per_die = (tiles + 7) / 8;
-    const int tile = (blockIdx.x & 7) * per_die + (blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= per_die || tile >= tiles) return;
+    const int split = block / p.grid, b0 = block - split * p.grid;  // p.grid: blocks of one split, a multiple of 8
+    const int tile = (b0 & 7) * per_die + (b0 >> 3);
+    if ((b0 >> 3) >= per_die || tile >= tiles) return;
     const int grp = tile / (8 * mt), in_grp = tile - grp * 8 * mt;
     const int gw = min(8, nt - grp * 8);
     const int m0 = in_grp / gw * BM, n0 = (grp * 8 + in_grp % gw) * BN;
@@ -187,7 +188,7 @@ __global__ __launch_bounds__(GT, 2) void k_product(Product p) {
     const int depth = MODE == DW ? cnt : p.k;
     const int nk = (depth + BK - 1) / BK;
     const int share = (nk + p.splits - 1) / p.splits;
-    const int k_first = min(nk, (int)blockIdx.y * share), k_end = min(nk, k_first + share);
+    const int k_first = min(nk, split * share), k_end = min(nk, k_first + share);
     const int per = k_end - k_first;
     const int steps = per * (PARTS == 3 ? 6 : 1);
 
@@ -368,7 +369,7 @@ __global__ __launch_bounds__(GT, 2) void k_product(Product p) {
             int room = (p.acc ? (int)p.ldacc : p.out_dim) - mb;
             asm volatile("" : "+v"(room));
             if (p.acc) {
-                float* q = p.acc + blockIdx.y * p.pacc + n * p.ldacc + mb;
+                float* q = p.acc + split * p.pacc + n * p.ldacc + mb;
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -410,12 +411,31 @@ __global__ __launch_bounds__(GT, 2) void k_product(Product p) {
     }
 }
 
+template <int MODE, int PARTS, int BM, class T>
+__global__ __launch_bounds__(GT, 2) void k_product(Product p) {
+    __shared__ __align__(16) bf16 s_tiles[STAGES * (BM + BN) * BK];
+    product<MODE, PARTS, BM, T>(p, blockIdx.x, s_tiles);
+}
+
+// dx and dw, which read the same dz, in one launch: together they fill the chip better, and small ones wait once.
+template <int PARTS, int BM, class T>
+__global__ __launch_bounds__(GT, 2) void k_product_pair(Product dx, Product dw) {
+    __shared__ __align__(16) bf16 s_tiles[STAGES * (BM + BN) * BK];
+    const int first = dx.grid * dx.splits;
+    if ((int)blockIdx.x < first)
+        product<DX, PARTS, BM, T>(dx, blockIdx.x, s_tiles);
+    else
+        product<DW, PARTS, BM, T>(dw, blockIdx.x - first, s_tiles);
+}
+
 // ---------------------------------------------------------------- labelled rows
 
-constexpr int LT = 1024;          // threads
-constexpr int LPT = 8;            // consecutive rows per thread
-constexpr int LROWS = LT * LPT;   // rows per block
+constexpr int LT = 256;            // threads
+constexpr int LPT = 8;             // consecutive rows per thread
+constexpr int LROWS = LT * LPT;    // rows per block
+constexpr int64_t LOOK_BACK = 32768;  // rows up to which a block counts the labels before its own rows itself
 
+// Sum of v over the threads below (all LT take part); total: over all.
 __device__ __forceinline__ int block_scan_excl(int v, int* s_w, int* total) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     int x = v;
@@ -427,6 +447,7 @@ __device__ __forceinline__ int block_scan_excl(int v, int* s_w, int* total) {
     if (lane == 63) s_w[w] = x;
     __syncthreads();
     int pre = 0, tot = 0;
+#pragma unroll
     for (int k = 0; k < LT / 64; ++k) {
         pre += k < w ? s_w[k] : 0;
         tot += s_w[k];
@@ -436,92 +457,134 @@ __device__ __forceinline__ int block_scan_excl(int v, int* s_w, int* total) {
     return pre + x - v;
 }
 
-__global__ __launch_bounds__(LT) void k_label_count(int64_t n, int vocab, const void* __restrict__ labels, bool wide,
-                                                    int32_t* __restrict__ block_count) {
+// The arrays that the labels give: rows[], the labelled rows in order; place[r],
+// the position of row r in it, or -1; their number; loss and lse (nullable),
+// cleared for the other rows; done, the joining blocks' counter, cleared.
+struct LabelRows {
+    int64_t n;
+    int vocab;
+    int wide;
+    const void* labels;
+    int32_t *rows, *place, *count, *done;
+    float *loss, *lse;
+};
+
+__global__ __launch_bounds__(LT) void k_label_count(LabelRows a, int32_t* __restrict__ block_count) {
     __shared__ int s_w[LT / 64];
-    const int64_t r0 = (int64_t)blockIdx.x * LROWS + threadIdx.x * LPT;
-    int c = 0;
+    const int64_t r0 = (int64_t)blockIdx.x * LROWS + threadIdx.x;
+    int c = 0, tot;
 #pragma unroll
-    for (int k = 0; k < LPT; ++k) c += r0 + k < n && row_index(labels, wide, r0 + k, vocab) >= 0;
-    int tot;
+    for (int k = 0; k < LPT; ++k)
+        c += r0 + k * LT < a.n && row_index(a.labels, a.wide, r0 + k * LT, a.vocab) >= 0;
     block_scan_excl(c, s_w, &tot);
     if (threadIdx.x == 0) block_count[blockIdx.x] = tot;
 }
 
-// rows[]: the labelled rows in order; place[r]: the position of row r in it, or
-// -1; the count. loss and lse (nullable) are cleared for rows without a label.
-__global__ __launch_bounds__(LT) void k_label_rows(int64_t n, int vocab, const void* __restrict__ labels, bool wide,
-                                                   const int32_t* __restrict__ block_count,
-                                                   int32_t* __restrict__ rows, int32_t* __restrict__ place,
-                                                   int32_t* __restrict__ count, float* __restrict__ loss,
-                                                   float* __restrict__ lse) {
-    __shared__ int s_w[LT / 64];
-    int base = 0;
-    if (gridDim.x > 1) {
-        int c = 0;
-        for (int k = threadIdx.x; k < (int)blockIdx.x; k += LT) c += block_count[k];
-        block_scan_excl(c, s_w, &base);
-    }
-    const int64_t r0 = (int64_t)blockIdx.x * LROWS + threadIdx.x * LPT;
+// The labels of block `b`'s rows; base: labelled rows before them. s_list
+// (nullable): the rows also go there. Returns the labelled rows up to the block's end.
+__device__ __forceinline__ int label_rows(const LabelRows& a, int b, int base, bool write, int* s_w, int* s_list) {
+    const int64_t r0 = (int64_t)b * LROWS + threadIdx.x * LPT;
     bool have[LPT];
-    int c = 0;
+    int c = 0, tot;
 #pragma unroll
     for (int k = 0; k < LPT; ++k) {
-        have[k] = r0 + k < n && row_index(labels, wide, r0 + k, vocab) >= 0;
+        have[k] = r0 + k < a.n && row_index(a.labels, a.wide, r0 + k, a.vocab) >= 0;
         c += have[k];
     }
-    int tot;
     int at = base + block_scan_excl(c, s_w, &tot);
 #pragma unroll
     for (int k = 0; k < LPT; ++k) {
         const int64_t r = r0 + k;
-        if (r >= n) break;
-        place[r] = have[k] ? at : -1;
+        if (r >= a.n) break;
+        if (write) {
+            a.place[r] = have[k] ? at : -1;
+            if (have[k]) a.rows[at] = (int32_t)r;
+            if (!have[k] && a.loss) a.loss[r] = 0.f;
+            if (!have[k] && a.lse) a.lse[r] = 0.f;
+        }
         if (have[k]) {
-            rows[at++] = (int32_t)r;
-        } else {
-            if (loss) loss[r] = 0.f;
-            if (lse) lse[r] = 0.f;
+            if (s_list) s_list[at] = (int)r;
+            ++at;
         }
     }
-    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *count = base + tot;
+    return base + tot;
 }
 
-// Rows into bfloat16 parts of kp columns (a multiple of BK, zero beyond dim).
-// With a list: the listed rows, and zero rows up to the next multiple of BN.
-template <class T, int PARTS>
-__global__ __launch_bounds__(256) void k_pack(int64_t rows, int dim, int kp, const T* __restrict__ x, int64_t xs,
-                                              bool wide, const int32_t* __restrict__ list,
-                                              const int32_t* __restrict__ count, bf16* __restrict__ out,
-                                              int64_t part) {
-    const int per = kp / 8;
-    int64_t live = rows, padded = rows;
-    if (list) {
-        live = *count;
+// block_count (nullable): the blocks' labelled rows, counted before.
+__global__ __launch_bounds__(LT) void k_label_rows(LabelRows a, const int32_t* __restrict__ block_count) {
+    __shared__ int s_w[LT / 64];
+    int c = 0, base;
+    if (block_count) {
+        for (int k = threadIdx.x; k < (int)blockIdx.x; k += LT) c += block_count[k];
+    } else {
+#pragma unroll 8
+        for (int64_t r = threadIdx.x; r < (int64_t)blockIdx.x * LROWS; r += LT)
+            c += row_index(a.labels, a.wide, r, a.vocab) >= 0;
+    }
+    block_scan_excl(c, s_w, &base);
+    const int end = label_rows(a, blockIdx.x, base, true, s_w, nullptr);
+    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
+        *a.count = end;
+        *a.done = 0;
+    }
+}
+
+// Rows into bfloat16 parts of kp columns (a multiple of BK, zero beyond dim):
+// the first x_blocks blocks pack x's labelled rows, and zero rows up to the
+// next multiple of BN, the others every row of w. SMALL: x has at most LROWS
+// rows, and each block makes the list of labelled rows for itself first (block
+// 0 also writes its arrays), which saves a launch.
+struct PackArgs {
+    int dim, kp, per_block;  // per_block: rows of a block
+    int x_blocks;
+    const void *x, *w;
+    int64_t xs, ws, w_rows;
+    bf16 *xp, *wp;
+    int64_t x_part, w_part;  // distance of the parts
+};
+
+template <class T, int PARTS, bool SMALL>
+__global__ __launch_bounds__(LT) void k_pack(LabelRows a, PackArgs p) {
+    __shared__ int s_w[LT / 64];
+    __shared__ int s_list[SMALL ? LROWS : 1];
+    const bool x = (int)blockIdx.x < p.x_blocks;
+    const int64_t r0 = (int64_t)(blockIdx.x - (x ? 0 : p.x_blocks)) * p.per_block;
+    int64_t live = p.w_rows, padded = p.w_rows;
+    if (x) {
+        if (SMALL) {
+            live = label_rows(a, 0, 0, blockIdx.x == 0, s_w, s_list);
+            __syncthreads();
+            if (blockIdx.x == 0 && threadIdx.x == 0) {
+                *a.count = (int)live;
+                *a.done = 0;
+            }
+        } else {
+            live = *a.count;
+        }
         padded = (live + BN - 1) / BN * BN;
     }
-    const int64_t total = padded * per;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / per;
-        const int c = (int)(i - r * per) * 8;
+    const int64_t left = padded - r0;
+    if (left <= 0) return;
+    const uint32_t per = p.kp / 8, total = (uint32_t)(left < p.per_block ? left : p.per_block) * per;
+    const T* src = static_cast<const T*>(x ? p.x : p.w);
+    const int64_t stride = x ? p.xs : p.ws, part = x ? p.x_part : p.w_part;
+    bf16* dst = x ? p.xp : p.wp;
+    for (uint32_t i = threadIdx.x; i < total; i += LT) {
+        const uint32_t rr = i / per;
+        const int64_t r = r0 + rr;
+        const int c = (int)(i - rr * per) * 8;
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = 0.f;
         if (r < live) {
-            const T* q = x + (list ? (int64_t)list[r] : r) * xs + c;
-            if (wide && c + 8 <= dim) {
-                constexpr int V = WIDE<T>;
+            const int64_t row = !x ? r : SMALL ? s_list[r] : a.rows[r];
+            constexpr int V = WIDE<T>;
 #pragma unroll
-                for (int k = 0; k < 8; k += V) {
-                    float t[V];
-                    load_row<V>(q + k, t);
+            for (int k = 0; k < 8; k += V) {
+                float t[V];
+                load_row(src + row * stride + c + k, p.dim - c - k, t);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) v[k + j] = t[j];
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (c + k < dim) v[k] = (float)q[k];
+                for (int j = 0; j < V; ++j) v[k + j] = t[j];
             }
         }
         bf16x8 o[PARTS];
@@ -540,7 +603,7 @@ __global__ __launch_bounds__(256) void k_pack(int64_t rows, int dim, int kp, con
             }
         }
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q) *reinterpret_cast<bf16x8*>(out + q * part + r * kp + c) = o[q];
+        for (int q = 0; q < PARTS; ++q) *reinterpret_cast<bf16x8*>(dst + q * part + r * p.kp + c) = o[q];
     }
 }
 
@@ -554,83 +617,120 @@ __device__ __forceinline__ float2 lse_join(float2 a, float2 b) {
 }
 
 constexpr int JR = 64;  // rows per block of the join
-constexpr int JT = 256;
+constexpr int JT = 1024;
 
 // Joins the slabs' (maximum, sum) pairs of each labelled row (and `state`, the
-// join of earlier pieces, with `more` pieces to come left there again), then
-// the row's loss; block_sum: the block's losses added.
+// join of earlier pieces; with `more` pieces to come the result is left there
+// again), then the row's loss. The block that ends last adds the blocks' losses
+// in block order: the mean.
 __global__ __launch_bounds__(JT) void k_lse_join(int slabs, int np, const float2* __restrict__ part,
                                                  const float* __restrict__ target, const int32_t* __restrict__ rows,
                                                  const int32_t* __restrict__ count, float2* __restrict__ state,
                                                  bool first, bool more, float* __restrict__ loss,
-                                                 float* __restrict__ lse, double* __restrict__ block_sum) {
-    __shared__ float2 s[JT / JR][JR];
-    __shared__ double s_sum;
+                                                 float* __restrict__ lse, double* __restrict__ block_sum,
+                                                 int32_t* __restrict__ done, float* __restrict__ mean,
+                                                 int32_t* __restrict__ count_out) {
+    constexpr int G = JT / JR;
+    __shared__ float2 s[G][JR];
+    __shared__ double s_sum[JT / 64];
+    __shared__ int s_last;
     const int j = threadIdx.x % JR, g = threadIdx.x / JR;
     const int n = blockIdx.x * JR + j, cnt = *count;
     float2 a = make_float2(-INFINITY, 0.f);
     if (n < cnt) {
         if (!first && g == 0) a = state[n];
-#pragma unroll 4
-        for (int k = g; k < slabs; k += JT / JR) a = lse_join(a, part[(int64_t)k * np + n]);
+#pragma unroll 8
+        for (int k = g; k < slabs; k += G) a = lse_join(a, part[(int64_t)k * np + n]);
     }
     s[g][j] = a;
     __syncthreads();
     if (g == 0) {
         double mine = 0.0;
         if (n < cnt) {
-            for (int k = 1; k < JT / JR; ++k) a = lse_join(a, s[k][j]);
+            for (int k = 1; k < G; ++k) a = lse_join(a, s[k][j]);
             if (more) {
                 state[n] = a;
             } else {
-                const float v = a.x + log2f(a.y) * LN2;
-                const float z = target[n];
+                const float z = target[n], ln = log2f(a.y) * LN2;
                 const int r = rows[n];
                 // (maximum - z) first: exact where they are close
-                const float ls = a.x == INFINITY ? a.x - z : (a.x - z) + log2f(a.y) * LN2;
-                lse[r] = v;
+                const float ls = a.x == INFINITY ? a.x - z : (a.x - z) + ln;
+                lse[r] = a.x + ln;
                 loss[r] = ls;
                 mine = (double)ls;
             }
         }
-        for (int off = 32; off > 0; off >>= 1) mine += __shfl_xor(mine, off);
-        if (j == 0) s_sum = mine;
+        if (!more) {
+            for (int off = 32; off > 0; off >>= 1) mine += __shfl_xor(mine, off);
+            if (j == 0) {
+                __hip_atomic_store(&block_sum[blockIdx.x], mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                s_last = __hip_atomic_fetch_add(done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                         (int)gridDim.x - 1;
+            }
+        }
     }
+    if (more) return;
     __syncthreads();
-    if (threadIdx.x == 0) block_sum[blockIdx.x] = s_sum;
-}
-
-__global__ __launch_bounds__(LT) void k_loss_mean(const double* __restrict__ block_sum,
-                                                  const int32_t* __restrict__ count, float* __restrict__ mean,
-                                                  int32_t* __restrict__ count_out) {
-    __shared__ double s[LT / 64];
-    const int cnt = *count, blocks = (cnt + JR - 1) / JR;
-    double a = 0.0;
-    for (int k = threadIdx.x; k < blocks; k += LT) a += block_sum[k];
-    for (int off = 32; off > 0; off >>= 1) a += __shfl_xor(a, off);
-    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = a;
+    if (!s_last) return;
+    double sum = 0.0;
+    for (int k = threadIdx.x; k < (int)gridDim.x; k += JT)
+        sum += __hip_atomic_load(&block_sum[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+    if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int k = 1; k < LT / 64; ++k) a += s[k];
-        *mean = cnt > 0 ? (float)(a / (double)cnt) : 0.f;
+        for (int k = 1; k < JT / 64; ++k) sum += s_sum[k];
+        *mean = cnt > 0 ? (float)(sum / (double)cnt) : 0.f;
         *count_out = cnt;
     }
 }
 
-// out[r] = the splits' rows added in order, through place (-1: a zero row) if given.
+// out[r] = the splits' rows of acc added in order, through place (-1: a zero row) if given.
+struct SplitJoin {
+    int64_t rows;
+    int splits;
+    const float* acc;
+    int64_t pacc;
+    const int32_t* place;
+    void* out;
+    int64_t ldout;
+    int blocks;
+};
+
+// Two joins in one launch: the first a.blocks blocks do a, the others b.
 template <class T>
-__global__ __launch_bounds__(256) void k_join_splits(int64_t rows, int dim, int splits, const float* __restrict__ acc,
-                                                     int64_t ldacc, int64_t pacc, const int32_t* __restrict__ place,
-                                                     T* __restrict__ out, int64_t ldout) {
-    const int lane = threadIdx.x & 63;
-    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.x * 4) {
-        const int64_t src = place ? place[r] : r;
-        for (int c = lane; c < dim; c += 64) {
-            float a = 0.f;
-            if (src >= 0)
+__global__ __launch_bounds__(256) void k_join_splits(SplitJoin a, SplitJoin b, int dim, int kp, int per_block) {
+    const bool second = (int)blockIdx.x >= a.blocks;
+    const SplitJoin& j = second ? b : a;
+    const int64_t r0 = (int64_t)(blockIdx.x - (second ? a.blocks : 0)) * per_block;
+    const int64_t left = j.rows - r0;
+    const uint32_t per = (dim + 3) / 4, total = (uint32_t)(left < per_block ? left : per_block) * per;
+    for (uint32_t i = threadIdx.x; i < total; i += 256) {
+        const uint32_t rr = i / per;
+        const int64_t r = r0 + rr;
+        const int c = (int)(i - rr * per) * 4;
+        const int64_t src = j.place ? j.place[r] : r;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (src >= 0) {
+            const float* q = j.acc + src * kp + c;
 #pragma unroll 8
-                for (int s = 0; s < splits; ++s) a += acc[s * pacc + src * ldacc + c];
-            out[r * ldout + c] = (T)a;
+            for (int s = 0; s < j.splits; ++s) {
+                const float4 t = *reinterpret_cast<const float4*>(q + s * j.pacc);
+                v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
+            }
+        }
+        T* o = static_cast<T*>(j.out) + r * j.ldout + c;
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        if (c + 4 <= dim) {
+            typedef T vec __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+            vec t;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k] = (T)f[k];
+            *reinterpret_cast<vec*>(o) = t;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if (c + k < dim) o[k] = (T)f[k];
         }
     }
 }
@@ -660,9 +760,9 @@ struct LossPlan {
     int parts, kp;
     int64_t np;                    // rows of x padded to the tile
     int64_t piece_f, piece_b;      // vocabulary rows per piece (multiples of 256)
-    int bm_z, bm_dx, bm_dw;        // tile rows: over the vocabulary, over dim
+    int bm_z, bm_d;                // tile rows: over the vocabulary, over dim
     int split_dx, split_dw;
-    size_t rows, place, count, block_count, xp, wp, part, target, state, block_sum, dz, dxp, dwp, total;
+    size_t rows, place, count, done, block_count, xp, wp, part, target, state, block_sum, dz, dxp, dwp, total;
 };
 
 LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
@@ -678,10 +778,10 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     L.piece_f = piece((int64_t)1 << 31);  // 8 bytes per 64 vocabulary rows: 256 MB
     L.piece_b = piece(((int64_t)1 << 28) / L.parts);  // 2 bytes per part: 512 MB
     L.bm_z = tile_rows(backward ? L.piece_b : L.piece_f, L.np);
-    L.bm_dx = tile_rows(L.kp, L.np);
-    L.bm_dw = tile_rows(L.kp, L.piece_b);
-    L.split_dx = splits_for(up(L.kp, L.bm_dx) / L.bm_dx * (L.np / BN), L.piece_b / BK, L.parts);
-    L.split_dw = splits_for(up(L.kp, L.bm_dw) / L.bm_dw * (L.piece_b / BN), L.np / BK, L.parts);
+    L.bm_d = tile_rows(L.kp, L.np < L.piece_b ? L.np : L.piece_b);
+    const int64_t mt = up(L.kp, L.bm_d) / L.bm_d;
+    L.split_dx = splits_for(mt * (L.np / BN), L.piece_b / BK, L.parts);
+    L.split_dw = splits_for(mt * (L.piece_b / BN), L.np / BK, L.parts);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -691,6 +791,7 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     L.rows = take((size_t)L.np * 4);
     L.place = take((size_t)L.np * 4);
     L.count = take(4);
+    L.done = take(4);
     L.block_count = take((size_t)(L.np / LROWS + 1) * 4);
     L.xp = take((size_t)L.parts * L.np * L.kp * 2);
     L.wp = take((size_t)L.parts * vocab * L.kp * 2);
@@ -713,47 +814,81 @@ struct Packed {
     int64_t ldw, pw;
 };
 
-template <class T>
-hipError_t label_rows(const LabelLossArgs& a, const LossPlan& L, char* ws, bool forward, Packed& pk, hipStream_t s) {
-    constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
-    int32_t *rows = (int32_t*)(ws + L.rows), *place = (int32_t*)(ws + L.place), *count = (int32_t*)(ws + L.count),
-            *bc = (int32_t*)(ws + L.block_count);
-    const int64_t want = (a.n + LROWS - 1) / LROWS;
-    const unsigned blocks = (unsigned)(want < 1 ? 1 : want);
-    if (blocks > 1) k_label_count<<<blocks, LT, 0, s>>>(a.n, a.vocab, a.labels, a.wide_labels, bc);
-    k_label_rows<<<blocks, LT, 0, s>>>(a.n, a.vocab, a.labels, a.wide_labels, bc, rows, place, count,
-                                       forward ? a.loss : nullptr, forward ? a.lse : nullptr);
-    auto grid = [&](int64_t r) {
-        const int64_t b = (r * (L.kp / 8) + 255) / 256;
-        return (unsigned)(b < 1 ? 1 : b > 8192 ? 8192 : b);
-    };
-    k_pack<T, PARTS><<<grid(L.np), 256, 0, s>>>(a.n, a.dim, L.kp, (const T*)a.x, a.x_stride,
-                                               (uintptr_t)a.x % 16 == 0 && a.x_stride % WIDE<T> == 0, rows, count,
-                                               (bf16*)(ws + L.xp), L.np * L.kp);
-    const bool w_wide = (uintptr_t)a.w % 16 == 0 && a.w_stride % WIDE<T> == 0;
-    if (PARTS == 1 && w_wide && a.dim == L.kp && a.w_stride <= 1 << 20) {  // the products read w where it is
-        pk.w = (const bf16*)a.w;
-        pk.ldw = a.w_stride;
-    } else {
-        k_pack<T, PARTS><<<grid(a.vocab), 256, 0, s>>>(a.vocab, a.dim, L.kp, (const T*)a.w, a.w_stride, w_wide, nullptr,
-                                                      nullptr, (bf16*)(ws + L.wp), (int64_t)a.vocab * L.kp);
-        pk.w = (const bf16*)(ws + L.wp);
-        pk.ldw = L.kp;
-    }
-    pk.pw = (int64_t)a.vocab * L.kp;
-    return hipGetLastError();
+// Sets the product's blocks per split for m rows and n columns.
+void set_grid(Product& p, int bm, int64_t m, int64_t n) {
+    const int64_t t = up(m, bm) / bm * (up(n, BN) / BN);
+    p.grid = (int)(t < 8 ? 8 : up(t, 8));
 }
 
 template <int MODE, int PARTS, class T>
-void launch_product(int bm, const Product& p, int64_t m, int64_t n, hipStream_t s) {
-    const int64_t t = up(m, bm) / bm * (up(n, BN) / BN);
-    const dim3 grid((unsigned)(t < 8 ? 8 : up(t, 8)), p.splits);
+void launch_product(int bm, const Product& p, hipStream_t s) {
+    const unsigned grid = (unsigned)p.grid * p.splits;
     if (bm == 256)
         k_product<MODE, PARTS, 256, T><<<grid, GT, 0, s>>>(p);
     else if (bm == 128)
         k_product<MODE, PARTS, 128, T><<<grid, GT, 0, s>>>(p);
     else
         k_product<MODE, PARTS, 64, T><<<grid, GT, 0, s>>>(p);
+}
+
+template <int PARTS, class T>
+void launch_pair(int bm, const Product& dx, const Product& dw, hipStream_t s) {
+    const unsigned grid = (unsigned)dx.grid * dx.splits + (unsigned)dw.grid * dw.splits;
+    if (bm == 256)
+        k_product_pair<PARTS, 256, T><<<grid, GT, 0, s>>>(dx, dw);
+    else if (bm == 128)
+        k_product_pair<PARTS, 128, T><<<grid, GT, 0, s>>>(dx, dw);
+    else
+        k_product_pair<PARTS, 64, T><<<grid, GT, 0, s>>>(dx, dw);
+}
+
+template <class T>
+hipError_t prepare(const LabelLossArgs& a, const LossPlan& L, char* ws, bool forward, Packed& pk, hipStream_t s) {
+    constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
+    LabelRows r{};
+    r.n = a.n;
+    r.vocab = a.vocab;
+    r.wide = a.wide_labels;
+    r.labels = a.labels;
+    r.rows = (int32_t*)(ws + L.rows);
+    r.place = (int32_t*)(ws + L.place);
+    r.count = (int32_t*)(ws + L.count);
+    r.done = (int32_t*)(ws + L.done);
+    r.loss = forward ? a.loss : nullptr;
+    r.lse = forward ? a.lse : nullptr;
+    PackArgs p{};
+    p.dim = a.dim;
+    p.kp = L.kp;
+    p.per_block = up(1024, L.kp / 8) / (L.kp / 8);  // about four 16-byte chunks a thread
+    p.x = a.x;
+    p.w = a.w;
+    p.xs = a.x_stride;
+    p.ws = a.w_stride;
+    p.xp = (bf16*)(ws + L.xp);
+    p.wp = (bf16*)(ws + L.wp);
+    p.x_part = L.np * L.kp;
+    p.w_part = (int64_t)a.vocab * L.kp;
+    p.x_blocks = (int)((L.np + p.per_block - 1) / p.per_block);
+    pk.pw = p.w_part;
+    if (PARTS == 1 && (uintptr_t)a.w % 16 == 0 && a.w_stride % 8 == 0 && a.dim == L.kp && a.w_stride <= 1 << 20) {
+        pk.w = (const bf16*)a.w;  // the products read w where it is
+        pk.ldw = a.w_stride;
+    } else {
+        p.w_rows = a.vocab;
+        pk.w = p.wp;
+        pk.ldw = L.kp;
+    }
+    const unsigned blocks = p.x_blocks + (unsigned)((p.w_rows + p.per_block - 1) / p.per_block);
+    if (a.n <= LROWS) {
+        k_pack<T, PARTS, true><<<blocks, LT, 0, s>>>(r, p);
+        return hipGetLastError();
+    }
+    int32_t* bc = a.n <= LOOK_BACK ? nullptr : (int32_t*)(ws + L.block_count);
+    const unsigned lb = (unsigned)((a.n + LROWS - 1) / LROWS);
+    if (bc) k_label_count<<<lb, LT, 0, s>>>(r, bc);
+    k_label_rows<<<lb, LT, 0, s>>>(r, bc);
+    k_pack<T, PARTS, false><<<blocks, LT, 0, s>>>(r, p);
+    return hipGetLastError();
 }
 
 template <class T>
@@ -777,7 +912,7 @@ hipError_t loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
     const LossPlan L = loss_plan(a.n, a.dim, a.vocab, PARTS == 1, false);
     Packed pk{};
-    hipError_t e = label_rows<T>(a, L, ws, true, pk, s);
+    hipError_t e = prepare<T>(a, L, ws, true, pk, s);
     if (e != hipSuccess) return e;
     float2 *part = (float2*)(ws + L.part), *state = (float2*)(ws + L.state);
     double* bs = (double*)(ws + L.block_sum);
@@ -795,14 +930,14 @@ hipError_t loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         p.v0 = (int)v0;
         p.part = part;
         p.target = (float*)(ws + L.target);
-        launch_product<LSE, PARTS, T>(L.bm_z, p, mv, a.n, s);
+        set_grid(p, L.bm_z, mv, a.n);
+        launch_product<LSE, PARTS, T>(L.bm_z, p, s);
         // every tile writes its slabs, so the last may lie beyond the vocabulary (an empty one)
         const int slabs = (int)(up(mv, L.bm_z) / (L.bm_z == 256 ? 128 : 64));
-        k_lse_join<<<(unsigned)(L.np / JR), JT, 0, s>>>(slabs, (int)L.np, part, p.target, p.rows,
-                                                       p.count, state, v0 == 0, v0 + L.piece_f < a.vocab, a.loss,
-                                                       a.lse, bs);
+        k_lse_join<<<(unsigned)(a.n > 0 ? (a.n + JR - 1) / JR : 1), JT, 0, s>>>(slabs, (int)L.np, part, p.target, p.rows, p.count, state,
+                                                             v0 == 0, v0 + L.piece_f < a.vocab, a.loss, a.lse, bs,
+                                                             (int32_t*)(ws + L.done), a.mean, a.count);
     }
-    k_loss_mean<<<1, LT, 0, s>>>(bs, (const int32_t*)(ws + L.count), a.mean, a.count);
     return hipGetLastError();
 }
 
@@ -811,7 +946,7 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
     const LossPlan L = loss_plan(a.n, a.dim, a.vocab, PARTS == 1, true);
     Packed pk{};
-    hipError_t e = label_rows<T>(a, L, ws, false, pk, s);
+    hipError_t e = prepare<T>(a, L, ws, false, pk, s);
     if (e != hipSuccess) return e;
     const bf16* xp = (const bf16*)(ws + L.xp);
     bf16* dz = (bf16*)(ws + L.dz);
@@ -831,58 +966,80 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         p.dz = dz;
         p.lddz = L.piece_b;
         p.pdz = L.np * L.piece_b;
-        launch_product<DZ, PARTS, T>(L.bm_z, p, mv, a.n, s);
+        set_grid(p, L.bm_z, mv, a.n);
+        launch_product<DZ, PARTS, T>(L.bm_z, p, s);
+        const bool last = v0 + L.piece_b >= a.vocab;
+        Product qx = product_base<T>(a, L, ws), qw = qx;
+        SplitJoin jx{}, jw{};
         if (a.dx) {
-            Product q = product_base<T>(a, L, ws);
-            q.a = p.a;
-            q.lda = pk.ldw;
-            q.pa = pk.pw;
-            q.b = dz;
-            q.ldb = L.piece_b;
-            q.pb = p.pdz;
-            q.m = L.kp;
-            q.k = (int)mv;
-            q.splits = L.split_dx;
-            q.acc = dxp;
-            q.ldacc = L.kp;
-            q.pacc = L.np * L.kp;
-            q.add = v0 > 0;
-            launch_product<DX, PARTS, T>(L.bm_dx, q, L.kp, a.n, s);
+            qx.a = p.a;
+            qx.lda = pk.ldw;
+            qx.pa = pk.pw;
+            qx.b = dz;
+            qx.ldb = L.piece_b;
+            qx.pb = p.pdz;
+            qx.m = L.kp;
+            qx.k = (int)mv;
+            qx.splits = L.split_dx;
+            qx.acc = dxp;
+            qx.ldacc = L.kp;
+            qx.pacc = L.np * L.kp;
+            qx.add = v0 > 0;
+            set_grid(qx, L.bm_d, L.kp, a.n);
+            if (last) {
+                jx.rows = a.n;
+                jx.splits = L.split_dx;
+                jx.acc = dxp;
+                jx.pacc = qx.pacc;
+                jx.place = (const int32_t*)(ws + L.place);
+                jx.out = a.dx;
+                jx.ldout = a.dx_stride;
+            }
         }
         if (a.dw) {
-            Product q = product_base<T>(a, L, ws);
-            q.a = xp;
-            q.lda = L.kp;
-            q.pa = L.np * L.kp;
-            q.b = dz;
-            q.ldb = L.piece_b;
-            q.pb = p.pdz;
-            q.m = L.kp;
-            q.n = (int)mv;
-            q.splits = L.split_dw;
+            qw.a = xp;
+            qw.lda = L.kp;
+            qw.pa = L.np * L.kp;
+            qw.b = dz;
+            qw.ldb = L.piece_b;
+            qw.pb = p.pdz;
+            qw.m = L.kp;
+            qw.n = (int)mv;
+            qw.splits = L.split_dw;
+            set_grid(qw, L.bm_d, L.kp, mv);
             T* out = (T*)a.dw + v0 * a.dw_stride;
             if (L.split_dw > 1) {
-                q.acc = dwp;
-                q.ldacc = L.kp;
-                q.pacc = L.piece_b * L.kp;
+                qw.acc = dwp;
+                qw.ldacc = L.kp;
+                qw.pacc = L.piece_b * L.kp;
+                jw.rows = mv;
+                jw.splits = L.split_dw;
+                jw.acc = dwp;
+                jw.pacc = qw.pacc;
+                jw.out = out;
+                jw.ldout = a.dw_stride;
             } else {
-                q.out = out;
-                q.ldout = a.dw_stride;
-                q.out_dim = a.dim;
-                q.out_wide = (uintptr_t)a.dw % (4 * sizeof(T)) == 0 && a.dw_stride % 4 == 0;
+                qw.out = out;
+                qw.ldout = a.dw_stride;
+                qw.out_dim = a.dim;
+                qw.out_wide = (uintptr_t)a.dw % (4 * sizeof(T)) == 0 && a.dw_stride % 4 == 0;
             }
-            launch_product<DW, PARTS, T>(L.bm_dw, q, L.kp, mv, s);
-            if (L.split_dw > 1)
-                k_join_splits<T><<<(unsigned)(mv < 16384 ? (mv + 3) / 4 : 4096), 256, 0, s>>>(
-                    mv, a.dim, L.split_dw, dwp, L.kp, q.pacc, nullptr, out, a.dw_stride);
         }
+        if (a.dx && a.dw)
+            launch_pair<PARTS, T>(L.bm_d, qx, qw, s);
+        else if (a.dx)
+            launch_product<DX, PARTS, T>(L.bm_d, qx, s);
+        else
+            launch_product<DW, PARTS, T>(L.bm_d, qw, s);
+        const int per = (a.dim + 3) / 4, per_block = (1024 + per - 1) / per;
+        jx.blocks = (int)((jx.rows + per_block - 1) / per_block);
+        jw.blocks = (int)((jw.rows + per_block - 1) / per_block);
+        if (jx.blocks + jw.blocks > 0)
+            k_join_splits<T><<<jx.blocks + jw.blocks, 256, 0, s>>>(jx, jw, a.dim, L.kp, per_block);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (a.dx && a.n > 0)
-        k_join_splits<T><<<(unsigned)(a.n < 16384 ? (a.n + 3) / 4 : 4096), 256, 0, s>>>(
-            a.n, a.dim, L.split_dx, dxp, L.kp, L.np * L.kp, (const int32_t*)(ws + L.place), (T*)a.dx, a.dx_stride);
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 }  // namespace

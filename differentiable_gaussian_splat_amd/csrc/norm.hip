@@ -7,7 +7,7 @@
 //
 // Both directions are bound by memory: the forward reads x and writes y once,
 // the backward reads x and dy and writes dx once. A row lies in the registers
-// of LPR lanes (8 lanes of a wave up to a whole block), so that its statistics
+// of LPR lanes (one lane up to a whole block), so that its statistics
 // cost no second read; the variance is the mean square of x - mean, not a
 // difference of sums. Blocks walk over the rows with the weights (and, in the
 // backward, the column sums of dw and db) in registers. Column sums go to the
@@ -44,13 +44,13 @@ __device__ __forceinline__ float row_sum(float v, float* s) {
     return v;
 }
 
-template <class T, int VEC, int LPR, int EPL>
+template <class T, int LPR, int EPL>
 __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __restrict__ x, int64_t xs,
                                                  const T* __restrict__ weight, const T* __restrict__ bias, float eps,
                                                  T* __restrict__ y, int64_t ys, float* __restrict__ mean_out,
                                                  float* __restrict__ rstd_out) {
     __shared__ float s_red[NB / 64];
-    constexpr int RPB = NB / LPR;
+    constexpr int RPB = NB / LPR, VEC = WIDE<T>;
     const int l = threadIdx.x % LPR;
     const float D = (float)dim;  // divided by, not multiplied by its reciprocal: the mean of equal values stays exact
     float w[EPL][VEC], b[EPL][VEC];
@@ -63,8 +63,8 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __
             b[e][k] = 0.f;
         }
         if (c < dim) {
-            if (weight) load_row<VEC>(weight + c, w[e]);
-            if (bias) load_row<VEC>(bias + c, b[e]);
+            if (weight) load_row(weight + c, dim - c, w[e]);
+            if (bias) load_row(bias + c, dim - c, b[e]);
         }
     }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < n; r0 += (int64_t)gridDim.x * RPB) {
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __
             const int c = (e * LPR + l) * VEC;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[e][k] = 0.f;
-            if (live && c < dim) load_row<VEC>(xr + c, v[e]);
+            if (live && c < dim) load_row(xr + c, dim - c, v[e]);
         }
 #pragma unroll
         for (int e = 0; e < EPL; ++e)
@@ -88,11 +88,11 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __
         float sq = 0.f;
 #pragma unroll
         for (int e = 0; e < EPL; ++e) {
-            const bool in = (e * LPR + l) * VEC < dim;
+            const int left = dim - (e * LPR + l) * VEC;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
                 v[e][k] -= mean;
-                sq = in ? fmaf(v[e][k], v[e][k], sq) : sq;
+                sq = k < left ? fmaf(v[e][k], v[e][k], sq) : sq;
             }
         }
         const float rstd = 1.0f / sqrtf(row_sum<LPR>(sq, s_red) / D + eps);
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __
             const int c = (e * LPR + l) * VEC;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[e][k] = fmaf(v[e][k] * rstd, w[e][k], b[e][k]);
-            if (c < dim) store_row<VEC>(y + r * ys + c, v[e]);
+            if (c < dim) store_row(y + r * ys + c, dim - c, v[e]);
         }
         if (l == 0) {
             if (mean_out) mean_out[r] = mean;
@@ -141,13 +141,13 @@ __global__ __launch_bounds__(NB) void k_norm_fwd_long(int64_t n, int dim, const 
 }
 
 // part (nullable): [gridDim.x][2][dim] column sums of dy xh and dy over the block's rows.
-template <class T, int VEC, int LPR, int EPL>
+template <class T, int LPR, int EPL>
 __global__ __launch_bounds__(NB) void k_norm_bwd(int64_t n, int dim, const T* __restrict__ x, int64_t xs,
                                                  const T* __restrict__ weight, const float* __restrict__ mean_in,
                                                  const float* __restrict__ rstd_in, const T* __restrict__ dy,
                                                  int64_t dys, T* __restrict__ dx, int64_t dxs,
                                                  float* __restrict__ part) {
-    constexpr int RPB = NB / LPR;
+    constexpr int RPB = NB / LPR, VEC = WIDE<T>;
     constexpr int COLS = LPR * EPL * VEC;
     __shared__ float s_red[NB / 64];
     __shared__ float s_acc[LPR < NB ? 2 * COLS : 1];
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(int64_t n, int dim, const T* __
             w[e][k] = 1.f;
             aw[e][k] = ab[e][k] = 0.f;
         }
-        if (weight && c < dim) load_row<VEC>(weight + c, w[e]);
+        if (weight && c < dim) load_row(weight + c, dim - c, w[e]);
     }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < n; r0 += (int64_t)gridDim.x * RPB) {
         const int64_t r = r0 + threadIdx.x / LPR;
@@ -174,8 +174,8 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(int64_t n, int dim, const T* __
 #pragma unroll
             for (int k = 0; k < VEC; ++k) xv[e][k] = gv[e][k] = 0.f;
             if (live && c < dim) {
-                load_row<VEC>(x + r * xs + c, xv[e]);
-                load_row<VEC>(dy + r * dys + c, gv[e]);
+                load_row(x + r * xs + c, dim - c, xv[e]);
+                load_row(dy + r * dys + c, dim - c, gv[e]);
             }
         }
         const float mean = live ? mean_in[r] : 0.f, rstd = live ? rstd_in[r] : 0.f;
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(int64_t n, int dim, const T* __
             const int c = (e * LPR + l) * VEC;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) gv[e][k] = rstd * (gv[e][k] - fmaf(xv[e][k], mx, mg));
-            if (c < dim) store_row<VEC>(dx + r * dxs + c, gv[e]);
+            if (c < dim) store_row(dx + r * dxs + c, dim - c, gv[e]);
         }
     }
     if (!part) return;
@@ -328,53 +328,37 @@ struct NormArgs {
     bool backward;
 };
 
-template <class T, int VEC, int LPR, int EPL>
-hipError_t norm_rows(const NormArgs& a, hipStream_t s) {
+template <class T, int LPR, int EPL>
+hipError_t norm_rows(NormArgs& a, int cap, hipStream_t s) {
+    const int64_t want = (a.n + NB / LPR - 1) / (NB / LPR);
+    a.blocks = (int)(want < cap ? want : cap);
     const T *x = (const T*)a.x, *w = (const T*)a.weight;
     if (a.backward)
-        k_norm_bwd<T, VEC, LPR, EPL><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, a.mean, a.rstd, (const T*)a.dy,
-                                                             a.dys, (T*)a.dx, a.dxs, a.part);
+        k_norm_bwd<T, LPR, EPL><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, a.mean, a.rstd, (const T*)a.dy, a.dys,
+                                                        (T*)a.dx, a.dxs, a.part);
     else
-        k_norm_fwd<T, VEC, LPR, EPL><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, (const T*)a.bias, a.eps, (T*)a.y,
-                                                             a.ys, a.mean, a.rstd);
+        k_norm_fwd<T, LPR, EPL><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, (const T*)a.bias, a.eps, (T*)a.y,
+                                                        a.ys, a.mean, a.rstd);
     return hipGetLastError();
 }
 
-// The lanes of a row and their elements: the fewest lanes that hold it with one
+// The lanes of a row and their accesses: the fewest lanes that hold it with one
 // access each up to a wave, then more accesses, then a block.
-template <class T, int VEC>
-hipError_t norm_pick(const NormArgs& a, hipStream_t s) {
-    const int v = (a.dim + VEC - 1) / VEC;
-    if (v <= 8) return norm_rows<T, VEC, 8, 1>(a, s);
-    if (v <= 16) return norm_rows<T, VEC, 16, 1>(a, s);
-    if (v <= 32) return norm_rows<T, VEC, 32, 1>(a, s);
-    if (v <= 64) return norm_rows<T, VEC, 64, 1>(a, s);
-    if (v <= 128) return norm_rows<T, VEC, 64, 2>(a, s);
-    if (v <= 256) return norm_rows<T, VEC, 64, 4>(a, s);
-    if (v <= 512) {
-        if constexpr (VEC < 8) return norm_rows<T, VEC, 64, 8>(a, s);
-        return norm_rows<T, VEC, NB, 2>(a, s);
-    }
-    if (v <= 1024) {
-        if constexpr (VEC == 1) return norm_rows<T, VEC, 64, 16>(a, s);
-        return norm_rows<T, VEC, NB, 4>(a, s);
-    }
-    if constexpr (VEC < 8) {
-        if (v <= 2048) return norm_rows<T, VEC, NB, 8>(a, s);
-        if constexpr (VEC == 1) {
-            if (v <= 4096) return norm_rows<T, VEC, NB, 16>(a, s);
-            if (v <= 8192) return norm_rows<T, VEC, NB, 32>(a, s);
-        }
-    }
-    return hipErrorInvalidValue;
-}
-
-int lanes_per_row(int dim, int vec) {
-    const int v = (dim + vec - 1) / vec;
-    if (v <= 8) return 8;
-    if (v <= 16) return 16;
-    if (v <= 32) return 32;
-    return v <= (vec == 8 ? 256 : vec == 4 ? 512 : 1024) ? 64 : NB;
+template <class T>
+hipError_t norm_pick(NormArgs& a, int cap, hipStream_t s) {
+    const int v = (a.dim + WIDE<T> - 1) / WIDE<T>;
+    if (v <= 1) return norm_rows<T, 1, 1>(a, cap, s);
+    if (v <= 2) return norm_rows<T, 2, 1>(a, cap, s);
+    if (v <= 4) return norm_rows<T, 4, 1>(a, cap, s);
+    if (v <= 8) return norm_rows<T, 8, 1>(a, cap, s);
+    if (v <= 16) return norm_rows<T, 16, 1>(a, cap, s);
+    if (v <= 32) return norm_rows<T, 32, 1>(a, cap, s);
+    if (v <= 64) return norm_rows<T, 64, 1>(a, cap, s);
+    if (v <= 128) return norm_rows<T, 64, 2>(a, cap, s);
+    if (v <= 256) return norm_rows<T, 64, 4>(a, cap, s);
+    if (v <= 512) return norm_rows<T, NB, 2>(a, cap, s);
+    if (v <= 1024) return norm_rows<T, NB, 4>(a, cap, s);
+    return norm_rows<T, NB, 8>(a, cap, s);  // float32 only: NORM_REG_DIM is 1024 accesses of bfloat16
 }
 
 constexpr int NORM_BLOCKS_FWD = 2048;
@@ -382,24 +366,17 @@ constexpr int NORM_BLOCKS_BWD = 1024;  // rows of the column-sum array
 
 template <class T>
 hipError_t norm_launch(NormArgs& a, hipStream_t s) {
-    const bool wide = wide_rows<T>(a.x, a.xs, a.dim) && wide_rows<T>(a.weight, 0, a.dim) &&
-                      wide_rows<T>(a.bias, 0, a.dim) && wide_rows<T>(a.y, a.ys, a.dim) &&
-                      wide_rows<T>(a.dy, a.dys, a.dim) && wide_rows<T>(a.dx, a.dxs, a.dim);
     const int cap = a.backward ? NORM_BLOCKS_BWD : NORM_BLOCKS_FWD;
-    const int64_t rpb = a.dim > NORM_REG_DIM ? 1 : NB / lanes_per_row(a.dim, wide ? WIDE<T> : 1);
-    const int64_t want = (a.n + rpb - 1) / rpb;
-    a.blocks = (int)(want < cap ? want : cap);
-    if (a.dim > NORM_REG_DIM) {
-        const T *x = (const T*)a.x, *w = (const T*)a.weight;
-        if (a.backward)
-            k_norm_bwd_long<T><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, a.mean, a.rstd, (const T*)a.dy, a.dys,
-                                                       (T*)a.dx, a.dxs, a.part);
-        else
-            k_norm_fwd_long<T><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, (const T*)a.bias, a.eps, (T*)a.y, a.ys,
-                                                       a.mean, a.rstd);
-        return hipGetLastError();
-    }
-    return wide ? norm_pick<T, WIDE<T>>(a, s) : norm_pick<T, 1>(a, s);
+    if (a.dim <= NORM_REG_DIM) return norm_pick<T>(a, cap, s);
+    a.blocks = (int)(a.n < cap ? a.n : cap);
+    const T *x = (const T*)a.x, *w = (const T*)a.weight;
+    if (a.backward)
+        k_norm_bwd_long<T><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, a.mean, a.rstd, (const T*)a.dy, a.dys,
+                                                   (T*)a.dx, a.dxs, a.part);
+    else
+        k_norm_fwd_long<T><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, (const T*)a.bias, a.eps, (T*)a.y, a.ys,
+                                                   a.mean, a.rstd);
+    return hipGetLastError();
 }
 
 template <class T>
