@@ -22,9 +22,11 @@ constexpr int WIDE = 16 / (int)sizeof(T);
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef bf16 bf16x8_any __attribute__((ext_vector_type(8), aligned(2)));
 
-// The WIDE<T> elements of a row at p, of which `left` are inside the row (the others read as 0).
+// The WIDE<T> elements of a row at p, of which `left` are inside the row (the
+// others read as 0). FULL: the row is whole accesses (left is not looked at).
+template <bool FULL>
 __device__ __forceinline__ void load_row(const float* p, int left, float (&v)[4]) {
-    if (left >= 4) {
+    if (FULL || left >= 4) {
         const f32x4_any t = *reinterpret_cast<const f32x4_any*>(p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = t[i];
@@ -34,8 +36,9 @@ __device__ __forceinline__ void load_row(const float* p, int left, float (&v)[4]
     }
 }
 
+template <bool FULL>
 __device__ __forceinline__ void load_row(const bf16* p, int left, float (&v)[8]) {
-    if (left >= 8) {
+    if (FULL || left >= 8) {
         const bf16x8_any t = *reinterpret_cast<const bf16x8_any*>(p);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (float)t[i];
@@ -45,9 +48,10 @@ __device__ __forceinline__ void load_row(const bf16* p, int left, float (&v)[8])
     }
 }
 
-// Stores the first `left` (or all) of WIDE<T> elements.
+// Stores the first `left` (FULL: all) of WIDE<T> elements.
+template <bool FULL>
 __device__ __forceinline__ void store_row(float* p, int left, const float (&v)[4]) {
-    if (left >= 4) {
+    if (FULL || left >= 4) {
         f32x4_any t;
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] = v[i];
@@ -59,8 +63,9 @@ __device__ __forceinline__ void store_row(float* p, int left, const float (&v)[4
     }
 }
 
+template <bool FULL>
 __device__ __forceinline__ void store_row(bf16* p, int left, const float (&v)[8]) {
-    if (left >= 8) {
+    if (FULL || left >= 8) {
         bf16x8_any t;
 #pragma unroll
         for (int i = 0; i < 8; ++i) t[i] = (bf16)v[i];

@@ -31,7 +31,7 @@ enum EmbedPass { LOOKUP, FEW_SUMS, RUN_SUMS };
 constexpr int run_threads(int lpr) { return lpr <= 2 ? 64 : lpr == 4 ? 128 : EB; }
 
 // LPR lanes per output row, 16 bytes each per step over the row.
-template <class T, int LPR>
+template <class T, int LPR, bool FULL>
 __global__ __launch_bounds__(EB) void k_embed(int64_t n, int dim, int vocab, const T* __restrict__ table, int64_t ts,
                                               const void* __restrict__ ids, bool wide, float scale,
                                               T* __restrict__ out, int64_t os) {
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(EB) void k_embed(int64_t n, int dim, int vocab, con
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[u][k] = 0.f;
             if (row[u] >= 0) {
-                load_row(table + row[u] * ts + c, dim - c, v[u]);
+                load_row<FULL>(table + row[u] * ts + c, dim - c, v[u]);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) v[u][k] *= scale;
             }
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(EB) void k_embed(int64_t n, int dim, int vocab, con
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + u * G;
-            if (r < n) store_row(out + r * os + c, dim - c, v[u]);
+            if (r < n) store_row<FULL>(out + r * os + c, dim - c, v[u]);
         }
     }
 }
@@ -83,12 +83,12 @@ __global__ __launch_bounds__(EB) void k_zero_rows(int rows, int dim, int lanes, 
     const float z[WIDE<T>] = {};
     const int l = threadIdx.x % lanes, per = EB / lanes;
     for (int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / lanes; r < rows; r += (int64_t)gridDim.x * per)
-        for (int c = l * WIDE<T>; c < dim; c += lanes * WIDE<T>) store_row(p + r * stride + c, dim - c, z);
+        for (int c = l * WIDE<T>; c < dim; c += lanes * WIDE<T>) store_row<false>(p + r * stride + c, dim - c, z);
 }
 
 // The gradient of few positions in one launch: a wave takes 64 / LPR rows of
 // the table in turn, and looks through the indices (in LDS) for each.
-template <class T, int LPR>
+template <class T, int LPR, bool FULL>
 __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, const void* __restrict__ ids, bool wide,
                                                   float scale, const T* __restrict__ dout, int64_t ds,
                                                   T* __restrict__ dtable, int64_t ts) {
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, con
                         if (mine) {
                             const int i = i0 + __ffsll((unsigned long long)mine) - 1;
                             mine &= mine - 1;
-                            if (c < dim) load_row(dout + (int64_t)i * ds + c, dim - c, t[u]);
+                            if (c < dim) load_row<FULL>(dout + (int64_t)i * ds + c, dim - c, t[u]);
                         }
                     }
 #pragma unroll
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, con
             }
 #pragma unroll
             for (int k = 0; k < VEC; ++k) acc[k] *= scale;
-            if (row < vocab && c < dim) store_row(dtable + (int64_t)row * ts + c, dim - c, acc);
+            if (row < vocab && c < dim) store_row<FULL>(dtable + (int64_t)row * ts + c, dim - c, acc);
         }
     }
 }
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, con
 // earlier block, and its last run where it goes on in the next (and began in
 // this one). tail_key[b]: that last run's key, or vocab; end_block[key]: the
 // block in which a run that came from an earlier block ends.
-template <class T, int LPR>
+template <class T, int LPR, bool FULL>
 __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
     int n, int dim, int vocab, const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos,
     const T* __restrict__ dout, int64_t ds, float scale, T* __restrict__ dtable, int64_t ts,
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
             kk[u] = s_tok[p + u];
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[u][k] = 0.f;
-            if (kk[u] != none && c < dim) load_row(dout + (int64_t)s_pos[p + u] * ds + c, dim - c, v[u]);
+            if (kk[u] != none && c < dim) load_row<FULL>(dout + (int64_t)s_pos[p + u] * ds + c, dim - c, v[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
                 } else if (c < dim) {  // a run between two others of the group is whole
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) acc[k] *= scale;
-                    store_row(dtable + (int64_t)cur * ts + c, dim - c, acc);
+                    store_row<FULL>(dtable + (int64_t)cur * ts + c, dim - c, acc);
                 }
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
 // Rows whose run crosses blocks: the last run of block b, then the first runs
 // of the blocks after it up to the one where it ends, a contiguous share per
 // row group, the groups joined in order.
-template <class T, int LPR>
+template <class T, int LPR, bool FULL>
 __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const uint32_t* __restrict__ tail_key,
                                                        const uint32_t* __restrict__ end_block,
                                                        const float* __restrict__ part, float scale,
@@ -280,7 +280,12 @@ __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const
         for (int j = j0; j < j1; ++j) {
             const float* q = part + ((size_t)(b + j) * 2 + (j == 0 ? 1 : 0)) * dim + c;
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) acc[k] += c + k < dim ? q[k] : 0.f;
+            for (int k = 0; k < VEC; k += 4) {
+                float t[4];
+                load_row<FULL>(q + k, dim - c - k, t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[k + i] += t[i];
+            }
         }
     }
     if (g < G)
@@ -296,7 +301,7 @@ __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const
     if (g == 0 && c < dim) {
 #pragma unroll
         for (int k = 0; k < VEC; ++k) acc[k] = s_sum[0][l * VEC + k] * scale;
-        store_row(dtable + (int64_t)key * ts + c, dim - c, acc);
+        store_row<FULL>(dtable + (int64_t)key * ts + c, dim - c, acc);
     }
 }
 
@@ -313,44 +318,49 @@ struct EmbedArgs {
     uint32_t *tail_key, *end_block;
 };
 
-template <class T, int LPR>
+template <class T, int LPR, bool FULL>
 hipError_t embed_rows(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
     if (pass == LOOKUP) {
         constexpr int G = EB / LPR;
         const int64_t blocks = (a.n + G * 4 - 1) / (G * 4);
-        k_embed<T, LPR><<<(unsigned)blocks, EB, 0, s>>>(a.n, a.dim, a.vocab, (const T*)a.src, a.ss, a.ids, a.wide,
+        k_embed<T, LPR, FULL><<<(unsigned)blocks, EB, 0, s>>>(a.n, a.dim, a.vocab, (const T*)a.src, a.ss, a.ids, a.wide,
                                                        a.scale, (T*)a.dst, a.ds);
         return hipGetLastError();
     }
     if (pass == FEW_SUMS) {
         const int64_t want = (a.vocab + EB / LPR - 1) / (EB / LPR);
-        k_embed_few<T, LPR><<<(unsigned)(want < 2048 ? want : 2048), EB, 0, s>>>(
+        k_embed_few<T, LPR, FULL><<<(unsigned)(want < 2048 ? want : 2048), EB, 0, s>>>(
             (int)a.n, a.dim, a.vocab, a.ids, a.wide, a.scale, (const T*)a.src, a.ss, (T*)a.dst, a.ds);
         return hipGetLastError();
     }
     constexpr int BT = run_threads(LPR) / LPR * RUN_TOKENS;
     const int nb = (int)((a.n + BT - 1) / BT);
     const dim3 grid(nb, (a.dim + LPR * WIDE<T> - 1) / (LPR * WIDE<T>));
-    k_embed_runs<T, LPR><<<grid, run_threads(LPR), 0, s>>>((int)a.n, a.dim, a.vocab, a.keys, a.pos, (const T*)a.src,
+    k_embed_runs<T, LPR, FULL><<<grid, run_threads(LPR), 0, s>>>((int)a.n, a.dim, a.vocab, a.keys, a.pos, (const T*)a.src,
                                                           a.ss, a.scale, (T*)a.dst, a.ds, a.part, a.tail_key,
                                                           a.end_block);
     if (nb > 1)
-        k_embed_join<T, LPR><<<grid, JOIN_T, 0, s>>>(a.dim, a.vocab, a.tail_key, a.end_block, a.part, a.scale,
+        k_embed_join<T, LPR, FULL><<<grid, JOIN_T, 0, s>>>(a.dim, a.vocab, a.tail_key, a.end_block, a.part, a.scale,
                                                     (T*)a.dst, a.ds);
     return hipGetLastError();
 }
 
 // The fewest lanes that hold a row with one 16-byte access each, up to a wave.
+template <class T, bool FULL>
+hipError_t embed_pick(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
+    const int v = (a.dim + WIDE<T> - 1) / WIDE<T>;
+    if (v <= 1) return embed_rows<T, 1, FULL>(a, pass, s);
+    if (v <= 2) return embed_rows<T, 2, FULL>(a, pass, s);
+    if (v <= 4) return embed_rows<T, 4, FULL>(a, pass, s);
+    if (v <= 8) return embed_rows<T, 8, FULL>(a, pass, s);
+    if (v <= 16) return embed_rows<T, 16, FULL>(a, pass, s);
+    if (v <= 32) return embed_rows<T, 32, FULL>(a, pass, s);
+    return embed_rows<T, 64, FULL>(a, pass, s);
+}
+
 template <class T>
 hipError_t embed_run(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
-    const int v = (a.dim + WIDE<T> - 1) / WIDE<T>;
-    if (v <= 1) return embed_rows<T, 1>(a, pass, s);
-    if (v <= 2) return embed_rows<T, 2>(a, pass, s);
-    if (v <= 4) return embed_rows<T, 4>(a, pass, s);
-    if (v <= 8) return embed_rows<T, 8>(a, pass, s);
-    if (v <= 16) return embed_rows<T, 16>(a, pass, s);
-    if (v <= 32) return embed_rows<T, 32>(a, pass, s);
-    return embed_rows<T, 64>(a, pass, s);
+    return a.dim % WIDE<T> == 0 ? embed_pick<T, true>(a, pass, s) : embed_pick<T, false>(a, pass, s);
 }
 
 template <class T>

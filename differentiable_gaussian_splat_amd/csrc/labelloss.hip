@@ -155,7 +155,10 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // exp(z - ref); the difference first, which is exact where the two are close
 __device__ __forceinline__ float exp_diff(float z, float ref) { return exp2_fast((z - ref) * LOG2E); }
 
-// One product, C[m][n] = sum_k A[m][k] B[n][k], by BM x 128 tiles; a lane
+// Rows staged for TM row blocks per wave (a power of two, for the staging's lanes).
+constexpr int staged_rows(int tm) { return tm == 1 ? 64 : tm == 2 ? 128 : 256; }
+
+// One product, C[m][n] = sum_k A[m][k] B[n][k], by 64 TM x 128 tiles; a lane
 // holds, for one n, runs of four consecutive m. PARTS: 1, or 3 for split
 // operands.
 //
@@ -164,14 +167,12 @@ __device__ __forceinline__ float exp_diff(float z, float ref) { return exp2_fast
 // step and frees the one before it. Loads past the last step are made with an
 // empty extent (they bring zeros), which keeps the count of loads in flight
 // the same in every step.
-template <int MODE, int PARTS, int BM, class T>
+template <int MODE, int PARTS, int TM, class T>
 __device__ __forceinline__ void product(const Product& p, int block, bf16* s_tiles) {
     constexpr bool TA = MODE == DX || MODE == DW, TB = MODE == DW;
-    constexpr int WM = BM == 64 ? 64 : BM / 2;       // rows of a wave's part
-    constexpr int WN = BM == 64 ? 32 : 64;           // columns
-    constexpr int MW = BM / WM;                      // waves along m
-    constexpr int TM = WM / 32, TN = WN / 32;
-    constexpr int STEP = (BM + BN) * BK;  // elements of one staged step: the a tile, then the b tile
+    constexpr int TN = 2, WM = 32 * TM, WN = 32 * TN;  // 2 x 2 waves of WM rows and WN columns
+    constexpr int BM = 2 * WM, SM = staged_rows(TM);
+    constexpr int STEP = (SM + BN) * BK;  // elements of one staged step: the a tile, then the b tile
     const int cnt = *p.count;
     const int nn = MODE == DW ? p.n : cnt;
     const int mt = (p.m + BM - 1) / BM, nt = (nn + BN - 1) / BN;
@@ -192,7 +193,7 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
     const int per = k_end - k_first;
     const int steps = per * (PARTS == 3 ? 6 : 1);
 
-    const Stage<BM, TA> sa(p.lda);
+    const Stage<SM, TA> sa(p.lda);
     const Stage<BN, TB> sb(p.ldb);
     const int a_rows = TA ? (MODE == DW ? p.np : p.k) : p.m;  // rows of the operand's memory
     const int b_rows = p.np;
@@ -207,11 +208,11 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
         const bf16* a = p.a + ia * p.pa + (TA ? k0 * p.lda + m0 : m0 * p.lda + k0);
         const bf16* b = p.b + ib * p.pb + (TB ? k0 * p.ldb + n0 : n0 * p.ldb + k0);
         const int64_t ea = TA ? (min((int64_t)BK, a_rows - k0) - 1) * p.lda + p.m - m0
-                              : (int64_t)(min(BM, a_rows - m0) - 1) * p.lda + BK;
+                              : (int64_t)(min(SM, a_rows - m0) - 1) * p.lda + BK;
         const int64_t eb = TB ? (min((int64_t)BK, b_rows - k0) - 1) * p.ldb + p.ldb - n0
                               : (int64_t)(min(BN, b_rows - n0) - 1) * p.ldb + BK;
         sa.load(a, live ? ea * 2 : 0, lds0 + buf * STEP * 2);
-        sb.load(b, live ? eb * 2 : 0, lds0 + (buf * STEP + BM * BK) * 2);
+        sb.load(b, live ? eb * 2 : 0, lds0 + (buf * STEP + SM * BK) * 2);
         if (++kt >= per) {
             kt = 0;
             ++pr;
@@ -219,7 +220,7 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
     };
 
     const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
-    const int wm = (w % MW) * WM, wn = (w / MW) * WN;
+    const int wm = (w % 2) * WM, wn = (w / 2) * WN;
     f32x16 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -228,20 +229,20 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-    constexpr int LOADS = Stage<BM, TA>::NI + Stage<BN, TB>::NI;  // of one step
+    constexpr int LOADS = Stage<SM, TA>::NI + Stage<BN, TB>::NI;  // of one step
     issue(0);
     issue(1);
     int buf = 0;
     for (int t = 0; t < steps; ++t) {
         step_barrier<LOADS>();
         issue(buf == 0 ? STAGES - 1 : buf - 1);
-        const bf16 *la = s_tiles + buf * STEP, *lb = la + BM * BK;
+        const bf16 *la = s_tiles + buf * STEP, *lb = la + SM * BK;
         buf = buf == STAGES - 1 ? 0 : buf + 1;
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
             bf16x8 fa[TM], fb[TN];
 #pragma unroll
-            for (int i = 0; i < TM; ++i) fa[i] = fragment<BM, TA>(la, wm + 32 * i, kk);
+            for (int i = 0; i < TM; ++i) fa[i] = fragment<SM, TA>(la, wm + 32 * i, kk);
 #pragma unroll
             for (int j = 0; j < TN; ++j) fb[j] = fragment<BN, TB>(lb, wn + 32 * j, kk);
 #pragma unroll
@@ -411,50 +412,41 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
     }
 }
 
-template <int MODE, int PARTS, int BM, class T>
+template <int MODE, int PARTS, int TM, class T>
 __global__ __launch_bounds__(GT, 2) void k_product(Product p) {
-    __shared__ __align__(16) bf16 s_tiles[STAGES * (BM + BN) * BK];
-    product<MODE, PARTS, BM, T>(p, blockIdx.x, s_tiles);
+    __shared__ __align__(16) bf16 s_tiles[STAGES * (staged_rows(TM) + BN) * BK];
+    product<MODE, PARTS, TM, T>(p, blockIdx.x, s_tiles);
 }
 
 // dx and dw, which read the same dz, in one launch: together they fill the chip better, and small ones wait once.
-template <int PARTS, int BM, class T>
+template <int PARTS, int TM, class T>
 __global__ __launch_bounds__(GT, 2) void k_product_pair(Product dx, Product dw) {
-    __shared__ __align__(16) bf16 s_tiles[STAGES * (BM + BN) * BK];
+    __shared__ __align__(16) bf16 s_tiles[STAGES * (staged_rows(TM) + BN) * BK];
     const int first = dx.grid * dx.splits;
     if ((int)blockIdx.x < first)
-        product<DX, PARTS, BM, T>(dx, blockIdx.x, s_tiles);
+        product<DX, PARTS, TM, T>(dx, blockIdx.x, s_tiles);
     else
-        product<DW, PARTS, BM, T>(dw, blockIdx.x - first, s_tiles);
+        product<DW, PARTS, TM, T>(dw, blockIdx.x - first, s_tiles);
 }
 
 // ---------------------------------------------------------------- labelled rows
 
 constexpr int LT = 256;            // threads
-constexpr int LPT = 8;             // consecutive rows per thread
+constexpr int LPT = 4;             // rows per thread
 constexpr int LROWS = LT * LPT;    // rows per block
 constexpr int64_t LOOK_BACK = 32768;  // rows up to which a block counts the labels before its own rows itself
 
-// Sum of v over the threads below (all LT take part); total: over all.
-__device__ __forceinline__ int block_scan_excl(int v, int* s_w, int* total) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    int x = v;
+// Sum of v over the block (all LT threads take part).
+__device__ __forceinline__ int block_sum(int v, int* s_w) {
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int y = __shfl_up(x, off);
-        if (lane >= off) x += y;
-    }
-    if (lane == 63) s_w[w] = x;
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+    if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = v;
     __syncthreads();
-    int pre = 0, tot = 0;
+    int t = 0;
 #pragma unroll
-    for (int k = 0; k < LT / 64; ++k) {
-        pre += k < w ? s_w[k] : 0;
-        tot += s_w[k];
-    }
+    for (int k = 0; k < LT / 64; ++k) t += s_w[k];
     __syncthreads();
-    *total = tot;
-    return pre + x - v;
+    return t;
 }
 
 // The arrays that the labels give: rows[], the labelled rows in order; place[r],
@@ -472,57 +464,68 @@ struct LabelRows {
 __global__ __launch_bounds__(LT) void k_label_count(LabelRows a, int32_t* __restrict__ block_count) {
     __shared__ int s_w[LT / 64];
     const int64_t r0 = (int64_t)blockIdx.x * LROWS + threadIdx.x;
-    int c = 0, tot;
+    int c = 0;
 #pragma unroll
     for (int k = 0; k < LPT; ++k)
         c += r0 + k * LT < a.n && row_index(a.labels, a.wide, r0 + k * LT, a.vocab) >= 0;
-    block_scan_excl(c, s_w, &tot);
-    if (threadIdx.x == 0) block_count[blockIdx.x] = tot;
+    c = block_sum(c, s_w);
+    if (threadIdx.x == 0) block_count[blockIdx.x] = c;
 }
 
-// The labels of block `b`'s rows; base: labelled rows before them. s_list
+// The labels of block `b`'s rows (a wave takes 64 LPT consecutive ones); `before`:
+// a count per thread that adds up to the labelled rows before the block. s_list
 // (nullable): the rows also go there. Returns the labelled rows up to the block's end.
-__device__ __forceinline__ int label_rows(const LabelRows& a, int b, int base, bool write, int* s_w, int* s_list) {
-    const int64_t r0 = (int64_t)b * LROWS + threadIdx.x * LPT;
-    bool have[LPT];
-    int c = 0, tot;
+__device__ __forceinline__ int label_rows(const LabelRows& a, int b, int before, bool write, int* s_w, int* s_list) {
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t r0 = (int64_t)b * LROWS + w * (64 * LPT) + lane;
+    uint64_t have[LPT];
+    int own = 0;
 #pragma unroll
     for (int k = 0; k < LPT; ++k) {
-        have[k] = r0 + k < a.n && row_index(a.labels, a.wide, r0 + k, a.vocab) >= 0;
-        c += have[k];
+        have[k] = __ballot(r0 + 64 * k < a.n && row_index(a.labels, a.wide, r0 + 64 * k, a.vocab) >= 0);
+        own += __popcll(have[k]);
     }
-    int at = base + block_scan_excl(c, s_w, &tot);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) before += __shfl_xor(before, off);
+    if (lane == 0) {
+        s_w[w] = before;
+        s_w[LT / 64 + w] = own;
+    }
+    __syncthreads();
+    int at = 0, end = 0;
+#pragma unroll
+    for (int k = 0; k < LT / 64; ++k) {
+        at += s_w[k] + (k < w ? s_w[LT / 64 + k] : 0);
+        end += s_w[k] + s_w[LT / 64 + k];
+    }
 #pragma unroll
     for (int k = 0; k < LPT; ++k) {
-        const int64_t r = r0 + k;
-        if (r >= a.n) break;
-        if (write) {
-            a.place[r] = have[k] ? at : -1;
-            if (have[k]) a.rows[at] = (int32_t)r;
-            if (!have[k] && a.loss) a.loss[r] = 0.f;
-            if (!have[k] && a.lse) a.lse[r] = 0.f;
-        }
-        if (have[k]) {
-            if (s_list) s_list[at] = (int)r;
-            ++at;
-        }
+        const int64_t r = r0 + 64 * k;
+        const bool mine = (have[k] >> lane) & 1;
+        const int to = at + __popcll(have[k] & (((uint64_t)1 << lane) - 1));
+        at += __popcll(have[k]);
+        if (mine && s_list) s_list[to] = (int)r;
+        if (!write || r >= a.n) continue;
+        a.place[r] = mine ? to : -1;
+        if (mine) a.rows[to] = (int32_t)r;
+        if (!mine && a.loss) a.loss[r] = 0.f;
+        if (!mine && a.lse) a.lse[r] = 0.f;
     }
-    return base + tot;
+    return end;
 }
 
 // block_count (nullable): the blocks' labelled rows, counted before.
 __global__ __launch_bounds__(LT) void k_label_rows(LabelRows a, const int32_t* __restrict__ block_count) {
-    __shared__ int s_w[LT / 64];
-    int c = 0, base;
+    __shared__ int s_w[2 * LT / 64];
+    int c = 0;
     if (block_count) {
         for (int k = threadIdx.x; k < (int)blockIdx.x; k += LT) c += block_count[k];
-    } else {
-#pragma unroll 8
-        for (int64_t r = threadIdx.x; r < (int64_t)blockIdx.x * LROWS; r += LT)
-            c += row_index(a.labels, a.wide, r, a.vocab) >= 0;
+    } else {  // whole blocks of rows before this one
+        for (int r = threadIdx.x; r < (int)blockIdx.x * LROWS; r += LROWS)
+#pragma unroll
+            for (int k = 0; k < LPT; ++k) c += row_index(a.labels, a.wide, r + k * LT, a.vocab) >= 0;
     }
-    block_scan_excl(c, s_w, &base);
-    const int end = label_rows(a, blockIdx.x, base, true, s_w, nullptr);
+    const int end = label_rows(a, blockIdx.x, c, true, s_w, nullptr);
     if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
         *a.count = end;
         *a.done = 0;
@@ -545,7 +548,7 @@ struct PackArgs {
 
 template <class T, int PARTS, bool SMALL>
 __global__ __launch_bounds__(LT) void k_pack(LabelRows a, PackArgs p) {
-    __shared__ int s_w[LT / 64];
+    __shared__ int s_w[2 * LT / 64];
     __shared__ int s_list[SMALL ? LROWS : 1];
     const bool x = (int)blockIdx.x < p.x_blocks;
     const int64_t r0 = (int64_t)(blockIdx.x - (x ? 0 : p.x_blocks)) * p.per_block;
@@ -582,7 +585,7 @@ __global__ __launch_bounds__(LT) void k_pack(LabelRows a, PackArgs p) {
 #pragma unroll
             for (int k = 0; k < 8; k += V) {
                 float t[V];
-                load_row(src + row * stride + c + k, p.dim - c - k, t);
+                load_row<false>(src + row * stride + c + k, p.dim - c - k, t);
 #pragma unroll
                 for (int j = 0; j < V; ++j) v[k + j] = t[j];
             }
@@ -742,11 +745,23 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // Blocks a launch needs to fill the chip; products with fewer tiles split their depth.
 constexpr int FILL = 512;
 
-// Tile rows of a product with m rows and n columns: the largest that still makes
-// enough tiles, and no more than m fills.
-int tile_rows(int64_t m, int64_t n) {
-    if (m > 128 && up(m, 256) / 256 * (up(n, BN) / BN) >= FILL / 2) return 256;
-    return m > 64 ? 128 : 64;
+// Row blocks per wave over the vocabulary: four (256 rows) where that makes
+// enough tiles, otherwise two.
+int tm_vocab(int64_t v, int64_t np) { return up(v, 256) / 256 * (np / BN) >= FILL / 2 ? 4 : 2; }
+
+// Row blocks per wave over dim: the fewest rows multiplied, weighted by what a
+// wave reads from LDS per multiplication (TM + 2 fragments for 2 TM of them).
+int tm_dim(int64_t kp) {
+    int best = 1;
+    int64_t least = 0;
+    for (int tm = 1; tm <= 4; ++tm) {
+        const int64_t cost = up(kp, 64 * tm) * (tm + 2) * 6 / tm;
+        if (tm == 1 || cost < least) {
+            best = tm;
+            least = cost;
+        }
+    }
+    return best;
 }
 
 int splits_for(int64_t tiles, int64_t nk, int parts) {
@@ -760,7 +775,7 @@ struct LossPlan {
     int parts, kp;
     int64_t np;                    // rows of x padded to the tile
     int64_t piece_f, piece_b;      // vocabulary rows per piece (multiples of 256)
-    int bm_z, bm_d;                // tile rows: over the vocabulary, over dim
+    int tm_z, tm_d;                // row blocks per wave: over the vocabulary, over dim
     int split_dx, split_dw;
     size_t rows, place, count, done, block_count, xp, wp, part, target, state, block_sum, dz, dxp, dwp, total;
 };
@@ -777,9 +792,9 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     };
     L.piece_f = piece((int64_t)1 << 31);  // 8 bytes per 64 vocabulary rows: 256 MB
     L.piece_b = piece(((int64_t)1 << 28) / L.parts);  // 2 bytes per part: 512 MB
-    L.bm_z = tile_rows(backward ? L.piece_b : L.piece_f, L.np);
-    L.bm_d = tile_rows(L.kp, L.np < L.piece_b ? L.np : L.piece_b);
-    const int64_t mt = up(L.kp, L.bm_d) / L.bm_d;
+    L.tm_z = tm_vocab(backward ? L.piece_b : L.piece_f, L.np);
+    L.tm_d = tm_dim(L.kp);
+    const int64_t mt = up(L.kp, 64 * L.tm_d) / (64 * L.tm_d);
     L.split_dx = splits_for(mt * (L.np / BN), L.piece_b / BK, L.parts);
     L.split_dw = splits_for(mt * (L.piece_b / BN), L.np / BK, L.parts);
     size_t o = 0;
@@ -815,31 +830,37 @@ struct Packed {
 };
 
 // Sets the product's blocks per split for m rows and n columns.
-void set_grid(Product& p, int bm, int64_t m, int64_t n) {
-    const int64_t t = up(m, bm) / bm * (up(n, BN) / BN);
+void set_grid(Product& p, int tm, int64_t m, int64_t n) {
+    const int64_t t = up(m, 64 * tm) / (64 * tm) * (up(n, BN) / BN);
     p.grid = (int)(t < 8 ? 8 : up(t, 8));
 }
 
 template <int MODE, int PARTS, class T>
-void launch_product(int bm, const Product& p, hipStream_t s) {
+void launch_product(int tm, const Product& p, hipStream_t s) {
     const unsigned grid = (unsigned)p.grid * p.splits;
-    if (bm == 256)
-        k_product<MODE, PARTS, 256, T><<<grid, GT, 0, s>>>(p);
-    else if (bm == 128)
-        k_product<MODE, PARTS, 128, T><<<grid, GT, 0, s>>>(p);
-    else
-        k_product<MODE, PARTS, 64, T><<<grid, GT, 0, s>>>(p);
+    if (tm == 4)
+        k_product<MODE, PARTS, 4, T><<<grid, GT, 0, s>>>(p);
+    else if (tm == 2)
+        k_product<MODE, PARTS, 2, T><<<grid, GT, 0, s>>>(p);
+    else if constexpr (MODE == DX || MODE == DW) {
+        if (tm == 3)
+            k_product<MODE, PARTS, 3, T><<<grid, GT, 0, s>>>(p);
+        else
+            k_product<MODE, PARTS, 1, T><<<grid, GT, 0, s>>>(p);
+    }
 }
 
 template <int PARTS, class T>
-void launch_pair(int bm, const Product& dx, const Product& dw, hipStream_t s) {
+void launch_pair(int tm, const Product& dx, const Product& dw, hipStream_t s) {
     const unsigned grid = (unsigned)dx.grid * dx.splits + (unsigned)dw.grid * dw.splits;
-    if (bm == 256)
-        k_product_pair<PARTS, 256, T><<<grid, GT, 0, s>>>(dx, dw);
-    else if (bm == 128)
-        k_product_pair<PARTS, 128, T><<<grid, GT, 0, s>>>(dx, dw);
+    if (tm == 4)
+        k_product_pair<PARTS, 4, T><<<grid, GT, 0, s>>>(dx, dw);
+    else if (tm == 3)
+        k_product_pair<PARTS, 3, T><<<grid, GT, 0, s>>>(dx, dw);
+    else if (tm == 2)
+        k_product_pair<PARTS, 2, T><<<grid, GT, 0, s>>>(dx, dw);
     else
-        k_product_pair<PARTS, 64, T><<<grid, GT, 0, s>>>(dx, dw);
+        k_product_pair<PARTS, 1, T><<<grid, GT, 0, s>>>(dx, dw);
 }
 
 template <class T>
@@ -930,10 +951,10 @@ hipError_t loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         p.v0 = (int)v0;
         p.part = part;
         p.target = (float*)(ws + L.target);
-        set_grid(p, L.bm_z, mv, a.n);
-        launch_product<LSE, PARTS, T>(L.bm_z, p, s);
+        set_grid(p, L.tm_z, mv, a.n);
+        launch_product<LSE, PARTS, T>(L.tm_z, p, s);
         // every tile writes its slabs, so the last may lie beyond the vocabulary (an empty one)
-        const int slabs = (int)(up(mv, L.bm_z) / (L.bm_z == 256 ? 128 : 64));
+        const int slabs = (int)(up(mv, 64 * L.tm_z) / (32 * L.tm_z));
         k_lse_join<<<(unsigned)(a.n > 0 ? (a.n + JR - 1) / JR : 1), JT, 0, s>>>(slabs, (int)L.np, part, p.target, p.rows, p.count, state,
                                                              v0 == 0, v0 + L.piece_f < a.vocab, a.loss, a.lse, bs,
                                                              (int32_t*)(ws + L.done), a.mean, a.count);
@@ -966,8 +987,8 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         p.dz = dz;
         p.lddz = L.piece_b;
         p.pdz = L.np * L.piece_b;
-        set_grid(p, L.bm_z, mv, a.n);
-        launch_product<DZ, PARTS, T>(L.bm_z, p, s);
+        set_grid(p, L.tm_z, mv, a.n);
+        launch_product<DZ, PARTS, T>(L.tm_z, p, s);
         const bool last = v0 + L.piece_b >= a.vocab;
         Product qx = product_base<T>(a, L, ws), qw = qx;
         SplitJoin jx{}, jw{};
@@ -985,7 +1006,7 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
             qx.ldacc = L.kp;
             qx.pacc = L.np * L.kp;
             qx.add = v0 > 0;
-            set_grid(qx, L.bm_d, L.kp, a.n);
+            set_grid(qx, L.tm_d, L.kp, a.n);
             if (last) {
                 jx.rows = a.n;
                 jx.splits = L.split_dx;
@@ -1006,7 +1027,7 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
             qw.m = L.kp;
             qw.n = (int)mv;
             qw.splits = L.split_dw;
-            set_grid(qw, L.bm_d, L.kp, mv);
+            set_grid(qw, L.tm_d, L.kp, mv);
             T* out = (T*)a.dw + v0 * a.dw_stride;
             if (L.split_dw > 1) {
                 qw.acc = dwp;
@@ -1026,11 +1047,11 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
             }
         }
         if (a.dx && a.dw)
-            launch_pair<PARTS, T>(L.bm_d, qx, qw, s);
+            launch_pair<PARTS, T>(L.tm_d, qx, qw, s);
         else if (a.dx)
-            launch_product<DX, PARTS, T>(L.bm_d, qx, s);
+            launch_product<DX, PARTS, T>(L.tm_d, qx, s);
         else
-            launch_product<DW, PARTS, T>(L.bm_d, qw, s);
+            launch_product<DW, PARTS, T>(L.tm_d, qw, s);
         const int per = (a.dim + 3) / 4, per_block = (1024 + per - 1) / per;
         jx.blocks = (int)((jx.rows + per_block - 1) / per_block);
         jw.blocks = (int)((jw.rows + per_block - 1) / per_block);

@@ -44,7 +44,7 @@ __device__ __forceinline__ float row_sum(float v, float* s) {
     return v;
 }
 
-template <class T, int LPR, int EPL>
+template <class T, int LPR, int EPL, bool FULL>
 __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __restrict__ x, int64_t xs,
                                                  const T* __restrict__ weight, const T* __restrict__ bias, float eps,
                                                  T* __restrict__ y, int64_t ys, float* __restrict__ mean_out,
@@ -63,8 +63,8 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __
             b[e][k] = 0.f;
         }
         if (c < dim) {
-            if (weight) load_row(weight + c, dim - c, w[e]);
-            if (bias) load_row(bias + c, dim - c, b[e]);
+            if (weight) load_row<FULL>(weight + c, dim - c, w[e]);
+            if (bias) load_row<FULL>(bias + c, dim - c, b[e]);
         }
     }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < n; r0 += (int64_t)gridDim.x * RPB) {
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __
             const int c = (e * LPR + l) * VEC;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[e][k] = 0.f;
-            if (live && c < dim) load_row(xr + c, dim - c, v[e]);
+            if (live && c < dim) load_row<FULL>(xr + c, dim - c, v[e]);
         }
 #pragma unroll
         for (int e = 0; e < EPL; ++e)
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
                 v[e][k] -= mean;
-                sq = k < left ? fmaf(v[e][k], v[e][k], sq) : sq;
+                sq = (FULL ? left > 0 : k < left) ? fmaf(v[e][k], v[e][k], sq) : sq;
             }
         }
         const float rstd = 1.0f / sqrtf(row_sum<LPR>(sq, s_red) / D + eps);
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __
             const int c = (e * LPR + l) * VEC;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[e][k] = fmaf(v[e][k] * rstd, w[e][k], b[e][k]);
-            if (c < dim) store_row(y + r * ys + c, dim - c, v[e]);
+            if (c < dim) store_row<FULL>(y + r * ys + c, dim - c, v[e]);
         }
         if (l == 0) {
             if (mean_out) mean_out[r] = mean;
@@ -141,7 +141,7 @@ __global__ __launch_bounds__(NB) void k_norm_fwd_long(int64_t n, int dim, const 
 }
 
 // part (nullable): [gridDim.x][2][dim] column sums of dy xh and dy over the block's rows.
-template <class T, int LPR, int EPL>
+template <class T, int LPR, int EPL, bool FULL>
 __global__ __launch_bounds__(NB) void k_norm_bwd(int64_t n, int dim, const T* __restrict__ x, int64_t xs,
                                                  const T* __restrict__ weight, const float* __restrict__ mean_in,
                                                  const float* __restrict__ rstd_in, const T* __restrict__ dy,
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(int64_t n, int dim, const T* __
             w[e][k] = 1.f;
             aw[e][k] = ab[e][k] = 0.f;
         }
-        if (weight && c < dim) load_row(weight + c, dim - c, w[e]);
+        if (weight && c < dim) load_row<FULL>(weight + c, dim - c, w[e]);
     }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < n; r0 += (int64_t)gridDim.x * RPB) {
         const int64_t r = r0 + threadIdx.x / LPR;
@@ -174,8 +174,8 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(int64_t n, int dim, const T* __
 #pragma unroll
             for (int k = 0; k < VEC; ++k) xv[e][k] = gv[e][k] = 0.f;
             if (live && c < dim) {
-                load_row(x + r * xs + c, dim - c, xv[e]);
-                load_row(dy + r * dys + c, dim - c, gv[e]);
+                load_row<FULL>(x + r * xs + c, dim - c, xv[e]);
+                load_row<FULL>(dy + r * dys + c, dim - c, gv[e]);
             }
         }
         const float mean = live ? mean_in[r] : 0.f, rstd = live ? rstd_in[r] : 0.f;
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(int64_t n, int dim, const T* __
             const int c = (e * LPR + l) * VEC;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) gv[e][k] = rstd * (gv[e][k] - fmaf(xv[e][k], mx, mg));
-            if (c < dim) store_row(dx + r * dxs + c, dim - c, gv[e]);
+            if (c < dim) store_row<FULL>(dx + r * dxs + c, dim - c, gv[e]);
         }
     }
     if (!part) return;
@@ -328,37 +328,37 @@ struct NormArgs {
     bool backward;
 };
 
-template <class T, int LPR, int EPL>
+template <class T, int LPR, int EPL, bool FULL>
 hipError_t norm_rows(NormArgs& a, int cap, hipStream_t s) {
     const int64_t want = (a.n + NB / LPR - 1) / (NB / LPR);
     a.blocks = (int)(want < cap ? want : cap);
     const T *x = (const T*)a.x, *w = (const T*)a.weight;
     if (a.backward)
-        k_norm_bwd<T, LPR, EPL><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, a.mean, a.rstd, (const T*)a.dy, a.dys,
+        k_norm_bwd<T, LPR, EPL, FULL><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, a.mean, a.rstd, (const T*)a.dy, a.dys,
                                                         (T*)a.dx, a.dxs, a.part);
     else
-        k_norm_fwd<T, LPR, EPL><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, (const T*)a.bias, a.eps, (T*)a.y,
+        k_norm_fwd<T, LPR, EPL, FULL><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, (const T*)a.bias, a.eps, (T*)a.y,
                                                         a.ys, a.mean, a.rstd);
     return hipGetLastError();
 }
 
 // The lanes of a row and their accesses: the fewest lanes that hold it with one
 // access each up to a wave, then more accesses, then a block.
-template <class T>
+template <class T, bool FULL>
 hipError_t norm_pick(NormArgs& a, int cap, hipStream_t s) {
     const int v = (a.dim + WIDE<T> - 1) / WIDE<T>;
-    if (v <= 1) return norm_rows<T, 1, 1>(a, cap, s);
-    if (v <= 2) return norm_rows<T, 2, 1>(a, cap, s);
-    if (v <= 4) return norm_rows<T, 4, 1>(a, cap, s);
-    if (v <= 8) return norm_rows<T, 8, 1>(a, cap, s);
-    if (v <= 16) return norm_rows<T, 16, 1>(a, cap, s);
-    if (v <= 32) return norm_rows<T, 32, 1>(a, cap, s);
-    if (v <= 64) return norm_rows<T, 64, 1>(a, cap, s);
-    if (v <= 128) return norm_rows<T, 64, 2>(a, cap, s);
-    if (v <= 256) return norm_rows<T, 64, 4>(a, cap, s);
-    if (v <= 512) return norm_rows<T, NB, 2>(a, cap, s);
-    if (v <= 1024) return norm_rows<T, NB, 4>(a, cap, s);
-    return norm_rows<T, NB, 8>(a, cap, s);  // float32 only: NORM_REG_DIM is 1024 accesses of bfloat16
+    if (v <= 1) return norm_rows<T, 1, 1, FULL>(a, cap, s);
+    if (v <= 2) return norm_rows<T, 2, 1, FULL>(a, cap, s);
+    if (v <= 4) return norm_rows<T, 4, 1, FULL>(a, cap, s);
+    if (v <= 8) return norm_rows<T, 8, 1, FULL>(a, cap, s);
+    if (v <= 16) return norm_rows<T, 16, 1, FULL>(a, cap, s);
+    if (v <= 32) return norm_rows<T, 32, 1, FULL>(a, cap, s);
+    if (v <= 64) return norm_rows<T, 64, 1, FULL>(a, cap, s);
+    if (v <= 128) return norm_rows<T, 64, 2, FULL>(a, cap, s);
+    if (v <= 256) return norm_rows<T, 64, 4, FULL>(a, cap, s);
+    if (v <= 512) return norm_rows<T, NB, 2, FULL>(a, cap, s);
+    if (v <= 1024) return norm_rows<T, NB, 4, FULL>(a, cap, s);
+    return norm_rows<T, NB, 8, FULL>(a, cap, s);  // float32 only: NORM_REG_DIM is 1024 accesses of bfloat16
 }
 
 constexpr int NORM_BLOCKS_FWD = 2048;
@@ -367,7 +367,8 @@ constexpr int NORM_BLOCKS_BWD = 1024;  // rows of the column-sum array
 template <class T>
 hipError_t norm_launch(NormArgs& a, hipStream_t s) {
     const int cap = a.backward ? NORM_BLOCKS_BWD : NORM_BLOCKS_FWD;
-    if (a.dim <= NORM_REG_DIM) return norm_pick<T>(a, cap, s);
+    if (a.dim <= NORM_REG_DIM)
+        return a.dim % WIDE<T> == 0 ? norm_pick<T, true>(a, cap, s) : norm_pick<T, false>(a, cap, s);
     a.blocks = (int)(a.n < cap ? a.n : cap);
     const T *x = (const T*)a.x, *w = (const T*)a.weight;
     if (a.backward)
