@@ -431,23 +431,10 @@ __global__ __launch_bounds__(GT, 2) void k_product_pair(Product dx, Product dw) 
 
 // ---------------------------------------------------------------- labelled rows
 
-constexpr int LT = 256;            // threads
-constexpr int LPT = 4;             // rows per thread
-constexpr int LROWS = LT * LPT;    // rows per block
-constexpr int64_t LOOK_BACK = 32768;  // rows up to which a block counts the labels before its own rows itself
-
-// Sum of v over the block (all LT threads take part).
-__device__ __forceinline__ int block_sum(int v, int* s_w) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-    if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = v;
-    __syncthreads();
-    int t = 0;
-#pragma unroll
-    for (int k = 0; k < LT / 64; ++k) t += s_w[k];
-    __syncthreads();
-    return t;
-}
+constexpr int LPT = 4;                // rows per thread
+constexpr int LT = 1024, LROWS = LT * LPT;  // threads and rows of a block that lists labelled rows
+constexpr int PT = 256, PROWS = PT * LPT;   // threads of a packing block, rows of which it can make the list itself
+constexpr int64_t LOOK_BACK = 65536;  // rows up to which a block counts the labels before its own rows itself
 
 // The arrays that the labels give: rows[], the labelled rows in order; place[r],
 // the position of row r in it, or -1; their number; loss and lse (nullable),
@@ -461,23 +448,30 @@ struct LabelRows {
     float *loss, *lse;
 };
 
+// block_count[b] = labelled rows of block b.
 __global__ __launch_bounds__(LT) void k_label_count(LabelRows a, int32_t* __restrict__ block_count) {
     __shared__ int s_w[LT / 64];
     const int64_t r0 = (int64_t)blockIdx.x * LROWS + threadIdx.x;
     int c = 0;
 #pragma unroll
     for (int k = 0; k < LPT; ++k)
-        c += r0 + k * LT < a.n && row_index(a.labels, a.wide, r0 + k * LT, a.vocab) >= 0;
-    c = block_sum(c, s_w);
-    if (threadIdx.x == 0) block_count[blockIdx.x] = c;
+        c += __popcll(__ballot(r0 + k * LT < a.n && row_index(a.labels, a.wide, r0 + k * LT, a.vocab) >= 0));
+    if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = c;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        c = 0;
+        for (int k = 0; k < LT / 64; ++k) c += s_w[k];
+        block_count[blockIdx.x] = c;
+    }
 }
 
 // The labels of block `b`'s rows (a wave takes 64 LPT consecutive ones); `before`:
 // a count per thread that adds up to the labelled rows before the block. s_list
 // (nullable): the rows also go there. Returns the labelled rows up to the block's end.
+template <int NT>
 __device__ __forceinline__ int label_rows(const LabelRows& a, int b, int before, bool write, int* s_w, int* s_list) {
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t r0 = (int64_t)b * LROWS + w * (64 * LPT) + lane;
+    const int64_t r0 = (int64_t)b * NT * LPT + w * (64 * LPT) + lane;
     uint64_t have[LPT];
     int own = 0;
 #pragma unroll
@@ -489,14 +483,14 @@ __device__ __forceinline__ int label_rows(const LabelRows& a, int b, int before,
     for (int off = 32; off > 0; off >>= 1) before += __shfl_xor(before, off);
     if (lane == 0) {
         s_w[w] = before;
-        s_w[LT / 64 + w] = own;
+        s_w[NT / 64 + w] = own;
     }
     __syncthreads();
     int at = 0, end = 0;
 #pragma unroll
-    for (int k = 0; k < LT / 64; ++k) {
-        at += s_w[k] + (k < w ? s_w[LT / 64 + k] : 0);
-        end += s_w[k] + s_w[LT / 64 + k];
+    for (int k = 0; k < NT / 64; ++k) {
+        at += s_w[k] + (k < w ? s_w[NT / 64 + k] : 0);
+        end += s_w[k] + s_w[NT / 64 + k];
     }
 #pragma unroll
     for (int k = 0; k < LPT; ++k) {
@@ -521,20 +515,22 @@ __global__ __launch_bounds__(LT) void k_label_rows(LabelRows a, const int32_t* _
     if (block_count) {
         for (int k = threadIdx.x; k < (int)blockIdx.x; k += LT) c += block_count[k];
     } else {  // whole blocks of rows before this one
-        for (int r = threadIdx.x; r < (int)blockIdx.x * LROWS; r += LROWS)
+        const int end = (int)blockIdx.x * LROWS;
+        for (int r = threadIdx.x; r < end; r += 16 * LT)
 #pragma unroll
-            for (int k = 0; k < LPT; ++k) c += row_index(a.labels, a.wide, r + k * LT, a.vocab) >= 0;
+            for (int k = 0; k < 16; ++k)
+                c += r + k * LT < end && row_index(a.labels, a.wide, r + k * LT, a.vocab) >= 0;
     }
-    const int end = label_rows(a, blockIdx.x, c, true, s_w, nullptr);
+    const int last = label_rows<LT>(a, blockIdx.x, c, true, s_w, nullptr);
     if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
-        *a.count = end;
+        *a.count = last;
         *a.done = 0;
     }
 }
 
 // Rows into bfloat16 parts of kp columns (a multiple of BK, zero beyond dim):
 // the first x_blocks blocks pack x's labelled rows, and zero rows up to the
-// next multiple of BN, the others every row of w. SMALL: x has at most LROWS
+// next multiple of BN, the others every row of w. SMALL: x has at most PROWS
 // rows, and each block makes the list of labelled rows for itself first (block
 // 0 also writes its arrays), which saves a launch.
 struct PackArgs {
@@ -547,15 +543,15 @@ struct PackArgs {
 };
 
 template <class T, int PARTS, bool SMALL>
-__global__ __launch_bounds__(LT) void k_pack(LabelRows a, PackArgs p) {
-    __shared__ int s_w[2 * LT / 64];
-    __shared__ int s_list[SMALL ? LROWS : 1];
+__global__ __launch_bounds__(PT) void k_pack(LabelRows a, PackArgs p) {
+    __shared__ int s_w[2 * PT / 64];
+    __shared__ int s_list[SMALL ? PROWS : 1];
     const bool x = (int)blockIdx.x < p.x_blocks;
     const int64_t r0 = (int64_t)(blockIdx.x - (x ? 0 : p.x_blocks)) * p.per_block;
     int64_t live = p.w_rows, padded = p.w_rows;
     if (x) {
         if (SMALL) {
-            live = label_rows(a, 0, 0, blockIdx.x == 0, s_w, s_list);
+            live = label_rows<PT>(a, 0, 0, blockIdx.x == 0, s_w, s_list);
             __syncthreads();
             if (blockIdx.x == 0 && threadIdx.x == 0) {
                 *a.count = (int)live;
@@ -572,7 +568,7 @@ __global__ __launch_bounds__(LT) void k_pack(LabelRows a, PackArgs p) {
     const T* src = static_cast<const T*>(x ? p.x : p.w);
     const int64_t stride = x ? p.xs : p.ws, part = x ? p.x_part : p.w_part;
     bf16* dst = x ? p.xp : p.wp;
-    for (uint32_t i = threadIdx.x; i < total; i += LT) {
+    for (uint32_t i = threadIdx.x; i < total; i += PT) {
         const uint32_t rr = i / per;
         const int64_t r = r0 + rr;
         const int c = (int)(i - rr * per) * 8;
@@ -764,10 +760,9 @@ int tm_dim(int64_t kp) {
     return best;
 }
 
-int splits_for(int64_t tiles, int64_t nk, int parts) {
-    int64_t s = tiles > 0 ? FILL / tiles : 1;
-    const int64_t most = nk * (parts == 3 ? 6 : 1) / 8;  // at least eight steps each
-    if (s > most) s = most;
+// Splits of a depth of nk steps, `share` of them to a block.
+int splits_for(int64_t nk, int64_t share) {
+    const int64_t s = (nk + share / 2) / share;
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
@@ -795,8 +790,13 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     L.tm_z = tm_vocab(backward ? L.piece_b : L.piece_f, L.np);
     L.tm_d = tm_dim(L.kp);
     const int64_t mt = up(L.kp, 64 * L.tm_d) / (64 * L.tm_d);
-    L.split_dx = splits_for(mt * (L.np / BN), L.piece_b / BK, L.parts);
-    L.split_dw = splits_for(mt * (L.piece_b / BN), L.np / BK, L.parts);
+    // dx and dw run in one launch: their depths are split so that all blocks have about one share of it
+    const int64_t nk_x = L.piece_b / BK, nk_w = L.np / BK;
+    const int64_t steps = mt * (L.np / BN) * nk_x + mt * (L.piece_b / BN) * nk_w;
+    const int64_t least = half ? 8 : 2;  // steps a block should have (of six products each in float32)
+    const int64_t share = steps / FILL > least ? steps / FILL : least;
+    L.split_dx = splits_for(nk_x, share);
+    L.split_dw = splits_for(nk_w, share);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -900,15 +900,15 @@ hipError_t prepare(const LabelLossArgs& a, const LossPlan& L, char* ws, bool for
         pk.ldw = L.kp;
     }
     const unsigned blocks = p.x_blocks + (unsigned)((p.w_rows + p.per_block - 1) / p.per_block);
-    if (a.n <= LROWS) {
-        k_pack<T, PARTS, true><<<blocks, LT, 0, s>>>(r, p);
+    if (a.n <= PROWS) {
+        k_pack<T, PARTS, true><<<blocks, PT, 0, s>>>(r, p);
         return hipGetLastError();
     }
     int32_t* bc = a.n <= LOOK_BACK ? nullptr : (int32_t*)(ws + L.block_count);
     const unsigned lb = (unsigned)((a.n + LROWS - 1) / LROWS);
     if (bc) k_label_count<<<lb, LT, 0, s>>>(r, bc);
     k_label_rows<<<lb, LT, 0, s>>>(r, bc);
-    k_pack<T, PARTS, false><<<blocks, LT, 0, s>>>(r, p);
+    k_pack<T, PARTS, false><<<blocks, PT, 0, s>>>(r, p);
     return hipGetLastError();
 }
 
