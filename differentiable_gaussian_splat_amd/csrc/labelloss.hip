@@ -97,7 +97,7 @@ struct Stage {
                 off[i] = (uint32_t)((r * ld + seg * 32 + (l % 4) * 8) * 2);
             } else {
                 const int r = (i * 4 + w) * 16 + l / 4;
-                off[i] = (uint32_t)((r * ld + ((l % 4) ^ ((r >> 1) & 3)) * 8) * 2);
+                off[i] = (uint32_t)((r * ld + ((l % 4) ^ ((r >> 2) & 3)) * 8) * 2);
             }
         }
     }
@@ -139,7 +139,7 @@ __device__ __forceinline__ bf16x8 fragment(const bf16* lds, int r0, int kk) {
         return v;
     } else {
         const int r = r0 + l % 32;
-        return *reinterpret_cast<const bf16x8*>(lds + r * BK + ((2 * kk + l / 32) ^ ((r >> 1) & 3)) * 8);
+        return *reinterpret_cast<const bf16x8*>(lds + r * BK + ((2 * kk + l / 32) ^ ((r >> 2) & 3)) * 8);
     }
 }
 
