@@ -25,6 +25,7 @@
 // contiguous runs. The pair counts are reduced first and copied to the host
 // asynchronously, so the host's wait for them overlaps the depth sort.
 #include "common.hpp"
+#include "elem.hpp"
 #include "launch.hpp"
 
 namespace gs {
@@ -654,16 +655,18 @@ constexpr int RADIX_INLINE_BLOCKS = 512;
 
 // bstart (nullable): the histogram and digit totals are already there, for
 // blocks of elements [bstart[b], bstart[b + 1]) (RADIX_INLINE_BLOCKS at most).
+// counted: they are already there for the usual blocks.
 template <class V>
 hipError_t radix_pass(SrcMem<V> src, int n, const u64* dcount, int shift, int bits, uint32_t* hist, uint32_t* rtot,
                       int pass, uint32_t* keys_out, V* vals_out, hipStream_t s, PieceTable pt = {},
-                      const u64* bstart = nullptr) {
+                      const u64* bstart = nullptr, bool counted = false) {
     const int nblocks = (n + RE - 1) / RE;
     if (nblocks == 0) return hipSuccess;
     uint32_t* tot = rtot + RT * 256 * (pass & 1);
     uint32_t* spare = rtot + RT * 256 * ((pass & 1) ^ 1);
     if (bstart && nblocks > RADIX_INLINE_BLOCKS) return hipErrorInvalidValue;
-    if (!bstart) k_radix_hist<<<nblocks, RB, 0, s>>>(src.keys, n, dcount, shift, bits, hist, tot);
+    if (!bstart && !counted)
+        k_radix_hist<<<nblocks, RB, 0, s>>>(src.keys, n, dcount, shift, bits, hist, tot);
     if (nblocks <= RADIX_INLINE_BLOCKS) {
         k_radix_scatter<true, V><<<nblocks, RB, 0, s>>>(src, n, dcount, shift, bits, hist, tot, spare, pt, bstart,
                                                         keys_out, vals_out);
@@ -1657,18 +1660,55 @@ size_t radix_sort_scratch(int64_t n) {
     return align256(((size_t)RADIX_TOTAL_WORDS + 256 * nblocks) * sizeof(uint32_t));
 }
 
-hipError_t launch_radix_sort(int n, uint32_t max_key, uint32_t* const keys[2], uint32_t* const vals[2], char* scratch,
-                             int* sorted_at, hipStream_t s) {
+// The first pass's keys, values and histogram: key = the index, or `rows` where it names no row.
+__global__ __launch_bounds__(RB) void k_index_keys(int n, int rows, const void* __restrict__ ids, bool wide, int bits,
+                                                 uint32_t* __restrict__ keys, uint32_t* __restrict__ pos,
+                                                 uint32_t* __restrict__ hist, uint32_t* __restrict__ tot) {
+    __shared__ uint32_t s_h[RW][256];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    for (int k = tid; k < RW * 256; k += RB) (&s_h[0][0])[k] = 0u;
+    const int p0 = blockIdx.x * RE;
+    const uint32_t mask = (1u << bits) - 1u;
+    int kk[RR];
+#pragma unroll
+    for (int r = 0; r < RR; ++r) {
+        const int p = p0 + (w * RR + r) * 64 + lane;
+        kk[r] = p < n ? row_index(ids, wide, p, rows) : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RR; ++r) {
+        const int p = p0 + (w * RR + r) * 64 + lane;
+        if (p < n) {
+            const uint32_t key = kk[r] < 0 ? (uint32_t)rows : (uint32_t)kk[r];
+            keys[p] = key;
+            pos[p] = (uint32_t)p;
+            atomicAdd(&s_h[w][key & mask], 1u);
+        }
+    }
+    __syncthreads();
+    if (tid < 256) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int k = 0; k < RW; ++k) c += s_h[k][tid];
+        hist[(size_t)blockIdx.x * 256 + tid] = c;
+        if (c) atomicAdd(&tot[(blockIdx.x % RT) * 256 + tid], c);
+    }
+}
+
+hipError_t launch_index_sort(int n, int rows, const void* ids, bool wide, uint32_t* const keys[2],
+                             uint32_t* const vals[2], char* scratch, int* sorted_at, hipStream_t s) {
     uint32_t* rtot = reinterpret_cast<uint32_t*>(scratch);
     uint32_t* hist = rtot + RADIX_TOTAL_WORDS;
     int bits = 1;
-    while (bits < 32 && (max_key >> bits) != 0u) ++bits;
+    while (bits < 32 && ((uint32_t)rows >> bits) != 0u) ++bits;
     const int passes = (bits + 7) / 8, per = (bits + passes - 1) / passes;
+    k_index_keys<<<(n + RE - 1) / RE, RB, 0, s>>>(n, rows, ids, wide, per, keys[0], vals[0], hist, rtot);
     int cur = 0;
     for (int p = 0; p < passes; ++p, cur ^= 1) {
         const int b = min(per, bits - p * per);
         hipError_t e = radix_pass(SrcMem<uint32_t>{keys[cur], vals[cur]}, n, nullptr, p * per, b, hist, rtot, p,
-                                  keys[cur ^ 1], vals[cur ^ 1], s);
+                                  keys[cur ^ 1], vals[cur ^ 1], s, {}, nullptr, p == 0);
         if (e != hipSuccess) return e;
     }
     *sorted_at = cur;

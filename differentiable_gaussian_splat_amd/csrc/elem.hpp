@@ -24,12 +24,14 @@ typedef bf16 bf16x8_any __attribute__((ext_vector_type(8), aligned(2)));
 
 // The WIDE<T> elements of a row at p, of which `left` are inside the row (the
 // others read as 0). FULL: the row is whole accesses (left is not looked at).
+// past: the elements behind the row may be read as well (they are masked), as
+// they may where another row follows: the row's end then costs no branch.
 template <bool FULL>
-__device__ __forceinline__ void load_row(const float* p, int left, float (&v)[4]) {
-    if (FULL || left >= 4) {
+__device__ __forceinline__ void load_row(const float* p, int left, bool past, float (&v)[4]) {
+    if (FULL || past || left >= 4) {
         const f32x4_any t = *reinterpret_cast<const f32x4_any*>(p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = t[i];
+        for (int i = 0; i < 4; ++i) v[i] = FULL || i < left ? t[i] : 0.f;
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = i < left ? p[i] : 0.f;
@@ -37,11 +39,11 @@ __device__ __forceinline__ void load_row(const float* p, int left, float (&v)[4]
 }
 
 template <bool FULL>
-__device__ __forceinline__ void load_row(const bf16* p, int left, float (&v)[8]) {
-    if (FULL || left >= 8) {
+__device__ __forceinline__ void load_row(const bf16* p, int left, bool past, float (&v)[8]) {
+    if (FULL || past || left >= 8) {
         const bf16x8_any t = *reinterpret_cast<const bf16x8_any*>(p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (float)t[i];
+        for (int i = 0; i < 8; ++i) v[i] = FULL || i < left ? (float)t[i] : 0.f;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = i < left ? (float)p[i] : 0.f;

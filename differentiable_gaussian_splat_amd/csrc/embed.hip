@@ -21,7 +21,7 @@ namespace gs {
 namespace {
 
 constexpr int EB = 256;         // threads per block
-constexpr int RUN_TOKENS = 32;  // sorted positions a row group sums
+constexpr int RUN_TOKENS = 16;  // sorted positions a row group sums, all loaded at once
 constexpr int JOIN_T = 1024;
 constexpr int FEW = 256;        // positions up to which one launch makes the gradient (a multiple of 64)
 
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(EB) void k_embed(int64_t n, int dim, int vocab, con
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[u][k] = 0.f;
             if (row[u] >= 0) {
-                load_row<FULL>(table + row[u] * ts + c, dim - c, v[u]);
+                load_row<FULL>(table + row[u] * ts + c, dim - c, ts != 0 && row[u] + 1 < vocab, v[u]);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) v[u][k] *= scale;
             }
@@ -65,21 +65,11 @@ __global__ __launch_bounds__(EB) void k_embed(int64_t n, int dim, int vocab, con
     }
 }
 
-// Sort keys (the index, or vocab where it names no row) and positions; the sort's digit totals cleared.
-__global__ __launch_bounds__(EB) void k_embed_keys(int n, int vocab, const void* __restrict__ ids, bool wide,
-                                                   uint32_t* __restrict__ keys, uint32_t* __restrict__ pos,
-                                                   uint32_t* __restrict__ totals, int n_totals) {
-    const int i = blockIdx.x * EB + threadIdx.x;
-    for (int k = i; k < n_totals; k += gridDim.x * EB) totals[k] = 0u;
-    if (i < n) {
-        const int r = row_index(ids, wide, i, vocab);
-        keys[i] = r < 0 ? (uint32_t)vocab : (uint32_t)r;
-        pos[i] = (uint32_t)i;
-    }
-}
-
+// Also clears the sort's digit totals.
 template <class T>
-__global__ __launch_bounds__(EB) void k_zero_rows(int rows, int dim, int lanes, T* __restrict__ p, int64_t stride) {
+__global__ __launch_bounds__(EB) void k_zero_rows(int rows, int dim, int lanes, T* __restrict__ p, int64_t stride,
+                                                  uint32_t* __restrict__ totals, int n_totals) {
+    for (int k = blockIdx.x * EB + threadIdx.x; k < n_totals; k += gridDim.x * EB) totals[k] = 0u;
     const float z[WIDE<T>] = {};
     const int l = threadIdx.x % lanes, per = EB / lanes;
     for (int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / lanes; r < rows; r += (int64_t)gridDim.x * per)
@@ -123,7 +113,7 @@ __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, con
                         if (mine) {
                             const int i = i0 + __ffsll((unsigned long long)mine) - 1;
                             mine &= mine - 1;
-                            if (c < dim) load_row<FULL>(dout + (int64_t)i * ds + c, dim - c, t[u]);
+                            if (c < dim) load_row<FULL>(dout + (int64_t)i * ds + c, dim - c, ds != 0 && i + 1 < n, t[u]);
                         }
                     }
 #pragma unroll
@@ -154,7 +144,7 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
     constexpr int G = NT / LPR;
     constexpr int BT = G * RUN_TOKENS;
     constexpr int VEC = WIDE<T>, CW = LPR * VEC;
-    constexpr int U = 8;
+    constexpr int U = RUN_TOKENS;
     __shared__ uint32_t s_tok[BT], s_pos[BT];
     __shared__ uint32_t s_key[2 * G];  // per group: its first run's key and, if another, its last run's
     __shared__ float s_sum[2 * G][CW];
@@ -186,7 +176,10 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
             kk[u] = s_tok[p + u];
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[u][k] = 0.f;
-            if (kk[u] != none && c < dim) load_row<FULL>(dout + (int64_t)s_pos[p + u] * ds + c, dim - c, v[u]);
+            if (kk[u] != none && c < dim) {
+                const int64_t row = s_pos[p + u];
+                load_row<FULL>(dout + row * ds + c, dim - c, ds != 0 && row + 1 < n, v[u]);
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -282,7 +275,7 @@ __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const
 #pragma unroll
             for (int k = 0; k < VEC; k += 4) {
                 float t[4];
-                load_row<FULL>(q + k, dim - c - k, t);
+                load_row<FULL>(q + k, dim - c - k, false, t);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[k + i] += t[i];
             }
@@ -364,11 +357,12 @@ hipError_t embed_run(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
 }
 
 template <class T>
-hipError_t zero_rows(int rows, int dim, void* p, int64_t stride, hipStream_t s) {
+hipError_t zero_rows(int rows, int dim, void* p, int64_t stride, char* totals, hipStream_t s) {
     int lanes = 1;
     while (lanes < 64 && lanes * WIDE<T> < dim) lanes *= 2;
     const int64_t want = ((int64_t)rows * lanes + EB - 1) / EB;
-    k_zero_rows<T><<<(unsigned)(want < 4096 ? want : 4096), EB, 0, s>>>(rows, dim, lanes, (T*)p, stride);
+    k_zero_rows<T><<<(unsigned)(want < 4096 ? want : 4096), EB, 0, s>>>(rows, dim, lanes, (T*)p, stride, (uint32_t*)totals,
+                                                                 RADIX_TOTAL_WORDS);
     return hipGetLastError();
 }
 
@@ -431,18 +425,14 @@ hipError_t launch_embed_bwd(int64_t n, int dim, int vocab, bool half, const void
     a.ds = dtable_stride;
     a.scale = scale;
     if (n <= FEW) return half ? embed_run<bf16>(a, FEW_SUMS, stream) : embed_run<float>(a, FEW_SUMS, stream);
-    hipError_t e = half ? zero_rows<bf16>(vocab, dim, dtable, dtable_stride, stream)
-                        : zero_rows<float>(vocab, dim, dtable, dtable_stride, stream);
-    if (e != hipSuccess) return e;
     const EmbedLayout L = embed_bwd_layout(n, dim, vocab);
+    hipError_t e = half ? zero_rows<bf16>(vocab, dim, dtable, dtable_stride, ws + L.sort, stream)
+                        : zero_rows<float>(vocab, dim, dtable, dtable_stride, ws + L.sort, stream);
+    if (e != hipSuccess) return e;
     uint32_t* keys[2] = {(uint32_t*)(ws + L.keys[0]), (uint32_t*)(ws + L.keys[1])};
     uint32_t* pos[2] = {(uint32_t*)(ws + L.pos[0]), (uint32_t*)(ws + L.pos[1])};
-    k_embed_keys<<<(unsigned)((n + EB - 1) / EB), EB, 0, stream>>>((int)n, vocab, ids, wide_ids, keys[0], pos[0],
-                                                                  (uint32_t*)(ws + L.sort), RADIX_TOTAL_WORDS);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
     int at = 0;
-    e = launch_radix_sort((int)n, vocab, keys, pos, ws + L.sort, &at, stream);
+    e = launch_index_sort((int)n, vocab, ids, wide_ids, keys, pos, ws + L.sort, &at, stream);
     if (e != hipSuccess) return e;
     a.keys = keys[at];
     a.pos = pos[at];

@@ -581,7 +581,7 @@ __global__ __launch_bounds__(PT) void k_pack(LabelRows a, PackArgs p) {
 #pragma unroll
             for (int k = 0; k < 8; k += V) {
                 float t[V];
-                load_row<false>(src + row * stride + c + k, p.dim - c - k, t);
+                load_row<false>(src + row * stride + c + k, p.dim - c - k, false, t);
 #pragma unroll
                 for (int j = 0; j < V; ++j) v[k + j] = t[j];
             }

@@ -151,14 +151,13 @@ hipError_t launch_adam_step(const AdamLr& lr, float beta1, float beta2, float ep
                             float* const v[5], float* scales, float* opacities, float* grad_norm,
                             hipStream_t stream);
 
-// Stable ascending sort of n < 2^31 - 4096 (key, value) pairs, keys <= max_key, by the binning's
-// radix passes. keys[0], vals[0] hold the input, the sorted pairs end in keys[*sorted_at],
-// vals[*sorted_at]; the other buffers are overwritten. The scratch's first RADIX_TOTAL_WORDS
-// words are zero on entry.
+// Positions 0..n-1 (n < 2^31 - 4096) sorted by the index they name, in order within an index, by the binning's
+// radix passes; indices outside [0, rows) come last, as `rows`. The sorted pairs end in keys[*sorted_at],
+// vals[*sorted_at]; the other buffers are overwritten. The scratch's first RADIX_TOTAL_WORDS words are zero on entry.
 constexpr int RADIX_TOTAL_WORDS = 4096;
 size_t radix_sort_scratch(int64_t n);
-hipError_t launch_radix_sort(int n, uint32_t max_key, uint32_t* const keys[2], uint32_t* const vals[2], char* scratch,
-                             int* sorted_at, hipStream_t s);
+hipError_t launch_index_sort(int n, int rows, const void* ids, bool wide, uint32_t* const keys[2],
+                             uint32_t* const vals[2], char* scratch, int* sorted_at, hipStream_t s);
 
 // Label learning (embed.hip, norm.hip, labelloss.hip). `half`: rows are bfloat16, otherwise
 // float32; strides count elements; index arrays are int64 with `wide_ids`, otherwise int32.

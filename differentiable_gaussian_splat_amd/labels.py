@@ -19,7 +19,7 @@ from __future__ import annotations
 
 import torch
 
-from .raster import _check, _nbytes, _stream, load_library
+from .raster import _check, load_library
 
 __all__ = ["gs_embed_fwd", "gs_embed_bwd_workspace_size", "gs_embed_bwd", "gs_layer_norm_fwd",
            "gs_layer_norm_bwd_workspace_size", "gs_layer_norm_bwd", "gs_label_loss_workspace_size",
@@ -84,6 +84,20 @@ def _opt(t):
     return None if t is None else t.data_ptr()
 
 
+def _workspace_of(t):
+    """A workspace's address and bytes (None: none)."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"a workspace must be a contiguous buffer on the GPU, got one on {t.device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _stream(stream, device):
+    """The stream's handle; the device's current stream if None (asked for by number: the object costs 2.5 us)."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
 # ------------------------------------------------------------------ thin C-ABI wrappers
 
 def gs_embed_fwd(table, ids, out, scale=1.0, stream=None):
@@ -92,9 +106,10 @@ def gs_embed_fwd(table, ids, out, scale=1.0, stream=None):
     vocab, dim = table.shape
     n = ids.shape[0]
     os_ = _matrix("out", out, table, n, dim)
-    ip, it = _index("ids", ids, n, table.get_device())
+    dev = table.get_device()
+    ip, it = _index("ids", ids, n, dev)
     st = load_library().gs_embed_fwd(n, dim, vocab, _DTYPES[table.dtype], table.data_ptr(), ts, ip, it, scale,
-                                     out.data_ptr(), os_, _stream(stream))
+                                     out.data_ptr(), os_, _stream(stream, dev))
     _check(st, "gs_embed_fwd")
 
 
@@ -107,9 +122,10 @@ def gs_embed_bwd(ids, dout, dtable, workspace, scale=1.0, stream=None):
     ds = _matrix("dout", dout)
     n, dim = dout.shape
     ts = _matrix("dtable", dtable, dout, None, dim)
-    ip, it = _index("ids", ids, n, dout.get_device())
+    dev = dout.get_device()
+    ip, it = _index("ids", ids, n, dev)
     st = load_library().gs_embed_bwd(n, dim, dtable.shape[0], _DTYPES[dout.dtype], ip, it, scale, dout.data_ptr(), ds,
-                                     dtable.data_ptr(), ts, _opt(workspace), _nbytes(workspace), _stream(stream))
+                                     dtable.data_ptr(), ts, *_workspace_of(workspace), _stream(stream, dev))
     _check(st, "gs_embed_bwd")
 
 
@@ -122,7 +138,7 @@ def gs_layer_norm_fwd(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, stream
     st = load_library().gs_layer_norm_fwd(n, dim, _DTYPES[dt], x.data_ptr(), xs,
                                           _vector("weight", weight, dim, dt, dev), _vector("bias", bias, dim, dt, dev),
                                           eps, y.data_ptr(), ys, _vector("mean", mean, n, torch.float32, dev),
-                                          _vector("rstd", rstd, n, torch.float32, dev), _stream(stream))
+                                          _vector("rstd", rstd, n, torch.float32, dev), _stream(stream, dev))
     _check(st, "gs_layer_norm_fwd")
 
 
@@ -141,8 +157,8 @@ def gs_layer_norm_bwd(x, weight, mean, rstd, dy, dx, dweight, dbias, workspace, 
                                           _vector("weight", weight, dim, dt, dev), _vector("mean", mean, n, f32, dev),
                                           _vector("rstd", rstd, n, f32, dev), dy.data_ptr(), dys, _opt(dx), dxs,
                                           _vector("dweight", dweight, dim, dt, dev),
-                                          _vector("dbias", dbias, dim, dt, dev), _opt(workspace), _nbytes(workspace),
-                                          _stream(stream))
+                                          _vector("dbias", dbias, dim, dt, dev), *_workspace_of(workspace),
+                                          _stream(stream, dev))
     _check(st, "gs_layer_norm_bwd")
 
 
@@ -161,8 +177,7 @@ def gs_label_loss_fwd(x, w, labels, loss, lse, mean, count, workspace, stream=No
     st = load_library().gs_label_loss_fwd(n, dim, w.shape[0], _DTYPES[x.dtype], x.data_ptr(), xs, w.data_ptr(), ws, ip,
                                           it, _vector("loss", loss, n, f32, dev), _vector("lse", lse, n, f32, dev),
                                           _vector("mean", mean, 1, f32, dev),
-                                          _vector("count", count, 1, torch.int32, dev), _opt(workspace),
-                                          _nbytes(workspace), _stream(stream))
+                                          _vector("count", count, 1, torch.int32, dev), *_workspace_of(workspace), _stream(stream, dev))
     _check(st, "gs_label_loss_fwd")
 
 
@@ -179,7 +194,7 @@ def gs_label_loss_bwd(x, w, labels, lse, dx, dw, workspace, dmean=None, dloss=No
     st = load_library().gs_label_loss_bwd(n, dim, w.shape[0], _DTYPES[x.dtype], x.data_ptr(), xs, w.data_ptr(), ws, ip,
                                           it, _vector("lse", lse, n, f32, dev), _vector("dmean", dmean, 1, f32, dev),
                                           _vector("dloss", dloss, n, f32, dev), _opt(dx), dxs, _opt(dw), dws,
-                                          _opt(workspace), _nbytes(workspace), _stream(stream))
+                                          *_workspace_of(workspace), _stream(stream, dev))
     _check(st, "gs_label_loss_bwd")
 
 
