@@ -24,11 +24,12 @@ typedef bf16 bf16x8_any __attribute__((ext_vector_type(8), aligned(2)));
 
 // The WIDE<T> elements of a row at p, of which `left` are inside the row (the
 // others read as 0). FULL: the row is whole accesses (left is not looked at).
-// past: the elements behind the row may be read as well (they are masked), as
-// they may where another row follows: the row's end then costs no branch.
+// room: elements from p to the end of the matrix. Where that is enough the
+// access may reach behind the row, and what it finds there is masked, so that
+// a row's end costs no branch; only the matrix's last elements take one.
 template <bool FULL>
-__device__ __forceinline__ void load_row(const float* p, int left, bool past, float (&v)[4]) {
-    if (FULL || past || left >= 4) {
+__device__ __forceinline__ void load_row(const float* p, int left, int64_t room, float (&v)[4]) {
+    if (FULL || room >= 4) {
         const f32x4_any t = *reinterpret_cast<const f32x4_any*>(p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = FULL || i < left ? t[i] : 0.f;
@@ -39,8 +40,8 @@ __device__ __forceinline__ void load_row(const float* p, int left, bool past, fl
 }
 
 template <bool FULL>
-__device__ __forceinline__ void load_row(const bf16* p, int left, bool past, float (&v)[8]) {
-    if (FULL || past || left >= 8) {
+__device__ __forceinline__ void load_row(const bf16* p, int left, int64_t room, float (&v)[8]) {
+    if (FULL || room >= 8) {
         const bf16x8_any t = *reinterpret_cast<const bf16x8_any*>(p);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = FULL || i < left ? (float)t[i] : 0.f;

@@ -52,7 +52,7 @@ __global__ __launch_bounds__(EB) void k_embed(int64_t n, int dim, int vocab, con
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[u][k] = 0.f;
             if (row[u] >= 0) {
-                load_row<FULL>(table + row[u] * ts + c, dim - c, ts != 0 && row[u] + 1 < vocab, v[u]);
+                load_row<FULL>(table + row[u] * ts + c, dim - c, (vocab - 1 - row[u]) * ts + dim - c, v[u]);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) v[u][k] *= scale;
             }
@@ -113,7 +113,7 @@ __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, con
                         if (mine) {
                             const int i = i0 + __ffsll((unsigned long long)mine) - 1;
                             mine &= mine - 1;
-                            if (c < dim) load_row<FULL>(dout + (int64_t)i * ds + c, dim - c, ds != 0 && i + 1 < n, t[u]);
+                            if (c < dim) load_row<FULL>(dout + (int64_t)i * ds + c, dim - c, (n - 1 - i) * ds + dim - c, t[u]);
                         }
                     }
 #pragma unroll
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
             for (int k = 0; k < VEC; ++k) v[u][k] = 0.f;
             if (kk[u] != none && c < dim) {
                 const int64_t row = s_pos[p + u];
-                load_row<FULL>(dout + row * ds + c, dim - c, ds != 0 && row + 1 < n, v[u]);
+                load_row<FULL>(dout + row * ds + c, dim - c, (n - 1 - row) * ds + dim - c, v[u]);
             }
         }
 #pragma unroll
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const
 #pragma unroll
             for (int k = 0; k < VEC; k += 4) {
                 float t[4];
-                load_row<FULL>(q + k, dim - c - k, false, t);
+                load_row<FULL>(q + k, dim - c - k, dim - c - k, t);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[k + i] += t[i];
             }

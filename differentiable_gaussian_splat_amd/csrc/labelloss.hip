@@ -581,7 +581,7 @@ __global__ __launch_bounds__(PT) void k_pack(LabelRows a, PackArgs p) {
 #pragma unroll
             for (int k = 0; k < 8; k += V) {
                 float t[V];
-                load_row<false>(src + row * stride + c + k, p.dim - c - k, false, t);
+                load_row<false>(src + row * stride + c + k, p.dim - c - k, p.dim - c - k, t);
 #pragma unroll
                 for (int j = 0; j < V; ++j) v[k + j] = t[j];
             }
@@ -618,6 +618,24 @@ __device__ __forceinline__ float2 lse_join(float2 a, float2 b) {
 constexpr int JR = 64;  // rows per block of the join
 constexpr int JT = 1024;
 
+// The mean loss from the blocks' sums, added in block order, by one block of NT threads.
+template <int NT>
+__device__ __forceinline__ void loss_mean(const double* block_sum, int blocks, int cnt, float* mean,
+                                          int32_t* count_out) {
+    __shared__ double s_sum[NT / 64];
+    double sum = 0.0;
+    for (int k = threadIdx.x; k < blocks; k += NT)
+        sum += __hip_atomic_load(&block_sum[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+    if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int k = 1; k < NT / 64; ++k) sum += s_sum[k];
+        *mean = cnt > 0 ? (float)(sum / (double)cnt) : 0.f;
+        *count_out = cnt;
+    }
+}
+
 // Joins the slabs' (maximum, sum) pairs of each labelled row (and `state`, the
 // join of earlier pieces; with `more` pieces to come the result is left there
 // again), then the row's loss. The block that ends last adds the blocks' losses
@@ -631,7 +649,6 @@ __global__ __launch_bounds__(JT) void k_lse_join(int slabs, int np, const float2
                                                  int32_t* __restrict__ count_out) {
     constexpr int G = JT / JR;
     __shared__ float2 s[G][JR];
-    __shared__ double s_sum[JT / 64];
     __shared__ int s_last;
     const int j = threadIdx.x % JR, g = threadIdx.x / JR;
     const int n = blockIdx.x * JR + j, cnt = *count;
@@ -670,18 +687,7 @@ __global__ __launch_bounds__(JT) void k_lse_join(int slabs, int np, const float2
     }
     if (more) return;
     __syncthreads();
-    if (!s_last) return;
-    double sum = 0.0;
-    for (int k = threadIdx.x; k < (int)gridDim.x; k += JT)
-        sum += __hip_atomic_load(&block_sum[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-    if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int k = 1; k < JT / 64; ++k) sum += s_sum[k];
-        *mean = cnt > 0 ? (float)(sum / (double)cnt) : 0.f;
-        *count_out = cnt;
-    }
+    if (s_last) loss_mean<JT>(block_sum, (int)gridDim.x, cnt, mean, count_out);
 }
 
 // out[r] = the splits' rows of acc added in order, through place (-1: a zero row) if given.
@@ -734,6 +740,16 @@ __global__ __launch_bounds__(256) void k_join_splits(SplitJoin a, SplitJoin b, i
     }
 }
 
+}  // namespace
+
+}  // namespace gs
+
+#include "fewlabels.hpp"
+
+namespace gs {
+
+namespace {
+
 // ---------------------------------------------------------------- plan
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -772,8 +788,15 @@ struct LossPlan {
     int64_t piece_f, piece_b;      // vocabulary rows per piece (multiples of 256)
     int tm_z, tm_d;                // row blocks per wave: over the vocabulary, over dim
     int split_dx, split_dw;
+    bool few;                      // few labels: no packing, no tiles
+    int few_tr, few_slabs, few_chunks;
+    size_t g;
     size_t rows, place, count, done, block_count, xp, wp, part, target, state, block_sum, dz, dxp, dwp, total;
 };
+
+// Few labels: rounded up to the gradient kernel's sizes, and its columns per thread.
+int few_bucket(int vocab) { return vocab <= 4 ? 4 : vocab <= 8 ? 8 : vocab <= 16 ? 16 : vocab <= 32 ? 32 : 64; }
+int few_columns(int vocab) { return vocab <= 8 ? 4 : vocab <= 16 ? 2 : 1; }
 
 LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     LossPlan L{};
@@ -808,6 +831,23 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     L.count = take(4);
     L.done = take(4);
     L.block_count = take((size_t)(L.np / LROWS + 1) * 4);
+    if (vocab <= FEW_LABELS) {
+        L.few = true;
+        const int cols = few_columns(vocab);
+        L.few_tr = 1;
+        while (L.few_tr < FT && L.few_tr * cols < dim) L.few_tr *= 2;
+        L.few_slabs = (dim + L.few_tr * cols - 1) / (L.few_tr * cols);
+        const int64_t most = 1024 / L.few_slabs < 64 ? 64 : 1024 / L.few_slabs > 256 ? 256 : 1024 / L.few_slabs;
+        const int64_t want = (n + FG - 1) / FG;
+        L.few_chunks = (int)(want < 1 ? 1 : want < most ? want : most);
+        L.block_sum = take((size_t)(L.np / FR + 1) * 8);
+        if (backward) {
+            L.g = take((size_t)L.np * few_bucket(vocab) * 4);
+            L.dwp = take((size_t)L.few_chunks * vocab * L.kp * 4);
+        }
+        L.total = o;
+        return L;
+    }
     L.xp = take((size_t)L.parts * L.np * L.kp * 2);
     L.wp = take((size_t)L.parts * vocab * L.kp * 2);
     if (backward) {
@@ -863,9 +903,7 @@ void launch_pair(int tm, const Product& dx, const Product& dw, hipStream_t s) {
         k_product_pair<PARTS, 1, T><<<grid, GT, 0, s>>>(dx, dw);
 }
 
-template <class T>
-hipError_t prepare(const LabelLossArgs& a, const LossPlan& L, char* ws, bool forward, Packed& pk, hipStream_t s) {
-    constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
+LabelRows label_arrays(const LabelLossArgs& a, const LossPlan& L, char* ws, bool forward) {
     LabelRows r{};
     r.n = a.n;
     r.vocab = a.vocab;
@@ -877,6 +915,20 @@ hipError_t prepare(const LabelLossArgs& a, const LossPlan& L, char* ws, bool for
     r.done = (int32_t*)(ws + L.done);
     r.loss = forward ? a.loss : nullptr;
     r.lse = forward ? a.lse : nullptr;
+    return r;
+}
+
+void list_rows(const LabelRows& r, const LossPlan& L, char* ws, hipStream_t s) {
+    int32_t* bc = r.n <= LOOK_BACK ? nullptr : (int32_t*)(ws + L.block_count);
+    const unsigned lb = (unsigned)(r.n > 0 ? (r.n + LROWS - 1) / LROWS : 1);
+    if (bc) k_label_count<<<lb, LT, 0, s>>>(r, bc);
+    k_label_rows<<<lb, LT, 0, s>>>(r, bc);
+}
+
+template <class T>
+hipError_t prepare(const LabelLossArgs& a, const LossPlan& L, char* ws, bool forward, Packed& pk, hipStream_t s) {
+    constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
+    const LabelRows r = label_arrays(a, L, ws, forward);
     PackArgs p{};
     p.dim = a.dim;
     p.kp = L.kp;
@@ -904,10 +956,7 @@ hipError_t prepare(const LabelLossArgs& a, const LossPlan& L, char* ws, bool for
         k_pack<T, PARTS, true><<<blocks, PT, 0, s>>>(r, p);
         return hipGetLastError();
     }
-    int32_t* bc = a.n <= LOOK_BACK ? nullptr : (int32_t*)(ws + L.block_count);
-    const unsigned lb = (unsigned)((a.n + LROWS - 1) / LROWS);
-    if (bc) k_label_count<<<lb, LT, 0, s>>>(r, bc);
-    k_label_rows<<<lb, LT, 0, s>>>(r, bc);
+    list_rows(r, L, ws, s);
     k_pack<T, PARTS, false><<<blocks, PT, 0, s>>>(r, p);
     return hipGetLastError();
 }
@@ -929,9 +978,76 @@ Product product_base(const LabelLossArgs& a, const LossPlan& L, char* ws) {
 }
 
 template <class T>
+hipError_t few_labels(const LabelLossArgs& a, const LossPlan& L, char* ws, bool forward, hipStream_t s) {
+    const LabelRows r = label_arrays(a, L, ws, forward);
+    list_rows(r, L, ws, s);
+    FewArgs f{};
+    f.n = a.n;
+    f.dim = a.dim;
+    f.vocab = a.vocab;
+    f.x = a.x;
+    f.w = a.w;
+    f.labels = a.labels;
+    f.xs = a.x_stride;
+    f.ws = a.w_stride;
+    f.wide_labels = a.wide_labels;
+    f.rows = r.rows;
+    f.place = r.place;
+    f.count = r.count;
+    f.loss = a.loss;
+    f.lse = a.lse;
+    f.mean = a.mean;
+    f.done = r.done;
+    f.count_out = a.count;
+    f.block_sum = (double*)(ws + L.block_sum);
+    f.dmean = a.dmean;
+    f.dloss = a.dloss;
+    const unsigned blocks = (unsigned)(a.n > 0 ? (a.n + FR - 1) / FR : 1);
+    if (forward) {
+        if (a.vocab <= 32)
+            k_few_logits<T, 1, true><<<blocks, FT, 0, s>>>(f);
+        else
+            k_few_logits<T, 2, true><<<blocks, FT, 0, s>>>(f);
+        return hipGetLastError();
+    }
+    f.g = (float*)(ws + L.g);
+    f.ldg = few_bucket(a.vocab);
+    f.dx = a.dx;
+    f.dxs = a.dx_stride;
+    f.dw = a.dw ? (float*)(ws + L.dwp) : nullptr;
+    f.kp = L.kp;
+    f.chunk = (a.n + L.few_chunks - 1) / L.few_chunks;
+    if (a.vocab <= 32)
+        k_few_logits<T, 1, false><<<blocks, FT, 0, s>>>(f);
+    else
+        k_few_logits<T, 2, false><<<blocks, FT, 0, s>>>(f);
+    const dim3 grid(L.few_chunks, L.few_slabs);
+    switch (f.ldg) {
+        case 4: k_few_grads<T, 4, 4><<<grid, FT, 0, s>>>(f, L.few_tr); break;
+        case 8: k_few_grads<T, 8, 4><<<grid, FT, 0, s>>>(f, L.few_tr); break;
+        case 16: k_few_grads<T, 16, 2><<<grid, FT, 0, s>>>(f, L.few_tr); break;
+        case 32: k_few_grads<T, 32, 1><<<grid, FT, 0, s>>>(f, L.few_tr); break;
+        default: k_few_grads<T, 64, 1><<<grid, FT, 0, s>>>(f, L.few_tr); break;
+    }
+    if (a.dw) {
+        SplitJoin j{}, none{};
+        j.rows = a.vocab;
+        j.splits = L.few_chunks;
+        j.acc = f.dw;
+        j.pacc = (int64_t)a.vocab * L.kp;
+        j.out = a.dw;
+        j.ldout = a.dw_stride;
+        j.blocks = a.vocab;
+        k_join_splits<T><<<j.blocks, 256, 0, s>>>(j, none, a.dim, L.kp, 1);
+    }
+    return hipGetLastError();
+}
+
+template <class T>
 hipError_t loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
     const LossPlan L = loss_plan(a.n, a.dim, a.vocab, PARTS == 1, false);
+    if (L.few) return few_labels<T>(a, L, ws, true, s);
     Packed pk{};
     hipError_t e = prepare<T>(a, L, ws, true, pk, s);
     if (e != hipSuccess) return e;
@@ -966,6 +1082,7 @@ template <class T>
 hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
     const LossPlan L = loss_plan(a.n, a.dim, a.vocab, PARTS == 1, true);
+    if (L.few) return few_labels<T>(a, L, ws, false, s);
     Packed pk{};
     hipError_t e = prepare<T>(a, L, ws, false, pk, s);
     if (e != hipSuccess) return e;

@@ -63,8 +63,8 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __
             b[e][k] = 0.f;
         }
         if (c < dim) {
-            if (weight) load_row<FULL>(weight + c, dim - c, false, w[e]);
-            if (bias) load_row<FULL>(bias + c, dim - c, false, b[e]);
+            if (weight) load_row<FULL>(weight + c, dim - c, dim - c, w[e]);
+            if (bias) load_row<FULL>(bias + c, dim - c, dim - c, b[e]);
         }
     }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < n; r0 += (int64_t)gridDim.x * RPB) {
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __
             const int c = (e * LPR + l) * VEC;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[e][k] = 0.f;
-            if (live && c < dim) load_row<FULL>(xr + c, dim - c, xs != 0 && r + 1 < n, v[e]);
+            if (live && c < dim) load_row<FULL>(xr + c, dim - c, (n - 1 - r) * xs + dim - c, v[e]);
         }
 #pragma unroll
         for (int e = 0; e < EPL; ++e)
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(int64_t n, int dim, const T* __
             w[e][k] = 1.f;
             aw[e][k] = ab[e][k] = 0.f;
         }
-        if (weight && c < dim) load_row<FULL>(weight + c, dim - c, false, w[e]);
+        if (weight && c < dim) load_row<FULL>(weight + c, dim - c, dim - c, w[e]);
     }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < n; r0 += (int64_t)gridDim.x * RPB) {
         const int64_t r = r0 + threadIdx.x / LPR;
@@ -174,8 +174,8 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(int64_t n, int dim, const T* __
 #pragma unroll
             for (int k = 0; k < VEC; ++k) xv[e][k] = gv[e][k] = 0.f;
             if (live && c < dim) {
-                load_row<FULL>(x + r * xs + c, dim - c, xs != 0 && r + 1 < n, xv[e]);
-                load_row<FULL>(dy + r * dys + c, dim - c, dys != 0 && r + 1 < n, gv[e]);
+                load_row<FULL>(x + r * xs + c, dim - c, (n - 1 - r) * xs + dim - c, xv[e]);
+                load_row<FULL>(dy + r * dys + c, dim - c, (n - 1 - r) * dys + dim - c, gv[e]);
             }
         }
         const float mean = live ? mean_in[r] : 0.f, rstd = live ? rstd_in[r] : 0.f;
