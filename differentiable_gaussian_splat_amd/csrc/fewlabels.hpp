@@ -2,10 +2,9 @@
 //
 // With up to FEW_LABELS labels the products are too flat for tiles: the call
 // is bound by reading x and writing dx. So nothing is packed: a block takes 32
-// labelled rows, its four waves each a share of the columns, with operands
-// straight from memory to the matrix units (float32 products in float32,
-// bfloat16 in bfloat16); their sums meet in LDS, where a row's whole softmax
-// is formed. The gradients take a column of w and of dw's sum per thread in
+// labelled rows and walks along them, its four waves each with a quarter of the
+// columns (float32 products in float32, bfloat16 in bfloat16); their sums meet
+// in LDS, where a row's whole softmax is formed. The gradients take a column of w and of dw's sum per thread in
 // registers and walk over the rows: 2 x labels operations for each element of
 // x read once and of dx written once, in float32 and without rounding dz.
 // dw's sums of the blocks' row chunks are joined in order by a second launch.
@@ -44,77 +43,92 @@ struct FewArgs {
     int64_t chunk;       // rows of a chunk
 };
 
-// Eight elements of a row (0 beyond `left`), widened; room: to the end of the matrix.
-__device__ __forceinline__ void load8(const float* p, int left, int64_t room, float (&v)[8]) {
-    float a[4], b[4];
-    load_row<false>(p, left, room, a);
-    load_row<false>(p + 4, left - 4, room - 4, b);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = a[i];
-        v[i + 4] = b[i];
-    }
-}
-__device__ __forceinline__ void load8(const bf16* p, int left, int64_t room, float (&v)[8]) {
-    load_row<false>(p, left, room, v);
-}
-
 // Sixteen depth elements of a 32 x 32 product; lane: row l % 32, elements 8 (l / 32) to + 7 of each operand.
-__device__ __forceinline__ f32x16 few_product(const float*, const float (&a)[8], const float (&b)[8], f32x16 c) {
+__device__ __forceinline__ f32x16 few_product(const float* a, const float* b, f32x16 c) {
+    float x[8], y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+    for (int i = 0; i < 8; i += 4) {
+        *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(a + i);
+        *reinterpret_cast<float4*>(y + i) = *reinterpret_cast<const float4*>(b + i);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[i], y[i], c, 0, 0, 0);
     return c;
 }
-__device__ __forceinline__ f32x16 few_product(const bf16*, const float (&a)[8], const float (&b)[8], f32x16 c) {
-    bf16x8 x, y;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = (bf16)a[i];
-        y[i] = (bf16)b[i];
-    }
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
+__device__ __forceinline__ f32x16 few_product(const bf16* a, const bf16* b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(a),
+                                                   *reinterpret_cast<const bf16x8*>(b), c, 0, 0, 0);
 }
 
 // The logits of 32 labelled rows, then (FORWARD) their losses and, by the block
-// that ends last, the mean, or dz. VT: 32-label tiles.
+// that ends last, the mean, or dz. VT: 32-label tiles. 128 columns at a time of
+// x's rows and of w go through LDS (read along the rows; a lane per row would
+// touch a line per lane), the next ones on their way in registers meanwhile.
 template <class T, int VT, bool FORWARD>
 __global__ __launch_bounds__(FT) void k_few_logits(FewArgs a) {
-    constexpr int VP = 32 * VT;
-    __shared__ float s_z[FT / 64][FR][VP + 1];
+    constexpr int VP = 32 * VT, V = WIDE<T>;
+    constexpr int KC = 128, PITCH = KC + V, CH = KC / V;  // columns, their row in LDS, 16-byte accesses of a row
+    constexpr int RS = FT / CH;                           // rows that the block's threads read at once
+    constexpr int NX = FR / RS, NW = VP / RS;
+    constexpr int TILES = (FR + VP) * PITCH * (int)sizeof(T), SUMS = FT / 64 * FR * (VP + 1) * 4;
+    __shared__ __align__(16) char s_mem[TILES > SUMS ? TILES : SUMS];
     __shared__ double s_loss[FR];
     __shared__ int s_last;
+    T* s_x = reinterpret_cast<T*>(s_mem);
+    T* s_w = s_x + FR * PITCH;
+    float(*s_z)[FR][VP + 1] = reinterpret_cast<float(*)[FR][VP + 1]>(s_mem);
     const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
     const int cnt = *a.count, n0 = blockIdx.x * FR;
     if (n0 < cnt) {
-        const int n = n0 + l % 32, h = l / 32;
-        const bool have = n < cnt;
-        const int64_t row = have ? a.rows[n] : 0;
-        const T* x = static_cast<const T*>(a.x) + row * a.xs + 8 * h;
-        const int64_t room = (a.n - 1 - row) * a.xs;  // behind the row
+        const int r0 = threadIdx.x / CH, c0 = threadIdx.x % CH * V;
+        int64_t row[NX];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) row[i] = n0 + r0 + i * RS < cnt ? a.rows[n0 + r0 + i * RS] : -1;
+        float xv[NX][V], wv[NW][V];
+        auto load = [&](int k0) {
+            const int c = k0 + c0, left = a.dim - c;
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const bool in = row[i] >= 0 && left > 0;
+                load_row<false>(static_cast<const T*>(a.x) + (in ? row[i] * a.xs + c : 0), in ? left : 0,
+                                in ? (a.n - 1 - row[i]) * a.xs + left : 0, xv[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                const int v = r0 + i * RS;
+                const bool in = v < a.vocab && left > 0;
+                load_row<false>(static_cast<const T*>(a.w) + (in ? v * a.ws + c : 0), in ? left : 0,
+                                in ? (a.vocab - 1 - v) * a.ws + left : 0, wv[i]);
+            }
+        };
         f32x16 acc[VT];
 #pragma unroll
         for (int t = 0; t < VT; ++t)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[t][e] = 0.f;
-#pragma unroll 2
-        for (int k0 = 16 * w; k0 < a.dim; k0 += 16 * (FT / 64)) {
-            const int left = a.dim - k0 - 8 * h;
-            float xv[8], wv[VT][8];
-            load8(x + k0, have ? left : 0, have ? room + left : 0, xv);
+        load(0);
+        for (int k0 = 0; k0 < a.dim; k0 += KC) {
+            __syncthreads();
 #pragma unroll
-            for (int t = 0; t < VT; ++t) {
-                const int v = l % 32 + 32 * t;
-                const bool in = v < a.vocab;
-                load8(static_cast<const T*>(a.w) + (int64_t)(in ? v : 0) * a.ws + 8 * h + k0, in ? left : 0,
-                      in ? (a.vocab - 1 - v) * a.ws + left : 0, wv[t]);
+            for (int i = 0; i < NX; ++i) store_row<true>(s_x + (r0 + i * RS) * PITCH + c0, V, xv[i]);
+#pragma unroll
+            for (int i = 0; i < NW; ++i) store_row<true>(s_w + (r0 + i * RS) * PITCH + c0, V, wv[i]);
+            __syncthreads();
+            if (k0 + KC < a.dim) load(k0 + KC);
+#pragma unroll
+            for (int s = 0; s < KC / 64; ++s) {  // a wave's quarter of the columns, 16 at a time
+                const int c = w * (KC / 4) + 16 * s + 8 * (l / 32);
+#pragma unroll
+                for (int t = 0; t < VT; ++t)
+                    acc[t] = few_product(s_w + (32 * t + l % 32) * PITCH + c, s_x + (l % 32) * PITCH + c, acc[t]);
             }
-#pragma unroll
-            for (int t = 0; t < VT; ++t) acc[t] = few_product((const T*)nullptr, wv[t], xv, acc[t]);
         }
+        __syncthreads();
 #pragma unroll
         for (int t = 0; t < VT; ++t)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s_z[w][l % 32][32 * t + 8 * (e / 4) + 4 * h + e % 4] = acc[t][e];
+            for (int e = 0; e < 16; ++e)
+                s_z[w][l % 32][32 * t + 8 * (e / 4) + 4 * (l / 32) + e % 4] = acc[t][e];
     }
     __syncthreads();
     // eight threads per row, each every eighth label

@@ -39,9 +39,13 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int BN = 128;         // columns of every product's tile (rows of x, or of the vocabulary)
-constexpr int BK = 32;          // depth of one staged step
 constexpr int GT = 256;         // threads: four waves, two blocks to a compute unit
-constexpr int STAGES = 3;       // steps in LDS: one read, two on their way
+// A staged step: 32 deep and three of them in LDS (one read, two on their way),
+// or, with the three parts of split operands side by side, 16 deep and two:
+// the six products of a step make up for the shorter way ahead.
+constexpr int step_depth(int parts) { return parts == 3 ? 16 : 32; }
+constexpr int step_buffers(int parts) { return parts == 3 ? 2 : 3; }
+constexpr int KPAD = 16;        // columns of packed operands are padded to it in float32, to twice it in bfloat16
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
 
@@ -78,13 +82,19 @@ __device__ __forceinline__ float up_of(const Product& p, int row, int cnt) {
     return u;
 }
 
-// Stages a T x BK operand tile into LDS: rows of 32 depth elements (64 bytes;
-// their 16-byte chunks are exchanged by the row, so that eight rows' chunks of
-// one depth spread over all banks) or, TR, depth rows of T elements (64-byte
-// segments exchanged by the depth row, for the transposing reads).
-template <int T, bool TR>
+// How a row's chunks are exchanged.
+template <int BK>
+__device__ __forceinline__ int chunk_turn(int r) {
+    return BK == 32 ? (r >> 2) & 3 : (r >> 3) & 1;
+}
+
+// Stages a T x BK operand tile into LDS: rows of BK depth elements (16-byte
+// chunks exchanged by the row, so that the sixteen lanes that read together
+// find one depth's chunks spread over all banks) or, TR, depth rows of T elements
+// (64-byte segments exchanged by the depth row, for the transposing reads).
+template <int T, bool TR, int BK>
 struct Stage {
-    static constexpr int NI = T / 64;  // 16-byte loads per lane
+    static constexpr int NI = T * BK / 2048;  // 16-byte loads per lane
     uint32_t off[NI];                  // byte offsets of the lane's chunks from the tile's first element
 
     __device__ __forceinline__ Stage(int64_t ld) {
@@ -96,8 +106,9 @@ struct Stage {
                 const int seg = ((l % (T / 8)) / 4) ^ (r & (T / 32 - 1) & 3);
                 off[i] = (uint32_t)((r * ld + seg * 32 + (l % 4) * 8) * 2);
             } else {
-                const int r = (i * 4 + w) * 16 + l / 4;
-                off[i] = (uint32_t)((r * ld + ((l % 4) ^ ((r >> 2) & 3)) * 8) * 2);
+                constexpr int C = BK / 8;  // chunks of a row
+                const int r = (i * 4 + w) * (64 / C) + l / C;
+                off[i] = (uint32_t)((r * ld + ((l % C) ^ chunk_turn<BK>(r)) * 8) * 2);
             }
         }
     }
@@ -124,7 +135,7 @@ struct Stage {
 };
 
 // The 8 depth elements of a lane for one 32-row fragment: row r0 + lane % 32, depth 16 kk + 8 (lane / 32).
-template <int T, bool TR>
+template <int T, bool TR, int BK>
 __device__ __forceinline__ bf16x8 fragment(const bf16* lds, int r0, int kk) {
     const int l = threadIdx.x & 63;
     if constexpr (TR) {
@@ -139,7 +150,7 @@ __device__ __forceinline__ bf16x8 fragment(const bf16* lds, int r0, int kk) {
         return v;
     } else {
         const int r = r0 + l % 32;
-        return *reinterpret_cast<const bf16x8*>(lds + r * BK + ((2 * kk + l / 32) ^ ((r >> 2) & 3)) * 8);
+        return *reinterpret_cast<const bf16x8*>(lds + r * BK + ((2 * kk + l / 32) ^ chunk_turn<BK>(r)) * 8);
     }
 }
 
@@ -156,13 +167,16 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 __device__ __forceinline__ float exp_diff(float z, float ref) { return exp2_fast((z - ref) * LOG2E); }
 
 // Rows staged for TM row blocks per wave (a power of two, for the staging's lanes).
-constexpr int staged_rows(int tm) { return tm == 1 ? 64 : tm == 2 ? 128 : 256; }
+constexpr int staged_rows(int tm, int parts) { return tm == 1 && parts == 1 ? 64 : tm <= 2 ? 128 : 256; }
+constexpr int tile_elements(int tm, int parts) {
+    return step_buffers(parts) * parts * (staged_rows(tm, parts) + BN) * step_depth(parts);
+}
 
 // One product, C[m][n] = sum_k A[m][k] B[n][k], by 64 TM x 128 tiles; a lane
 // holds, for one n, runs of four consecutive m. PARTS: 1, or 3 for split
 // operands.
 //
-// The loop keeps three steps in LDS: while one is multiplied the next two are
+// The loop keeps several steps in LDS: while one is multiplied the next are
 // loaded straight to LDS, and one barrier a step both publishes the arrived
 // step and frees the one before it. Loads past the last step are made with an
 // empty extent (they bring zeros), which keeps the count of loads in flight
@@ -171,8 +185,8 @@ template <int MODE, int PARTS, int TM, class T>
 __device__ __forceinline__ void product(const Product& p, int block, bf16* s_tiles) {
     constexpr bool TA = MODE == DX || MODE == DW, TB = MODE == DW;
     constexpr int TN = 2, WM = 32 * TM, WN = 32 * TN;  // 2 x 2 waves of WM rows and WN columns
-    constexpr int BM = 2 * WM, SM = staged_rows(TM);
-    constexpr int STEP = (SM + BN) * BK;  // elements of one staged step: the a tile, then the b tile
+    constexpr int BM = 2 * WM, SM = staged_rows(TM, PARTS), BK = step_depth(PARTS), BUFS = step_buffers(PARTS);
+    constexpr int STEP = PARTS * (SM + BN) * BK;  // elements of one staged step: the a tile's parts, then the b tile's
     const int cnt = *p.count;
     const int nn = MODE == DW ? p.n : cnt;
     const int mt = (p.m + BM - 1) / BM, nt = (nn + BN - 1) / BN;
@@ -190,33 +204,30 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
     const int nk = (depth + BK - 1) / BK;
     const int share = (nk + p.splits - 1) / p.splits;
     const int k_first = min(nk, split * share), k_end = min(nk, k_first + share);
-    const int per = k_end - k_first;
-    const int steps = per * (PARTS == 3 ? 6 : 1);
+    const int steps = k_end - k_first;
 
-    const Stage<SM, TA> sa(p.lda);
-    const Stage<BN, TB> sb(p.ldb);
+    const Stage<SM, TA, BK> sa(p.lda);
+    const Stage<BN, TB, BK> sb(p.ldb);
     const int a_rows = TA ? (MODE == DW ? p.np : p.k) : p.m;  // rows of the operand's memory
     const int b_rows = p.np;
-    // the next step to load: depth step kt of part pair pr
-    int kt = 0, pr = 0;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_tiles;
+    int kt = 0;  // the next step to load
     auto issue = [&](int buf) {
-        const bool live = pr < (PARTS == 3 ? 6 : 1) && per > 0;
-        const int ia = PARTS == 3 ? (0x001012 >> (4 * pr)) & 3 : 0;  // 2 1 0 1 0 0
-        const int ib = PARTS == 3 ? (0x010210 >> (4 * pr)) & 3 : 0;  // 0 1 2 0 1 0
+        const bool live = kt < steps;
         const int64_t k0 = live ? (k_first + kt) * BK : 0;
-        const bf16* a = p.a + ia * p.pa + (TA ? k0 * p.lda + m0 : m0 * p.lda + k0);
-        const bf16* b = p.b + ib * p.pb + (TB ? k0 * p.ldb + n0 : n0 * p.ldb + k0);
+        const bf16* a = p.a + (TA ? k0 * p.lda + m0 : m0 * p.lda + k0);
+        const bf16* b = p.b + (TB ? k0 * p.ldb + n0 : n0 * p.ldb + k0);
         const int64_t ea = TA ? (min((int64_t)BK, a_rows - k0) - 1) * p.lda + p.m - m0
                               : (int64_t)(min(SM, a_rows - m0) - 1) * p.lda + BK;
         const int64_t eb = TB ? (min((int64_t)BK, b_rows - k0) - 1) * p.ldb + p.ldb - n0
                               : (int64_t)(min(BN, b_rows - n0) - 1) * p.ldb + BK;
-        sa.load(a, live ? ea * 2 : 0, lds0 + buf * STEP * 2);
-        sb.load(b, live ? eb * 2 : 0, lds0 + (buf * STEP + SM * BK) * 2);
-        if (++kt >= per) {
-            kt = 0;
-            ++pr;
-        }
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)
+            sa.load(a + q * p.pa, live ? ea * 2 : 0, lds0 + (buf * STEP + q * SM * BK) * 2);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)
+            sb.load(b + q * p.pb, live ? eb * 2 : 0, lds0 + (buf * STEP + PARTS * SM * BK + q * BN * BK) * 2);
+        ++kt;
     };
 
     const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
@@ -229,27 +240,35 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-    constexpr int LOADS = Stage<SM, TA>::NI + Stage<BN, TB>::NI;  // of one step
-    issue(0);
-    issue(1);
+    constexpr int LOADS = PARTS * (Stage<SM, TA, BK>::NI + Stage<BN, TB, BK>::NI);  // of one step
+    for (int t = 0; t < BUFS - 1; ++t) issue(t);
     int buf = 0;
     for (int t = 0; t < steps; ++t) {
-        step_barrier<LOADS>();
-        issue(buf == 0 ? STAGES - 1 : buf - 1);
-        const bf16 *la = s_tiles + buf * STEP, *lb = la + SM * BK;
-        buf = buf == STAGES - 1 ? 0 : buf + 1;
+        step_barrier<(BUFS - 2) * LOADS>();
+        issue(buf == 0 ? BUFS - 1 : buf - 1);
+        const bf16 *la = s_tiles + buf * STEP, *lb = la + PARTS * SM * BK;
+        buf = buf == BUFS - 1 ? 0 : buf + 1;
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
-            bf16x8 fa[TM], fb[TN];
+            bf16x8 fa[PARTS][TM], fb[PARTS][TN];
 #pragma unroll
-            for (int i = 0; i < TM; ++i) fa[i] = fragment<SM, TA>(la, wm + 32 * i, kk);
+            for (int q = PARTS - 1; q >= 0; --q) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb[j] = fragment<BN, TB>(lb, wn + 32 * j, kk);
+                for (int i = 0; i < TM; ++i) fa[q][i] = fragment<SM, TA, BK>(la + q * SM * BK, wm + 32 * i, kk);
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+                for (int j = 0; j < TN; ++j) fb[q][j] = fragment<BN, TB, BK>(lb + q * BN * BK, wn + 32 * j, kk);
+            }
+            // the products of parts whose sizes add up to 2^-16 of the operands' and more, smallest first
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+            for (int sum = PARTS - 1; sum >= 0; --sum)
+#pragma unroll
+                for (int q = sum; q >= 0; --q)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int j = 0; j < TN; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[q][i], fb[sum - q][j], acc[i][j], 0,
+                                                                               0, 0);
         }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last step
@@ -414,14 +433,14 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
 
 template <int MODE, int PARTS, int TM, class T>
 __global__ __launch_bounds__(GT, 2) void k_product(Product p) {
-    __shared__ __align__(16) bf16 s_tiles[STAGES * (staged_rows(TM) + BN) * BK];
+    __shared__ __align__(16) bf16 s_tiles[tile_elements(TM, PARTS)];
     product<MODE, PARTS, TM, T>(p, blockIdx.x, s_tiles);
 }
 
 // dx and dw, which read the same dz, in one launch: together they fill the chip better, and small ones wait once.
 template <int PARTS, int TM, class T>
 __global__ __launch_bounds__(GT, 2) void k_product_pair(Product dx, Product dw) {
-    __shared__ __align__(16) bf16 s_tiles[STAGES * (staged_rows(TM) + BN) * BK];
+    __shared__ __align__(16) bf16 s_tiles[tile_elements(TM, PARTS)];
     const int first = dx.grid * dx.splits;
     if ((int)blockIdx.x < first)
         product<DX, PARTS, TM, T>(dx, blockIdx.x, s_tiles);
@@ -434,7 +453,7 @@ __global__ __launch_bounds__(GT, 2) void k_product_pair(Product dx, Product dw) 
 constexpr int LPT = 4;                // rows per thread
 constexpr int LT = 1024, LROWS = LT * LPT;  // threads and rows of a block that lists labelled rows
 constexpr int PT = 256, PROWS = PT * LPT;   // threads of a packing block, rows of which it can make the list itself
-constexpr int64_t LOOK_BACK = 65536;  // rows up to which a block counts the labels before its own rows itself
+constexpr int64_t LOOK_BACK = 8192;  // rows up to which a block counts the labels before its own rows itself
 
 // The arrays that the labels give: rows[], the labelled rows in order; place[r],
 // the position of row r in it, or -1; their number; loss and lse (nullable),
@@ -528,7 +547,7 @@ __global__ __launch_bounds__(LT) void k_label_rows(LabelRows a, const int32_t* _
     }
 }
 
-// Rows into bfloat16 parts of kp columns (a multiple of BK, zero beyond dim):
+// Rows into bfloat16 parts of kp columns (whole steps, zero beyond dim):
 // the first x_blocks blocks pack x's labelled rows, and zero rows up to the
 // next multiple of BN, the others every row of w. SMALL: x has at most PROWS
 // rows, and each block makes the list of labelled rows for itself first (block
@@ -801,7 +820,7 @@ int few_columns(int vocab) { return vocab <= 8 ? 4 : vocab <= 16 ? 2 : 1; }
 LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     LossPlan L{};
     L.parts = half ? 1 : 3;
-    L.kp = (int)up(dim, BK);
+    L.kp = (int)up(dim, half ? 2 * KPAD : KPAD);
     L.np = up(n > 0 ? n : 1, BN);
     const int64_t vp = up(vocab, 256);
     auto piece = [&](int64_t budget) {  // vocabulary rows whose per-row cost fits the budget
@@ -814,9 +833,10 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     L.tm_d = tm_dim(L.kp);
     const int64_t mt = up(L.kp, 64 * L.tm_d) / (64 * L.tm_d);
     // dx and dw run in one launch: their depths are split so that all blocks have about one share of it
-    const int64_t nk_x = L.piece_b / BK, nk_w = L.np / BK;
+    const int bk = step_depth(L.parts);
+    const int64_t nk_x = L.piece_b / bk, nk_w = L.np / bk;
     const int64_t steps = mt * (L.np / BN) * nk_x + mt * (L.piece_b / BN) * nk_w;
-    const int64_t least = half ? 8 : 2;  // steps a block should have (of six products each in float32)
+    const int64_t least = half ? 8 : 4;  // steps a block should have (of six products each in float32)
     const int64_t share = steps / FILL > least ? steps / FILL : least;
     L.split_dx = splits_for(nk_x, share);
     L.split_dw = splits_for(nk_w, share);
