@@ -19,46 +19,51 @@ constexpr int WIDE = 16 / (int)sizeof(T);
 // 16 bytes at an address that is aligned to the element only: gfx950 takes
 // 16-byte global accesses at any address, so rows of odd lengths and strides
 // need no narrower ones.
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-typedef bf16 bf16x8_any __attribute__((ext_vector_type(8), aligned(2)));
+template <class T>
+using wide_t = T __attribute__((ext_vector_type(WIDE<T>)));
+template <class T>
+using wide_any = T __attribute__((ext_vector_type(WIDE<T>), aligned(sizeof(T))));
 
-// The WIDE<T> elements of a row at p, of which `left` are inside the row (the
-// others read as 0). FULL: the row is whole accesses (left is not looked at).
-// room: elements from p to the end of the matrix. Where that is enough the
-// access may reach behind the row, and what it finds there is masked, so that
-// a row's end costs no branch; only the matrix's last elements take one.
-template <bool FULL>
-__device__ __forceinline__ void load_row(const float* p, int left, int64_t room, float (&v)[4]) {
-    if (FULL || room >= 4) {
-        const f32x4_any t = *reinterpret_cast<const f32x4_any*>(p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = FULL || i < left ? t[i] : 0.f;
+// The WIDE<T> elements of a row at p, as they are in memory. left: of them
+// inside the row; room: from p to the end of the matrix. Where the room is
+// enough the access may reach behind the row; what it finds there is masked by
+// `widen` or `clip`, so that a row's end costs no branch (only the matrix's
+// last elements do). Masked later and not here, where it would wait for the
+// load. FULL: the row is whole accesses, and none of this is looked at.
+template <bool FULL, class T>
+__device__ __forceinline__ wide_t<T> load_row(const T* p, int left, int64_t room) {
+    wide_t<T> t;
+    if (FULL || room >= WIDE<T>) {
+        t = *reinterpret_cast<const wide_any<T>*>(p);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = i < left ? p[i] : 0.f;
+        for (int i = 0; i < WIDE<T>; ++i) t[i] = i < left ? p[i] : (T)0.f;
     }
+    return t;
 }
 
-template <bool FULL>
-__device__ __forceinline__ void load_row(const bf16* p, int left, int64_t room, float (&v)[8]) {
-    if (FULL || room >= 8) {
-        const bf16x8_any t = *reinterpret_cast<const bf16x8_any*>(p);
+template <bool FULL, class T>
+__device__ __forceinline__ wide_t<T> clip(wide_t<T> t, int left) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = FULL || i < left ? (float)t[i] : 0.f;
-    } else {
+    for (int i = 0; i < WIDE<T>; ++i) t[i] = FULL || i < left ? t[i] : (T)0.f;
+    return t;
+}
+
+template <bool FULL, class T, int V>
+__device__ __forceinline__ void widen(wide_t<T> t, int left, float (&v)[V]) {
+    static_assert(V == WIDE<T>, "");
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? (float)p[i] : 0.f;
-    }
+    for (int i = 0; i < V; ++i) v[i] = FULL || i < left ? (float)t[i] : 0.f;
 }
 
 // Stores the first `left` (FULL: all) of WIDE<T> elements.
 template <bool FULL>
 __device__ __forceinline__ void store_row(float* p, int left, const float (&v)[4]) {
     if (FULL || left >= 4) {
-        f32x4_any t;
+        wide_any<float> t;
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] = v[i];
-        *reinterpret_cast<f32x4_any*>(p) = t;
+        *reinterpret_cast<wide_any<float>*>(p) = t;
     } else {
 #pragma unroll
         for (int i = 0; i < 3; ++i)
@@ -69,10 +74,10 @@ __device__ __forceinline__ void store_row(float* p, int left, const float (&v)[4
 template <bool FULL>
 __device__ __forceinline__ void store_row(bf16* p, int left, const float (&v)[8]) {
     if (FULL || left >= 8) {
-        bf16x8_any t;
+        wide_any<bf16> t;
 #pragma unroll
         for (int i = 0; i < 8; ++i) t[i] = (bf16)v[i];
-        *reinterpret_cast<bf16x8_any*>(p) = t;
+        *reinterpret_cast<wide_any<bf16>*>(p) = t;
     } else {
 #pragma unroll
         for (int i = 0; i < 7; ++i)

@@ -46,21 +46,21 @@ __global__ __launch_bounds__(EB) void k_embed(int64_t n, int dim, int vocab, con
         row[u] = r < n ? row_index(ids, wide, r, vocab) : -1;
     }
     for (int c = l * VEC; c < dim; c += LPR * VEC) {
-        float v[U][VEC];
+        wide_t<T> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) v[u][k] = 0.f;
-            if (row[u] >= 0) {
-                load_row<FULL>(table + row[u] * ts + c, dim - c, (vocab - 1 - row[u]) * ts + dim - c, v[u]);
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) v[u][k] *= scale;
-            }
+            raw[u] = (T)0.f;
+            if (row[u] >= 0)
+                raw[u] = load_row<FULL>(table + row[u] * ts + c, dim - c, (vocab - 1 - row[u]) * ts + dim - c);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + u * G;
-            if (r < n) store_row<FULL>(out + r * os + c, dim - c, v[u]);
+            float v[VEC];
+            widen<true, T>(raw[u], dim - c, v);  // what is behind the row is not stored
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) v[k] = row[u] >= 0 ? v[k] * scale : 0.f;
+            if (r < n) store_row<FULL>(out + r * os + c, dim - c, v);
         }
     }
 }
@@ -105,21 +105,24 @@ __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, con
                     mine = q == sub ? m : mine;
                 }
                 while (mine) {
-                    float t[U][VEC];
+                    wide_t<T> raw[U];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-#pragma unroll
-                        for (int k = 0; k < VEC; ++k) t[u][k] = 0.f;
+                        raw[u] = (T)0.f;
                         if (mine) {
                             const int i = i0 + __ffsll((unsigned long long)mine) - 1;
                             mine &= mine - 1;
-                            if (c < dim) load_row<FULL>(dout + (int64_t)i * ds + c, dim - c, (n - 1 - i) * ds + dim - c, t[u]);
+                            if (c < dim)
+                                raw[u] = load_row<FULL>(dout + (int64_t)i * ds + c, dim - c, (n - 1 - i) * ds + dim - c);
                         }
                     }
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
+                    for (int u = 0; u < U; ++u) {
+                        float t[VEC];
+                        widen<true, T>(raw[u], dim - c, t);
 #pragma unroll
-                        for (int k = 0; k < VEC; ++k) acc[k] += t[u][k];
+                        for (int k = 0; k < VEC; ++k) acc[k] += t[k];
+                    }
                 }
             }
 #pragma unroll
@@ -170,15 +173,14 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
     for (int p = p0; p < p0 + RUN_TOKENS; p += U) {
         if (s_tok[p] == none) break;  // sorted last: nothing follows
         uint32_t kk[U];
-        float v[U][VEC];
+        wide_t<T> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             kk[u] = s_tok[p + u];
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) v[u][k] = 0.f;
+            raw[u] = (T)0.f;
             if (kk[u] != none && c < dim) {
                 const int64_t row = s_pos[p + u];
-                load_row<FULL>(dout + row * ds + c, dim - c, (n - 1 - row) * ds + dim - c, v[u]);
+                raw[u] = load_row<FULL>(dout + row * ds + c, dim - c, (n - 1 - row) * ds + dim - c);
             }
         }
 #pragma unroll
@@ -197,8 +199,10 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
                 for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
                 cur = kk[u];
             }
+            float v[VEC];
+            widen<true, T>(raw[u], dim - c, v);  // sums of what is behind the row are not stored
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) acc[k] += v[u][k];
+            for (int k = 0; k < VEC; ++k) acc[k] += v[k];
         }
     }
 #pragma unroll
@@ -274,8 +278,7 @@ __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const
             const float* q = part + ((size_t)(b + j) * 2 + (j == 0 ? 1 : 0)) * dim + c;
 #pragma unroll
             for (int k = 0; k < VEC; k += 4) {
-                float t[4];
-                load_row<FULL>(q + k, dim - c - k, dim - c - k, t);
+                const wide_t<float> t = load_row<FULL>(q + k, dim - c - k, dim - c - k);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[k + i] += t[i];
             }

@@ -84,21 +84,23 @@ __global__ __launch_bounds__(FT) void k_few_logits(FewArgs a) {
         int64_t row[NX];
 #pragma unroll
         for (int i = 0; i < NX; ++i) row[i] = n0 + r0 + i * RS < cnt ? a.rows[n0 + r0 + i * RS] : -1;
-        float xv[NX][V], wv[NW][V];
+        wide_t<T> xv[NX], wv[NW];
         auto load = [&](int k0) {
             const int c = k0 + c0, left = a.dim - c;
 #pragma unroll
             for (int i = 0; i < NX; ++i) {
                 const bool in = row[i] >= 0 && left > 0;
-                load_row<false>(static_cast<const T*>(a.x) + (in ? row[i] * a.xs + c : 0), in ? left : 0,
-                                in ? (a.n - 1 - row[i]) * a.xs + left : 0, xv[i]);
+                xv[i] = (T)0.f;
+                if (in) xv[i] = load_row<false>(static_cast<const T*>(a.x) + row[i] * a.xs + c, left,
+                                                (a.n - 1 - row[i]) * a.xs + left);
             }
 #pragma unroll
             for (int i = 0; i < NW; ++i) {
                 const int v = r0 + i * RS;
                 const bool in = v < a.vocab && left > 0;
-                load_row<false>(static_cast<const T*>(a.w) + (in ? v * a.ws + c : 0), in ? left : 0,
-                                in ? (a.vocab - 1 - v) * a.ws + left : 0, wv[i]);
+                wv[i] = (T)0.f;
+                if (in) wv[i] = load_row<false>(static_cast<const T*>(a.w) + v * a.ws + c, left,
+                                                (a.vocab - 1 - v) * a.ws + left);
             }
         };
         f32x16 acc[VT];
@@ -110,9 +112,13 @@ __global__ __launch_bounds__(FT) void k_few_logits(FewArgs a) {
         for (int k0 = 0; k0 < a.dim; k0 += KC) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < NX; ++i) store_row<true>(s_x + (r0 + i * RS) * PITCH + c0, V, xv[i]);
+            for (int i = 0; i < NX; ++i)
+                *reinterpret_cast<wide_t<T>*>(s_x + (r0 + i * RS) * PITCH + c0) =
+                    clip<false, T>(xv[i], a.dim - k0 - c0);
 #pragma unroll
-            for (int i = 0; i < NW; ++i) store_row<true>(s_w + (r0 + i * RS) * PITCH + c0, V, wv[i]);
+            for (int i = 0; i < NW; ++i)
+                *reinterpret_cast<wide_t<T>*>(s_w + (r0 + i * RS) * PITCH + c0) =
+                    clip<false, T>(wv[i], a.dim - k0 - c0);
             __syncthreads();
             if (k0 + KC < a.dim) load(k0 + KC);
 #pragma unroll
@@ -196,22 +202,26 @@ __global__ __launch_bounds__(FT) void k_few_logits(FewArgs a) {
     if (s_last) loss_mean<FT>(a.block_sum, (int)gridDim.x, cnt, a.mean, a.count_out);
 }
 
+// C columns of a row as they are in memory (0 beyond `left`).
 template <int C, class T>
-__device__ __forceinline__ void load_cols(const T* p, int left, float (&v)[C]) {
-    typedef T vec __attribute__((ext_vector_type(C), aligned(sizeof(T))));
-    if (left >= C) {
-        if constexpr (C == 1) {
-            v[0] = (float)*p;
+struct Cols {
+    T v[C];
+    __device__ __forceinline__ void load(const T* p, int left) {
+        typedef T vec __attribute__((ext_vector_type(C), aligned(sizeof(T))));
+        if (left >= C) {
+            if constexpr (C == 1) {
+                v[0] = *p;
+            } else {
+                const vec t = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+                for (int i = 0; i < C; ++i) v[i] = t[i];
+            }
         } else {
-            const vec t = *reinterpret_cast<const vec*>(p);
 #pragma unroll
-            for (int i = 0; i < C; ++i) v[i] = (float)t[i];
+            for (int i = 0; i < C; ++i) v[i] = i < left ? p[i] : (T)0.f;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = i < left ? (float)p[i] : 0.f;
     }
-}
+};
 
 template <int C, class T>
 __device__ __forceinline__ void store_cols(T* p, int left, const float (&v)[C]) {
@@ -246,7 +256,12 @@ __global__ __launch_bounds__(FT) void k_few_grads(FewArgs a, int tr) {
     for (int v = 0; v < VB; ++v) {
 #pragma unroll
         for (int k = 0; k < C; ++k) w[v][k] = acc[v][k] = 0.f;
-        if (a.dx && v < a.vocab && left > 0) load_cols<C>(static_cast<const T*>(a.w) + v * a.ws + c, left, w[v]);
+        if (a.dx && v < a.vocab && left > 0) {
+            Cols<C, T> t;
+            t.load(static_cast<const T*>(a.w) + v * a.ws + c, left);
+#pragma unroll
+            for (int k = 0; k < C; ++k) w[v][k] = (float)t.v[k];
+        }
     }
     const int64_t first = blockIdx.x * a.chunk, end = first + a.chunk < a.n ? first + a.chunk : a.n;
     for (int64_t r0 = first; r0 < end; r0 += FG) {
@@ -260,15 +275,15 @@ __global__ __launch_bounds__(FT) void k_few_grads(FewArgs a, int tr) {
         __syncthreads();
         constexpr int U = 4;
         for (int i0 = grp; i0 < FG; i0 += U * groups) {
-            float x[U][C];
+            Cols<C, T> x[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = i0 + u * groups;
 #pragma unroll
-                for (int k = 0; k < C; ++k) x[u][k] = 0.f;
+                for (int k = 0; k < C; ++k) x[u].v[k] = (T)0.f;
                 // a row without a label is not read
                 if (a.dw && i < FG && s_place[i] >= 0 && left > 0)
-                    load_cols<C>(static_cast<const T*>(a.x) + (r0 + i) * a.xs + c, left, x[u]);
+                    x[u].load(static_cast<const T*>(a.x) + (r0 + i) * a.xs + c, left);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -284,7 +299,7 @@ __global__ __launch_bounds__(FT) void k_few_grads(FewArgs a, int tr) {
 #pragma unroll
                         for (int k = 0; k < C; ++k) {
                             d[k] = fmaf(g, w[v][k], d[k]);
-                            acc[v][k] = fmaf(g, x[u][k], acc[v][k]);
+                            acc[v][k] = fmaf(g, (float)x[u].v[k], acc[v][k]);
                         }
                     }
                 if (a.dx && left > 0) store_cols<C>(static_cast<T*>(a.dx) + (r0 + i) * a.dxs + c, left, d);

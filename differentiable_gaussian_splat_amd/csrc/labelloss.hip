@@ -597,12 +597,17 @@ __global__ __launch_bounds__(PT) void k_pack(LabelRows a, PackArgs p) {
         if (r < live) {
             const int64_t row = !x ? r : SMALL ? s_list[r] : a.rows[r];
             constexpr int V = WIDE<T>;
+            const int64_t room = ((x ? a.n : p.w_rows) - 1 - row) * stride + p.dim - c;
+            wide_t<T> raw[8 / V];
 #pragma unroll
-            for (int k = 0; k < 8; k += V) {
+            for (int k = 0; k < 8 / V; ++k)
+                raw[k] = load_row<false>(src + row * stride + c + k * V, p.dim - c - k * V, room - k * V);
+#pragma unroll
+            for (int k = 0; k < 8 / V; ++k) {
                 float t[V];
-                load_row<false>(src + row * stride + c + k, p.dim - c - k, p.dim - c - k, t);
+                widen<false, T>(raw[k], p.dim - c - k * V, t);
 #pragma unroll
-                for (int j = 0; j < V; ++j) v[k + j] = t[j];
+                for (int j = 0; j < V; ++j) v[k * V + j] = t[j];
             }
         }
         bf16x8 o[PARTS];

@@ -63,23 +63,25 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(int64_t n, int dim, const T* __
             b[e][k] = 0.f;
         }
         if (c < dim) {
-            if (weight) load_row<FULL>(weight + c, dim - c, dim - c, w[e]);
-            if (bias) load_row<FULL>(bias + c, dim - c, dim - c, b[e]);
+            if (weight) widen<FULL, T>(load_row<FULL>(weight + c, dim - c, dim - c), dim - c, w[e]);
+            if (bias) widen<FULL, T>(load_row<FULL>(bias + c, dim - c, dim - c), dim - c, b[e]);
         }
     }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < n; r0 += (int64_t)gridDim.x * RPB) {
         const int64_t r = r0 + threadIdx.x / LPR;
         const bool live = r < n;  // a row past the end is computed from zeros and not stored
         const T* xr = x + r * xs;
+        wide_t<T> raw[EPL];
         float v[EPL][VEC];
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < EPL; ++e) {
             const int c = (e * LPR + l) * VEC;
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) v[e][k] = 0.f;
-            if (live && c < dim) load_row<FULL>(xr + c, dim - c, (n - 1 - r) * xs + dim - c, v[e]);
+            raw[e] = (T)0.f;
+            if (live && c < dim) raw[e] = load_row<FULL>(xr + c, dim - c, (n - 1 - r) * xs + dim - c);
         }
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) widen<FULL, T>(raw[e], dim - (e * LPR + l) * VEC, v[e]);
 #pragma unroll
         for (int e = 0; e < EPL; ++e)
 #pragma unroll
@@ -162,21 +164,26 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(int64_t n, int dim, const T* __
             w[e][k] = 1.f;
             aw[e][k] = ab[e][k] = 0.f;
         }
-        if (weight && c < dim) load_row<FULL>(weight + c, dim - c, dim - c, w[e]);
+        if (weight && c < dim) widen<FULL, T>(load_row<FULL>(weight + c, dim - c, dim - c), dim - c, w[e]);
     }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < n; r0 += (int64_t)gridDim.x * RPB) {
         const int64_t r = r0 + threadIdx.x / LPR;
         const bool live = r < n;
+        wide_t<T> rx[EPL], rg[EPL];
         float xv[EPL][VEC], gv[EPL][VEC];
 #pragma unroll
         for (int e = 0; e < EPL; ++e) {
             const int c = (e * LPR + l) * VEC;
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) xv[e][k] = gv[e][k] = 0.f;
+            rx[e] = rg[e] = (T)0.f;
             if (live && c < dim) {
-                load_row<FULL>(x + r * xs + c, dim - c, (n - 1 - r) * xs + dim - c, xv[e]);
-                load_row<FULL>(dy + r * dys + c, dim - c, (n - 1 - r) * dys + dim - c, gv[e]);
+                rx[e] = load_row<FULL>(x + r * xs + c, dim - c, (n - 1 - r) * xs + dim - c);
+                rg[e] = load_row<FULL>(dy + r * dys + c, dim - c, (n - 1 - r) * dys + dim - c);
             }
+        }
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            widen<FULL, T>(rx[e], dim - (e * LPR + l) * VEC, xv[e]);
+            widen<FULL, T>(rg[e], dim - (e * LPR + l) * VEC, gv[e]);
         }
         const float mean = live ? mean_in[r] : 0.f, rstd = live ? rstd_in[r] : 0.f;
         float sg = 0.f, sx = 0.f;
