@@ -21,7 +21,8 @@ namespace gs {
 namespace {
 
 constexpr int EB = 256;         // threads per block
-constexpr int RUN_TOKENS = 16;  // sorted positions a row group sums, all loaded at once
+constexpr int RUN_FEWEST = 16;  // sorted positions a row group sums, all loaded at once; twice that ...
+constexpr int64_t RUN_LONG = 400000;  // ... from this many positions on: fewer partial sums to join
 constexpr int JOIN_T = 1024;
 constexpr int FEW = 256;        // positions up to which one launch makes the gradient (a multiple of 64)
 
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, con
 // earlier block, and its last run where it goes on in the next (and began in
 // this one). tail_key[b]: that last run's key, or vocab; end_block[key]: the
 // block in which a run that came from an earlier block ends.
-template <class T, int LPR, bool FULL>
+template <class T, int LPR, bool FULL, int RUN_TOKENS>
 __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
     int n, int dim, int vocab, const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos,
     const T* __restrict__ dout, int64_t ds, float scale, T* __restrict__ dtable, int64_t ts,
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
     constexpr int G = NT / LPR;
     constexpr int BT = G * RUN_TOKENS;
     constexpr int VEC = WIDE<T>, CW = LPR * VEC;
-    constexpr int U = RUN_TOKENS;
+    constexpr int U = RUN_FEWEST;
     __shared__ uint32_t s_tok[BT], s_pos[BT];
     __shared__ uint32_t s_key[2 * G];  // per group: its first run's key and, if another, its last run's
     __shared__ float s_sum[2 * G][CW];
@@ -314,6 +315,20 @@ struct EmbedArgs {
     uint32_t *tail_key, *end_block;
 };
 
+template <class T, int LPR, bool FULL, int RUN_TOKENS>
+hipError_t embed_sums(const EmbedArgs& a, hipStream_t s) {
+    constexpr int BT = run_threads(LPR) / LPR * RUN_TOKENS;
+    const int nb = (int)((a.n + BT - 1) / BT);
+    const dim3 grid(nb, (a.dim + LPR * WIDE<T> - 1) / (LPR * WIDE<T>));
+    k_embed_runs<T, LPR, FULL, RUN_TOKENS><<<grid, run_threads(LPR), 0, s>>>(
+        (int)a.n, a.dim, a.vocab, a.keys, a.pos, (const T*)a.src, a.ss, a.scale, (T*)a.dst, a.ds, a.part, a.tail_key,
+        a.end_block);
+    if (nb > 1)
+        k_embed_join<T, LPR, FULL><<<grid, JOIN_T, 0, s>>>(a.dim, a.vocab, a.tail_key, a.end_block, a.part, a.scale,
+                                                          (T*)a.dst, a.ds);
+    return hipGetLastError();
+}
+
 template <class T, int LPR, bool FULL>
 hipError_t embed_rows(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
     if (pass == LOOKUP) {
@@ -329,16 +344,8 @@ hipError_t embed_rows(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
             (int)a.n, a.dim, a.vocab, a.ids, a.wide, a.scale, (const T*)a.src, a.ss, (T*)a.dst, a.ds);
         return hipGetLastError();
     }
-    constexpr int BT = run_threads(LPR) / LPR * RUN_TOKENS;
-    const int nb = (int)((a.n + BT - 1) / BT);
-    const dim3 grid(nb, (a.dim + LPR * WIDE<T> - 1) / (LPR * WIDE<T>));
-    k_embed_runs<T, LPR, FULL><<<grid, run_threads(LPR), 0, s>>>((int)a.n, a.dim, a.vocab, a.keys, a.pos, (const T*)a.src,
-                                                          a.ss, a.scale, (T*)a.dst, a.ds, a.part, a.tail_key,
-                                                          a.end_block);
-    if (nb > 1)
-        k_embed_join<T, LPR, FULL><<<grid, JOIN_T, 0, s>>>(a.dim, a.vocab, a.tail_key, a.end_block, a.part, a.scale,
-                                                    (T*)a.dst, a.ds);
-    return hipGetLastError();
+    return a.n < RUN_LONG ? embed_sums<T, LPR, FULL, RUN_FEWEST>(a, s)
+                          : embed_sums<T, LPR, FULL, 2 * RUN_FEWEST>(a, s);
 }
 
 // The fewest lanes that hold a row with one 16-byte access each, up to a wave.
@@ -372,7 +379,7 @@ hipError_t zero_rows(int rows, int dim, void* p, int64_t stride, char* totals, h
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // The fewest positions per block (64 lanes per row) bound the block count.
-int64_t max_blocks(int64_t n) { return (n + EB / 64 * RUN_TOKENS - 1) / (EB / 64 * RUN_TOKENS); }
+int64_t max_blocks(int64_t n) { return (n + EB / 64 * RUN_FEWEST - 1) / (EB / 64 * RUN_FEWEST); }
 
 }  // namespace
 
