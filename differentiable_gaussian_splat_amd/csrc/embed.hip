@@ -83,7 +83,7 @@ template <class T, int LPR, bool FULL>
 __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, const void* __restrict__ ids, bool wide,
                                                   float scale, const T* __restrict__ dout, int64_t ds,
                                                   T* __restrict__ dtable, int64_t ts) {
-    constexpr int VEC = WIDE<T>, U = 4;
+    constexpr int VEC = WIDE<T>, U = 8;
     __shared__ int s_id[FEW];
     for (int i = threadIdx.x; i < FEW; i += EB) s_id[i] = i < n ? row_index(ids, wide, i, vocab) : -1;
     __syncthreads();
@@ -91,8 +91,8 @@ __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, con
     const int wave = (int)(blockIdx.x * (EB / 64)) + (int)(threadIdx.x >> 6), waves = (int)gridDim.x * (EB / 64);
     for (int64_t v0 = (int64_t)wave * (64 / LPR); v0 < vocab; v0 += (int64_t)waves * (64 / LPR)) {
         const int row = (int)v0 + sub;  // of this lane group
-        // positions of the group's row, 64 at a time
-        for (int c = (lane % LPR) * VEC; c - (lane % LPR) * VEC < dim; c += LPR * VEC) {
+        const int c = (blockIdx.y * LPR + lane % LPR) * VEC;
+        {
             float acc[VEC];
 #pragma unroll
             for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
@@ -340,7 +340,8 @@ hipError_t embed_rows(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
     }
     if (pass == FEW_SUMS) {
         const int64_t want = (a.vocab + EB / LPR - 1) / (EB / LPR);
-        k_embed_few<T, LPR, FULL><<<(unsigned)(want < 2048 ? want : 2048), EB, 0, s>>>(
+        const dim3 grid((unsigned)(want < 2048 ? want : 2048), (a.dim + LPR * WIDE<T> - 1) / (LPR * WIDE<T>));
+        k_embed_few<T, LPR, FULL><<<grid, EB, 0, s>>>(
             (int)a.n, a.dim, a.vocab, a.ids, a.wide, a.scale, (const T*)a.src, a.ss, (T*)a.dst, a.ds);
         return hipGetLastError();
     }

@@ -76,9 +76,10 @@ struct Product {
     int out_dim, out_wide;
 };
 
-__device__ __forceinline__ float up_of(const Product& p, int row, int cnt) {
-    float u = p.dloss ? p.dloss[row] : 0.f;
-    if (p.dmean) u += p.dmean[0] / (float)cnt;
+// The upstream gradient of a labelled row's loss.
+__device__ __forceinline__ float up_of(const float* dmean, const float* dloss, int row, int cnt) {
+    float u = dloss ? dloss[row] : 0.f;
+    if (dmean) u += dmean[0] / (float)cnt;
     return u;
 }
 
@@ -332,7 +333,7 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
                             if (at == 32 * i + 8 * (e / 4) + e % 4 && lab >= 0) p.target[n] = acc[i][j][e];
             } else {
                 const float ref = row >= 0 ? p.lse[row] * LOG2E : 0.f;
-                const float up = row >= 0 ? up_of(p, row, cnt) : 0.f;
+                const float up = row >= 0 ? up_of(p.dmean, p.dloss, row, cnt) : 0.f;
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -639,6 +640,12 @@ __device__ __forceinline__ float2 lse_join(float2 a, float2 b) {
     return make_float2(m, a.y * fa + b.y * fb);
 }
 
+// exp(z - top) where top is a maximum that may be infinite: an entry equal to it counts 1 (+inf) or 0 (-inf).
+__device__ __forceinline__ float exp_share(float z, float top) {
+    if (!(top > -INFINITY)) return z != z ? z : 0.f;
+    return z == top ? 1.f : exp_diff(z, top);
+}
+
 constexpr int JR = 64;  // rows per block of the join
 constexpr int JT = 1024;
 
@@ -768,7 +775,7 @@ __global__ __launch_bounds__(256) void k_join_splits(SplitJoin a, SplitJoin b, i
 
 }  // namespace gs
 
-#include "fewlabels.hpp"
+#include "flatloss.hpp"
 
 namespace gs {
 
@@ -806,21 +813,39 @@ int splits_for(int64_t nk, int64_t share) {
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
+enum Side { NEITHER, LABELS, ROWS };
+
+// Which side is short enough for the flat kernels. Their gradients' operations
+// grow with the short side, the tiled products' cost with the next 128 of it.
+// float32 products (six of bfloat16) lose up to SHORT: 46272 x 896 x 64 with
+// gradients 0.51 ms flat, 0.68 tiled (x 65); 16 x 1024 x 65536 0.35 and 0.90.
+// bfloat16 ones win from 16 labels on (46272 x 896 x 20: 0.42 flat, 0.29
+// tiled), and over few rows unless all of it is small (16 x 32 x 1000: 29 us
+// flat, 33 tiled; 16 x 64 x 20000: 52 and 44).
+Side short_side(int64_t n, int dim, int vocab, bool half) {
+    const int most = half ? 16 : SHORT;
+    if (vocab <= most) return LABELS;
+    if (n > 0 && n <= most && (!half || (int64_t)vocab * dim <= 1 << 20)) return ROWS;
+    return NEITHER;
+}
+
 struct LossPlan {
     int parts, kp;
     int64_t np;                    // rows of x padded to the tile
     int64_t piece_f, piece_b;      // vocabulary rows per piece (multiples of 256)
     int tm_z, tm_d;                // row blocks per wave: over the vocabulary, over dim
     int split_dx, split_dw;
-    bool few;                      // few labels: no packing, no tiles
-    int few_tr, few_slabs, few_chunks;
+    Side shorter;                  // a short side: no packing, no tiles
+    int flat_tr, flat_slabs, flat_chunks;
     size_t g;
     size_t rows, place, count, done, block_count, xp, wp, part, target, state, block_sum, dz, dxp, dwp, total;
 };
 
-// Few labels: rounded up to the gradient kernel's sizes, and its columns per thread.
-int few_bucket(int vocab) { return vocab <= 4 ? 4 : vocab <= 8 ? 8 : vocab <= 16 ? 16 : vocab <= 32 ? 32 : 64; }
-int few_columns(int vocab) { return vocab <= 8 ? 4 : vocab <= 16 ? 2 : 1; }
+constexpr int ROW_BLOCKS = 512;  // blocks of the few rows' forward: slabs to join
+
+// The short side's rows rounded up to the gradient kernel's sizes, and its columns per thread.
+int few_bucket(int64_t vocab) { return vocab <= 4 ? 4 : vocab <= 8 ? 8 : vocab <= 16 ? 16 : vocab <= 32 ? 32 : 64; }
+int few_columns(int64_t vocab) { return vocab <= 8 ? 4 : vocab <= 16 ? 2 : 1; }
 
 LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     LossPlan L{};
@@ -856,19 +881,24 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     L.count = take(4);
     L.done = take(4);
     L.block_count = take((size_t)(L.np / LROWS + 1) * 4);
-    if (vocab <= FEW_LABELS) {
-        L.few = true;
-        const int cols = few_columns(vocab);
-        L.few_tr = 1;
-        while (L.few_tr < FT && L.few_tr * cols < dim) L.few_tr *= 2;
-        L.few_slabs = (dim + L.few_tr * cols - 1) / (L.few_tr * cols);
-        const int64_t most = 1024 / L.few_slabs < 64 ? 64 : 1024 / L.few_slabs > 256 ? 256 : 1024 / L.few_slabs;
-        const int64_t want = (n + FG - 1) / FG;
-        L.few_chunks = (int)(want < 1 ? 1 : want < most ? want : most);
+    L.shorter = short_side(n, dim, vocab, half);
+    if (L.shorter != NEITHER) {
+        const int64_t few = L.shorter == LABELS ? vocab : n, rows = L.shorter == LABELS ? n : vocab;
+        const int cols = few_columns(few);
+        L.flat_tr = 1;
+        while (L.flat_tr < FT && L.flat_tr * cols < dim) L.flat_tr *= 2;
+        L.flat_slabs = (dim + L.flat_tr * cols - 1) / (L.flat_tr * cols);
+        const int64_t most = 1024 / L.flat_slabs < 64 ? 64 : 1024 / L.flat_slabs > 256 ? 256 : 1024 / L.flat_slabs;
+        const int64_t want = (rows + FG - 1) / FG;
+        L.flat_chunks = (int)(want < 1 ? 1 : want < most ? want : most);
         L.block_sum = take((size_t)(L.np / FR + 1) * 8);
+        if (L.shorter == ROWS) {
+            L.part = take((size_t)ROW_BLOCKS * SHORT * 8);
+            L.target = take((size_t)SHORT * 4);
+        }
         if (backward) {
-            L.g = take((size_t)L.np * few_bucket(vocab) * 4);
-            L.dwp = take((size_t)L.few_chunks * vocab * L.kp * 4);
+            L.g = take((size_t)(rows > 0 ? rows : 1) * few_bucket(few) * 4);
+            L.dwp = take((size_t)L.flat_chunks * (few > 0 ? few : 1) * L.kp * 4);
         }
         L.total = o;
         return L;
@@ -1002,68 +1032,102 @@ Product product_base(const LabelLossArgs& a, const LossPlan& L, char* ws) {
     return p;
 }
 
+template <class T, bool FORWARD>
+void flat_logits(const FlatArgs& f, Side side, int64_t few, unsigned blocks, hipStream_t s) {
+    if (side == LABELS) {
+        if (few <= 32)
+            k_few_labels<T, 1, FORWARD><<<blocks, FT, 0, s>>>(f);
+        else
+            k_few_labels<T, 2, FORWARD><<<blocks, FT, 0, s>>>(f);
+    } else if (few <= 32) {
+        k_few_rows<T, 1, FORWARD><<<blocks, FT, 0, s>>>(f);
+    } else {
+        k_few_rows<T, 2, FORWARD><<<blocks, FT, 0, s>>>(f);
+    }
+}
+
 template <class T>
-hipError_t few_labels(const LabelLossArgs& a, const LossPlan& L, char* ws, bool forward, hipStream_t s) {
-    const LabelRows r = label_arrays(a, L, ws, forward);
-    list_rows(r, L, ws, s);
-    FewArgs f{};
+hipError_t flat_loss(const LabelLossArgs& a, const LossPlan& L, char* ws, bool forward, hipStream_t s) {
+    const bool few_labels = L.shorter == LABELS;
+    const int64_t few = few_labels ? a.vocab : a.n, rows = few_labels ? a.n : a.vocab;
+    FlatArgs f{};
     f.n = a.n;
     f.dim = a.dim;
     f.vocab = a.vocab;
     f.x = a.x;
     f.w = a.w;
-    f.labels = a.labels;
     f.xs = a.x_stride;
     f.ws = a.w_stride;
-    f.wide_labels = a.wide_labels;
-    f.rows = r.rows;
-    f.place = r.place;
-    f.count = r.count;
-    f.loss = a.loss;
-    f.lse = a.lse;
-    f.mean = a.mean;
-    f.done = r.done;
+    f.labels = label_arrays(a, L, ws, forward);
     f.count_out = a.count;
+    f.mean = a.mean;
     f.block_sum = (double*)(ws + L.block_sum);
+    f.part = (float2*)(ws + L.part);
+    f.target = (float*)(ws + L.target);
+    f.lse = a.lse;
     f.dmean = a.dmean;
     f.dloss = a.dloss;
-    const unsigned blocks = (unsigned)(a.n > 0 ? (a.n + FR - 1) / FR : 1);
+    f.g = (float*)(ws + L.g);
+    f.ldg = few_bucket(few);
+    if (few_labels) list_rows(f.labels, L, ws, s);
+    const int64_t tiles = rows > 0 ? (rows + FR - 1) / FR : 1;
     if (forward) {
-        if (a.vocab <= 32)
-            k_few_logits<T, 1, true><<<blocks, FT, 0, s>>>(f);
-        else
-            k_few_logits<T, 2, true><<<blocks, FT, 0, s>>>(f);
+        const unsigned blocks = (unsigned)(few_labels || tiles < ROW_BLOCKS ? tiles : ROW_BLOCKS);
+        flat_logits<T, true>(f, L.shorter, few, blocks, s);
+        if (!few_labels)
+            k_lse_join<<<1, JT, 0, s>>>((int)blocks, SHORT, f.part, f.target, f.labels.rows, f.labels.count, nullptr,
+                                        true, false, a.loss, a.lse, f.block_sum, f.labels.done, a.mean, a.count);
         return hipGetLastError();
     }
-    f.g = (float*)(ws + L.g);
-    f.ldg = few_bucket(a.vocab);
-    f.dx = a.dx;
-    f.dxs = a.dx_stride;
-    f.dw = a.dw ? (float*)(ws + L.dwp) : nullptr;
-    f.kp = L.kp;
-    f.chunk = (a.n + L.few_chunks - 1) / L.few_chunks;
-    if (a.vocab <= 32)
-        k_few_logits<T, 1, false><<<blocks, FT, 0, s>>>(f);
-    else
-        k_few_logits<T, 2, false><<<blocks, FT, 0, s>>>(f);
-    const dim3 grid(L.few_chunks, L.few_slabs);
-    switch (f.ldg) {
-        case 4: k_few_grads<T, 4, 4><<<grid, FT, 0, s>>>(f, L.few_tr); break;
-        case 8: k_few_grads<T, 8, 4><<<grid, FT, 0, s>>>(f, L.few_tr); break;
-        case 16: k_few_grads<T, 16, 2><<<grid, FT, 0, s>>>(f, L.few_tr); break;
-        case 32: k_few_grads<T, 32, 1><<<grid, FT, 0, s>>>(f, L.few_tr); break;
-        default: k_few_grads<T, 64, 1><<<grid, FT, 0, s>>>(f, L.few_tr); break;
+    flat_logits<T, false>(f, L.shorter, few, (unsigned)tiles, s);
+    FlatGrads g{};
+    g.rows = rows;
+    g.dim = a.dim;
+    g.kp = L.kp;
+    g.g = f.g;
+    g.ldg = f.ldg;
+    g.chunk = (rows + L.flat_chunks - 1) / L.flat_chunks;
+    void* dshort = few_labels ? a.dw : a.dx;
+    g.dshort = dshort ? (float*)(ws + L.dwp) : nullptr;
+    g.out_rows = (int)few;
+    if (few_labels) {
+        g.place = f.labels.place;
+        g.lp = a.x;
+        g.ls = a.x_stride;
+        g.sp = a.w;
+        g.ss = a.w_stride;
+        g.short_rows = a.vocab;
+        g.dlong = a.dx;
+        g.dls = a.dx_stride;
+    } else {
+        g.lp = a.w;
+        g.ls = a.w_stride;
+        g.sp = a.x;
+        g.ss = a.x_stride;
+        g.list = f.labels.rows;
+        g.count = f.labels.count;
+        g.dlong = a.dw;
+        g.dls = a.dw_stride;
     }
-    if (a.dw) {
+    const dim3 grid(L.flat_chunks, L.flat_slabs);
+    switch (g.ldg) {
+        case 4: k_flat_grads<T, 4, 4><<<grid, FT, 0, s>>>(g, L.flat_tr); break;
+        case 8: k_flat_grads<T, 8, 4><<<grid, FT, 0, s>>>(g, L.flat_tr); break;
+        case 16: k_flat_grads<T, 16, 2><<<grid, FT, 0, s>>>(g, L.flat_tr); break;
+        case 32: k_flat_grads<T, 32, 1><<<grid, FT, 0, s>>>(g, L.flat_tr); break;
+        default: k_flat_grads<T, 64, 1><<<grid, FT, 0, s>>>(g, L.flat_tr); break;
+    }
+    if (dshort) {
         SplitJoin j{}, none{};
-        j.rows = a.vocab;
-        j.splits = L.few_chunks;
-        j.acc = f.dw;
-        j.pacc = (int64_t)a.vocab * L.kp;
-        j.out = a.dw;
-        j.ldout = a.dw_stride;
-        j.blocks = a.vocab;
-        k_join_splits<T><<<j.blocks, 256, 0, s>>>(j, none, a.dim, L.kp, 1);
+        j.rows = few;
+        j.splits = L.flat_chunks;
+        j.acc = g.dshort;
+        j.pacc = few * L.kp;
+        j.place = few_labels ? nullptr : f.labels.place;
+        j.out = dshort;
+        j.ldout = few_labels ? a.dw_stride : a.dx_stride;
+        j.blocks = (int)few;
+        if (few > 0) k_join_splits<T><<<j.blocks, 256, 0, s>>>(j, none, a.dim, L.kp, 1);
     }
     return hipGetLastError();
 }
@@ -1072,7 +1136,7 @@ template <class T>
 hipError_t loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
     const LossPlan L = loss_plan(a.n, a.dim, a.vocab, PARTS == 1, false);
-    if (L.few) return few_labels<T>(a, L, ws, true, s);
+    if (L.shorter != NEITHER) return flat_loss<T>(a, L, ws, true, s);
     Packed pk{};
     hipError_t e = prepare<T>(a, L, ws, true, pk, s);
     if (e != hipSuccess) return e;
@@ -1107,7 +1171,7 @@ template <class T>
 hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
     const LossPlan L = loss_plan(a.n, a.dim, a.vocab, PARTS == 1, true);
-    if (L.few) return few_labels<T>(a, L, ws, false, s);
+    if (L.shorter != NEITHER) return flat_loss<T>(a, L, ws, false, s);
     Packed pk{};
     hipError_t e = prepare<T>(a, L, ws, false, pk, s);
     if (e != hipSuccess) return e;
