@@ -787,23 +787,32 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // Blocks a launch needs to fill the chip; products with fewer tiles split their depth.
 constexpr int FILL = 512;
+constexpr int FEW_TM = 1;
 
-// Row blocks per wave over the vocabulary: four (256 rows) where that makes
-// enough tiles, otherwise two.
-int tm_vocab(int64_t v, int64_t np) { return up(v, 256) / 256 * (np / BN) >= FILL / 2 ? 4 : 2; }
+// What m rows cost in tiles of 64 tm: the rows multiplied, weighted by what a
+// wave reads from LDS per multiplication (tm + 2 fragments for 2 tm of them).
+int64_t tile_cost(int64_t m, int tm) { return up(m, 64 * tm) * (tm + 2) * 6 / tm; }
 
-// Row blocks per wave over dim: the fewest rows multiplied, weighted by what a
-// wave reads from LDS per multiplication (TM + 2 fragments for 2 TM of them).
-int tm_dim(int64_t kp) {
-    int best = 1;
+// Row blocks per wave over the vocabulary: the cheapest of those that make
+// enough tiles, otherwise FEW_TM (short tiles: their epilogue is what there is to wait for).
+int tm_vocab(int64_t v, int64_t np) {
+    int best = FEW_TM;
     int64_t least = 0;
     for (int tm = 1; tm <= 4; ++tm) {
-        const int64_t cost = up(kp, 64 * tm) * (tm + 2) * 6 / tm;
-        if (tm == 1 || cost < least) {
+        if (up(v, 64 * tm) / (64 * tm) * (np / BN) < FILL / 2) continue;
+        if (least == 0 || tile_cost(v, tm) <= least) {
             best = tm;
-            least = cost;
+            least = tile_cost(v, tm);
         }
     }
+    return best;
+}
+
+// Row blocks per wave over dim (whose products split their depth to make enough tiles): the cheapest.
+int tm_dim(int64_t kp) {
+    int best = 1;
+    for (int tm = 2; tm <= 4; ++tm)
+        if (tile_cost(kp, tm) < tile_cost(kp, best)) best = tm;
     return best;
 }
 
@@ -832,7 +841,7 @@ Side short_side(int64_t n, int dim, int vocab, bool half) {
 struct LossPlan {
     int parts, kp;
     int64_t np;                    // rows of x padded to the tile
-    int64_t piece_f, piece_b;      // vocabulary rows per piece (multiples of 256)
+    int64_t piece_f, piece_b;      // vocabulary rows per piece (whole tiles)
     int tm_z, tm_d;                // row blocks per wave: over the vocabulary, over dim
     int split_dx, split_dw;
     Side shorter;                  // a short side: no packing, no tiles
@@ -852,19 +861,19 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     L.parts = half ? 1 : 3;
     L.kp = (int)up(dim, half ? 2 * KPAD : KPAD);
     L.np = up(n > 0 ? n : 1, BN);
-    const int64_t vp = up(vocab, 256);
-    auto piece = [&](int64_t budget) {  // vocabulary rows whose per-row cost fits the budget
-        const int64_t v = budget / L.np / 256 * 256;
-        return v < 256 ? 256 : v > vp ? vp : v;
+    L.tm_z = tm_vocab(vocab, L.np);
+    const int64_t unit = 64 * L.tm_z, vp = up(vocab, unit);
+    auto piece = [&](int64_t budget) {  // vocabulary rows whose per-row cost fits the budget, in whole tiles
+        const int64_t v = budget / L.np / unit * unit;
+        return v < unit ? unit : v > vp ? vp : v;
     };
-    L.piece_f = piece((int64_t)1 << 31);  // 8 bytes per 64 vocabulary rows: 256 MB
+    L.piece_f = piece((int64_t)1 << 30);  // 8 bytes per 32 vocabulary rows at least: 256 MB
     L.piece_b = piece(((int64_t)1 << 28) / L.parts);  // 2 bytes per part: 512 MB
-    L.tm_z = tm_vocab(backward ? L.piece_b : L.piece_f, L.np);
     L.tm_d = tm_dim(L.kp);
     const int64_t mt = up(L.kp, 64 * L.tm_d) / (64 * L.tm_d);
     // dx and dw run in one launch: their depths are split so that all blocks have about one share of it
     const int bk = step_depth(L.parts);
-    const int64_t nk_x = L.piece_b / bk, nk_w = L.np / bk;
+    const int64_t nk_x = (L.piece_b + bk - 1) / bk, nk_w = L.np / bk;
     const int64_t steps = mt * (L.np / BN) * nk_x + mt * (L.piece_b / BN) * nk_w;
     const int64_t least = half ? 8 : 4;  // steps a block should have (of six products each in float32)
     const int64_t share = steps / FILL > least ? steps / FILL : least;
@@ -910,7 +919,7 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
         L.dxp = take((size_t)L.split_dx * L.np * L.kp * 4);
         L.dwp = L.split_dw > 1 ? take((size_t)L.split_dw * L.piece_b * L.kp * 4) : 0;
     } else {
-        L.part = take((size_t)(L.piece_f / 64) * L.np * 8);
+        L.part = take((size_t)(L.piece_f / (32 * L.tm_z)) * L.np * 8);
         L.target = take((size_t)L.np * 4);
         L.state = take((size_t)L.np * 8);
         L.block_sum = take((size_t)(L.np / JR + 1) * 8);
@@ -935,14 +944,12 @@ void launch_product(int tm, const Product& p, hipStream_t s) {
     const unsigned grid = (unsigned)p.grid * p.splits;
     if (tm == 4)
         k_product<MODE, PARTS, 4, T><<<grid, GT, 0, s>>>(p);
+    else if (tm == 3)
+        k_product<MODE, PARTS, 3, T><<<grid, GT, 0, s>>>(p);
     else if (tm == 2)
         k_product<MODE, PARTS, 2, T><<<grid, GT, 0, s>>>(p);
-    else if constexpr (MODE == DX || MODE == DW) {
-        if (tm == 3)
-            k_product<MODE, PARTS, 3, T><<<grid, GT, 0, s>>>(p);
-        else
-            k_product<MODE, PARTS, 1, T><<<grid, GT, 0, s>>>(p);
-    }
+    else
+        k_product<MODE, PARTS, 1, T><<<grid, GT, 0, s>>>(p);
 }
 
 template <int PARTS, class T>
