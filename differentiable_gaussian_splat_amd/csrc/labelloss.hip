@@ -20,13 +20,14 @@
 // cost nothing and reach no sum.
 //
 // Types. bfloat16 rows are multiplied as they are, with float32 sums; dz is
-// rounded to bfloat16 (half a step, 2^-9 of each value, independent between
-// entries, so it stays below the rounding of dx and dw to the same type).
+// rounded to bfloat16 (half a step, at most 2^-8 of each value, independent
+// between entries, so that it stays below the rounding of dx and dw to the same type).
 // float32 rows are split into three bfloat16 parts (8 + 8 + 8 bits: the value
 // to 2^-24) and six products of parts are summed, smallest first; what is left
 // out is below 2^-24 of the product of magnitudes, a float32 product's own
 // rounding. The matrix units take bfloat16 sixteen times as fast as float32,
-// so six products are cheaper than one.
+// so six products are cheaper than one. Where one side is short the kernels of
+// flatloss.hpp take over.
 #include "elem.hpp"
 #include "launch.hpp"
 
@@ -827,8 +828,8 @@ enum Side { NEITHER, LABELS, ROWS };
 // Which side is short enough for the flat kernels. Their gradients' operations
 // grow with the short side, the tiled products' cost with the next 128 of it.
 // float32 products (six of bfloat16) lose up to SHORT: 46272 x 896 x 64 with
-// gradients 0.51 ms flat, 0.68 tiled (x 65); 16 x 1024 x 65536 0.35 and 0.90.
-// bfloat16 ones win from 16 labels on (46272 x 896 x 20: 0.42 flat, 0.29
+// gradients 0.38 ms flat, 0.59 tiled (x 65); 64 x 1024 x 65536 0.52 and 0.92.
+// bfloat16 ones win from 16 labels on (46272 x 896 x 20: 0.42 flat, 0.26
 // tiled), and over few rows unless all of it is small (16 x 32 x 1000: 29 us
 // flat, 33 tiled; 16 x 64 x 20000: 52 and 44).
 Side short_side(int64_t n, int dim, int vocab, bool half) {
@@ -854,7 +855,7 @@ constexpr int ROW_BLOCKS = 512;  // blocks of the few rows' forward: slabs to jo
 
 // The short side's rows rounded up to the gradient kernel's sizes, and its columns per thread.
 int few_bucket(int64_t vocab) { return vocab <= 4 ? 4 : vocab <= 8 ? 8 : vocab <= 16 ? 16 : vocab <= 32 ? 32 : 64; }
-int few_columns(int64_t vocab) { return vocab <= 8 ? 4 : vocab <= 16 ? 2 : 1; }
+int few_columns(int64_t vocab) { return vocab <= 8 ? 4 : 2; }
 
 LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     LossPlan L{};
@@ -896,7 +897,7 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
         const int cols = few_columns(few);
         L.flat_tr = 1;
         while (L.flat_tr < FT && L.flat_tr * cols < dim) L.flat_tr *= 2;
-        L.flat_slabs = (dim + L.flat_tr * cols - 1) / (L.flat_tr * cols);
+        L.flat_slabs = few <= 16 ? (dim + L.flat_tr * cols - 1) / (L.flat_tr * cols) : (dim + 127) / 128;
         const int64_t most = 1024 / L.flat_slabs < 64 ? 64 : 1024 / L.flat_slabs > 256 ? 256 : 1024 / L.flat_slabs;
         const int64_t want = (rows + FG - 1) / FG;
         L.flat_chunks = (int)(want < 1 ? 1 : want < most ? want : most);
@@ -1039,18 +1040,20 @@ Product product_base(const LabelLossArgs& a, const LossPlan& L, char* ws) {
     return p;
 }
 
+template <class T, int VT, bool FORWARD>
+void flat_logits(const FlatArgs& f, Side side, unsigned blocks, hipStream_t s) {
+    if (side == LABELS)
+        k_few_labels<T, VT, FORWARD><<<blocks, FT, 0, s>>>(f);
+    else
+        k_few_rows<T, VT, FORWARD><<<blocks, FT, 0, s>>>(f);
+}
+
 template <class T, bool FORWARD>
 void flat_logits(const FlatArgs& f, Side side, int64_t few, unsigned blocks, hipStream_t s) {
-    if (side == LABELS) {
-        if (few <= 32)
-            k_few_labels<T, 1, FORWARD><<<blocks, FT, 0, s>>>(f);
-        else
-            k_few_labels<T, 2, FORWARD><<<blocks, FT, 0, s>>>(f);
-    } else if (few <= 32) {
-        k_few_rows<T, 1, FORWARD><<<blocks, FT, 0, s>>>(f);
-    } else {
-        k_few_rows<T, 2, FORWARD><<<blocks, FT, 0, s>>>(f);
+    if constexpr (sizeof(T) == 4) {
+        if (few > 32) return flat_logits<T, 2, FORWARD>(f, side, blocks, s);
     }
+    flat_logits<T, 1, FORWARD>(f, side, blocks, s);
 }
 
 template <class T>
@@ -1093,7 +1096,7 @@ hipError_t flat_loss(const LabelLossArgs& a, const LossPlan& L, char* ws, bool f
     g.kp = L.kp;
     g.g = f.g;
     g.ldg = f.ldg;
-    g.chunk = (rows + L.flat_chunks - 1) / L.flat_chunks;
+    g.chunk = up((rows + L.flat_chunks - 1) / L.flat_chunks, FR);
     void* dshort = few_labels ? a.dw : a.dx;
     g.dshort = dshort ? (float*)(ws + L.dwp) : nullptr;
     g.out_rows = (int)few;
@@ -1117,12 +1120,17 @@ hipError_t flat_loss(const LabelLossArgs& a, const LossPlan& L, char* ws, bool f
         g.dls = a.dw_stride;
     }
     const dim3 grid(L.flat_chunks, L.flat_slabs);
-    switch (g.ldg) {
-        case 4: k_flat_grads<T, 4, 4><<<grid, FT, 0, s>>>(g, L.flat_tr); break;
-        case 8: k_flat_grads<T, 8, 4><<<grid, FT, 0, s>>>(g, L.flat_tr); break;
-        case 16: k_flat_grads<T, 16, 2><<<grid, FT, 0, s>>>(g, L.flat_tr); break;
-        case 32: k_flat_grads<T, 32, 1><<<grid, FT, 0, s>>>(g, L.flat_tr); break;
-        default: k_flat_grads<T, 64, 1><<<grid, FT, 0, s>>>(g, L.flat_tr); break;
+    if (g.ldg == 4)
+        k_flat_grads<T, 4, 4><<<grid, FT, 0, s>>>(g, L.flat_tr);
+    else if (g.ldg == 8)
+        k_flat_grads<T, 8, 4><<<grid, FT, 0, s>>>(g, L.flat_tr);
+    else if (g.ldg == 16)
+        k_flat_grads<T, 16, 2><<<grid, FT, 0, s>>>(g, L.flat_tr);
+    else if constexpr (sizeof(T) == 4) {
+        if (g.ldg == 32)
+            k_flat_products<1><<<grid, FT, 0, s>>>(g);
+        else
+            k_flat_products<2><<<grid, FT, 0, s>>>(g);
     }
     if (dshort) {
         SplitJoin j{}, none{};
