@@ -1660,7 +1660,8 @@ size_t radix_sort_scratch(int64_t n) {
     return align256(((size_t)RADIX_TOTAL_WORDS + 256 * nblocks) * sizeof(uint32_t));
 }
 
-// The first pass's keys, values and histogram: key = the index, or `rows` where it names no row.
+// The first pass's keys, values and histogram: key = the index; a position whose index names no row gets the last
+// row's key and INDEX_NONE in its value (a key of its own would cost a table of 2^8 or 2^16 rows a pass more).
 __global__ __launch_bounds__(RB) void k_index_keys(int n, int rows, const void* __restrict__ ids, bool wide, int bits,
                                                  uint32_t* __restrict__ keys, uint32_t* __restrict__ pos,
                                                  uint32_t* __restrict__ hist, uint32_t* __restrict__ tot) {
@@ -1680,9 +1681,9 @@ __global__ __launch_bounds__(RB) void k_index_keys(int n, int rows, const void* 
     for (int r = 0; r < RR; ++r) {
         const int p = p0 + (w * RR + r) * 64 + lane;
         if (p < n) {
-            const uint32_t key = kk[r] < 0 ? (uint32_t)rows : (uint32_t)kk[r];
+            const uint32_t key = kk[r] < 0 ? (uint32_t)rows - 1u : (uint32_t)kk[r];
             keys[p] = key;
-            pos[p] = (uint32_t)p;
+            pos[p] = (uint32_t)p | (kk[r] < 0 ? INDEX_NONE : 0u);
             atomicAdd(&s_h[w][key & mask], 1u);
         }
     }
@@ -1701,7 +1702,7 @@ hipError_t launch_index_sort(int n, int rows, const void* ids, bool wide, uint32
     uint32_t* rtot = reinterpret_cast<uint32_t*>(scratch);
     uint32_t* hist = rtot + RADIX_TOTAL_WORDS;
     int bits = 1;
-    while (bits < 32 && ((uint32_t)rows >> bits) != 0u) ++bits;
+    while (bits < 32 && (((uint32_t)rows - 1u) >> bits) != 0u) ++bits;
     const int passes = (bits + 7) / 8, per = (bits + passes - 1) / passes;
     k_index_keys<<<(n + RE - 1) / RE, RB, 0, s>>>(n, rows, ids, wide, per, keys[0], vals[0], hist, rtot);
     int cur = 0;

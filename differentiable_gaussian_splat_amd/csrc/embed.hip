@@ -172,14 +172,14 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
     for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
     bool lead = true;  // still in the group's first run
     for (int p = p0; p < p0 + RUN_TOKENS; p += U) {
-        if (s_tok[p] == none) break;  // sorted last: nothing follows
+        if (s_tok[p] == none) break;  // past the positions
         uint32_t kk[U];
         wide_t<T> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             kk[u] = s_tok[p + u];
             raw[u] = (T)0.f;
-            if (kk[u] != none && c < dim) {
+            if (kk[u] != none && c < dim && !(s_pos[p + u] & INDEX_NONE)) {
                 const int64_t row = s_pos[p + u];
                 raw[u] = load_row<FULL>(dout + row * ds + c, dim - c, (n - 1 - row) * ds + dim - c);
             }
