@@ -298,7 +298,7 @@ hipError_t scan(Load ld, Store st, int n, const u64* dcount, u64* partials, u64*
 //   k_radix_scatter: stable scatter with those offsets.
 constexpr int PIECE = 256;           // super-tile entries one wave walks in the per-tile passes
 constexpr int RB = 1024;             // threads per radix block (16 waves)
-constexpr int RE = 4096;             // elements per radix block
+constexpr int RE = 4096;             // elements per radix block (index sorts of few elements: RB)
 constexpr int RW = RB / 64;          // waves per radix block
 constexpr int RR = RE / RB;          // elements per thread
 constexpr int RT = 8;                // rows of the digit-total buffers
@@ -326,8 +326,10 @@ __device__ __forceinline__ uint32_t digit_excl_scan(uint32_t v, uint32_t* s_w) {
     return tid < 256 ? pre + x - v : 0u;
 }
 
+template <int RR>
 __global__ __launch_bounds__(RB) void k_radix_hist(const uint32_t* __restrict__ keys, int n, const u64* dcount, int shift, int bits,
                                                  uint32_t* __restrict__ hist, uint32_t* __restrict__ tot) {
+    constexpr int RE = RB * RR;
     __shared__ uint32_t s_h[RW][256];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     for (int k = tid; k < RW * 256; k += RB) (&s_h[0][0])[k] = 0u;
@@ -522,15 +524,15 @@ __device__ __forceinline__ void digit_bases(const uint32_t* __restrict__ tot, ui
 // piece table). bstart (nullable, INLINE only): block b owns elements
 // [bstart[b], bstart[b + 1]) (at most RE; the last block ends at the count)
 // instead of [b RE, b RE + RE).
-template <bool INLINE, class V>
+template <bool INLINE, class V, int RR>
 __global__ __launch_bounds__(RB) void k_radix_scatter(SrcMem<V> src, int n, const u64* dcount, int shift, int bits,
                                                     const uint32_t* __restrict__ offsets,
                                                     const uint32_t* __restrict__ dtot, uint32_t* __restrict__ spare,
                                                     PieceTable pt, const u64* __restrict__ bstart,
                                                     uint32_t* __restrict__ keys_out, V* __restrict__ vals_out) {
-    static_assert(sizeof(V) * RE >= 16 * RW * 64, "the waves' column sums fit in s_vals");
+    constexpr int RE = RB * RR, SUMS = 16 * RW * 64 / (int)sizeof(V);
     __shared__ uint32_t s_keys[RE];
-    __shared__ __align__(16) V s_vals[RE];  // INLINE: first the waves' column sums of hist, 256 words each
+    __shared__ __align__(16) V s_vals[RE > SUMS ? RE : SUMS];  // INLINE: first the waves' column sums of hist, 256 words each
     __shared__ uint32_t s_wcnt[RW][256];  // per-wave digit counts, then each wave's first slot per digit
     __shared__ uint32_t s_dstart[256];
     __shared__ uint32_t s_gbase[256];
@@ -656,29 +658,32 @@ constexpr int RADIX_INLINE_BLOCKS = 512;
 // bstart (nullable): the histogram and digit totals are already there, for
 // blocks of elements [bstart[b], bstart[b + 1]) (RADIX_INLINE_BLOCKS at most).
 // counted: they are already there for the usual blocks.
-template <class V>
+template <int PER = RR, class V>
 hipError_t radix_pass(SrcMem<V> src, int n, const u64* dcount, int shift, int bits, uint32_t* hist, uint32_t* rtot,
                       int pass, uint32_t* keys_out, V* vals_out, hipStream_t s, PieceTable pt = {},
                       const u64* bstart = nullptr, bool counted = false) {
-    const int nblocks = (n + RE - 1) / RE;
+    const int nblocks = (n + RB * PER - 1) / (RB * PER);
     if (nblocks == 0) return hipSuccess;
     uint32_t* tot = rtot + RT * 256 * (pass & 1);
     uint32_t* spare = rtot + RT * 256 * ((pass & 1) ^ 1);
     if (bstart && nblocks > RADIX_INLINE_BLOCKS) return hipErrorInvalidValue;
     if (!bstart && !counted)
-        k_radix_hist<<<nblocks, RB, 0, s>>>(src.keys, n, dcount, shift, bits, hist, tot);
+        k_radix_hist<PER><<<nblocks, RB, 0, s>>>(src.keys, n, dcount, shift, bits, hist, tot);
     if (nblocks <= RADIX_INLINE_BLOCKS) {
-        k_radix_scatter<true, V><<<nblocks, RB, 0, s>>>(src, n, dcount, shift, bits, hist, tot, spare, pt, bstart,
+        k_radix_scatter<true, V, PER><<<nblocks, RB, 0, s>>>(src, n, dcount, shift, bits, hist, tot, spare, pt, bstart,
                                                         keys_out, vals_out);
         return hipGetLastError();
     }
-    if (pt.pfirst)
-        k_radix_offsets<true><<<256, 64, 0, s>>>(nblocks, hist, tot, spare, pt.S, pt.sr, pt.pfirst, pt.npieces);
-    else
-        k_radix_offsets<false><<<256, 64, 0, s>>>(nblocks, hist, tot, spare, 0, nullptr, nullptr, nullptr);
-    k_radix_scatter<false, V><<<nblocks, RB, 0, s>>>(src, n, dcount, shift, bits, hist, nullptr, nullptr, {},
-                                                     nullptr, keys_out, vals_out);
-    return hipGetLastError();
+    if constexpr (PER == RR) {  // shorter blocks are for fewer
+        if (pt.pfirst)
+            k_radix_offsets<true><<<256, 64, 0, s>>>(nblocks, hist, tot, spare, pt.S, pt.sr, pt.pfirst, pt.npieces);
+        else
+            k_radix_offsets<false><<<256, 64, 0, s>>>(nblocks, hist, tot, spare, 0, nullptr, nullptr, nullptr);
+        k_radix_scatter<false, V, PER><<<nblocks, RB, 0, s>>>(src, n, dcount, shift, bits, hist, nullptr, nullptr, {},
+                                                              nullptr, keys_out, vals_out);
+        return hipGetLastError();
+    }
+    return hipErrorInvalidValue;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -1655,20 +1660,26 @@ hipError_t launch_bin_emit(int n, int P, int P1, int TX, int TY, const float* de
 
 static_assert(RADIX_TOTAL_WORDS == 2 * RT * 256, "two digit-total buffers");
 
+// Up to this many positions a block takes RB of them: four times the blocks, each a quarter as long (65536
+// positions: a scatter 7.0 -> 5.2 us); beyond, the blocks' sums over each other's counts outgrow that.
+constexpr int64_t SHORT_SORT = 256 * 1024;
+
 size_t radix_sort_scratch(int64_t n) {
-    const size_t nblocks = ((size_t)n + RE - 1) / RE;
+    const size_t short_blocks = ((size_t)(n < SHORT_SORT ? n : SHORT_SORT) + RB - 1) / RB;
+    const size_t nblocks = std::max(short_blocks, ((size_t)n + RE - 1) / RE);
     return align256(((size_t)RADIX_TOTAL_WORDS + 256 * nblocks) * sizeof(uint32_t));
 }
 
 // The first pass's keys, values and histogram: key = the index; a position whose index names no row gets the last
 // row's key and INDEX_NONE in its value (a key of its own would cost a table of 2^8 or 2^16 rows a pass more).
+template <int RR>
 __global__ __launch_bounds__(RB) void k_index_keys(int n, int rows, const void* __restrict__ ids, bool wide, int bits,
                                                  uint32_t* __restrict__ keys, uint32_t* __restrict__ pos,
                                                  uint32_t* __restrict__ hist, uint32_t* __restrict__ tot) {
     __shared__ uint32_t s_h[RW][256];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     for (int k = tid; k < RW * 256; k += RB) (&s_h[0][0])[k] = 0u;
-    const int p0 = blockIdx.x * RE;
+    const int p0 = blockIdx.x * RB * RR;
     const uint32_t mask = (1u << bits) - 1u;
     int kk[RR];
 #pragma unroll
@@ -1697,23 +1708,35 @@ __global__ __launch_bounds__(RB) void k_index_keys(int n, int rows, const void* 
     }
 }
 
-hipError_t launch_index_sort(int n, int rows, const void* ids, bool wide, uint32_t* const keys[2],
-                             uint32_t* const vals[2], char* scratch, int* sorted_at, hipStream_t s) {
+namespace {
+
+template <int PER>
+hipError_t index_sort(int n, int rows, const void* ids, bool wide, uint32_t* const keys[2], uint32_t* const vals[2],
+                      char* scratch, int* sorted_at, hipStream_t s) {
     uint32_t* rtot = reinterpret_cast<uint32_t*>(scratch);
     uint32_t* hist = rtot + RADIX_TOTAL_WORDS;
     int bits = 1;
     while (bits < 32 && (((uint32_t)rows - 1u) >> bits) != 0u) ++bits;
     const int passes = (bits + 7) / 8, per = (bits + passes - 1) / passes;
-    k_index_keys<<<(n + RE - 1) / RE, RB, 0, s>>>(n, rows, ids, wide, per, keys[0], vals[0], hist, rtot);
+    k_index_keys<PER><<<(n + RB * PER - 1) / (RB * PER), RB, 0, s>>>(n, rows, ids, wide, per, keys[0], vals[0], hist,
+                                                                     rtot);
     int cur = 0;
     for (int p = 0; p < passes; ++p, cur ^= 1) {
         const int b = min(per, bits - p * per);
-        hipError_t e = radix_pass(SrcMem<uint32_t>{keys[cur], vals[cur]}, n, nullptr, p * per, b, hist, rtot, p,
-                                  keys[cur ^ 1], vals[cur ^ 1], s, {}, nullptr, p == 0);
+        hipError_t e = radix_pass<PER>(SrcMem<uint32_t>{keys[cur], vals[cur]}, n, nullptr, p * per, b, hist, rtot, p,
+                                       keys[cur ^ 1], vals[cur ^ 1], s, {}, nullptr, p == 0);
         if (e != hipSuccess) return e;
     }
     *sorted_at = cur;
     return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_index_sort(int n, int rows, const void* ids, bool wide, uint32_t* const keys[2],
+                             uint32_t* const vals[2], char* scratch, int* sorted_at, hipStream_t s) {
+    return n <= SHORT_SORT ? index_sort<1>(n, rows, ids, wide, keys, vals, scratch, sorted_at, s)
+                           : index_sort<RR>(n, rows, ids, wide, keys, vals, scratch, sorted_at, s);
 }
 
 }  // namespace gs
