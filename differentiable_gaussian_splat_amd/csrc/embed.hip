@@ -13,6 +13,12 @@
 // is thus spread over as many blocks as any other half, there are no atomics,
 // and the sums are the same bit for bit from run to run. All sums are float32,
 // rounded once.
+//
+// A million rows of 64 float32 from a table of 16384, with the gradient: 187 us,
+// of it the lookup 61 (256 MB written, 4.2 TB/s of the 4.8 that a copy reaches),
+// the runs 78 (256 MB gathered row by row, 3.3 TB/s), the sort 36. 65536 rows of
+// 512 bfloat16 with two fifths of them one word: 84 us, the sort 18 of it, five
+// short launches bound by their latency.
 #include "elem.hpp"
 #include "launch.hpp"
 
@@ -24,7 +30,9 @@ constexpr int EB = 256;         // threads per block
 constexpr int RUN_FEWEST = 16;  // sorted positions a row group sums, all loaded at once; twice that ...
 constexpr int64_t RUN_LONG = 400000;  // ... from this many positions on: fewer partial sums to join
 constexpr int JOIN_T = 1024;
-constexpr int FEW = 256;        // positions up to which one launch makes the gradient (a multiple of 64)
+// Positions up to which one launch makes the gradient (a multiple of 64): 33 x 32 from 500 rows 3.5 us, 30 us by
+// the sort; a row that all positions name is summed by one lane group, 8 at a time, hence not for more.
+constexpr int FEW = 256;
 
 enum EmbedPass { LOOKUP, FEW_SUMS, RUN_SUMS };
 

@@ -183,6 +183,14 @@ constexpr int tile_elements(int tm, int parts) {
 // step and frees the one before it. Loads past the last step are made with an
 // empty extent (they bring zeros), which keeps the count of loads in flight
 // the same in every step.
+//
+// 8192 x 1024 x 65536 bfloat16: LSE 1.12 ms (0.98 PFLOP/s), DZ 1.28 (0.86),
+// DX and DW together 2.02 (1.09); a large library product reaches 1.25 to 1.49,
+// the matrix units alone on random data 1.84 (they are held by the chip's power:
+// 2.4 on zeros). The units are busy 52 to 56 % of the time at 1.8 GHz; LDS is
+// read without bank conflicts and 20 % of the time. 256 x 256 tiles (by eight
+// waves, or by four of 128 x 128), reads of the next fragments ahead of the
+// barrier, and raised priority of the products all measured within 3 %.
 template <int MODE, int PARTS, int TM, class T>
 __device__ __forceinline__ void product(const Product& p, int block, bf16* s_tiles) {
     constexpr bool TA = MODE == DX || MODE == DW, TB = MODE == DW;

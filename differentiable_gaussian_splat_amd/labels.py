@@ -18,6 +18,7 @@ above are autograd wrappers that allocate them. An index outside the table
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .raster import _check, load_library
 
@@ -177,7 +178,8 @@ def gs_label_loss_fwd(x, w, labels, loss, lse, mean, count, workspace, stream=No
     st = load_library().gs_label_loss_fwd(n, dim, w.shape[0], _DTYPES[x.dtype], x.data_ptr(), xs, w.data_ptr(), ws, ip,
                                           it, _vector("loss", loss, n, f32, dev), _vector("lse", lse, n, f32, dev),
                                           _vector("mean", mean, 1, f32, dev),
-                                          _vector("count", count, 1, torch.int32, dev), *_workspace_of(workspace), _stream(stream, dev))
+                                          _vector("count", count, 1, torch.int32, dev), *_workspace_of(workspace),
+                                          _stream(stream, dev))
     _check(st, "gs_label_loss_fwd")
 
 
@@ -223,6 +225,7 @@ class _EmbedFn(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         (ids,) = ctx.saved_tensors
         dout = _rows(dout)
@@ -253,6 +256,7 @@ class _LayerNormFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         dy = _rows(dy)
@@ -285,6 +289,7 @@ class _LabelLossFn(torch.autograd.Function):
         return mean.reshape(()), loss, count
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dmean, dloss, _):
         x, w, labels, lse = ctx.saved_tensors
         if dmean is None and dloss is None:

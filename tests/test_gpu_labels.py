@@ -350,7 +350,7 @@ ONE = lambda: torch.ones(1, device=DEV)
                                          (129, 65, 129), (300, 129, 2000), (1000, 64, 20), (513, 256, 777),
                                          (260, 512, 4099), (9000, 16, 130), (7000, 300, 3), (700, 1030, 8),
                                          (40_000, 5, 16), (4100, 96, 33), (100, 2100, 64), (3000, 4, 65), (64, 100, 3000),
-                                         (33, 1003, 515), (16, 40, 20_001), (3, 7, 66), (65, 20, 300), (20, 2000, 700)])
+                                         (33, 1003, 515), (16, 40, 20_001), (3, 7, 66), (65, 20, 300), (20, 2000, 700), (70, 5000, 150)])
 def test_loss(n, dim, vocab, dtype):
     x, w, labels, g = loss_inputs(n + vocab, n, dim, vocab, dtype, wide=bool(n % 2))
     check_loss(x, w, labels, dmean=ONE())
