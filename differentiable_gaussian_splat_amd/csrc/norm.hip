@@ -23,6 +23,10 @@
 #include "elem.hpp"
 #include "launch.hpp"
 
+// Products are rounded before they are subtracted (fused only where fmaf says
+// so): a difference that is zero in the formula, as dx of rows of one column, is zero.
+#pragma clang fp contract(off)
+
 namespace gs {
 
 namespace {

@@ -262,6 +262,16 @@ def test_norm_constant_rows_and_empty():
     assert (dw == 0).all() and (db == 0).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_norm_of_one_column(dtype):
+    """A row of one column has no variance: y is the bias, dx and dweight are zero, exactly."""
+    g = gen(14)
+    x, dy = randn(g, 500, 1, dtype=dtype), randn(g, 500, 1, dtype=dtype)
+    w, b = torch.full((1,), 1.3, dtype=dtype, device=DEV), torch.full((1,), -0.7, dtype=dtype, device=DEV)
+    y, dx = check_norm(x, w, b, dy)
+    assert (y == b).all() and (dx == 0).all()
+
+
 def test_norm_bad_row_stays_in_its_row():
     g = gen(13)
     x = randn(g, 20, 48)
