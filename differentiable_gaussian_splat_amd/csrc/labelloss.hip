@@ -21,7 +21,8 @@
 //
 // Types. bfloat16 rows are multiplied as they are, with float32 sums; dz is
 // rounded to bfloat16 (half a step, at most 2^-8 of each value, independent
-// between entries, so that it stays below the rounding of dx and dw to the same type).
+// between entries, so that it stays below the rounding of dx and dw to the same type;
+// of the label's entry, most of a row's gradient, the rest is kept and added to dx).
 // float32 rows are split into three bfloat16 parts (8 + 8 + 8 bits: the value
 // to 2^-24) and six products of parts are summed, smallest first; what is left
 // out is below 2^-24 of the product of magnitudes, a float32 product's own
@@ -68,6 +69,7 @@ struct Product {
     float* target;                // LSE: z at the label
     const float *lse, *dmean, *dloss;
     bf16* dz;                     // DZ: [parts][np][lddz]
+    float* rest;                  // DZ, one part: per row, what the label's entry lost to bfloat16
     int64_t lddz, pdz;
     float* acc;                   // DX, DW with splits: [split][rows][ldacc]
     int64_t ldacc, pacc;
@@ -347,12 +349,21 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) acc[i][j][e] = exp2_fast(fmaf(acc[i][j][e], LOG2E, -ref));
-                if (hit)
+                if (hit) {
+                    float own = 0.f;
+                    bool here = false;
 #pragma unroll
                     for (int i = 0; i < TM; ++i)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            acc[i][j][e] -= at == 32 * i + 8 * (e / 4) + e % 4 ? 1.f : 0.f;
+                        for (int e = 0; e < 16; ++e) {
+                            const bool is = at == 32 * i + 8 * (e / 4) + e % 4;
+                            acc[i][j][e] -= is ? 1.f : 0.f;
+                            own = is ? acc[i][j][e] : own;
+                            here = here || is;
+                        }
+                    own *= up;
+                    if (PARTS == 1 && here && lab >= 0) p.rest[n] = own - (float)(bf16)own;
+                }
                 // rows past the labelled ones have z = 0 and up = 0
                 if (edge)
 #pragma unroll
@@ -731,6 +742,7 @@ __global__ __launch_bounds__(JT) void k_lse_join(int slabs, int np, const float2
 }
 
 // out[r] = the splits' rows of acc added in order, through place (-1: a zero row) if given.
+// rest (nullable): per row of acc, a multiple of the row of w that the label names, added on top.
 struct SplitJoin {
     int64_t rows;
     int splits;
@@ -740,6 +752,10 @@ struct SplitJoin {
     void* out;
     int64_t ldout;
     int blocks;
+    const float* rest;
+    const void *labels, *w;
+    int wide, vocab;
+    int64_t ws;
 };
 
 // Two joins in one launch: the first a.blocks blocks do a, the others b.
@@ -765,7 +781,14 @@ __global__ __launch_bounds__(256) void k_join_splits(SplitJoin a, SplitJoin b, i
             }
         }
         T* o = static_cast<T*>(j.out) + r * j.ldout + c;
-        const float f[4] = {v.x, v.y, v.z, v.w};
+        float f[4] = {v.x, v.y, v.z, v.w};
+        if (j.rest && src >= 0) {
+            const T* w = static_cast<const T*>(j.w) + row_index(j.labels, j.wide, r, j.vocab) * j.ws + c;
+            const float rest = j.rest[src];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c + k < dim) f[k] = fmaf(rest, (float)w[k], f[k]);
+        }
         if (c + 4 <= dim) {
             typedef T vec __attribute__((ext_vector_type(4), aligned(sizeof(T))));
             vec t;
@@ -856,7 +879,7 @@ struct LossPlan {
     Side shorter;                  // a short side: no packing, no tiles
     int flat_tr, flat_slabs, flat_chunks;
     size_t g;
-    size_t rows, place, count, done, block_count, xp, wp, part, target, state, block_sum, dz, dxp, dwp, total;
+    size_t rows, place, count, done, block_count, xp, wp, part, target, state, block_sum, dz, rest, dxp, dwp, total;
 };
 
 constexpr int ROW_BLOCKS = 512;  // blocks of the few rows' forward: slabs to join
@@ -925,6 +948,7 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     L.wp = take((size_t)L.parts * vocab * L.kp * 2);
     if (backward) {
         L.dz = take((size_t)L.parts * L.np * L.piece_b * 2);
+        L.rest = take((size_t)L.np * 4);
         L.dxp = take((size_t)L.split_dx * L.np * L.kp * 4);
         L.dwp = L.split_dw > 1 ? take((size_t)L.split_dw * L.piece_b * L.kp * 4) : 0;
     } else {
@@ -1216,6 +1240,7 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         p.dz = dz;
         p.lddz = L.piece_b;
         p.pdz = L.np * L.piece_b;
+        p.rest = (float*)(ws + L.rest);
         set_grid(p, L.tm_z, mv, a.n);
         launch_product<DZ, PARTS, T>(L.tm_z, p, s);
         const bool last = v0 + L.piece_b >= a.vocab;
@@ -1244,6 +1269,14 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
                 jx.place = (const int32_t*)(ws + L.place);
                 jx.out = a.dx;
                 jx.ldout = a.dx_stride;
+                if (PARTS == 1) {
+                    jx.rest = p.rest;
+                    jx.labels = a.labels;
+                    jx.wide = a.wide_labels;
+                    jx.vocab = a.vocab;
+                    jx.w = a.w;
+                    jx.ws = a.w_stride;
+                }
             }
         }
         if (a.dw) {

@@ -367,6 +367,19 @@ def test_loss(n, dim, vocab, dtype):
     check_loss(x, w, labels, dloss=torch.rand(n, generator=g, device=DEV))
 
 
+def test_loss_keeps_what_the_label_entry_rounds_away():
+    """Rows whose gradient is mostly the label's entry, near -0.9: dx is off by little more than its own rounding
+    (a uniform rounding of a half step has a third of its square on average; twice that leaves room for dz's others)."""
+    x, w, labels, _ = loss_inputs(37, 300, 64, 101, BF16, missing=0.0)
+    dx = run_loss(x, w, labels, dmean=ONE())[4]
+    X, W = x.double(), w.double()
+    dz = torch.softmax(X @ W.t(), 1).scatter_add_(1, labels[:, None], torch.full((300, 1), -1.0, dtype=torch.float64,
+                                                                                device=DEV)) / 300
+    ref = dz @ W
+    own = (ref.to(BF16).double() - ref).norm() / ref.norm()
+    assert (dx.double() - ref).norm() / ref.norm() <= 1.25 * own
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 def test_loss_both_upstream_gradients(dtype):
     x, w, labels, g = loss_inputs(21, 200, 40, 333, dtype)
