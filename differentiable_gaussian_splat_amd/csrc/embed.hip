@@ -122,7 +122,8 @@ __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, con
                             const int i = i0 + __ffsll((unsigned long long)mine) - 1;
                             mine &= mine - 1;
                             if (c < dim)
-                                raw[u] = load_row<FULL>(dout + (int64_t)i * ds + c, dim - c, (n - 1 - i) * ds + dim - c);
+                                raw[u] = load_row<FULL>(dout + (int64_t)i * ds + c, dim - c,
+                                                        (n - 1 - i) * ds + dim - c);
                         }
                     }
 #pragma unroll
@@ -380,8 +381,8 @@ hipError_t zero_rows(int rows, int dim, void* p, int64_t stride, char* totals, h
     int lanes = 1;
     while (lanes < 64 && lanes * WIDE<T> < dim) lanes *= 2;
     const int64_t want = ((int64_t)rows * lanes + EB - 1) / EB;
-    k_zero_rows<T><<<(unsigned)(want < 4096 ? want : 4096), EB, 0, s>>>(rows, dim, lanes, (T*)p, stride, (uint32_t*)totals,
-                                                                 RADIX_TOTAL_WORDS);
+    k_zero_rows<T><<<(unsigned)(want < 4096 ? want : 4096), EB, 0, s>>>(rows, dim, lanes, (T*)p, stride,
+                                                                 (uint32_t*)totals, RADIX_TOTAL_WORDS);
     return hipGetLastError();
 }
 

@@ -290,7 +290,8 @@ __global__ __launch_bounds__(FT) void k_few_rows(FlatArgs a) {
     if (!FORWARD) return;
     float2 j = make_float2(top, sum);
 #pragma unroll
-    for (int off = TPS / 2; off > 0; off >>= 1) j = lse_join(j, make_float2(__shfl_xor(j.x, off), __shfl_xor(j.y, off)));
+    for (int off = TPS / 2; off > 0; off >>= 1)
+        j = lse_join(j, make_float2(__shfl_xor(j.x, off), __shfl_xor(j.y, off)));
     if (sub == 0 && s < cnt) a.part[(int64_t)blockIdx.x * SHORT + s] = j;
 }
 
@@ -358,7 +359,8 @@ template <class T, int VB, int C>
 __global__ __launch_bounds__(FT) void k_flat_grads(FlatGrads a, int tr) {
     __shared__ float s_g[FG][VB];
     __shared__ int s_place[FG];
-    __shared__ float s_red[VB * C * FT];  // sums of the waves (or their pairs), where several long rows are taken at once
+    // sums of the waves (or their pairs), where several long rows are taken at once
+    __shared__ float s_red[VB * C * FT];
     const int groups = FT / tr, grp = threadIdx.x / tr, t = threadIdx.x % tr;
     const int c = (blockIdx.y * tr + t) * C, left = a.dim - c;
     const int ns = a.count ? *a.count : a.short_rows;
@@ -544,8 +546,8 @@ __global__ __launch_bounds__(FT) void k_flat_products(FlatGrads a) {
             for (int r = 0; r < FR; r += 2)
 #pragma unroll
                 for (int t = 0; t < VT; ++t)
-                    sums[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(s_l[r + h][col], s_g[32 * t + l % 32][r + h], sums[t],
-                                                                  0, 0, 0);
+                    sums[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(s_l[r + h][col], s_g[32 * t + l % 32][r + h],
+                                                                  sums[t], 0, 0, 0);
         __syncthreads();
     }
     if (!a.dshort) return;

@@ -1207,9 +1207,9 @@ hipError_t loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         launch_product<LSE, PARTS, T>(L.tm_z, p, s);
         // every tile writes its slabs, so the last may lie beyond the vocabulary (an empty one)
         const int slabs = (int)(up(mv, 64 * L.tm_z) / (32 * L.tm_z));
-        k_lse_join<<<(unsigned)(a.n > 0 ? (a.n + JR - 1) / JR : 1), JT, 0, s>>>(slabs, (int)L.np, part, p.target, p.rows, p.count, state,
-                                                             v0 == 0, v0 + L.piece_f < a.vocab, a.loss, a.lse, bs,
-                                                             (int32_t*)(ws + L.done), a.mean, a.count);
+        k_lse_join<<<(unsigned)(a.n > 0 ? (a.n + JR - 1) / JR : 1), JT, 0, s>>>(
+            slabs, (int)L.np, part, p.target, p.rows, p.count, state, v0 == 0, v0 + L.piece_f < a.vocab, a.loss, a.lse,
+            bs, (int32_t*)(ws + L.done), a.mean, a.count);
     }
     return hipGetLastError();
 }

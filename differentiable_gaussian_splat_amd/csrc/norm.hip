@@ -351,8 +351,8 @@ hipError_t norm_rows(NormArgs& a, int cap, hipStream_t s) {
     a.blocks = (int)(want < cap ? want : cap);
     const T *x = (const T*)a.x, *w = (const T*)a.weight;
     if (a.backward)
-        k_norm_bwd<T, LPR, EPL, FULL><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, a.mean, a.rstd, (const T*)a.dy, a.dys,
-                                                        (T*)a.dx, a.dxs, a.part);
+        k_norm_bwd<T, LPR, EPL, FULL><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, a.mean, a.rstd, (const T*)a.dy,
+                                                        a.dys, (T*)a.dx, a.dxs, a.part);
     else
         k_norm_fwd<T, LPR, EPL, FULL><<<a.blocks, NB, 0, s>>>(a.n, a.dim, x, a.xs, w, (const T*)a.bias, a.eps, (T*)a.y,
                                                         a.ys, a.mean, a.rstd);

@@ -99,7 +99,8 @@ def check_embed(table, ids, dout, scale):
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 @pytest.mark.parametrize("n,dim,vocab", [(1, 1, 1), (1, 64, 5), (33, 32, 500), (64, 7, 3), (129, 8, 2), (1000, 24, 17),
-                                         (513, 65, 1000), (4097, 128, 255), (2050, 300, 256), (777, 1030, 70_000), (450_000, 9, 1000)])
+                                         (513, 65, 1000), (4097, 128, 255), (2050, 300, 256), (777, 1030, 70_000),
+                                         (450_000, 9, 1000)])
 def test_embed(n, dim, vocab, dtype):
     g = gen(n + dim)
     table, dout = randn(g, vocab, dim, dtype=dtype), randn(g, n, dim, dtype=dtype)
@@ -165,7 +166,8 @@ def test_embed_offsets_past_32_bits():
     dout = randn(gen(7), 5, dim, dtype=BF16)
     ws = ws_of(L.gs_embed_bwd_workspace_size(5, dim, vocab, BF16))
     L.gs_embed_bwd(ids, dout, table, ws, 1.0)
-    within("dtable", table[ids[1:]], torch.stack([dout[1], dout[2], dout[3], (dout[0].float() + dout[4].float()).to(BF16)]),
+    within("dtable", table[ids[1:]],
+           torch.stack([dout[1], dout[2], dout[3], (dout[0].float() + dout[4].float()).to(BF16)]),
            torch.zeros((), device=DEV, dtype=torch.float64))
     table[ids] = 0
     assert int(torch.count_nonzero(table.view(torch.int32))) == 0
@@ -359,8 +361,9 @@ ONE = lambda: torch.ones(1, device=DEV)
 @pytest.mark.parametrize("n,dim,vocab", [(1, 1, 1), (1, 64, 1000), (2, 8, 2), (48, 32, 1000), (128, 64, 128),
                                          (129, 65, 129), (300, 129, 2000), (1000, 64, 20), (513, 256, 777),
                                          (260, 512, 4099), (9000, 16, 130), (7000, 300, 3), (700, 1030, 8),
-                                         (40_000, 5, 16), (4100, 96, 33), (100, 2100, 64), (3000, 4, 65), (64, 100, 3000),
-                                         (33, 1003, 515), (16, 40, 20_001), (3, 7, 66), (65, 20, 300), (20, 2000, 700), (70, 5000, 150)])
+                                         (40_000, 5, 16), (4100, 96, 33), (100, 2100, 64), (3000, 4, 65),
+                                         (64, 100, 3000), (33, 1003, 515), (16, 40, 20_001), (3, 7, 66), (65, 20, 300),
+                                         (20, 2000, 700), (70, 5000, 150)])
 def test_loss(n, dim, vocab, dtype):
     x, w, labels, g = loss_inputs(n + vocab, n, dim, vocab, dtype, wide=bool(n % 2))
     check_loss(x, w, labels, dmean=ONE())
