@@ -152,8 +152,9 @@ hipError_t launch_adam_step(const AdamLr& lr, float beta1, float beta2, float ep
                             hipStream_t stream);
 
 // Positions 0..n-1 (n <= 2^30) sorted by the index they name, in order within an index, by the binning's radix
-// passes; those whose index names none of the rows stand among the last row's, marked INDEX_NONE. The sorted pairs end in keys[*sorted_at],
-// vals[*sorted_at]; the other buffers are overwritten. The scratch's first RADIX_TOTAL_WORDS words are zero on entry.
+// passes; those whose index names none of the rows stand among the last row's, marked INDEX_NONE. The sorted pairs
+// end in keys[*sorted_at], vals[*sorted_at]; the other buffers are overwritten. The scratch's first RADIX_TOTAL_WORDS
+// words are zero on entry.
 constexpr int RADIX_TOTAL_WORDS = 4096;
 constexpr uint32_t INDEX_NONE = 0x80000000u;
 size_t radix_sort_scratch(int64_t n);

@@ -109,6 +109,20 @@ def test_embed(n, dim, vocab, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("skew", [0.0, 3.0])
+@pytest.mark.parametrize("n,dim,vocab", [(257, 2, 5), (258, 12, 70_000), (511, 65, 300), (1023, 600, 31), (4095, 1, 4096),
+                                         (8191, 40, 1), (8192, 9, 2000), (8193, 9, 2000), (16_385, 7, 40)])
+def test_embed_ties(n, dim, vocab, skew, dtype):
+    """Runs of equal indices of all lengths, within and across groups and blocks, and positions that name no row."""
+    g = gen(n + dim)
+    table, dout = randn(g, vocab, dim, dtype=dtype), randn(g, n, dim, dtype=dtype)
+    ids = (torch.rand(n, generator=g, device=DEV) ** (1 + skew) * (vocab + 1)).long() - 1
+    check_embed(table, ids, dout, 0.5)
+    once, again = run_embed(table, ids, dout, 0.5)[1], run_embed(table, ids, dout, 0.5)[1]
+    assert torch.equal(once, again)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 def test_embed_long_runs(dtype):
     """One code that most rows name, runs that end at block borders, a code per row."""
     g = gen(3)
