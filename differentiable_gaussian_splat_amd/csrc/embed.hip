@@ -27,8 +27,13 @@ namespace gs {
 namespace {
 
 constexpr int EB = 256;         // threads per block
-constexpr int RUN_FEWEST = 16;  // sorted positions a row group sums, all loaded at once; twice that ...
+constexpr int RUN_USUAL = 16;  // sorted positions a row group sums, all loaded at once; twice that ...
 constexpr int64_t RUN_LONG = 400000;  // ... from this many positions on: fewer partial sums to join
+// Where there are few blocks, a group's sums one after the other take the time, so it has fewer, up to RUN_SHORT
+// positions (3487 x 2 bf16 10.5 us against 16, 300 x 64 5.3 and a join of 2.7 against 6.8, 8192 x 64 float32 4.9
+// against 5.7; 32768 x 500 would take 17 and a join of 11 against 16 and 4.6).
+constexpr int RUN_FEW = 4;
+constexpr int64_t RUN_SHORT = 8192;
 constexpr int JOIN_T = 1024;
 // Positions up to which one launch makes the gradient (a multiple of 64): 33 x 32 from 500 rows 3.5 us, 30 us by
 // the sort; a row that all positions name is summed by one lane group, 8 at a time, hence not for more.
@@ -201,6 +206,21 @@ __global__ __launch_bounds__(EB) void k_embed_few(int n, int dim, int vocab, con
     }
 }
 
+// The first `left` of four columns.
+template <class T>
+__device__ __forceinline__ void store_four(T* p, int left, float4 v) {
+    typedef T vec __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+    if (left >= 4) {
+        vec t;
+        t[0] = (T)v.x, t[1] = (T)v.y, t[2] = (T)v.z, t[3] = (T)v.w;
+        *reinterpret_cast<vec*>(p) = t;
+    } else {
+        p[0] = (T)v.x;
+        if (left > 1) p[1] = (T)v.y;
+        if (left > 2) p[2] = (T)v.z;
+    }
+}
+
 // Sums of equal-key runs. Block b (of column chunk blockIdx.y) takes the sorted
 // positions [b BT, (b + 1) BT), group g of LPR lanes RUN_TOKENS of them. part
 // holds two rows of dim per block: the block's first run where it began in an
@@ -216,17 +236,17 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
     constexpr int G = NT / LPR;
     constexpr int BT = G * RUN_TOKENS;
     constexpr int VEC = WIDE<T>, CW = LPR * VEC;
-    constexpr int U = RUN_FEWEST;
+    constexpr int U = RUN_TOKENS < RUN_USUAL ? RUN_TOKENS : RUN_USUAL;
     __shared__ uint32_t s_tok[BT], s_pos[BT];
-    __shared__ uint32_t s_key[2 * G];  // per group: its first run's key and, if another, its last run's
-    __shared__ float s_sum[2 * G][CW];
+    __shared__ uint32_t s_key[2 * G + 4];  // per group: its first run's key and its last run's, if one, the same
+    __shared__ alignas(16) float s_sum[2 * G][CW];
     const uint32_t none = (uint32_t)vocab;
     const int g = threadIdx.x / LPR, l = threadIdx.x % LPR;
     const int c0 = blockIdx.y * CW, c = c0 + l * VEC;
     const int b0 = blockIdx.x * BT, b1 = min(n, b0 + BT);
     for (int i = threadIdx.x; i < BT; i += NT) {
         s_tok[i] = b0 + i < b1 ? keys[b0 + i] : none;
-        s_pos[i] = b0 + i < b1 ? pos[b0 + i] : 0u;
+        s_pos[i] = b0 + i < b1 ? pos[b0 + i] : INDEX_NONE;
     }
     const uint32_t before = b0 > 0 ? keys[b0 - 1] : none;
     const uint32_t after = b1 < n ? keys[b1] : none;
@@ -239,18 +259,21 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
     bool lead = true;  // still in the group's first run
+#pragma unroll 1
     for (int p = p0; p < p0 + RUN_TOKENS; p += U) {
         if (s_tok[p] == none) break;  // past the positions
-        uint32_t kk[U];
+        uint32_t kk[U], at[U];
         wide_t<T> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             kk[u] = s_tok[p + u];
+            at[u] = s_pos[p + u];  // past the positions: INDEX_NONE
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             raw[u] = (T)0.f;
-            if (kk[u] != none && c < dim && !(s_pos[p + u] & INDEX_NONE)) {
-                const int64_t row = s_pos[p + u];
-                raw[u] = load_row<FULL>(dout + row * ds + c, dim - c, (n - 1 - row) * ds + dim - c);
-            }
+            if (c < dim && !(at[u] & INDEX_NONE))
+                raw[u] = load_row<FULL>(dout + at[u] * ds + c, dim - c, (n - 1 - (int)at[u]) * ds + dim - c);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -275,48 +298,54 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
         }
     }
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) s_sum[2 * g + (lead ? 0 : 1)][l * VEC + k] = acc[k];
+    for (int k = 0; k < VEC; ++k) {
+        s_sum[2 * g + 1][l * VEC + k] = lead ? 0.f : acc[k];
+        if (lead) s_sum[2 * g][l * VEC + k] = acc[k];
+    }
     if (l == 0) {
         s_key[2 * g] = first;
-        s_key[2 * g + 1] = lead ? none : cur;
+        s_key[2 * g + 1] = cur;
     }
+    if (threadIdx.x < 4) s_key[2 * G + threadIdx.x] = none;
     __syncthreads();
 
-    // the groups' first and last runs in order, one thread per column
-    for (int j = threadIdx.x; j < CW; j += NT) {
-        const bool col = c0 + j < dim;
-        uint32_t run = none;
-        float sum = 0.f;
-        bool open = false;      // the run began in an earlier block
-        bool has_tail = false;  // the block's last run goes on and began here
-        auto close = [&](bool goes_on) {
-            if (run == none) return;
-            if (open) {
-                if (col) part[(size_t)blockIdx.x * 2 * dim + c0 + j] = sum;
-                if (!goes_on && j == 0 && blockIdx.y == 0) end_block[run] = blockIdx.x;
-            } else if (goes_on) {
-                if (col) part[((size_t)blockIdx.x * 2 + 1) * dim + c0 + j] = sum;
-                has_tail = true;
-            } else if (col) {
-                dtable[(int64_t)run * ts + c0 + j] = (T)(sum * scale);
+    // one thread per run and four columns: the sums of the groups that hold it, in order
+    for (int i = threadIdx.x; i < 2 * G * (CW / 4); i += NT) {
+        const int e = i / (CW / 4), j = i % (CW / 4) * 4;
+        const uint32_t run = s_key[e];
+        if (run == none || (e > 0 && s_key[e - 1] == run)) continue;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        int f = e;
+        for (bool same = true; same; f += 4) {
+            uint32_t key[4];
+            float4 x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                key[u] = s_key[f + u];
+                x[u] = *reinterpret_cast<const float4*>(&s_sum[min(f + u, 2 * G - 1)][j]);
             }
-        };
-        bool any = false;
-        for (int e = 0; e < 2 * G; ++e) {
-            const uint32_t key = s_key[e];
-            const float x = s_sum[e][j];
-            if (key == none) continue;
-            if (key != run) {
-                close(false);
-                open = !any && key == before;
-                any = true;
-                run = key;
-                sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                same = same && key[u] == run;
+                sum.x += same ? x[u].x : 0.f;
+                sum.y += same ? x[u].y : 0.f;
+                sum.z += same ? x[u].z : 0.f;
+                sum.w += same ? x[u].w : 0.f;
             }
-            sum += x;
         }
-        close(run == after);
-        if (j == 0 && blockIdx.y == 0) tail_key[blockIdx.x] = has_tail ? run : none;
+        // the block's last run is its last position's
+        const bool last = run == s_tok[b1 - 1 - b0], open = e == 0 && run == before, goes_on = last && run == after;
+        const int left = dim - (c0 + j);
+        if (j == 0 && blockIdx.y == 0) {
+            if (open && !goes_on) end_block[run] = blockIdx.x;
+            if (last) tail_key[blockIdx.x] = goes_on && !open ? run : none;
+        }
+        if (left <= 0) continue;
+        if (open || goes_on)
+            store_four(part + ((size_t)blockIdx.x * 2 + (open ? 0 : 1)) * dim + c0 + j, left, sum);
+        else
+            store_four(dtable + (int64_t)run * ts + c0 + j, left,
+                       make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale));
     }
 }
 
@@ -413,8 +442,9 @@ hipError_t embed_rows(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
             (int)a.n, a.dim, a.vocab, a.ids, a.wide, a.scale, (const T*)a.src, a.ss, (T*)a.dst, a.ds);
         return hipGetLastError();
     }
-    return a.n < RUN_LONG ? embed_sums<T, LPR, FULL, RUN_FEWEST>(a, s)
-                          : embed_sums<T, LPR, FULL, 2 * RUN_FEWEST>(a, s);
+    return a.n <= RUN_SHORT  ? embed_sums<T, LPR, FULL, RUN_FEW>(a, s)
+           : a.n < RUN_LONG ? embed_sums<T, LPR, FULL, RUN_USUAL>(a, s)
+                            : embed_sums<T, LPR, FULL, 2 * RUN_USUAL>(a, s);
 }
 
 // The fewest lanes that hold a row with one 16-byte access each, up to a wave.
@@ -456,7 +486,10 @@ hipError_t zero_rows(const EmbedArgs& a, uint32_t* keys, uint32_t* pos, char* to
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // The fewest positions per block (64 lanes per row) bound the block count.
-int64_t max_blocks(int64_t n) { return (n + EB / 64 * RUN_FEWEST - 1) / (EB / 64 * RUN_FEWEST); }
+int64_t max_blocks(int64_t n) {
+    const int64_t per = EB / 64 * (n <= RUN_SHORT ? RUN_FEW : RUN_USUAL);
+    return (n + per - 1) / per;
+}
 
 }  // namespace
 
