@@ -4,17 +4,17 @@
 //   dT_v  = s sum_{i: ids_i = v} dout_i
 //
 // The lookup is bound by the rows it reads and writes. The gradient sorts the
-// positions by their index (the radix sort of the tile binning), so that a
-// row's contributions stand side by side: blocks then sum runs of equal
-// indices over a fixed number of sorted positions each, write the rows whose
-// run lies inside the block, and leave the first and last run, where it goes
-// on in a neighbouring block, as a partial sum. A last launch adds the partial
-// sums of each such row in block order. A row that half of the positions name
-// is thus spread over as many blocks as any other half, there are no atomics,
-// and the sums are the same bit for bit from run to run. All sums are float32,
-// rounded once.
+// positions by their index (the radix sort of the tile binning; up to 8192 by
+// ranking each among all), so that a row's contributions stand side by side:
+// blocks then sum runs of equal indices over a fixed number of sorted positions
+// each, write the rows whose run lies inside the block, and leave the first and
+// last run, where it goes on in a neighbouring block, as a partial sum. A last
+// launch adds the partial sums of each such row in block order. A row that half
+// of the positions name is thus spread over as many blocks as any other half,
+// there are no atomics, and the sums are the same bit for bit from run to run.
+// All sums are float32, rounded once.
 //
-// A million rows of 64 float32 from a table of 16384, with the gradient: 187 us,
+// A million rows of 64 float32 from a table of 16384, with the gradient: 186 us,
 // of it the lookup 61 (256 MB written, 4.2 TB/s of the 4.8 that a copy reaches),
 // the runs 78 (256 MB gathered row by row, 3.3 TB/s), the sort 36. 65536 rows of
 // 512 bfloat16 with two fifths of them one word: 84 us, the sort 18 of it, five

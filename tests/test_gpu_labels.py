@@ -110,8 +110,9 @@ def test_embed(n, dim, vocab, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 @pytest.mark.parametrize("skew", [0.0, 3.0])
-@pytest.mark.parametrize("n,dim,vocab", [(257, 2, 5), (258, 12, 70_000), (511, 65, 300), (1023, 600, 31), (4095, 1, 4096),
-                                         (8191, 40, 1), (8192, 9, 2000), (8193, 9, 2000), (16_385, 7, 40)])
+@pytest.mark.parametrize("n,dim,vocab", [(257, 2, 5), (258, 12, 70_000), (511, 65, 300), (1023, 600, 31),
+                                         (4095, 1, 4096), (8191, 40, 1), (8192, 9, 2000), (8193, 9, 2000),
+                                         (16_385, 7, 40)])
 def test_embed_ties(n, dim, vocab, skew, dtype):
     """Runs of equal indices of all lengths, within and across groups and blocks, and positions that name no row."""
     g = gen(n + dim)
