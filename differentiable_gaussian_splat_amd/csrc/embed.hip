@@ -12,7 +12,8 @@
 // launch adds the partial sums of each such row in block order. A row that half
 // of the positions name is thus spread over as many blocks as any other half,
 // there are no atomics, and the sums are the same bit for bit from run to run.
-// All sums are float32, rounded once.
+// All sums are float32, rounded once. The vocabulary loss sums weighed rows by
+// label in the same way (WeighedRows).
 //
 // A million rows of 64 float32 from a table of 16384, with the gradient: 186 us,
 // of it the lookup 61 (256 MB written, 4.2 TB/s of the 4.8 that a copy reaches),
@@ -226,27 +227,40 @@ __device__ __forceinline__ void store_four(T* p, int left, float4 v) {
 // holds two rows of dim per block: the block's first run where it began in an
 // earlier block, and its last run where it goes on in the next (and began in
 // this one). tail_key[b]: that last run's key, or vocab; end_block[key]: the
-// block in which a run that came from an earlier block ends.
-template <class T, int LPR, bool FULL, int RUN_TOKENS>
+// block in which a run that came from an earlier block ends. WEIGHED: the sums
+// of w instead; a run's row of them is numbered by one of its positions.
+template <class T, int LPR, bool FULL, int RUN_TOKENS, bool WEIGHED>
 __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
     int n, int dim, int vocab, const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos,
     const T* __restrict__ dout, int64_t ds, float scale, T* __restrict__ dtable, int64_t ts,
-    float* __restrict__ part, uint32_t* __restrict__ tail_key, uint32_t* __restrict__ end_block) {
+    float* __restrict__ part, uint32_t* __restrict__ tail_key, uint32_t* __restrict__ end_block, WeighedRows w) {
     constexpr int NT = run_threads(LPR);
     constexpr int G = NT / LPR;
     constexpr int BT = G * RUN_TOKENS;
     constexpr int VEC = WIDE<T>, CW = LPR * VEC;
     constexpr int U = RUN_TOKENS < RUN_USUAL ? RUN_TOKENS : RUN_USUAL;
     __shared__ uint32_t s_tok[BT], s_pos[BT];
+    __shared__ float s_weight[WEIGHED ? BT : 1];
     __shared__ uint32_t s_key[2 * G + 4];  // per group: its first run's key and its last run's, if one, the same
     __shared__ alignas(16) float s_sum[2 * G][CW];
     const uint32_t none = (uint32_t)vocab;
     const int g = threadIdx.x / LPR, l = threadIdx.x % LPR;
     const int c0 = blockIdx.y * CW, c = c0 + l * VEC;
     const int b0 = blockIdx.x * BT, b1 = min(n, b0 + BT);
+    if (WEIGHED && (keys[b1 - 1] < w.first || keys[b0] >= w.last)) {
+        if (threadIdx.x == 0 && blockIdx.y == 0) tail_key[blockIdx.x] = none;
+        return;
+    }
+    auto taken = [&](uint32_t key) { return !WEIGHED || (key >= w.first && key < w.last); };
     for (int i = threadIdx.x; i < BT; i += NT) {
-        s_tok[i] = b0 + i < b1 ? keys[b0 + i] : none;
-        s_pos[i] = b0 + i < b1 ? pos[b0 + i] : INDEX_NONE;
+        const uint32_t key = b0 + i < b1 ? keys[b0 + i] : none;
+        uint32_t at = b0 + i < b1 ? pos[b0 + i] : INDEX_NONE;
+        if constexpr (WEIGHED) {
+            at = !(at & INDEX_NONE) && taken(key) ? (uint32_t)w.place[at] : INDEX_NONE;
+            s_weight[i] = at & INDEX_NONE ? 0.f : w.weight[at];
+        }
+        s_tok[i] = key;
+        s_pos[i] = at;
     }
     const uint32_t before = b0 > 0 ? keys[b0 - 1] : none;
     const uint32_t after = b1 < n ? keys[b1] : none;
@@ -282,10 +296,19 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) s_sum[2 * g][l * VEC + k] = acc[k];
                     lead = false;
-                } else if (c < dim) {  // a run between two others of the group is whole
+                } else if (c < dim && taken(cur)) {  // a run between two others of the group is whole
+                    if constexpr (WEIGHED) {
+                        const int64_t to = b0 + p + u - 1;  // its last position
+                        if (c == 0) w.slot[cur] = (int32_t)to + 1;
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) acc[k] *= scale;
-                    store_row<FULL>(dtable + (int64_t)cur * ts + c, dim - c, acc);
+                        for (int k = 0; k < VEC; k += 4)
+                            store_four(w.sums + to * w.ld + c + k, 4,
+                                       make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) acc[k] *= scale;
+                        store_row<FULL>(dtable + (int64_t)cur * ts + c, dim - c, acc);
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
@@ -294,7 +317,7 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
             float v[VEC];
             widen<true, T>(raw[u], dim - c, v);  // sums of what is behind the row are not stored
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) acc[k] += v[k];
+            for (int k = 0; k < VEC; ++k) acc[k] = WEIGHED ? fmaf(s_weight[p + u], v[k], acc[k]) : acc[k] + v[k];
         }
     }
 #pragma unroll
@@ -334,15 +357,21 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
             }
         }
         // the block's last run is its last position's
-        const bool last = run == s_tok[b1 - 1 - b0], open = e == 0 && run == before, goes_on = last && run == after;
+        const bool last = run == s_tok[b1 - 1 - b0], open = e == 0 && run == before && taken(run),
+                   goes_on = last && run == after && taken(run);
         const int left = dim - (c0 + j);
         if (j == 0 && blockIdx.y == 0) {
             if (open && !goes_on) end_block[run] = blockIdx.x;
             if (last) tail_key[blockIdx.x] = goes_on && !open ? run : none;
         }
-        if (left <= 0) continue;
+        if (left <= 0 || !taken(run)) continue;
+        // of the run's positions: its group's first, or last
+        const int64_t to = b0 + (e % 2 == 0 ? e / 2 * RUN_TOKENS : min(e / 2 * RUN_TOKENS + RUN_TOKENS, b1 - b0) - 1);
+        if (WEIGHED && !open && !goes_on && c0 + j == 0) w.slot[run] = (int32_t)to + 1;
         if (open || goes_on)
             store_four(part + ((size_t)blockIdx.x * 2 + (open ? 0 : 1)) * dim + c0 + j, left, sum);
+        else if constexpr (WEIGHED)
+            store_four(w.sums + to * w.ld + c0 + j, left, sum);
         else
             store_four(dtable + (int64_t)run * ts + c0 + j, left,
                        make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale));
@@ -352,11 +381,11 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
 // Rows whose run crosses blocks: the last run of block b, then the first runs
 // of the blocks after it up to the one where it ends, a contiguous share per
 // row group, the groups joined in order.
-template <class T, int LPR, bool FULL>
+template <class T, int LPR, bool FULL, bool WEIGHED>
 __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const uint32_t* __restrict__ tail_key,
                                                        const uint32_t* __restrict__ end_block,
                                                        const float* __restrict__ part, float scale,
-                                                       T* __restrict__ dtable, int64_t ts) {
+                                                       T* __restrict__ dtable, int64_t ts, WeighedRows w) {
     constexpr int VEC = WIDE<T>, CW = LPR * VEC;
     constexpr int G = JOIN_T / LPR < 64 ? JOIN_T / LPR : 64;  // groups that take part
     __shared__ float s_sum[G][CW];
@@ -393,9 +422,16 @@ __global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const
         __syncthreads();
     }
     if (g == 0 && c < dim) {
+        if constexpr (WEIGHED) {
+            const int64_t to = (int64_t)(b + 1) * w.per_block - 1;  // the run's last position in block b
+            if (c == 0) w.slot[key] = (int32_t)to + 1;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) acc[k] = s_sum[0][l * VEC + k] * scale;
-        store_row<FULL>(dtable + (int64_t)key * ts + c, dim - c, acc);
+            for (int k = 0; k < VEC; ++k) w.sums[to * w.ld + c + k] = s_sum[0][l * VEC + k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) acc[k] = s_sum[0][l * VEC + k] * scale;
+            store_row<FULL>(dtable + (int64_t)key * ts + c, dim - c, acc);
+        }
     }
 }
 
@@ -410,20 +446,30 @@ struct EmbedArgs {
     const uint32_t *keys, *pos;
     float* part;
     uint32_t *tail_key, *end_block;
+    WeighedRows weighed;
 };
 
-template <class T, int LPR, bool FULL, int RUN_TOKENS>
+template <class T, int LPR, bool FULL, int RUN_TOKENS, bool WEIGHED = false>
 hipError_t embed_sums(const EmbedArgs& a, hipStream_t s) {
     constexpr int BT = run_threads(LPR) / LPR * RUN_TOKENS;
     const int nb = (int)((a.n + BT - 1) / BT);
     const dim3 grid(nb, (a.dim + LPR * WIDE<T> - 1) / (LPR * WIDE<T>));
-    k_embed_runs<T, LPR, FULL, RUN_TOKENS><<<grid, run_threads(LPR), 0, s>>>(
+    WeighedRows w = a.weighed;
+    w.per_block = BT;
+    k_embed_runs<T, LPR, FULL, RUN_TOKENS, WEIGHED><<<grid, run_threads(LPR), 0, s>>>(
         (int)a.n, a.dim, a.vocab, a.keys, a.pos, (const T*)a.src, a.ss, a.scale, (T*)a.dst, a.ds, a.part, a.tail_key,
-        a.end_block);
+        a.end_block, w);
     if (nb > 1)
-        k_embed_join<T, LPR, FULL><<<grid, JOIN_T, 0, s>>>(a.dim, a.vocab, a.tail_key, a.end_block, a.part, a.scale,
-                                                          (T*)a.dst, a.ds);
+        k_embed_join<T, LPR, FULL, WEIGHED><<<grid, JOIN_T, 0, s>>>(a.dim, a.vocab, a.tail_key, a.end_block, a.part,
+                                                                   a.scale, (T*)a.dst, a.ds, w);
     return hipGetLastError();
+}
+
+template <class T, int LPR, bool FULL, bool WEIGHED = false>
+hipError_t embed_runs(const EmbedArgs& a, hipStream_t s) {
+    return a.n <= RUN_SHORT  ? embed_sums<T, LPR, FULL, RUN_FEW, WEIGHED>(a, s)
+           : a.n < RUN_LONG ? embed_sums<T, LPR, FULL, RUN_USUAL, WEIGHED>(a, s)
+                            : embed_sums<T, LPR, FULL, 2 * RUN_USUAL, WEIGHED>(a, s);
 }
 
 template <class T, int LPR, bool FULL>
@@ -442,9 +488,7 @@ hipError_t embed_rows(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
             (int)a.n, a.dim, a.vocab, a.ids, a.wide, a.scale, (const T*)a.src, a.ss, (T*)a.dst, a.ds);
         return hipGetLastError();
     }
-    return a.n <= RUN_SHORT  ? embed_sums<T, LPR, FULL, RUN_FEW>(a, s)
-           : a.n < RUN_LONG ? embed_sums<T, LPR, FULL, RUN_USUAL>(a, s)
-                            : embed_sums<T, LPR, FULL, 2 * RUN_USUAL>(a, s);
+    return embed_runs<T, LPR, FULL>(a, s);
 }
 
 // The fewest lanes that hold a row with one 16-byte access each, up to a wave.
@@ -560,6 +604,47 @@ hipError_t launch_embed_bwd(int64_t n, int dim, int vocab, bool half, const void
     a.tail_key = (uint32_t*)(ws + L.tail_key);
     a.end_block = (uint32_t*)(ws + L.end_block);
     return half ? embed_run<bf16>(a, RUN_SUMS, stream) : embed_run<float>(a, RUN_SUMS, stream);
+}
+
+hipError_t launch_rows_by_index(int64_t n, int rows, const void* ids, bool wide_ids, int ld, int32_t* slot, char* ws,
+                                int* sorted_at, hipStream_t stream) {
+    const EmbedLayout L = embed_bwd_layout(n, ld, rows);
+    uint32_t* keys[2] = {(uint32_t*)(ws + L.keys[0]), (uint32_t*)(ws + L.keys[1])};
+    uint32_t* pos[2] = {(uint32_t*)(ws + L.pos[0]), (uint32_t*)(ws + L.pos[1])};
+    EmbedArgs a{};
+    a.n = n;
+    a.dim = 1;  // of the table that is cleared: slot
+    a.vocab = rows;
+    a.wide = wide_ids;
+    a.ids = ids;
+    a.dst = slot;
+    a.ds = 1;
+    *sorted_at = 0;
+    const hipError_t e = zero_rows<float>(a, keys[0], pos[0], ws + L.sort, stream);
+    if (e != hipSuccess || n <= RANK_MOST) return e;
+    return launch_index_sort((int)n, rows, ids, wide_ids, keys, pos, ws + L.sort, sorted_at, stream);
+}
+
+hipError_t launch_weighed_rows(int64_t n, int rows, int sorted_at, const WeighedRows& w, char* ws,
+                               hipStream_t stream) {
+    const EmbedLayout L = embed_bwd_layout(n, (int)w.ld, rows);
+    EmbedArgs a{};
+    a.n = n;
+    a.dim = (int)w.ld;
+    a.vocab = rows;
+    a.src = w.src;
+    a.ss = w.ld;
+    a.keys = (const uint32_t*)(ws + L.keys[sorted_at]);
+    a.pos = (const uint32_t*)(ws + L.pos[sorted_at]);
+    a.part = (float*)(ws + L.part);
+    a.tail_key = (uint32_t*)(ws + L.tail_key);
+    a.end_block = (uint32_t*)(ws + L.end_block);
+    a.weighed = w;
+    if (w.ld <= 32) return embed_runs<bf16, 4, true, true>(a, stream);
+    if (w.ld <= 64) return embed_runs<bf16, 8, true, true>(a, stream);
+    if (w.ld <= 128) return embed_runs<bf16, 16, true, true>(a, stream);
+    if (w.ld <= 256) return embed_runs<bf16, 32, true, true>(a, stream);
+    return embed_runs<bf16, 64, true, true>(a, stream);
 }
 
 }  // namespace gs

@@ -167,6 +167,27 @@ struct EmbedLayout {
     size_t keys[2], pos[2], sort, part, tail_key, end_block, total;
 };
 EmbedLayout embed_bwd_layout(int64_t n, int dim, int vocab);
+
+// Sums of weighed rows by index: for each index v in [first, last) that a position names,
+//     sums[slot[v] - 1] = sum over the positions i with index v of weight[place[i]] src[place[i]]
+// in float32, in a fixed order (src: bfloat16 rows of ld elements, ld a multiple of 32; sums: [n][ld]; slot 0: an
+// index that nothing names). launch_rows_by_index comes first: it sorts the n >= 1 positions into ws (of
+// embed_bwd_layout(n, ld, rows)) and clears slot.
+struct WeighedRows {
+    const void* src;
+    const int32_t* place;
+    const float* weight;
+    int64_t ld;
+    float* sums;
+    int32_t* slot;
+    uint32_t first, last;
+    int per_block;  // set by the launch
+};
+hipError_t launch_rows_by_index(int64_t n, int rows, const void* ids, bool wide_ids, int ld, int32_t* slot, char* ws,
+                                int* sorted_at, hipStream_t stream);
+hipError_t launch_weighed_rows(int64_t n, int rows, int sorted_at, const WeighedRows& w, char* ws,
+                               hipStream_t stream);
+
 hipError_t launch_embed_fwd(int64_t n, int dim, int vocab, bool half, const void* table, int64_t table_stride,
                             const void* ids, bool wide_ids, float scale, void* out, int64_t out_stride,
                             hipStream_t stream);

@@ -603,7 +603,8 @@ gs_status gs_mb_atomic(float *records, int64_t n_records, int64_t n_ops, int32_t
  *   of two rows in elements (an input's may be 0: one row for all; otherwise
  *   at least the columns). They hold `dtype` elements, GS_F32 or GS_BF16, one
  *   type per call; statistics, losses and lse are float32. Sums and statistics
- *   are formed in float32 or wider and rounded once.
+ *   are formed in float32 or wider and rounded once (but see the bfloat16
+ *   gradients of gs_label_loss_bwd).
  * - Index arrays hold `index_type` elements, GS_I32 or GS_I64. An index
  *   outside [0, vocab) names nothing: its row takes no part (use -1).
  * - Results are the same bit for bit from run to run (no atomics), and are
@@ -676,6 +677,10 @@ gs_status gs_label_loss_fwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype
  * dmean[0] / labelled rows (dmean[1], of their mean); either may be NULL, not
  * both. dx[n, dim] (zero rows where there is no label), dw[vocab, dim], each
  * nullable. Workspace: gs_label_loss_workspace_size with backward = 1.
+ * With bfloat16 rows the gradient of the logits, dz, is rounded to bfloat16 on
+ * its way into dx and dw (each entry by 2^-8 of itself at most), except where
+ * vocab <= 16, n <= 16 with vocab * dim <= 2^20, or the entry is its row's
+ * label's: those stay float32.
  */
 gs_status gs_label_loss_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, const void *x,
                             int64_t x_stride, const void *w, int64_t w_stride, const void *labels,

@@ -1,0 +1,86 @@
+"""Edges of the label-learning operators: what bfloat16 keeps of a gradient.
+
+Tolerances are the operators' own error bounds, as in test_gpu_labels.py (U:
+the float32 half step; a bfloat16 value is off by 2^-8 of itself at most).
+"""
+import pytest
+import torch
+
+from tests.test_gpu_labels import BF16, DEV, ONE, U, gen, half_step, loss_inputs, randn, run_loss, within
+
+pytestmark = pytest.mark.gpu
+
+
+def loss_bounds(x, w, labels, up):
+    """Losses and gradients in 64 bits, each with its bound. up: the upstream gradient of each row's loss.
+
+    A logit is off by (dim + 8) U of its terms' magnitudes, lse by that of the logits it is made of and by roundings
+    at its own size, an entry of dz by what they make of it. A bfloat16 dz is rounded (2^-8), the label's entry is not.
+    """
+    X, W, dtype = x.double(), w.double(), x.dtype
+    n, vocab, dim = x.shape[0], w.shape[0], x.shape[1]
+    have = (labels >= 0) & (labels < vocab)
+    lab = labels.long().clamp(0, vocab - 1)[:, None]
+    Z = X @ W.t()
+    ze = (X.abs() @ W.abs().t()) * ((dim + 8) * U)
+    S = torch.logsumexp(Z, 1)
+    p = torch.exp(Z - S[:, None])
+    se = (p * ze).sum(1) + (64 + vocab / 256) * U + 4 * U * S.abs()
+    zl = Z.gather(1, lab)[:, 0]
+    loss = torch.where(have, S - zl, 0.0)
+    loss_tol = torch.where(have, se + ze.gather(1, lab)[:, 0] + 4 * U * (S.abs() + zl.abs()), 0.0)
+    up = torch.where(have, up.double(), 0.0)[:, None]
+    dz = p.scatter_add(1, lab, torch.full_like(up, -1.0)) * up
+    through = torch.full_like(dz, 2.0 ** -8 if dtype == BF16 else 4 * U).scatter_(1, lab, 4 * U)
+    dze = up.abs() * p * (ze + se[:, None] + 8 * U * (1 + Z.abs() + S.abs()[:, None])) + dz.abs() * (through + 4 * U)
+    dze += 2.0 ** -126
+    ut = half_step(dtype)
+    dx, dw = dz @ W, dz.t() @ X
+    dx_tol = dze @ W.abs() + (dz.abs() @ W.abs()) * ((vocab + 80) * U) + dx.abs() * ut
+    dw_tol = dze.t() @ X.abs() + (dz.abs().t() @ X.abs()) * ((n + 80) * U) + dw.abs() * ut
+    return dict(loss=(loss, loss_tol), dx=(dx, dx_tol), dw=(dw, dw_tol), dz=dz)
+
+
+# ------------------------------------------------------------------ the label's entry
+
+@pytest.mark.parametrize("n,dim,vocab", [(300, 64, 101), (700, 96, 5000), (9001, 40, 20_000), (5000, 16, 60_000)])
+def test_loss_label_entry_is_not_rounded(n, dim, vocab):
+    """bfloat16: dx and dw are off by their own rounding and by dz's other entries', not by the label's entry's."""
+    x, w, labels, _ = loss_inputs(40 + n, n, dim, vocab, BF16)
+    if vocab == 60_000:  # the backward's pieces of the vocabulary end at 52224
+        labels[:6] = torch.tensor([0, 52_223, 52_224, 52_225, 59_999, 52_223], device=DEV)
+    _, _, _, count, dx, dw = run_loss(x, w, labels, dmean=ONE())
+    ref = loss_bounds(x, w, labels, torch.full((n,), 1.0 / int(count), device=DEV))
+    within("dx", dx, *ref["dx"])
+    within("dw", dw, *ref["dw"])
+
+
+@pytest.mark.parametrize("n", [300, 2900, 12_345])
+@pytest.mark.parametrize("rows", ["own", "shared"])
+def test_loss_dw_is_little_more_than_rounded(n, rows):
+    """dw's error in norm is little more than its own rounding: a uniform rounding of a half step has a third of its
+    square on average, and 1.25 leaves room for dz's other entries. shared: equal rows (one code), most of one label."""
+    x, w, labels, g = loss_inputs(41, n, 64, 501, BF16, missing=0.1)
+    if rows == "shared":
+        code = (torch.rand(n, generator=g, device=DEV) ** 3 * 80).long()
+        labels = torch.where(labels >= 0, code * 6, -1)
+        x = (randn(g, 80, 64) + 2 * w[torch.arange(80, device=DEV) * 6].float()).to(BF16)[code]
+    count, dw = (lambda r: (int(r[3]), r[5]))(run_loss(x, w, labels, dmean=ONE()))
+    ref = loss_bounds(x, w, labels, torch.full((n,), 1.0 / count, device=DEV))["dw"][0]
+    own = (ref.to(BF16).double() - ref).norm()
+    named = torch.bincount(labels[labels >= 0], minlength=501) > 0
+    assert (dw.double() - ref)[named].norm() <= 1.25 * own
+
+
+def test_loss_label_entries_of_one_label():
+    """Nearly all rows name one label: its gradient is one long sum, in a fixed order."""
+    n, dim, vocab = 20_000, 72, 300
+    x, w, labels, g = loss_inputs(42, n, dim, vocab, BF16, missing=0.0)
+    labels = torch.where(torch.rand(n, generator=g, device=DEV) < 0.9, 299, labels)
+    labels[::7] = -1
+    up = torch.rand(n, generator=g, device=DEV)
+    a, b = (run_loss(x, w, labels, dloss=up) for _ in range(2))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    ref = loss_bounds(x, w, labels, up)
+    within("dx", a[4], *ref["dx"])
+    within("dw", a[5], *ref["dw"])
