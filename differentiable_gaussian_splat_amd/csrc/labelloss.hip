@@ -370,7 +370,13 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
                         }
                     if (PARTS == 1 && here && lab >= 0) p.own[n] = own * up;
                 }
-                // rows past the labelled ones have z = 0 and up = 0
+                // dz is zero for rows past the labelled ones (read up to whole steps by dw's product; z there is no
+                // number where a label's row is infinite) and past the vocabulary
+                if (__any(row < 0))
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[i][j][e] = row < 0 ? 0.f : acc[i][j][e];
                 if (edge)
 #pragma unroll
                     for (int i = 0; i < TM; ++i)

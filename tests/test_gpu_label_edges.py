@@ -1,4 +1,4 @@
-"""Edges of the label-learning operators: what bfloat16 keeps of a gradient.
+"""Edges of the label-learning operators: what bfloat16 keeps of a gradient, masked labels.
 
 Tolerances are the operators' own error bounds, as in test_gpu_labels.py (U:
 the float32 half step; a bfloat16 value is off by 2^-8 of itself at most).
@@ -84,3 +84,30 @@ def test_loss_label_entries_of_one_label():
     ref = loss_bounds(x, w, labels, up)
     within("dx", a[4], *ref["dx"])
     within("dw", a[5], *ref["dw"])
+
+
+# ------------------------------------------------------------------ masked labels
+
+@pytest.mark.parametrize("dtype", [BF16], ids=["bf16"])
+@pytest.mark.parametrize("vocab", [48, 64, 65, 600, 1800])
+@pytest.mark.parametrize("n", [128, 150, 160, 161])
+def test_loss_labels_masked_by_infinity(n, vocab, dtype):
+    """A constant feature column with -inf in some label rows takes those labels out: the others' losses and gradients
+    are those of a vocabulary without them, and theirs are zero."""
+    x, w, labels, _ = loss_inputs(43, n, 32, vocab, dtype, missing=0.0)
+    x[:, 0] = 1.0
+    w[:, 0] = 0.0
+    kept = torch.arange(vocab, device=DEV) % 3 != 1
+    labels = labels // 3 * 3
+    if n == 161:
+        labels[160] = -1
+    sub = torch.where(labels >= 0, (torch.cumsum(kept, 0) - 1)[labels.clamp(min=0)], -1)
+    cnt = int((labels >= 0).sum())
+    up = torch.full((n,), 1.0 / cnt, device=DEV)
+    ref = loss_bounds(x, w[kept], sub, up)
+    w[~kept, 0] = -float("inf")
+    loss, lse, mean, count, dx, dw = run_loss(x, w, labels, dmean=ONE())
+    within("loss", loss, *ref["loss"])
+    within("dx", dx[:, 1:], ref["dx"][0][:, 1:], ref["dx"][1][:, 1:])
+    within("dw", dw[kept], *ref["dw"])
+    assert (dw[~kept] == 0).all()
