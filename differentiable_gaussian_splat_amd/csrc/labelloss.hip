@@ -180,6 +180,36 @@ constexpr int tile_elements(int tm, int parts) {
     return step_buffers(parts) * parts * (staged_rows(tm, parts) + BN) * step_depth(parts);
 }
 
+// The logits of split operands that are no number because one of their values is infinite, or too large for a part's
+// product: the value stands in its first part alone, and its products with the other operand's later parts (0, or of
+// the other sign) are wrong. Where the six products give no number, the product of the first parts alone is the
+// logit: infinite (the other products would not change that), or no number in earnest. Read straight from the packed
+// operands: rows of a from p.a + m, of b from p.b + n.
+template <int TM, int TN>
+__device__ __forceinline__ void first_parts(const Product& p, int m, int n, f32x16 (&acc)[TM][TN]) {
+    const int l = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) bad = bad || acc[i][j][e] != acc[i][j][e];
+            if (!__any(bad)) continue;
+            const bf16* a = p.a + min(m + 32 * i + l % 32, p.m - 1) * p.lda + 8 * (l / 32);
+            const bf16* b = p.b + (n + 32 * j + l % 32) * p.ldb + 8 * (l / 32);
+            f32x16 z;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z[e] = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < p.k; k += 16)
+                z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(a + k),
+                                                           *reinterpret_cast<const bf16x8*>(b + k), z, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = acc[i][j][e] != acc[i][j][e] ? z[e] : acc[i][j][e];
+        }
+}
+
 // One product, C[m][n] = sum_k A[m][k] B[n][k], by 64 TM x 128 tiles; a lane
 // holds, for one n, runs of four consecutive m. PARTS: 1, or 3 for split
 // operands.
@@ -292,6 +322,7 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
     // element e of acc[i][j]: m = mb + 32 i + 8 (e / 4) + e % 4, n = nb + 32 j
     const int mb = m0 + wm + 4 * (l / 32), nb = n0 + wn + l % 32;
     if constexpr (MODE == LSE || MODE == DZ) {
+        if constexpr (PARTS == 3) first_parts(p, m0 + wm, n0 + wn, acc);
         const bool edge = m0 + BM > p.m;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
@@ -669,7 +700,7 @@ __global__ __launch_bounds__(PT) void k_pack(LabelRows a, PackArgs p) {
             o[0][k] = (bf16)v[k];
             if (PARTS == 3) {
                 // a value that would round up to infinity keeps its leading bits instead; an
-                // infinite or NaN value stays in its first part alone
+                // infinite or NaN value stays in its first part alone (first_parts sees to its products)
                 const bool fin = fabsf(v[k]) < INFINITY;
                 if (fin && !(fabsf((float)o[0][k]) < INFINITY))
                     o[0][k] = (bf16)__uint_as_float(__float_as_uint(v[k]) & 0xffff0000u);

@@ -6,7 +6,7 @@ the float32 half step; a bfloat16 value is off by 2^-8 of itself at most).
 import pytest
 import torch
 
-from tests.test_gpu_labels import BF16, DEV, ONE, U, gen, half_step, loss_inputs, randn, run_loss, within
+from tests.test_gpu_labels import BF16, DEV, F32, IDS, ONE, TYPES, U, gen, half_step, loss_inputs, randn, run_loss, within
 
 pytestmark = pytest.mark.gpu
 
@@ -88,7 +88,7 @@ def test_loss_label_entries_of_one_label():
 
 # ------------------------------------------------------------------ masked labels
 
-@pytest.mark.parametrize("dtype", [BF16], ids=["bf16"])
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 @pytest.mark.parametrize("vocab", [48, 64, 65, 600, 1800])
 @pytest.mark.parametrize("n", [128, 150, 160, 161])
 def test_loss_labels_masked_by_infinity(n, vocab, dtype):
@@ -111,3 +111,30 @@ def test_loss_labels_masked_by_infinity(n, vocab, dtype):
     within("dx", dx[:, 1:], ref["dx"][0][:, 1:], ref["dx"][1][:, 1:])
     within("dw", dw[kept], *ref["dw"])
     assert (dw[~kept] == 0).all()
+
+
+def test_loss_float32_logits_past_the_largest_number():
+    """A feature of 1e5 on the lowest value: the logit is -inf, however the product is split."""
+    x, w, labels, _ = loss_inputs(44, 150, 32, 600, F32, missing=0.0)
+    labels = labels // 2 * 2
+    w[:, 0] = 0.0
+    ref = loss_bounds(x, w[::2], labels // 2, torch.full((150,), 1.0 / 150, device=DEV))
+    x[:, 0] = 100_200.3
+    w[1::2, 0] = torch.finfo(F32).min
+    r = run_loss(x, w, labels, dmean=ONE())
+    within("loss", r[0], *ref["loss"])
+    assert (r[5][1::2] == 0).all() and r[5].isfinite().all() and r[4].isfinite().all()
+
+
+def test_loss_float32_infinite_feature_stays_in_its_row():
+    x, w, labels, _ = loss_inputs(45, 200, 40, 300, F32, missing=0.0)
+    ref = run_loss(x, w, labels, dmean=ONE())[0]
+    x[7, 3], x[100, 0] = float("inf"), -float("inf")
+    loss, lse = run_loss(x, w, labels, dmean=ONE())[:2]
+    ok = torch.ones(200, dtype=torch.bool, device=DEV)
+    ok[[7, 100]] = False
+    assert torch.equal(loss[ok], ref[ok])
+    # the largest logit is +inf: lse is, and the loss is (unless the label's logit is +inf too: no number)
+    at = torch.stack([x[7, 3] * w[labels[7], 3], x[100, 0] * w[labels[100], 0]])
+    assert (lse[[7, 100]] == float("inf")).all()
+    assert torch.equal(loss[[7, 100]].isnan(), at > 0) and (loss[[7, 100]][at < 0] == float("inf")).all()
