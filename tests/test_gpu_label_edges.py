@@ -1,4 +1,5 @@
-"""Edges of the label-learning operators: what bfloat16 keeps of a gradient, masked labels.
+"""Edges of the label-learning operators: what bfloat16 keeps of a gradient,
+masked labels, confident rows.
 
 Tolerances are the operators' own error bounds, as in test_gpu_labels.py (U:
 the float32 half step; a bfloat16 value is off by 2^-8 of itself at most).
@@ -113,6 +114,27 @@ def test_loss_labels_masked_by_infinity(n, vocab, dtype):
     assert (dw[~kept] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("mask", ["inf", "lowest", "half"])
+@pytest.mark.parametrize("first", [0, 100])
+def test_loss_whole_tiles_of_masked_labels(first, mask, dtype):
+    """Only 150 neighbouring labels of 1800 are left, so that whole tiles hold masked ones alone."""
+    n, vocab = 150, 1800
+    x, w, labels, _ = loss_inputs(49, n, 32, vocab, dtype, missing=0.0)
+    x[:, 0] = 1.0
+    w[:, 0] = 0.0
+    kept = slice(first, first + 150)
+    labels = labels % 150 + first
+    ref = loss_bounds(x, w[kept], labels - first, torch.full((n,), 1.0 / n, device=DEV))
+    low = {"inf": -float("inf"), "lowest": torch.finfo(dtype).min, "half": torch.finfo(dtype).min / 2}[mask]
+    w[:first, 0], w[first + 150:, 0] = low, low
+    loss, lse, mean, count, dx, dw = run_loss(x, w, labels, dmean=ONE())
+    within("loss", loss, *ref["loss"])
+    within("dx", dx[:, 1:], ref["dx"][0][:, 1:], ref["dx"][1][:, 1:])
+    within("dw", dw[kept], *ref["dw"])
+    assert (dw[:first] == 0).all() and (dw[first + 150:] == 0).all()
+
+
 def test_loss_float32_logits_past_the_largest_number():
     """A feature of 1e5 on the lowest value: the logit is -inf, however the product is split."""
     x, w, labels, _ = loss_inputs(44, 150, 32, 600, F32, missing=0.0)
@@ -138,3 +160,34 @@ def test_loss_float32_infinite_feature_stays_in_its_row():
     at = torch.stack([x[7, 3] * w[labels[7], 3], x[100, 0] * w[labels[100], 0]])
     assert (lse[[7, 100]] == float("inf")).all()
     assert torch.equal(loss[[7, 100]].isnan(), at > 0) and (loss[[7, 100]][at < 0] == float("inf")).all()
+
+
+# ------------------------------------------------------------------ confident rows
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("vocab", [60, 700])
+@pytest.mark.parametrize("size", [100.0, 1000.0])
+def test_loss_of_confident_rows(size, vocab, dtype):
+    """Rows whose label's logit (of 100 to 2000) leads by 40 and more: the loss is no less than zero and at most a few
+    float32 steps of one (an exponential, its correction and a logarithm, 2 U each)."""
+    g = gen(46)
+    w = randn(g, vocab, 64)
+    w = (w / w.norm(dim=1, keepdim=True)).to(dtype)
+    labels = torch.randint(0, vocab, (300,), generator=g, device=DEV)
+    x = (w[labels].float() * (size * (1 + torch.rand((300, 1), generator=g, device=DEV)))).to(dtype)
+    Z = x.double() @ w.double().t()
+    lead = Z.gather(1, labels[:, None])[:, 0] - Z.scatter(1, labels[:, None], -1e9).max(1).values
+    assert float(lead.min()) > 30
+    loss = run_loss(x, w, labels, dmean=ONE())[0]
+    assert (loss >= 0).all() and (loss <= 8 * U).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("vocab", [60, 700])
+def test_loss_is_never_negative(vocab, dtype):
+    """Labels leading by 0 to 30, where the other labels' share fades below float32's step."""
+    x, w, labels, g = loss_inputs(47, 3000, 32, vocab, dtype, missing=0.0)
+    x = (x.float() * torch.logspace(0, 2.5, 3000, device=DEV)[:, None]).to(dtype)
+    labels = (x.float() @ w.float().t()).argmax(1)
+    loss = run_loss(x, w, labels, dmean=ONE())[0]
+    assert (loss >= 0).all()
