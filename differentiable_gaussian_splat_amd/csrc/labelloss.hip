@@ -171,8 +171,10 @@ __device__ __forceinline__ void step_barrier() {
 // 2^x; results below 2^-126 are 0
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// exp(z - ref); the difference first, which is exact where the two are close: one multiply-add with a scaled reference
-// (8192 x 256 x 50021 forward 255 us, so 258) is off by the rounding of that, which grows with the logit and not its term
+// exp(z - ref); the difference first, which is exact where the two are close. One multiply-add with a scaled reference
+// would be off by the rounding of that, which grows with the logit and not with its term (8192 x 256 x 50021 forward
+// 255 us, so 258; 5003 x 129 x 8191 float32 with gradients 330 and 332). The backward's reference, lse, is one float32:
+// p is off by half a step of it, and p of a label whose logit exceeds the others' by more than lse can hold is 1.
 __device__ __forceinline__ float exp_diff(float z, float ref) { return exp2_fast((z - ref) * LOG2E); }
 
 // Rows staged for TM row blocks per wave (a power of two, for the staging's lanes).
@@ -378,12 +380,12 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
                         for (int e = 0; e < 16; ++e)
                             if (at == 32 * i + 8 * (e / 4) + e % 4 && lab >= 0) p.target[n] = acc[i][j][e];
             } else {
-                const float ref = row >= 0 ? p.lse[row] * LOG2E : 0.f;
+                const float lse = row >= 0 ? p.lse[row] : 0.f;
                 const float up = row >= 0 ? up_of(p.dmean, p.dloss, row, cnt) : 0.f;
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[i][j][e] = exp2_fast(fmaf(acc[i][j][e], LOG2E, -ref));
+                    for (int e = 0; e < 16; ++e) acc[i][j][e] = exp_diff(acc[i][j][e], lse);
                 if (hit) {
                     float own = 0.f;
                     bool here = false;
@@ -1404,7 +1406,9 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         own.ld = L.kp;
         own.sums = (float*)(ws + L.own_sums);
         own.slot = slot;
-        if (!few) e = launch_rows_by_index(a.n, a.vocab, a.labels, a.wide_labels, L.kp, slot, ws + L.by_label, &sorted_at, s);
+        if (!few)
+            e = launch_rows_by_index(a.n, a.vocab, a.labels, a.wide_labels, L.kp, slot, ws + L.by_label, &sorted_at,
+                                     s);
         if (e != hipSuccess) return e;
     }
     for (int64_t v0 = 0; v0 < a.vocab; v0 += L.piece_b) {

@@ -169,7 +169,7 @@ def test_loss_float32_infinite_feature_stays_in_its_row():
 @pytest.mark.parametrize("size", [100.0, 1000.0])
 def test_loss_of_confident_rows(size, vocab, dtype):
     """Rows whose label's logit (of 100 to 2000) leads by 40 and more: the loss is no less than zero and at most a few
-    float32 steps of one (an exponential, its correction and a logarithm, 2 U each)."""
+    float32 steps of one (an exponential, its correction and a logarithm, 2 U each), p - 1 likewise."""
     g = gen(46)
     w = randn(g, vocab, 64)
     w = (w / w.norm(dim=1, keepdim=True)).to(dtype)
@@ -178,8 +178,12 @@ def test_loss_of_confident_rows(size, vocab, dtype):
     Z = x.double() @ w.double().t()
     lead = Z.gather(1, labels[:, None])[:, 0] - Z.scatter(1, labels[:, None], -1e9).max(1).values
     assert float(lead.min()) > 30
-    loss = run_loss(x, w, labels, dmean=ONE())[0]
+    up = torch.rand(300, generator=g, device=DEV)
+    loss, lse, _, _, dx, dw = run_loss(x, w, labels, dloss=up)
     assert (loss >= 0).all() and (loss <= 8 * U).all()
+    assert (dx.double().abs() <= 16 * U * w.double().abs().max()).all()
+    dw_tol = torch.zeros((vocab, 64), dtype=torch.float64, device=DEV).index_add_(0, labels, x.double().abs())
+    assert (dw.double().abs() <= 16 * U * (dw_tol + 1e-3)).all()
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
