@@ -382,18 +382,20 @@ __global__ __launch_bounds__(run_threads(LPR)) void k_embed_runs(
 // of the blocks after it up to the one where it ends, a contiguous share per
 // row group, the groups joined in order.
 template <class T, int LPR, bool FULL, bool WEIGHED>
-__global__ __launch_bounds__(JOIN_T) void k_embed_join(int dim, int vocab, const uint32_t* __restrict__ tail_key,
+__global__ __launch_bounds__(JOIN_T) void k_embed_join(int first, int dim, int vocab,
+                                                       const uint32_t* __restrict__ tail_key,
                                                        const uint32_t* __restrict__ end_block,
                                                        const float* __restrict__ part, float scale,
                                                        T* __restrict__ dtable, int64_t ts, WeighedRows w) {
     constexpr int VEC = WIDE<T>, CW = LPR * VEC;
     constexpr int G = JOIN_T / LPR < 64 ? JOIN_T / LPR : 64;  // groups that take part
     __shared__ float s_sum[G][CW];
-    const uint32_t key = tail_key[blockIdx.x];
+    const int b = first + (int)blockIdx.x;
+    const uint32_t key = tail_key[b];
     if (key == (uint32_t)vocab) return;
     const int g = threadIdx.x / LPR, l = threadIdx.x % LPR;
     const int c = blockIdx.y * CW + l * VEC;
-    const int b = blockIdx.x, cnt = (int)end_block[key] - b + 1;
+    const int cnt = (int)end_block[key] - b + 1;
     const int per = (cnt + G - 1) / G;
     const int j0 = g * per, j1 = g < G ? min(cnt, j0 + per) : 0;
     float acc[VEC];
@@ -459,9 +461,10 @@ hipError_t embed_sums(const EmbedArgs& a, hipStream_t s) {
     k_embed_runs<T, LPR, FULL, RUN_TOKENS, WEIGHED><<<grid, run_threads(LPR), 0, s>>>(
         (int)a.n, a.dim, a.vocab, a.keys, a.pos, (const T*)a.src, a.ss, a.scale, (T*)a.dst, a.ds, a.part, a.tail_key,
         a.end_block, w);
-    if (nb > 1)
-        k_embed_join<T, LPR, FULL, WEIGHED><<<grid, JOIN_T, 0, s>>>(a.dim, a.vocab, a.tail_key, a.end_block, a.part,
-                                                                   a.scale, (T*)a.dst, a.ds, w);
+    for (int64_t b0 = 0; nb > 1 && b0 < nb; b0 += MOST_BLOCKS)
+        k_embed_join<T, LPR, FULL, WEIGHED><<<dim3((unsigned)(nb - b0 < MOST_BLOCKS ? nb - b0 : MOST_BLOCKS), grid.y),
+                                              JOIN_T, 0, s>>>((int)b0, a.dim, a.vocab, a.tail_key, a.end_block, a.part,
+                                                              a.scale, (T*)a.dst, a.ds, w);
     return hipGetLastError();
 }
 
@@ -475,10 +478,13 @@ hipError_t embed_runs(const EmbedArgs& a, hipStream_t s) {
 template <class T, int LPR, bool FULL>
 hipError_t embed_rows(const EmbedArgs& a, EmbedPass pass, hipStream_t s) {
     if (pass == LOOKUP) {
-        constexpr int G = EB / LPR;
-        const int64_t blocks = (a.n + G * 4 - 1) / (G * 4);
-        k_embed<T, LPR, FULL><<<(unsigned)blocks, EB, 0, s>>>(a.n, a.dim, a.vocab, (const T*)a.src, a.ss, a.ids, a.wide,
-                                                       a.scale, (T*)a.dst, a.ds);
+        constexpr int64_t PER = EB / LPR * 4, MOST = PER * MOST_BLOCKS;  // rows of a block and of a launch
+        for (int64_t r = 0; r < a.n; r += MOST) {
+            const int64_t rows = a.n - r < MOST ? a.n - r : MOST;
+            k_embed<T, LPR, FULL><<<(unsigned)((rows + PER - 1) / PER), EB, 0, s>>>(
+                rows, a.dim, a.vocab, (const T*)a.src, a.ss, (const char*)a.ids + r * (a.wide ? 8 : 4), a.wide, a.scale,
+                (T*)a.dst + r * a.ds, a.ds);
+        }
         return hipGetLastError();
     }
     if (pass == FEW_SUMS) {

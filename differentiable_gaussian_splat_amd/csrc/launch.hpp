@@ -161,6 +161,10 @@ size_t radix_sort_scratch(int64_t n);
 hipError_t launch_index_sort(int n, int rows, const void* ids, bool wide, uint32_t* const keys[2],
                              uint32_t* const vals[2], char* scratch, int* sorted_at, hipStream_t s);
 
+// Blocks of a launch at most (of 1024 threads or fewer): a grid holds less than 2^32 threads along an axis. Kernels of
+// which larger inputs need more are launched in parts, each told its first block.
+constexpr int64_t MOST_BLOCKS = 1 << 21;
+
 // Label learning (embed.hip, norm.hip, labelloss.hip). `half`: rows are bfloat16, otherwise
 // float32; strides count elements; index arrays are int64 with `wide_ids`, otherwise int32.
 struct EmbedLayout {

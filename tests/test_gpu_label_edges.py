@@ -1,5 +1,5 @@
 """Edges of the label-learning operators: what bfloat16 keeps of a gradient,
-masked labels, confident rows.
+masked labels, confident rows, large counts.
 
 Tolerances are the operators' own error bounds, as in test_gpu_labels.py (U:
 the float32 half step; a bfloat16 value is off by 2^-8 of itself at most).
@@ -7,6 +7,7 @@ the float32 half step; a bfloat16 value is off by 2^-8 of itself at most).
 import pytest
 import torch
 
+from differentiable_gaussian_splat_amd import labels as L
 from tests.test_gpu_labels import BF16, DEV, F32, IDS, ONE, TYPES, U, gen, half_step, loss_inputs, randn, run_loss, within
 
 pytestmark = pytest.mark.gpu
@@ -195,3 +196,49 @@ def test_loss_is_never_negative(vocab, dtype):
     labels = (x.float() @ w.float().t()).argmax(1)
     loss = run_loss(x, w, labels, dmean=ONE())[0]
     assert (loss >= 0).all()
+
+
+# ------------------------------------------------------------------ large counts
+
+def room(gib):
+    """Skips where the card has less memory free (a shared one)."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gib * 2 ** 30:
+        pytest.skip(f"needs {gib} GiB of device memory")
+
+
+def test_embed_of_more_rows_than_one_launch():
+    """2^28 rows and a wave for each: 2^32 threads, more than a grid may have along an axis."""
+    room(150)
+    n, dim, vocab = (1 << 28) + 5, 257, 100
+    g = gen(50)
+    table = randn(g, vocab, dim, dtype=BF16)
+    ids = torch.randint(-1, vocab, (n,), generator=g, device=DEV, dtype=torch.int32)
+    out = torch.empty((n, dim), dtype=BF16, device=DEV)
+    L.gs_embed_fwd(table, ids, out, 2.0)
+    rows = torch.cat([torch.arange(100, device=DEV), torch.arange(n - 100, n, device=DEV),
+                      torch.arange((1 << 25) - 50, (1 << 25) + 50, device=DEV),
+                      torch.randint(0, n, (300_000,), generator=g, device=DEV)])
+    want = torch.where(ids[rows, None] >= 0, table[ids[rows].long().clamp(min=0)] * 2, 0)
+    assert torch.equal(out[rows], want)
+    del out
+    torch.cuda.empty_cache()
+
+
+def test_embed_gradient_of_more_rows_than_one_launch():
+    """2^29 positions, four lane groups to a block: the join's blocks of 1024 threads pass 2^32 threads. The sums are of
+    ones, exact in float32."""
+    room(60)
+    n, dim, vocab = (1 << 29) + 300, 129, 4096
+    g = gen(51)
+    ids = torch.randint(-1, vocab, (n,), generator=g, device=DEV, dtype=torch.int32)
+    ids[-200:] = 4095
+    dtable = torch.empty((vocab, dim), device=DEV)
+    ws = torch.empty(L.gs_embed_bwd_workspace_size(n, dim, vocab, F32), dtype=torch.uint8, device=DEV)
+    L.gs_embed_bwd(ids, torch.ones((1, dim), device=DEV).expand(n, dim), dtable, ws, 1.0)
+    del ws
+    count = torch.zeros(vocab + 1, dtype=torch.int64, device=DEV)
+    for part in ids.split(1 << 26):
+        count += torch.bincount(part.long() + 1, minlength=vocab + 1)
+    assert torch.equal(dtable.long(), count[1:, None].expand(vocab, dim))
+    torch.cuda.empty_cache()
