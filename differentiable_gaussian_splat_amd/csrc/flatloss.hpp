@@ -152,14 +152,14 @@ struct FlatTile {
 // Few labels: the losses of 32 labelled rows (FORWARD, and by the block that
 // ends last the mean), or their dz.
 template <class T, int VT, bool FORWARD>
-__global__ __launch_bounds__(FT) void k_few_labels(FlatArgs a) {
+__global__ __launch_bounds__(FT) void k_few_labels(FlatArgs a, BlockRange range) {
     using Tile = FlatTile<T, VT>;
     constexpr int VP = Tile::VP;
     __shared__ __align__(16) char s_mem[Tile::BYTES];
     __shared__ double s_loss[FR];
     __shared__ int s_last;
     const int l = threadIdx.x & 63;
-    const int cnt = *a.labels.count, n0 = blockIdx.x * FR;
+    const int block = range.first + (int)blockIdx.x, cnt = *a.labels.count, n0 = block * FR;
     if (n0 < cnt)
         Tile::run(s_mem, static_cast<const T*>(a.x), a.xs, a.n,
                   [&](int i) { return n0 + i < cnt ? (int64_t)a.labels.rows[n0 + i] : (int64_t)-1; },
@@ -214,12 +214,12 @@ __global__ __launch_bounds__(FT) void k_few_labels(FlatArgs a) {
     if (threadIdx.x == 0) {
         double s = 0.0;
         for (int k = 0; k < FR; ++k) s += s_loss[k];
-        __hip_atomic_store(&a.block_sum[blockIdx.x], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(&a.block_sum[block], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         s_last =
-            __hip_atomic_fetch_add(a.labels.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+            __hip_atomic_fetch_add(a.labels.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == range.all - 1;
     }
     __syncthreads();
-    if (s_last) loss_mean<FT>(a.block_sum, (int)gridDim.x, cnt, a.mean, a.count_out);
+    if (s_last) loss_mean<FT>(a.block_sum, range.all, cnt, a.mean, a.count_out);
 }
 
 // Few rows (n <= SHORT): per block the (maximum, sum) pairs of every row over

@@ -816,6 +816,18 @@ __device__ __forceinline__ float exp_share(float z, float top) {
     return z == top ? 1.f : exp_diff(z, top);
 }
 
+// The blocks of one launch among all that a kernel takes for its rows.
+struct BlockRange {
+    int first, all;
+};
+
+// Calls launch(blocks, range) for the launches that `all` blocks take.
+template <class F>
+void launch_ranges(int64_t all, F launch) {
+    for (int64_t first = 0; first < all; first += MOST_BLOCKS)
+        launch((unsigned)(all - first < MOST_BLOCKS ? all - first : MOST_BLOCKS), BlockRange{(int)first, (int)all});
+}
+
 constexpr int JR = 64;  // rows per block of the join
 constexpr int JT = 1024;
 
@@ -839,9 +851,9 @@ __device__ __forceinline__ void loss_mean(const double* block_sum, int blocks, i
 
 // Joins the slabs' (maximum, sum) pairs of each labelled row (and `state`, the
 // join of earlier pieces; with `more` pieces to come the result is left there
-// again), then the row's loss. The block that ends last adds the blocks' losses
-// in block order: the mean.
-__global__ __launch_bounds__(JT) void k_lse_join(int slabs, int np, const float2* __restrict__ part,
+// again), then the row's loss. Of all launches' blocks the one that ends last adds
+// the blocks' losses in block order: the mean.
+__global__ __launch_bounds__(JT) void k_lse_join(BlockRange range, int slabs, int np, const float2* __restrict__ part,
                                                  const float* __restrict__ target, const int32_t* __restrict__ rows,
                                                  const int32_t* __restrict__ count, float2* __restrict__ state,
                                                  bool first, bool more, float* __restrict__ loss,
@@ -852,7 +864,7 @@ __global__ __launch_bounds__(JT) void k_lse_join(int slabs, int np, const float2
     __shared__ float2 s[G][JR];
     __shared__ int s_last;
     const int j = threadIdx.x % JR, g = threadIdx.x / JR;
-    const int n = blockIdx.x * JR + j, cnt = *count;
+    const int block = range.first + (int)blockIdx.x, n = block * JR + j, cnt = *count;
     float2 a = make_float2(-INFINITY, 0.f);
     if (n < cnt) {
         if (!first && g == 0) a = state[n];
@@ -880,15 +892,15 @@ __global__ __launch_bounds__(JT) void k_lse_join(int slabs, int np, const float2
         if (!more) {
             for (int off = 32; off > 0; off >>= 1) mine += __shfl_xor(mine, off);
             if (j == 0) {
-                __hip_atomic_store(&block_sum[blockIdx.x], mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_store(&block_sum[block], mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 s_last = __hip_atomic_fetch_add(done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-                         (int)gridDim.x - 1;
+                         range.all - 1;
             }
         }
     }
     if (more) return;
     __syncthreads();
-    if (s_last) loss_mean<JT>(block_sum, (int)gridDim.x, cnt, mean, count_out);
+    if (s_last) loss_mean<JT>(block_sum, range.all, cnt, mean, count_out);
 }
 
 // out[r] = the splits' rows of acc added in order, through place (-1: a zero row) if given.
@@ -1242,19 +1254,23 @@ Product product_base(const LabelLossArgs& a, const LossPlan& L, char* ws) {
 }
 
 template <class T, int VT, bool FORWARD>
-void flat_logits(const FlatArgs& f, Side side, unsigned blocks, hipStream_t s) {
-    if (side == LABELS)
-        k_few_labels<T, VT, FORWARD><<<blocks, FT, 0, s>>>(f);
-    else
-        k_few_rows<T, VT, FORWARD><<<blocks, FT, 0, s>>>(f);
+void flat_logits(const FlatArgs& f, Side side, int64_t tiles, hipStream_t s) {
+    if (side == LABELS) {
+        launch_ranges(tiles, [&](unsigned blocks, BlockRange range) {
+            k_few_labels<T, VT, FORWARD><<<blocks, FT, 0, s>>>(f, range);
+        });
+    } else {  // whose blocks walk over the tiles
+        const int64_t most = FORWARD ? ROW_BLOCKS : MOST_BLOCKS;
+        k_few_rows<T, VT, FORWARD><<<(unsigned)(tiles < most ? tiles : most), FT, 0, s>>>(f);
+    }
 }
 
 template <class T, bool FORWARD>
-void flat_logits(const FlatArgs& f, Side side, int64_t few, unsigned blocks, hipStream_t s) {
+void flat_logits(const FlatArgs& f, Side side, int64_t few, int64_t tiles, hipStream_t s) {
     if constexpr (sizeof(T) == 4) {
-        if (few > 32) return flat_logits<T, 2, FORWARD>(f, side, blocks, s);
+        if (few > 32) return flat_logits<T, 2, FORWARD>(f, side, tiles, s);
     }
-    flat_logits<T, 1, FORWARD>(f, side, blocks, s);
+    flat_logits<T, 1, FORWARD>(f, side, tiles, s);
 }
 
 template <class T>
@@ -1283,14 +1299,14 @@ hipError_t flat_loss(const LabelLossArgs& a, const LossPlan& L, char* ws, bool f
     if (few_labels) list_rows(f.labels, L, ws, s);
     const int64_t tiles = rows > 0 ? (rows + FR - 1) / FR : 1;
     if (forward) {
-        const unsigned blocks = (unsigned)(few_labels || tiles < ROW_BLOCKS ? tiles : ROW_BLOCKS);
-        flat_logits<T, true>(f, L.shorter, few, blocks, s);
+        flat_logits<T, true>(f, L.shorter, few, tiles, s);
         if (!few_labels)
-            k_lse_join<<<1, JT, 0, s>>>((int)blocks, SHORT, f.part, f.target, f.labels.rows, f.labels.count, nullptr,
-                                        true, false, a.loss, a.lse, f.block_sum, f.labels.done, a.mean, a.count);
+            k_lse_join<<<1, JT, 0, s>>>({0, 1}, (int)(tiles < ROW_BLOCKS ? tiles : ROW_BLOCKS), SHORT, f.part, f.target,
+                                        f.labels.rows, f.labels.count, nullptr, true, false, a.loss, a.lse, f.block_sum,
+                                        f.labels.done, a.mean, a.count);
         return hipGetLastError();
     }
-    flat_logits<T, false>(f, L.shorter, few, (unsigned)tiles, s);
+    flat_logits<T, false>(f, L.shorter, few, tiles, s);
     FlatGrads g{};
     g.rows = rows;
     g.dim = a.dim;
@@ -1376,9 +1392,11 @@ hipError_t loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         launch_product<LSE, PARTS, T>(L.tm_z, p, s);
         // every tile writes its slabs, so the last may lie beyond the vocabulary (an empty one)
         const int slabs = (int)(up(mv, 64 * L.tm_z) / (32 * L.tm_z));
-        k_lse_join<<<(unsigned)(a.n > 0 ? (a.n + JR - 1) / JR : 1), JT, 0, s>>>(
-            slabs, (int)L.np, part, p.target, p.rows, p.count, state, v0 == 0, v0 + L.piece_f < a.vocab, a.loss, a.lse,
-            bs, (int32_t*)(ws + L.done), a.mean, a.count);
+        launch_ranges(a.n > 0 ? (a.n + JR - 1) / JR : 1, [&](unsigned blocks, BlockRange range) {
+            k_lse_join<<<blocks, JT, 0, s>>>(range, slabs, (int)L.np, part, p.target, p.rows, p.count, state, v0 == 0,
+                                             v0 + L.piece_f < a.vocab, a.loss, a.lse, bs, (int32_t*)(ws + L.done),
+                                             a.mean, a.count);
+        });
     }
     return hipGetLastError();
 }

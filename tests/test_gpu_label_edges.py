@@ -242,3 +242,73 @@ def test_embed_gradient_of_more_rows_than_one_launch():
         count += torch.bincount(part.long() + 1, minlength=vocab + 1)
     assert torch.equal(dtable.long(), count[1:, None].expand(vocab, dim))
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("few", [True, False], ids=["few labels", "tiles"])
+def test_loss_of_more_rows_than_one_launch(few):
+    """2^29 rows against three labels, 2^28 against 17 in bfloat16: the blocks of 32 (64) rows pass 2^32 threads. All
+    rows are one row of x, so that each label has one loss and one gradient."""
+    room(90)
+    n, dim, vocab, dtype = ((1 << 29) + 37, 4, 3, F32) if few else ((1 << 28) + 37, 8, 17, BF16)
+    g = gen(52)
+    x, w = randn(g, 1, dim, dtype=dtype), randn(g, vocab, dim, dtype=dtype)
+    labels = torch.randint(-1, vocab, (n,), generator=g, device=DEV, dtype=torch.int32)
+    labels[-8:] = torch.tensor([0, 1, 2, -1, 0, 1, 2, -1], device=DEV)
+    loss, lse = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    mean, count = torch.empty(1, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+    ws = torch.empty(L.gs_label_loss_workspace_size(n, dim, vocab, dtype, few), dtype=torch.uint8, device=DEV)
+    L.gs_label_loss_fwd(x.expand(n, dim), w, labels, loss, lse, mean, count, ws)
+    ref = loss_bounds(x.expand(vocab, dim), w, torch.arange(vocab, device=DEV), torch.full((vocab,), 0.5, device=DEV))
+    table = torch.cat([ref["loss"][0], torch.zeros(1, dtype=torch.float64, device=DEV)])
+    total, have = 0.0, 0
+    for i in range(0, n, 1 << 26):
+        lab = labels[i:i + (1 << 26)].long()
+        part = loss[i:i + (1 << 26)]
+        assert (part - table.float()[lab]).abs().max() <= float(ref["loss"][1].max()) + U * float(table.max())
+        assert (part[lab < 0] == 0).all()
+        total, have = total + float(part.double().sum()), have + int((lab >= 0).sum())
+    assert int(count) == have
+    assert abs(float(mean) - total / have) <= 2 * U * total / have
+    if few:
+        dx = torch.empty((n, dim), device=DEV)
+        L.gs_label_loss_bwd(x.expand(n, dim), w, labels, lse, dx, None, ws, dloss=loss.fill_(0.5))
+        want = torch.cat([ref["dx"][0], torch.zeros((1, dim), dtype=torch.float64, device=DEV)]).float()
+        tol = float(ref["dx"][1].max()) + U * float(want.abs().max())
+        for i in range(0, n, 1 << 24):
+            assert (dx[i:i + (1 << 24)] - want[labels[i:i + (1 << 24)].long()]).abs().max() <= tol
+        del dx
+    del loss, lse, ws, labels
+    torch.cuda.empty_cache()
+
+
+def test_loss_of_more_labels_than_one_launch():
+    """Three rows against 2^29 labels: the gradient's blocks of 32 labels pass 2^32 threads. A thread adds 2^15 tiles'
+    sums one after the other, each sum off by U."""
+    room(40)
+    n, dim, vocab = 3, 2, (1 << 29) + 37
+    x, w, labels, g = loss_inputs(53, n, dim, 1000, F32, missing=0.0)
+    w = torch.randn((vocab, dim), generator=g, device=DEV)
+    labels = torch.tensor([vocab - 1, 5, 1 << 28], device=DEV)
+    up = torch.tensor([0.5, 1.0, 2.0], device=DEV)
+    loss, lse = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    mean, count = torch.empty(1, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+    dw = torch.empty((vocab, dim), device=DEV)
+    ws = torch.empty(L.gs_label_loss_workspace_size(n, dim, vocab, F32, True), dtype=torch.uint8, device=DEV)
+    L.gs_label_loss_fwd(x, w, labels, loss, lse, mean, count, ws)
+    L.gs_label_loss_bwd(x, w, labels, lse, None, dw, ws, dloss=up)
+    del ws
+    X = x.double()
+    total = torch.zeros(n, dtype=torch.float64, device=DEV)
+    for part in w.split(1 << 25):
+        total += torch.exp(part.double() @ X.t()).sum(0)
+    S, rel = torch.log(total), (2 ** 15 + 64) * U
+    within("lse", lse, S, rel + 4 * U * S)
+    Z = (X * w[labels].double()).sum(1)
+    within("loss", loss, S - Z, rel + 8 * U * (S + Z.abs()))
+    rows = torch.cat([labels, torch.randint(0, vocab, (100_000,), generator=g, device=DEV)])
+    p = torch.exp(w[rows].double() @ X.t() - S)
+    dz = (p - (rows[:, None] == labels[None, :]).double()) * up.double()
+    tol = (p * up.double()) @ X.abs() * (rel + 32 * U * S.max()) + (dz.abs() @ X.abs()) * 16 * U
+    within("dw", dw[rows], dz @ X, tol)
+    del w, dw
+    torch.cuda.empty_cache()
