@@ -138,7 +138,7 @@ struct Stage {
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
                              lds + (i * 4 + w) * 1024),
                          "v"(off[i]), "s"(r)
-                         : "memory");
+                         : "memory", "m0");
     }
 };
 
