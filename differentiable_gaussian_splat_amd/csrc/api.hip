@@ -1150,6 +1150,7 @@ gs_status gs_embed_fwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, con
         g_err[0] = 0;
         TRY(check_rows(fn, n, dim, vocab, dtype));
         TRY(check_index(fn, ids, index_type, n));
+        REQUIRE(isfinite(scale), "%s: scale must be finite", fn);
         TRY(check_matrix(fn, "table", table, table_stride, vocab, dim, dtype, true, false));
         TRY(check_matrix(fn, "out", out, out_stride, n, dim, dtype, false, false));
         if (n == 0) return GS_OK;
@@ -1173,6 +1174,7 @@ gs_status gs_embed_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, con
         g_err[0] = 0;
         TRY(check_rows(fn, n, dim, vocab, dtype));
         TRY(check_index(fn, ids, index_type, n));
+        REQUIRE(isfinite(scale), "%s: scale must be finite", fn);
         TRY(check_matrix(fn, "dout", dout, dout_stride, n, dim, dtype, true, false));
         TRY(check_matrix(fn, "dtable", dtable, dtable_stride, vocab, dim, dtype, false, false));
         TRY(check_workspace(fn, workspace, workspace_bytes, gs_embed_bwd_workspace_size(n, dim, vocab, dtype)));

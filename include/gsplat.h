@@ -621,7 +621,7 @@ gs_status gs_mb_atomic(float *records, int64_t n_records, int64_t n_ops, int32_t
 
 /*
  * gs_embed_fwd -- out[i] = scale * table[ids[i]], a zero row where ids[i] names
- * no row. table[vocab, dim], ids[n], out[n, dim].
+ * no row. table[vocab, dim], ids[n], out[n, dim]; scale is finite.
  */
 gs_status gs_embed_fwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, const void *table,
                        int64_t table_stride, const void *ids, int32_t index_type, float scale, void *out,
