@@ -105,7 +105,7 @@ def gs_embed_fwd(table, ids, out, scale=1.0, stream=None):
     """out[i] = scale * table[ids[i]]; zero rows where ids[i] names no row."""
     ts = _matrix("table", table)
     vocab, dim = table.shape
-    n = ids.shape[0]
+    n = ids.numel()  # of one dimension, as _index sees to
     os_ = _matrix("out", out, table, n, dim)
     dev = table.get_device()
     ip, it = _index("ids", ids, n, dev)
@@ -218,7 +218,7 @@ class _EmbedFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, table, ids, scale):
         table, ids = _rows(table), ids.contiguous()
-        out = torch.empty((ids.shape[0], table.shape[1]), dtype=table.dtype, device=table.device)
+        out = torch.empty((ids.numel(), table.shape[1]), dtype=table.dtype, device=table.device)
         gs_embed_fwd(table, ids, out, scale)
         ctx.save_for_backward(ids)
         ctx.scale, ctx.vocab = scale, table.shape[0]
