@@ -8,7 +8,8 @@ import pytest
 import torch
 
 from differentiable_gaussian_splat_amd import labels as L
-from tests.test_gpu_labels import BF16, DEV, F32, IDS, ONE, TYPES, U, gen, half_step, loss_inputs, randn, run_loss, within
+from tests.test_gpu_labels import (BF16, DEV, F32, IDS, ONE, TYPES, U, check_embed, gen, half_step, loss_inputs, randn,
+                                   run_loss, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -205,6 +206,30 @@ def room(gib):
     torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < gib * 2 ** 30:
         pytest.skip(f"needs {gib} GiB of device memory")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("n,dim,vocab", [(70_001, 24, 3001), (40_000, 16, 30_001)])
+def test_loss_of_many_rows(n, dim, vocab, dtype):
+    """Several pieces of the vocabulary in the backward of either type, and in the forward of the second size."""
+    x, w, labels, g = loss_inputs(54, n, dim, vocab, dtype)
+    up = torch.rand(n, generator=g, device=DEV)
+    loss, _, _, count, dx, dw = run_loss(x, w, labels, dloss=up)
+    ref = loss_bounds(x, w, labels, up)
+    assert int(count) == int((labels >= 0).sum())
+    within("loss", loss, *ref["loss"])
+    within("dx", dx, *ref["dx"])
+    within("dw", dw, *ref["dw"])
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("vocab", [200, 70_000])
+def test_embed_gradient_of_millions(vocab):
+    """Beyond 2097152 positions the sort's offsets come from a launch of their own."""
+    g = gen(55)
+    n, dim = 2_500_007, 3
+    ids = (torch.rand(n, generator=g, device=DEV) ** 2 * (vocab + 1)).long() - 1
+    check_embed(randn(g, vocab, dim), ids, randn(g, n, dim), 1.5)
 
 
 def test_embed_of_more_rows_than_one_launch():
