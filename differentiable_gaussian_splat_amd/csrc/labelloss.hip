@@ -20,11 +20,12 @@
 // cost nothing and reach no sum.
 //
 // Types. bfloat16 rows are multiplied as they are, with float32 sums. Between
-// the products dz is bfloat16 (each entry off by half a step, 2^-8 of itself, at
-// most: float32 would take twice the bytes and three times the products), but for
-// the label's entry, most of a row's gradient: that one stays float32 and joins
-// dx and dw apart, in dw as sums over the rows of each label in a fixed order
-// (300 x 64 x 101: 6 us of 43; 8192 x 1024 x 65536: 56 us of 4.2 ms).
+// the products dz is two bfloat16 parts (to 2^-16 of each entry) where the
+// products are small. Where they are large it is one (each entry off by half a
+// step, 2^-8 of itself, at most: a second would take twice the bytes and twice the
+// products), but for the label's entry, most of a row's gradient: that one stays
+// float32 and joins dx and dw apart, in dw as sums over the rows of each label in
+// a fixed order (8192 x 1024 x 65536: 53 us of 4.4 ms).
 // float32 rows are split into three bfloat16 parts (8 + 8 + 8 bits: the value
 // to 2^-24) and six products of parts are summed, smallest first; what is left
 // out is below 2^-24 of the product of magnitudes, a float32 product's own
@@ -46,9 +47,9 @@ constexpr int BN = 128;         // columns of every product's tile (rows of x, o
 constexpr int GT = 256;         // threads: four waves, two blocks to a compute unit
 // A staged step: 32 deep and three of them in LDS (one read, two on their way),
 // or, with the three parts of split operands side by side, 16 deep and two:
-// the six products of a step make up for the shorter way ahead.
+// the six products of a step make up for the shorter way ahead. dz in two parts: 32 deep and two.
 constexpr int step_depth(int parts) { return parts == 3 ? 16 : 32; }
-constexpr int step_buffers(int parts) { return parts == 3 ? 2 : 3; }
+constexpr int step_buffers(int parts_b) { return parts_b > 1 ? 2 : 3; }
 constexpr int KPAD = 16;        // columns of packed operands are padded to it in float32, to twice it in bfloat16
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
@@ -71,7 +72,7 @@ struct Product {
     float* target;                // LSE: z at the label
     const float *lse, *dmean, *dloss;
     bf16* dz;                     // DZ: [parts][np][lddz]
-    float* own;                   // DZ, one part: per row, the label's entry (0 in dz)
+    float* own;                   // DZ, one part of dz: per row, the label's entry (0 in dz)
     int64_t lddz, pdz;
     float* acc;                   // DX, DW with splits: [split][rows][ldacc]
     int64_t ldacc, pacc;
@@ -79,7 +80,7 @@ struct Product {
     void* out;                    // DW without splits
     int64_t ldout;
     int out_dim, out_wide;
-    const int32_t* slot;          // DW, one part without splits: per column of dz, its row of own_sums + 1, or 0
+    const int32_t* slot;          // DW, one part of dz, no splits: per column of dz, its row of own_sums + 1, or 0
     const float* own_sums;        // the labels' entries times x, by label: [row][ldacc]
 };
 
@@ -179,9 +180,11 @@ __device__ __forceinline__ float exp_diff(float z, float ref) { return exp2_fast
 
 // Rows staged for TM row blocks per wave (a power of two, for the staging's lanes).
 constexpr int staged_rows(int tm, int parts) { return tm == 1 && parts == 1 ? 64 : tm <= 2 ? 128 : 256; }
-constexpr int tile_elements(int tm, int parts) {
-    return step_buffers(parts) * parts * (staged_rows(tm, parts) + BN) * step_depth(parts);
+constexpr int tile_elements(int tm, int parts, int parts_b) {
+    return step_buffers(parts_b) * (parts * staged_rows(tm, parts) + parts_b * BN) * step_depth(parts);
 }
+// The parts of operand b: dz's where it is one.
+constexpr int parts_of_b(int mode, int parts, int dzp) { return mode == DX || mode == DW ? dzp : parts; }
 
 // The logits of split operands that are no number because one of their values is infinite, or too large for a part's
 // product: the value stands in its first part alone, and its products with the other operand's later parts (0, or of
@@ -215,7 +218,7 @@ __device__ __forceinline__ void first_parts(const Product& p, int m, int n, f32x
 
 // One product, C[m][n] = sum_k A[m][k] B[n][k], by 64 TM x 128 tiles; a lane
 // holds, for one n, runs of four consecutive m. PARTS: 1, or 3 for split
-// operands.
+// operands; DZP: dz's parts.
 //
 // The loop keeps several steps in LDS: while one is multiplied the next are
 // loaded straight to LDS, and one barrier a step both publishes the arrived
@@ -230,12 +233,13 @@ __device__ __forceinline__ void first_parts(const Product& p, int m, int n, f32x
 // read without bank conflicts and 20 % of the time. 256 x 256 tiles (by eight
 // waves, or by four of 128 x 128), reads of the next fragments ahead of the
 // barrier, and raised priority of the products all measured within 3 %.
-template <int MODE, int PARTS, int TM, class T>
+template <int MODE, int PARTS, int DZP, int TM, class T>
 __device__ __forceinline__ void product(const Product& p, int block, bf16* s_tiles) {
     constexpr bool TA = MODE == DX || MODE == DW, TB = MODE == DW;
     constexpr int TN = 2, WM = 32 * TM, WN = 32 * TN;  // 2 x 2 waves of WM rows and WN columns
-    constexpr int BM = 2 * WM, SM = staged_rows(TM, PARTS), BK = step_depth(PARTS), BUFS = step_buffers(PARTS);
-    constexpr int STEP = PARTS * (SM + BN) * BK;  // elements of one staged step: the a tile's parts, then the b tile's
+    constexpr int PB = parts_of_b(MODE, PARTS, DZP);
+    constexpr int BM = 2 * WM, SM = staged_rows(TM, PARTS), BK = step_depth(PARTS), BUFS = step_buffers(PB);
+    constexpr int STEP = (PARTS * SM + PB * BN) * BK;  // elements of one staged step: the a tile's parts, then the b tile's
     const int cnt = *p.count;
     const int nn = MODE == DW ? p.n : cnt;
     const int mt = (p.m + BM - 1) / BM, nt = (nn + BN - 1) / BN;
@@ -274,7 +278,7 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
         for (int q = 0; q < PARTS; ++q)
             sa.load(a + q * p.pa, live ? ea * 2 : 0, lds0 + (buf * STEP + q * SM * BK) * 2);
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q)
+        for (int q = 0; q < PB; ++q)
             sb.load(b + q * p.pb, live ? eb * 2 : 0, lds0 + (buf * STEP + PARTS * SM * BK + q * BN * BK) * 2);
         ++kt;
     };
@@ -289,7 +293,7 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-    constexpr int LOADS = PARTS * (Stage<SM, TA, BK>::NI + Stage<BN, TB, BK>::NI);  // of one step
+    constexpr int LOADS = PARTS * Stage<SM, TA, BK>::NI + PB * Stage<BN, TB, BK>::NI;  // of one step
     for (int t = 0; t < BUFS - 1; ++t) issue(t);
     int buf = 0;
     for (int t = 0; t < steps; ++t) {
@@ -299,19 +303,20 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
         buf = buf == BUFS - 1 ? 0 : buf + 1;
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
-            bf16x8 fa[PARTS][TM], fb[PARTS][TN];
+            bf16x8 fa[PARTS][TM], fb[PB][TN];
 #pragma unroll
-            for (int q = PARTS - 1; q >= 0; --q) {
+            for (int q = PB - 1; q >= 0; --q) {  // PB >= PARTS
 #pragma unroll
-                for (int i = 0; i < TM; ++i) fa[q][i] = fragment<SM, TA, BK>(la + q * SM * BK, wm + 32 * i, kk);
+                for (int i = 0; i < TM; ++i)
+                    if (q < PARTS) fa[q][i] = fragment<SM, TA, BK>(la + q * SM * BK, wm + 32 * i, kk);
 #pragma unroll
                 for (int j = 0; j < TN; ++j) fb[q][j] = fragment<BN, TB, BK>(lb + q * BN * BK, wn + 32 * j, kk);
             }
             // the products of parts whose sizes add up to 2^-16 of the operands' and more, smallest first
 #pragma unroll
-            for (int sum = PARTS - 1; sum >= 0; --sum)
+            for (int sum = PB - 1; sum >= 0; --sum)
 #pragma unroll
-                for (int q = sum; q >= 0; --q)
+                for (int q = sum < PARTS ? sum : PARTS - 1; q >= 0; --q)
 #pragma unroll
                     for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -395,13 +400,13 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
                         for (int e = 0; e < 16; ++e) {
                             const bool is = at == 32 * i + 8 * (e / 4) + e % 4;
                             acc[i][j][e] -= is ? 1.f : 0.f;
-                            if (PARTS == 1) {
+                            if (DZP == 1) {
                                 own = is ? acc[i][j][e] : own;
                                 acc[i][j][e] = is ? 0.f : acc[i][j][e];
                             }
                             here = here || is;
                         }
-                    if (PARTS == 1 && here && lab >= 0) p.own[n] = own * up;
+                    if (DZP == 1 && here && lab >= 0) p.own[n] = own * up;
                 }
                 // dz is zero for rows past the labelled ones (read up to whole steps by dw's product; z there is no
                 // number where a label's row is infinite) and past the vocabulary
@@ -428,7 +433,7 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
 #pragma unroll
                         for (int c = 0; c < 8; ++c) g[c] = acc[i][j][e + c] * up;
 #pragma unroll
-                        for (int c = 0; c < PARTS; ++c) {
+                        for (int c = 0; c < DZP; ++c) {
                             union {
                                 bf16x4 v[2];
                                 uint32_t u[4];
@@ -437,7 +442,7 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
                             for (int k = 0; k < 8; ++k) {
                                 const bf16 b = (bf16)g[k];
                                 o.v[k / 4][k % 4] = b;
-                                if (c + 1 < PARTS) g[k] -= (float)b;
+                                if (c + 1 < DZP) g[k] -= (float)b;
                             }
                             auto x0 = __builtin_amdgcn_permlane32_swap(o.u[0], o.u[2], false, false);
                             auto x1 = __builtin_amdgcn_permlane32_swap(o.u[1], o.u[3], false, false);
@@ -471,7 +476,7 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
                     }
             } else {
                 T* q = static_cast<T*>(p.out) + n * p.ldout + mb;
-                if constexpr (MODE == DW && PARTS == 1) {
+                if constexpr (MODE == DW && DZP == 1) {
                     const int slot = p.slot[n];
                     if (slot) {
                         const float* own = p.own_sums + (int64_t)(slot - 1) * p.ldacc + mb;
@@ -514,21 +519,21 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
     }
 }
 
-template <int MODE, int PARTS, int TM, class T>
+template <int MODE, int PARTS, int DZP, int TM, class T>
 __global__ __launch_bounds__(GT, 2) void k_product(Product p) {
-    __shared__ __align__(16) bf16 s_tiles[tile_elements(TM, PARTS)];
-    product<MODE, PARTS, TM, T>(p, blockIdx.x, s_tiles);
+    __shared__ __align__(16) bf16 s_tiles[tile_elements(TM, PARTS, parts_of_b(MODE, PARTS, DZP))];
+    product<MODE, PARTS, DZP, TM, T>(p, blockIdx.x, s_tiles);
 }
 
 // dx and dw, which read the same dz, in one launch: together they fill the chip better, and small ones wait once.
-template <int PARTS, int TM, class T>
+template <int PARTS, int DZP, int TM, class T>
 __global__ __launch_bounds__(GT, 2) void k_product_pair(Product dx, Product dw) {
-    __shared__ __align__(16) bf16 s_tiles[tile_elements(TM, PARTS)];
+    __shared__ __align__(16) bf16 s_tiles[tile_elements(TM, PARTS, DZP)];
     const int first = dx.grid * dx.splits;
     if ((int)blockIdx.x < first)
-        product<DX, PARTS, TM, T>(dx, blockIdx.x, s_tiles);
+        product<DX, PARTS, DZP, TM, T>(dx, blockIdx.x, s_tiles);
     else
-        product<DW, PARTS, TM, T>(dw, blockIdx.x - first, s_tiles);
+        product<DW, PARTS, DZP, TM, T>(dw, blockIdx.x - first, s_tiles);
 }
 
 // ---------------------------------------------------------------- labelled rows
@@ -642,15 +647,12 @@ struct PackArgs {
     int64_t xs, ws, w_rows;
     bf16 *xp, *wp;
     int64_t x_part, w_part;  // distance of the parts
-    int32_t* slot;           // nullable: vocab words to clear
 };
 
 template <class T, int PARTS, bool SMALL>
 __global__ __launch_bounds__(PT) void k_pack(LabelRows a, PackArgs p) {
     __shared__ int s_w[2 * PT / 64];
     __shared__ int s_list[SMALL ? PROWS : 1];
-    if (p.slot)
-        for (int64_t v = blockIdx.x * PT + threadIdx.x; v < a.vocab; v += (int64_t)gridDim.x * PT) p.slot[v] = 0;
     const bool x = (int)blockIdx.x < p.x_blocks;
     const int64_t r0 = (int64_t)(blockIdx.x - (x ? 0 : p.x_blocks)) * p.per_block;
     int64_t live = p.w_rows, padded = p.w_rows;
@@ -714,91 +716,6 @@ __global__ __launch_bounds__(PT) void k_pack(LabelRows a, PackArgs p) {
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) *reinterpret_cast<bf16x8*>(dst + q * part + r * p.kp + c) = o[q];
     }
-}
-
-// ---------------------------------------------------------------- the labels' own entries
-
-constexpr int OWN_T = 256;
-// Rows up to which each looks through all labels for its own: n^2 comparisons, but one launch (1000 rows: 9.7 us,
-// sorted and summed 14 in three launches; 4000: 21 and 20). Beyond, the rows are sorted by label.
-constexpr int OWN_FEW = 4096;
-
-// Few rows' part of dw from the labels' entries of dz: a block per labelled row, of which the first of its label
-// sums own x over that label's rows (in order per lane group, then over the groups) into its row of sums.
-__global__ __launch_bounds__(OWN_T) void k_own_sums(LabelRows a, WeighedRows w) {
-    __shared__ uint16_t s_list[OWN_FEW];
-    __shared__ int s_count[OWN_T / 64];
-    __shared__ __align__(16) float s_sum[OWN_T * 8];
-    const int i = blockIdx.x;
-    if (i >= *a.count) return;
-    const int row = a.rows[i], lab = row_index(a.labels, a.wide, row, a.vocab);
-    if ((uint32_t)lab < w.first || (uint32_t)lab >= w.last) return;
-    const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int strips = ((int)a.n + OWN_T - 1) / OWN_T;  // of 64 rows for each wave, one after the other
-    auto names = [&](int k) {
-        const int r = (wv * strips + k) * 64 + lane;
-        return r < a.n && row_index(a.labels, a.wide, r, a.vocab) == lab;
-    };
-    int own = 0;
-    bool earlier = false;
-#pragma unroll 4
-    for (int k = 0; k < strips; ++k) {
-        const bool m = names(k);
-        earlier = earlier || (m && (wv * strips + k) * 64 + lane < row);
-        own += __popcll(__ballot(m));
-    }
-    if (lane == 0) s_count[wv] = own;
-    if (__syncthreads_or(earlier)) return;
-    int to = 0, rows = 0;
-    for (int k = 0; k < OWN_T / 64; ++k) {
-        to += k < wv ? s_count[k] : 0;
-        rows += s_count[k];
-    }
-    if (own)
-        for (int k = 0; k < strips; ++k) {
-            const bool m = names(k);
-            const uint64_t all = __ballot(m);
-            if (m)
-                s_list[to + __popcll(all & (((uint64_t)1 << lane) - 1))] =
-                    (uint16_t)w.place[(wv * strips + k) * 64 + lane];
-            to += __popcll(all);
-        }
-    __syncthreads();
-    int tr = 4;  // lanes per row, 16 bytes each
-    while (tr < OWN_T && tr * 8 < w.ld) tr *= 2;
-    const int groups = OWN_T / tr, g = threadIdx.x / tr, l = threadIdx.x % tr;
-    for (int64_t c0 = 0; c0 < w.ld; c0 += OWN_T * 8) {
-        const int64_t c = c0 + l * 8;
-        float acc[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-        if (c < w.ld)
-#pragma unroll 8
-            for (int k = g; k < rows; k += groups) {
-                const int at = s_list[k];
-                const float f = w.weight[at];
-                const bf16x8 v = *reinterpret_cast<const bf16x8*>(static_cast<const bf16*>(w.src) + at * w.ld + c);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = fmaf(f, (float)v[e], acc[e]);
-            }
-        const int used = min(groups, rows);
-        if (used > 1) {
-            __syncthreads();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s_sum[e * OWN_T + threadIdx.x] = acc[e];
-            __syncthreads();
-            if (g == 0)
-                for (int q = 1; q < used; ++q)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] += s_sum[e * OWN_T + q * tr + l];
-        }
-        if (g == 0 && c < w.ld) {
-            float4* d = reinterpret_cast<float4*>(w.sums + i * w.ld + c);
-            d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            d[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-        }
-    }
-    if (threadIdx.x == 0) w.slot[lab] = i + 1;
 }
 
 // ---------------------------------------------------------------- joins
@@ -1044,7 +961,7 @@ Side short_side(int64_t n, int dim, int vocab, bool half) {
 }
 
 struct LossPlan {
-    int parts, kp;
+    int parts, dzp, kp;            // of the operands, of dz
     int64_t np;                    // rows of x padded to the tile
     int64_t piece_f, piece_b;      // vocabulary rows per piece (whole tiles)
     int tm_z, tm_d;                // row blocks per wave: over the vocabulary, over dim
@@ -1053,7 +970,7 @@ struct LossPlan {
     int flat_tr, flat_slabs, flat_chunks;
     size_t g;
     size_t rows, place, count, done, block_count, xp, wp, part, target, state, block_sum, dz, own, dxp, dwp, total;
-    size_t by_label, slot, own_sums;  // bfloat16's backward: the rows by label, and their sums
+    size_t by_label, slot, own_sums;  // one part of dz: the rows by label, and their sums
 };
 
 constexpr int ROW_BLOCKS = 512;  // blocks of the few rows' forward: slabs to join
@@ -1062,11 +979,19 @@ constexpr int ROW_BLOCKS = 512;  // blocks of the few rows' forward: slabs to jo
 int few_bucket(int64_t vocab) { return vocab <= 4 ? 4 : vocab <= 8 ? 8 : vocab <= 16 ? 16 : vocab <= 32 ? 32 : 64; }
 int few_columns(int64_t vocab) { return vocab <= 8 ? 4 : 2; }
 
+// bfloat16 dz is in two parts (to 2^-16) where that costs less than keeping the labels' entries apart: up to so many
+// multiplications in a product. With gradients, us, two parts and apart (and with plain bfloat16 dz): 300 x 64 x 101
+// 36, 50 (37); 4000 x 64 x 2000 69, 88 (65); 46272 x 896 x 20 271, 332 (291); 65536 x 64 x 500 191, 195 (158); beyond,
+// 65536 x 64 x 1000 258, 239 (200); 300 x 64 x 100000 191, 152 (139); 20000 x 256 x 3000 318, 286 (254); but
+// 8192 x 512 x 1000 135, 154 (119).
+constexpr int64_t TWO_PARTS = (int64_t)1 << 31;
+
 LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     LossPlan L{};
     L.parts = half ? 1 : 3;
     L.kp = (int)up(dim, half ? 2 * KPAD : KPAD);
     L.np = up(n > 0 ? n : 1, BN);
+    L.dzp = !half ? 3 : (double)L.np * L.kp * vocab <= (double)TWO_PARTS ? 2 : 1;
     L.tm_z = tm_vocab(vocab, L.np);
     const int64_t unit = 64 * L.tm_z, vp = up(vocab, unit);
     auto piece = [&](int64_t budget) {  // vocabulary rows whose per-row cost fits the budget, in whole tiles
@@ -1074,7 +999,7 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
         return v < unit ? unit : v > vp ? vp : v;
     };
     L.piece_f = piece((int64_t)1 << 30);  // 8 bytes per 32 vocabulary rows at least: 256 MB
-    L.piece_b = piece(((int64_t)1 << 28) / L.parts);  // 2 bytes per part: 512 MB
+    L.piece_b = piece(((int64_t)1 << 28) / L.dzp);  // 2 bytes per part: 512 MB, or one tile's where that is more
     L.tm_d = tm_dim(L.kp);
     const int64_t mt = up(L.kp, 64 * L.tm_d) / (64 * L.tm_d);
     // dx and dw run in one launch: their depths are split so that all blocks have about one share of it
@@ -1121,10 +1046,10 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
     L.xp = take((size_t)L.parts * L.np * L.kp * 2);
     L.wp = take((size_t)L.parts * vocab * L.kp * 2);
     if (backward) {
-        L.dz = take((size_t)L.parts * L.np * L.piece_b * 2);
-        if (half) {
+        L.dz = take((size_t)L.dzp * L.np * L.piece_b * 2);
+        if (L.dzp == 1) {
             L.own = take((size_t)L.np * 4);
-            if (n > OWN_FEW) L.by_label = take(embed_bwd_layout(n, L.kp, vocab).total);
+            L.by_label = take(embed_bwd_layout(n, L.kp, vocab).total);
             L.slot = take((size_t)vocab * 4);
             L.own_sums = take((size_t)L.np * L.kp * 4);
         }
@@ -1151,30 +1076,30 @@ void set_grid(Product& p, int tm, int64_t m, int64_t n) {
     p.grid = (int)(t < 8 ? 8 : up(t, 8));
 }
 
-template <int MODE, int PARTS, class T>
+template <int MODE, int PARTS, int DZP, class T>
 void launch_product(int tm, const Product& p, hipStream_t s) {
     const unsigned grid = (unsigned)p.grid * p.splits;
     if (tm == 4)
-        k_product<MODE, PARTS, 4, T><<<grid, GT, 0, s>>>(p);
+        k_product<MODE, PARTS, DZP, 4, T><<<grid, GT, 0, s>>>(p);
     else if (tm == 3)
-        k_product<MODE, PARTS, 3, T><<<grid, GT, 0, s>>>(p);
+        k_product<MODE, PARTS, DZP, 3, T><<<grid, GT, 0, s>>>(p);
     else if (tm == 2)
-        k_product<MODE, PARTS, 2, T><<<grid, GT, 0, s>>>(p);
+        k_product<MODE, PARTS, DZP, 2, T><<<grid, GT, 0, s>>>(p);
     else
-        k_product<MODE, PARTS, 1, T><<<grid, GT, 0, s>>>(p);
+        k_product<MODE, PARTS, DZP, 1, T><<<grid, GT, 0, s>>>(p);
 }
 
-template <int PARTS, class T>
+template <int PARTS, int DZP, class T>
 void launch_pair(int tm, const Product& dx, const Product& dw, hipStream_t s) {
     const unsigned grid = (unsigned)dx.grid * dx.splits + (unsigned)dw.grid * dw.splits;
     if (tm == 4)
-        k_product_pair<PARTS, 4, T><<<grid, GT, 0, s>>>(dx, dw);
+        k_product_pair<PARTS, DZP, 4, T><<<grid, GT, 0, s>>>(dx, dw);
     else if (tm == 3)
-        k_product_pair<PARTS, 3, T><<<grid, GT, 0, s>>>(dx, dw);
+        k_product_pair<PARTS, DZP, 3, T><<<grid, GT, 0, s>>>(dx, dw);
     else if (tm == 2)
-        k_product_pair<PARTS, 2, T><<<grid, GT, 0, s>>>(dx, dw);
+        k_product_pair<PARTS, DZP, 2, T><<<grid, GT, 0, s>>>(dx, dw);
     else
-        k_product_pair<PARTS, 1, T><<<grid, GT, 0, s>>>(dx, dw);
+        k_product_pair<PARTS, DZP, 1, T><<<grid, GT, 0, s>>>(dx, dw);
 }
 
 LabelRows label_arrays(const LabelLossArgs& a, const LossPlan& L, char* ws, bool forward) {
@@ -1200,8 +1125,7 @@ void list_rows(const LabelRows& r, const LossPlan& L, char* ws, hipStream_t s) {
 }
 
 template <class T>
-hipError_t prepare(const LabelLossArgs& a, const LossPlan& L, char* ws, bool forward, Packed& pk, int32_t* slot,
-                   hipStream_t s) {
+hipError_t prepare(const LabelLossArgs& a, const LossPlan& L, char* ws, bool forward, Packed& pk, hipStream_t s) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
     const LabelRows r = label_arrays(a, L, ws, forward);
     PackArgs p{};
@@ -1216,7 +1140,6 @@ hipError_t prepare(const LabelLossArgs& a, const LossPlan& L, char* ws, bool for
     p.wp = (bf16*)(ws + L.wp);
     p.x_part = L.np * L.kp;
     p.w_part = (int64_t)a.vocab * L.kp;
-    p.slot = slot;
     p.x_blocks = (int)((L.np + p.per_block - 1) / p.per_block);
     pk.pw = p.w_part;
     if (PARTS == 1 && (uintptr_t)a.w % 16 == 0 && a.w_stride % 8 == 0 && a.dim == L.kp && a.w_stride <= 1 << 20) {
@@ -1370,7 +1293,7 @@ hipError_t loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
     const LossPlan L = loss_plan(a.n, a.dim, a.vocab, PARTS == 1, false);
     if (L.shorter != NEITHER) return flat_loss<T>(a, L, ws, true, s);
     Packed pk{};
-    hipError_t e = prepare<T>(a, L, ws, true, pk, nullptr, s);
+    hipError_t e = prepare<T>(a, L, ws, true, pk, s);
     if (e != hipSuccess) return e;
     float2 *part = (float2*)(ws + L.part), *state = (float2*)(ws + L.state);
     double* bs = (double*)(ws + L.block_sum);
@@ -1389,7 +1312,7 @@ hipError_t loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         p.part = part;
         p.target = (float*)(ws + L.target);
         set_grid(p, L.tm_z, mv, a.n);
-        launch_product<LSE, PARTS, T>(L.tm_z, p, s);
+        launch_product<LSE, PARTS, PARTS, T>(L.tm_z, p, s);
         // every tile writes its slabs, so the last may lie beyond the vocabulary (an empty one)
         const int slabs = (int)(up(mv, 64 * L.tm_z) / (32 * L.tm_z));
         launch_ranges(a.n > 0 ? (a.n + JR - 1) / JR : 1, [&](unsigned blocks, BlockRange range) {
@@ -1401,17 +1324,14 @@ hipError_t loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <class T>
-hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
+template <class T, int DZP>
+hipError_t loss_bwd(const LabelLossArgs& a, const LossPlan& L, char* ws, hipStream_t s) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
-    const LossPlan L = loss_plan(a.n, a.dim, a.vocab, PARTS == 1, true);
-    if (L.shorter != NEITHER) return flat_loss<T>(a, L, ws, false, s);
     Packed pk{};
-    const bool apart = PARTS == 1 && a.dw;  // the labels' entries join dw apart
-    const bool few = a.n <= OWN_FEW;
-    int32_t* slot = (int32_t*)(ws + L.slot);
-    hipError_t e = prepare<T>(a, L, ws, false, pk, apart && few ? slot : nullptr, s);
+    hipError_t e = prepare<T>(a, L, ws, false, pk, s);
     if (e != hipSuccess) return e;
+    const bool apart = DZP == 1 && a.dw;  // the labels' entries join dw apart (and dx)
+    int32_t* slot = (int32_t*)(ws + L.slot);
     const bf16* xp = (const bf16*)(ws + L.xp);
     bf16* dz = (bf16*)(ws + L.dz);
     float *dxp = (float*)(ws + L.dxp), *dwp = (float*)(ws + L.dwp);
@@ -1424,9 +1344,7 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         own.ld = L.kp;
         own.sums = (float*)(ws + L.own_sums);
         own.slot = slot;
-        if (!few)
-            e = launch_rows_by_index(a.n, a.vocab, a.labels, a.wide_labels, L.kp, slot, ws + L.by_label, &sorted_at,
-                                     s);
+        e = launch_rows_by_index(a.n, a.vocab, a.labels, a.wide_labels, L.kp, slot, ws + L.by_label, &sorted_at, s);
         if (e != hipSuccess) return e;
     }
     for (int64_t v0 = 0; v0 < a.vocab; v0 += L.piece_b) {
@@ -1446,14 +1364,11 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
         p.pdz = L.np * L.piece_b;
         p.own = (float*)(ws + L.own);
         set_grid(p, L.tm_z, mv, a.n);
-        launch_product<DZ, PARTS, T>(L.tm_z, p, s);
+        launch_product<DZ, PARTS, DZP, T>(L.tm_z, p, s);
         if (apart) {
             own.first = (uint32_t)v0;
             own.last = (uint32_t)(v0 + mv);
-            if (!few)
-                e = launch_weighed_rows(a.n, a.vocab, sorted_at, own, ws + L.by_label, s);
-            else if (a.n > 0)
-                k_own_sums<<<(unsigned)a.n, OWN_T, 0, s>>>(label_arrays(a, L, ws, false), own);
+            e = launch_weighed_rows(a.n, a.vocab, sorted_at, own, ws + L.by_label, s);
             if (e != hipSuccess) return e;
         }
         const bool last = v0 + L.piece_b >= a.vocab;
@@ -1482,7 +1397,7 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
                 jx.place = (const int32_t*)(ws + L.place);
                 jx.out = a.dx;
                 jx.ldout = a.dx_stride;
-                if (PARTS == 1) {
+                if (DZP == 1) {
                     jx.own = p.own;
                     jx.labels = a.labels;
                     jx.wide = a.wide_labels;
@@ -1531,11 +1446,11 @@ hipError_t loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t s) {
             }
         }
         if (a.dx && a.dw)
-            launch_pair<PARTS, T>(L.tm_d, qx, qw, s);
+            launch_pair<PARTS, DZP, T>(L.tm_d, qx, qw, s);
         else if (a.dx)
-            launch_product<DX, PARTS, T>(L.tm_d, qx, s);
+            launch_product<DX, PARTS, DZP, T>(L.tm_d, qx, s);
         else
-            launch_product<DW, PARTS, T>(L.tm_d, qw, s);
+            launch_product<DW, PARTS, DZP, T>(L.tm_d, qw, s);
         const int per = (a.dim + 3) / 4, per_block = (1024 + per - 1) / per;
         jx.blocks = (int)((jx.rows + per_block - 1) / per_block);
         jw.blocks = (int)((jw.rows + per_block - 1) / per_block);
@@ -1560,7 +1475,12 @@ hipError_t launch_label_loss_fwd(const LabelLossArgs& a, char* ws, hipStream_t s
 }
 
 hipError_t launch_label_loss_bwd(const LabelLossArgs& a, char* ws, hipStream_t stream) {
-    return a.half ? loss_bwd<bf16>(a, ws, stream) : loss_bwd<float>(a, ws, stream);
+    const LossPlan L = loss_plan(a.n, a.dim, a.vocab, a.half, true);
+    if (L.shorter != NEITHER)
+        return a.half ? flat_loss<bf16>(a, L, ws, false, stream) : flat_loss<float>(a, L, ws, false, stream);
+    return !a.half      ? loss_bwd<float, 3>(a, L, ws, stream)
+           : L.dzp == 2 ? loss_bwd<bf16, 2>(a, L, ws, stream)
+                        : loss_bwd<bf16, 1>(a, L, ws, stream);
 }
 
 }  // namespace gs

@@ -677,10 +677,11 @@ gs_status gs_label_loss_fwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype
  * dmean[0] / labelled rows (dmean[1], of their mean); either may be NULL, not
  * both. dx[n, dim] (zero rows where there is no label), dw[vocab, dim], each
  * nullable. Workspace: gs_label_loss_workspace_size with backward = 1.
- * With bfloat16 rows the gradient of the logits, dz, is rounded to bfloat16 on
- * its way into dx and dw (each entry by 2^-8 of itself at most), except where
- * vocab <= 16, n <= 16 with vocab * dim <= 2^20, or the entry is its row's
- * label's: those stay float32.
+ * With bfloat16 rows the gradient of the logits, dz, is rounded on its way into
+ * dx and dw: each entry by 2^-16 of itself at most where n * dim * vocab is up to
+ * 2^31 or somewhat less (n, dim rounded up to multiples of 128, 32), by 2^-8
+ * beyond, except its row's label's entry, which stays float32. (All of dz does
+ * with vocab <= 16, or n <= 16 and vocab * dim <= 2^20.)
  */
 gs_status gs_label_loss_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype, const void *x,
                             int64_t x_stride, const void *w, int64_t w_stride, const void *labels,

@@ -75,11 +75,11 @@ def test_loss_dw_is_little_more_than_rounded(n, rows):
     assert (dw.double() - ref)[named].norm() <= 1.25 * own
 
 
-def test_loss_label_entries_of_one_label():
+@pytest.mark.parametrize("n,dim,vocab", [(20_000, 72, 300), (20_000, 200, 3000), (3000, 1030, 2000)])
+def test_loss_label_entries_of_one_label(n, dim, vocab):
     """Nearly all rows name one label: its gradient is one long sum, in a fixed order."""
-    n, dim, vocab = 20_000, 72, 300
     x, w, labels, g = loss_inputs(42, n, dim, vocab, BF16, missing=0.0)
-    labels = torch.where(torch.rand(n, generator=g, device=DEV) < 0.9, 299, labels)
+    labels = torch.where(torch.rand(n, generator=g, device=DEV) < 0.9, vocab - 1, labels)
     labels[::7] = -1
     up = torch.rand(n, generator=g, device=DEV)
     a, b = (run_loss(x, w, labels, dloss=up) for _ in range(2))
