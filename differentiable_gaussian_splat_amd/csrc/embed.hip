@@ -11,7 +11,8 @@
 // last run, where it goes on in a neighbouring block, as a partial sum. A last
 // launch adds the partial sums of each such row in block order. A row that half
 // of the positions name is thus spread over as many blocks as any other half,
-// there are no atomics, and the sums are the same bit for bit from run to run.
+// and the sums are the same bit for bit from run to run: no atomic takes part in
+// them (the sort counts digits with integer ones, which come out the same).
 // All sums are float32, rounded once. The vocabulary loss sums weighed rows by
 // label in the same way (WeighedRows).
 //
@@ -29,7 +30,9 @@ namespace {
 
 constexpr int EB = 256;         // threads per block
 constexpr int RUN_USUAL = 16;  // sorted positions a row group sums, all loaded at once; twice that ...
-constexpr int64_t RUN_LONG = 400000;  // ... from this many positions on: fewer partial sums to join
+// ... from this many positions on: fewer partial sums to join (us, 16 and 32 positions: 1M x 64 float32 189 and 186,
+// 400000 x 64 94.5 and 93.5, 250000 x 64 62.7 and 61, 100000 x 64 37.8 and 38.9)
+constexpr int64_t RUN_LONG = 400000;
 // Where there are few blocks, a group's sums one after the other take the time, so it has fewer, up to RUN_SHORT
 // positions (3487 x 2 bf16 10.5 us against 16, 300 x 64 5.3 and a join of 2.7 against 6.8, 8192 x 64 float32 4.9
 // against 5.7; 32768 x 500 would take 17 and a join of 11 against 16 and 4.6).

@@ -16,8 +16,9 @@
 //             two products read it: dx += dz w and dw = dz^T x.
 // Rows without a label are left out before the products: a list of the
 // labelled rows is made first, x is packed through it, and the number of tiles
-// follows the count on the device, so unlabelled rows (whatever they hold)
-// cost nothing and reach no sum.
+// follows the count on the device, so unlabelled rows (whatever they hold) are
+// not multiplied and reach no sum. Tile sizes, splits and workspace are chosen on
+// the host for all rows, so that few labelled ones leave parts of the chip idle.
 //
 // Types. bfloat16 rows are multiplied as they are, with float32 sums. Between
 // the products dz is two bfloat16 parts (to 2^-16 of each entry) where the
@@ -26,10 +27,10 @@
 // products), but for the label's entry, most of a row's gradient: that one stays
 // float32 and joins dx and dw apart, in dw as sums over the rows of each label in
 // a fixed order (8192 x 1024 x 65536: 53 us of 4.4 ms).
-// float32 rows are split into three bfloat16 parts (8 + 8 + 8 bits: the value
-// to 2^-24) and six products of parts are summed, smallest first; what is left
-// out is below 2^-24 of the product of magnitudes, a float32 product's own
-// rounding. The matrix units take bfloat16 sixteen times as fast as float32,
+// float32 rows are split into three bfloat16 parts (8 + 8 + 8 bits, all of the
+// value) and six products of parts are summed, smallest first; the three left
+// out are below 2 x 2^-24 + 2^-32 of the product of magnitudes, near a float32
+// product's own rounding. The matrix units take bfloat16 sixteen times as fast as float32,
 // so six products are cheaper than one. Where one side is short the kernels of
 // flatloss.hpp take over.
 #include "elem.hpp"
@@ -226,11 +227,12 @@ __device__ __forceinline__ void first_parts(const Product& p, int m, int n, f32x
 // empty extent (they bring zeros), which keeps the count of loads in flight
 // the same in every step.
 //
-// 8192 x 1024 x 65536 bfloat16: LSE 1.12 ms (0.98 PFLOP/s), DZ 1.28 (0.86),
-// DX and DW together 2.02 (1.09); a large library product reaches 1.25 to 1.49,
-// the matrix units alone on random data 1.84 (they are held by the chip's power:
-// 2.4 on zeros). The units are busy 52 to 56 % of the time at 1.8 GHz; LDS is
-// read without bank conflicts and 20 % of the time. 256 x 256 tiles (by eight
+// 8192 x 1024 x 65536 bfloat16: LSE 1.16 ms (0.95 PFLOP/s), DZ 1.29 (0.85),
+// DX and DW together 2.08 (1.06); a large library product reaches 1.25 to 1.49,
+// the matrix units alone on random data 1.84 (2.4 on zeros). The units are busy
+// 52 % of the time in LSE, 43 in DZ and 57 in the pair, at 1.8 GHz: the epilogues
+// run beside no product, and what holds the rest was not found. LDS is read
+// without bank conflicts and 20 % of the time. 256 x 256 tiles (by eight
 // waves, or by four of 128 x 128), reads of the next fragments ahead of the
 // barrier, and raised priority of the products all measured within 3 %.
 template <int MODE, int PARTS, int DZP, int TM, class T>
@@ -239,7 +241,7 @@ __device__ __forceinline__ void product(const Product& p, int block, bf16* s_til
     constexpr int TN = 2, WM = 32 * TM, WN = 32 * TN;  // 2 x 2 waves of WM rows and WN columns
     constexpr int PB = parts_of_b(MODE, PARTS, DZP);
     constexpr int BM = 2 * WM, SM = staged_rows(TM, PARTS), BK = step_depth(PARTS), BUFS = step_buffers(PB);
-    constexpr int STEP = (PARTS * SM + PB * BN) * BK;  // elements of one staged step: the a tile's parts, then the b tile's
+    constexpr int STEP = (PARTS * SM + PB * BN) * BK;  // elements of a staged step: the a tile's parts, then the b tile's
     const int cnt = *p.count;
     const int nn = MODE == DW ? p.n : cnt;
     const int mt = (p.m + BM - 1) / BM, nt = (nn + BN - 1) / BN;
@@ -950,9 +952,9 @@ enum Side { NEITHER, LABELS, ROWS };
 // grow with the short side, the tiled products' cost with the next 128 of it.
 // float32 products (six of bfloat16) lose up to SHORT: 46272 x 896 x 64 with
 // gradients 0.38 ms flat, 0.59 tiled (x 65); 64 x 1024 x 65536 0.52 and 0.92.
-// bfloat16 ones win from 16 labels on (46272 x 896 x 20: 0.42 flat, 0.26
+// tiled bfloat16 ones win from 17 labels on (46272 x 896 x 20: 0.42 flat, 0.28
 // tiled), and over few rows unless all of it is small (16 x 32 x 1000: 29 us
-// flat, 33 tiled; 16 x 64 x 20000: 52 and 44).
+// flat, 31 tiled; 16 x 64 x 8000: 43 and 39; x 20000: 53 and 50).
 Side short_side(int64_t n, int dim, int vocab, bool half) {
     const int most = half ? 16 : SHORT;
     if (vocab <= most) return LABELS;
@@ -998,7 +1000,7 @@ LossPlan loss_plan(int64_t n, int dim, int vocab, bool half, bool backward) {
         const int64_t v = budget / L.np / unit * unit;
         return v < unit ? unit : v > vp ? vp : v;
     };
-    L.piece_f = piece((int64_t)1 << 30);  // 8 bytes per 32 vocabulary rows at least: 256 MB
+    L.piece_f = piece((int64_t)1 << 30);  // 8 bytes per 32 vocabulary rows at most: 256 MB (or one tile's)
     L.piece_b = piece(((int64_t)1 << 28) / L.dzp);  // 2 bytes per part: 512 MB, or one tile's where that is more
     L.tm_d = tm_dim(L.kp);
     const int64_t mt = up(L.kp, 64 * L.tm_d) / (64 * L.tm_d);

@@ -1,7 +1,7 @@
 """Learning labels of a scene: feature codebook, layer normalisation, vocabulary loss.
 
-A scene's Gaussians (or the pixels of a view) carry features that are scored
-against a vocabulary of labels. Three operators do that, each with its
+A scene's Gaussians (or any other rows) carry features that are scored against a
+vocabulary of labels. Three operators do that, each with its
 gradients, in float32 or bfloat16:
 
 - :func:`embed` looks a feature codebook up by each Gaussian's code;
