@@ -8,8 +8,8 @@ import pytest
 import torch
 
 from differentiable_gaussian_splat_amd import labels as L
-from tests.test_gpu_labels import (BF16, DEV, F32, IDS, ONE, TYPES, U, check_embed, gen, half_step, loss_inputs, randn,
-                                   run_loss, within)
+from tests.test_gpu_labels import (BF16, DEV, F32, IDS, ONE, TYPES, U, check_embed, empty, gen, half_step, loss_inputs,
+                                   randn, run_loss, within, ws_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -56,6 +56,30 @@ def test_loss_label_entry_is_not_rounded(n, dim, vocab):
     ref = loss_bounds(x, w, labels, torch.full((n,), 1.0 / int(count), device=DEV))
     within("dx", dx, *ref["dx"])
     within("dw", dw, *ref["dw"])
+
+
+def test_loss_label_entries_of_many_rows():
+    """From 400,000 rows on a lane group sums 32 of a label."""
+    n, vocab = 450_001, 201
+    x, w, labels, g = loss_inputs(56, n, 20, vocab, BF16)
+    up = torch.rand(n, generator=g, device=DEV)
+    dx, dw = run_loss(x, w, labels, dloss=up)[4:]
+    ref = loss_bounds(x, w, labels, up)
+    within("dx", dx, *ref["dx"])
+    within("dw", dw, *ref["dw"])
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("n,dim,vocab", [(700, 96, 500), (3000, 256, 4000)])
+def test_loss_either_gradient_alone(n, dim, vocab):
+    x, w, labels, _ = loss_inputs(57, n, dim, vocab, BF16)
+    both = run_loss(x, w, labels, dmean=ONE())
+    ws = ws_of(L.gs_label_loss_workspace_size(n, dim, vocab, BF16, True))
+    dx, dw = empty(n, dim, dtype=BF16), empty(vocab, dim, dtype=BF16)
+    L.gs_label_loss_bwd(x, w, labels, both[1], dx, None, ws, dmean=ONE())
+    ws.fill_(0xFF)
+    L.gs_label_loss_bwd(x, w, labels, both[1], None, dw, ws, dmean=ONE())
+    assert torch.equal(dx, both[4]) and torch.equal(dw, both[5])
 
 
 @pytest.mark.parametrize("n", [300, 2900, 12_345])
