@@ -157,7 +157,7 @@ def prepare(case, seed):
     s = dict(case=case)
     if case["op"] == "clip":
         sizes = _sizes(case)
-        kinds = {"f32": [torch.float32], "bf16": [torch.bfloat16], "both": [torch.float32, torch.bfloat16]}[case["dtype"]]
+        kinds = [torch.float32, torch.bfloat16] if case["dtype"] == "both" else [TYPES[case["dtype"]]]
         kinds = [kinds[i % len(kinds)] for i in range(len(sizes))]
         # gradients of a factor of a hundred between tensors, as groups of parameters have
         size_of = [10.0 ** (i % 3 - 2) for i in range(len(sizes))]
