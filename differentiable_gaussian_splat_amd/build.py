@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgsplat_hip.so")
 SOURCES = ["api.hip", "preprocess.hip", "binsort.hip", "render.hip", "surfel.hip", "optim.hip",
-           "embed.hip", "norm.hip", "labelloss.hip", "microbench.hip"]
+           "embed.hip", "norm.hip", "rmsnorm.hip", "scores.hip", "labelloss.hip", "clip.hip", "microbench.hip"]
 
 ARCH = "gfx950"
 CFLAGS = [

@@ -12,6 +12,7 @@
 #include "../../include/gsplat.h"
 #include "common.hpp"
 #include "launch.hpp"
+#include "rows8.hpp"
 
 namespace {
 
@@ -1138,6 +1139,35 @@ bool rows_ok(int64_t n, int64_t dim, int64_t vocab, int32_t dtype) {
         if (st_ != GS_OK) return st_;      \
     } while (0)
 
+// The inputs that both forms of the root-mean-square normalisation share, and the sum they hand on.
+gs_status check_rms_inputs(const char* fn, int64_t n, int64_t dim, int32_t dtype, const void* x, int64_t x_stride,
+                           const void* residual, int64_t residual_stride, const void* weight, float eps,
+                           const void* sum, int64_t sum_stride) {
+    REQUIRE(isfinite(eps) && eps >= 0.f, "%s: eps must be finite and >= 0", fn);
+    TRY(check_matrix(fn, "x", x, x_stride, n, dim, dtype, true, false));
+    TRY(check_matrix(fn, "residual", residual, residual_stride, n, dim, dtype, true, true));
+    TRY(check_matrix(fn, "weight", weight, dim, 1, dim, dtype, true, true));
+    TRY(check_matrix(fn, "sum", sum, sum_stride, n, dim, dtype, false, true));
+    REQUIRE(residual || !sum, "%s: sum needs a residual", fn);
+    return GS_OK;
+}
+
+// Rows in 8 bits and their scales.
+gs_status check_rows8(const char* fn, const char* name, const void* q, int64_t stride, const void* scales,
+                      int64_t scales_stride, int64_t rows, int64_t cols, bool input) {
+    REQUIRE(rows == 0 || (q && scales), "%s: %s and its scales must not be NULL", fn, name);
+    REQUIRE(aligned(q, 16) && stride % 16 == 0, "%s: %s's rows must be 16-byte aligned", fn, name);
+    REQUIRE((stride >= cols && stride <= (int64_t)1 << 22) || (input && stride == 0),
+            "%s: %s's row stride must be in [%lld, 2^22]%s, got %lld", fn, name, (long long)cols, input ? " or 0" : "",
+            (long long)stride);
+    const int64_t groups = (cols / gs::Q8_BLOCK + 3) / 4 * 4;
+    REQUIRE(aligned(scales, 4) && scales_stride % 4 == 0, "%s: %s's rows of scales must be 4-byte aligned", fn, name);
+    REQUIRE((scales_stride >= groups && scales_stride <= (int64_t)1 << 22) || (input && scales_stride == 0),
+            "%s: %s's scales' row stride must be in [%lld, 2^22]%s, got %lld", fn, name, (long long)groups,
+            input ? " or 0" : "", (long long)scales_stride);
+    return GS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1323,6 +1353,162 @@ gs_status gs_label_loss_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype
         return hip_check(gs::launch_label_loss_bwd(a, (char*)workspace, (hipStream_t)stream), fn);
     } catch (...) {
         return fail(GS_ERR_HIP, "gs_label_loss_bwd: unexpected exception");
+    }
+}
+
+gs_status gs_rms_norm_fwd(int64_t n, int32_t dim, int32_t dtype, const void* x, int64_t x_stride,
+                          const void* residual, int64_t residual_stride, const void* weight, float eps, void* sum,
+                          int64_t sum_stride, void* y, int64_t y_stride, float* rstd, void* stream) {
+    try {
+        static const char* fn = "gs_rms_norm_fwd";
+        g_err[0] = 0;
+        TRY(check_rows(fn, n, dim, 1, dtype));
+        TRY(check_rms_inputs(fn, n, dim, dtype, x, x_stride, residual, residual_stride, weight, eps, sum, sum_stride));
+        TRY(check_matrix(fn, "y", y, y_stride, n, dim, dtype, false, false));
+        REQUIRE(aligned(rstd, 4), "%s: misaligned rstd", fn);
+        if (n == 0) return GS_OK;
+        return hip_check(gs::launch_rms_fwd(n, dim, dtype == GS_BF16, x, x_stride, residual, residual_stride, weight,
+                                            eps, sum, sum_stride, y, y_stride, rstd, (hipStream_t)stream),
+                         fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_rms_norm_fwd: unexpected exception");
+    }
+}
+
+size_t gs_rms_norm_bwd_workspace_size(int64_t n, int32_t dim, int32_t dtype) {
+    return rows_ok(n, dim, 1, dtype) ? gs::rms_bwd_workspace(n, dim) : 0;
+}
+
+gs_status gs_rms_norm_bwd(int64_t n, int32_t dim, int32_t dtype, const void* h, int64_t h_stride, const void* weight,
+                          const float* rstd, const void* dy, int64_t dy_stride, const void* dsum,
+                          int64_t dsum_stride, void* dx, int64_t dx_stride, void* dweight, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    try {
+        static const char* fn = "gs_rms_norm_bwd";
+        g_err[0] = 0;
+        TRY(check_rows(fn, n, dim, 1, dtype));
+        TRY(check_matrix(fn, "h", h, h_stride, n, dim, dtype, true, false));
+        TRY(check_matrix(fn, "weight", weight, dim, 1, dim, dtype, true, true));
+        REQUIRE(n == 0 || rstd, "%s: rstd must not be NULL", fn);
+        REQUIRE(aligned(rstd, 4), "%s: misaligned rstd", fn);
+        TRY(check_matrix(fn, "dy", dy, dy_stride, n, dim, dtype, true, false));
+        TRY(check_matrix(fn, "dsum", dsum, dsum_stride, n, dim, dtype, true, true));
+        TRY(check_matrix(fn, "dx", dx, dx_stride, n, dim, dtype, false, true));
+        TRY(check_matrix(fn, "dweight", dweight, dim, 1, dim, dtype, false, true));
+        if (dweight)
+            TRY(check_workspace(fn, workspace, workspace_bytes, gs_rms_norm_bwd_workspace_size(n, dim, dtype)));
+        return hip_check(gs::launch_rms_bwd(n, dim, dtype == GS_BF16, h, h_stride, weight, rstd, dy, dy_stride, dsum,
+                                            dsum_stride, dx, dx_stride, dweight, (float*)workspace,
+                                            (hipStream_t)stream),
+                         fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_rms_norm_bwd: unexpected exception");
+    }
+}
+
+gs_status gs_rms_norm_q8(int64_t n, int32_t dim, int32_t dtype, const void* x, int64_t x_stride, const void* residual,
+                         int64_t residual_stride, const void* weight, float eps, void* sum, int64_t sum_stride,
+                         void* q, int64_t q_stride, void* scales, int64_t scales_stride, void* stream) {
+    try {
+        static const char* fn = "gs_rms_norm_q8";
+        g_err[0] = 0;
+        TRY(check_rows(fn, n, dim, 1, dtype));
+        TRY(check_rms_inputs(fn, n, dim, dtype, x, x_stride, residual, residual_stride, weight, eps, sum, sum_stride));
+        TRY(check_rows8(fn, "q", q, q_stride, scales, scales_stride, n, gs::q8_cols(dim), false));
+        if (n == 0) return GS_OK;
+        return hip_check(gs::launch_rms_q8(n, dim, dtype == GS_BF16, x, x_stride, residual, residual_stride, weight,
+                                           eps, sum, sum_stride, (uint8_t*)q, q_stride, (uint8_t*)scales,
+                                           scales_stride, (hipStream_t)stream),
+                         fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_rms_norm_q8: unexpected exception");
+    }
+}
+
+gs_status gs_quantize_q8(int64_t n, int32_t dim, int32_t dtype, const void* x, int64_t x_stride, void* q,
+                         int64_t q_stride, void* scales, int64_t scales_stride, void* stream) {
+    try {
+        static const char* fn = "gs_quantize_q8";
+        g_err[0] = 0;
+        TRY(check_rows(fn, n, dim, 1, dtype));
+        TRY(check_matrix(fn, "x", x, x_stride, n, dim, dtype, true, false));
+        TRY(check_rows8(fn, "q", q, q_stride, scales, scales_stride, n, gs::q8_cols(dim), false));
+        if (n == 0) return GS_OK;
+        return hip_check(gs::launch_quantize_q8(n, dim, dtype == GS_BF16, x, x_stride, (uint8_t*)q, q_stride,
+                                                (uint8_t*)scales, scales_stride, (hipStream_t)stream),
+                         fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_quantize_q8: unexpected exception");
+    }
+}
+
+gs_status gs_label_scores_q8(int64_t n, int32_t cols, int64_t vocab, int32_t dtype, const void* q, int64_t q_stride,
+                             const void* q_scales, int64_t q_scales_stride, const void* w, int64_t w_stride,
+                             const void* w_scales, int64_t w_scales_stride, void* out, int64_t out_stride,
+                             void* stream) {
+    try {
+        static const char* fn = "gs_label_scores_q8";
+        g_err[0] = 0;
+        TRY(check_rows(fn, n, cols, vocab, dtype));
+        REQUIRE(cols % gs::Q8_BLOCK == 0, "%s: cols must be a multiple of %d, got %d", fn, gs::Q8_BLOCK, cols);
+        TRY(check_rows8(fn, "q", q, q_stride, q_scales, q_scales_stride, n, cols, true));
+        TRY(check_rows8(fn, "w", w, w_stride, w_scales, w_scales_stride, vocab, cols, true));
+        TRY(check_matrix(fn, "out", out, out_stride, n, vocab, dtype, false, false));
+        if (n == 0) return GS_OK;
+        gs::ScoreArgs a{};
+        a.n = n;
+        a.vocab = vocab;
+        a.cols = cols;
+        a.half = dtype == GS_BF16;
+        a.q = (const uint8_t*)q;
+        a.qs = q_stride;
+        a.qscales = (const uint8_t*)q_scales;
+        a.qss = q_scales_stride;
+        a.w = (const uint8_t*)w;
+        a.ws = w_stride;
+        a.wscales = (const uint8_t*)w_scales;
+        a.wss = w_scales_stride;
+        a.out = out;
+        a.os = out_stride;
+        return hip_check(gs::launch_label_scores(a, (hipStream_t)stream), fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_label_scores_q8: unexpected exception");
+    }
+}
+
+size_t gs_clip_grads_workspace_size(int32_t tensors) {
+    return tensors >= 0 && tensors <= GS_CLIP_MAX_TENSORS ? gs::clip_workspace(tensors) : 0;
+}
+
+gs_status gs_clip_grads(int32_t tensors, const void* const* grads, void* const* outs, const int64_t* numels,
+                        const int32_t* dtypes, float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    try {
+        static const char* fn = "gs_clip_grads";
+        g_err[0] = 0;
+        REQUIRE(tensors >= 0 && tensors <= GS_CLIP_MAX_TENSORS, "%s: tensors must be in [0, %d], got %d", fn,
+                GS_CLIP_MAX_TENSORS, tensors);
+        REQUIRE(max_norm >= 0.f, "%s: max_norm must be >= 0", fn);
+        REQUIRE(tensors == 0 || (grads && numels && dtypes), "%s: grads, numels and dtypes must not be NULL", fn);
+        for (int i = 0; i < tensors; ++i) {
+            REQUIRE(numels[i] >= 0 && numels[i] <= (int64_t)1 << 40, "%s: tensor %d's size must be in [0, 2^40], got %lld",
+                    fn, i, (long long)numels[i]);
+            if (dtypes[i] != GS_F32 && dtypes[i] != GS_BF16)
+                return fail(GS_ERR_UNSUPPORTED, "%s: tensor %d's dtype must be GS_F32 or GS_BF16, got %d", fn, i,
+                            dtypes[i]);
+            if (numels[i] == 0) continue;
+            REQUIRE(grads[i] && (!outs || outs[i]), "%s: tensor %d is NULL", fn, i);
+            const int size = dtypes[i] == GS_F32 ? 4 : 2;
+            REQUIRE(aligned(grads[i], size) && (!outs || aligned(outs[i], size)), "%s: tensor %d is misaligned", fn, i);
+        }
+        REQUIRE(norm, "%s: norm must not be NULL", fn);
+        REQUIRE(aligned(norm, 4), "%s: misaligned norm", fn);
+        TRY(check_workspace(fn, workspace, workspace_bytes, gs_clip_grads_workspace_size(tensors)));
+        return hip_check(gs::launch_clip_grads(tensors, grads, outs, numels, dtypes, max_norm, norm, (char*)workspace,
+                                               (hipStream_t)stream),
+                         fn);
+    } catch (...) {
+        return fail(GS_ERR_HIP, "gs_clip_grads: unexpected exception");
     }
 }
 

@@ -207,6 +207,42 @@ hipError_t launch_norm_bwd(int64_t n, int dim, bool half, const void* x, int64_t
                            const float* mean, const float* rstd, const void* dy, int64_t dys, void* dx, int64_t dxs,
                            void* dweight, void* dbias, float* part, hipStream_t stream);
 
+// Sums over the nblk rows of part (of `width` columns each): the first dim columns' to a, the others' to b (either may
+// be null).
+hipError_t launch_column_sums(bool half, int nblk, int width, int dim, const float* part, void* a, void* b,
+                              hipStream_t stream);
+
+// Root-mean-square normalisation after a residual's addition, and rows in 8 bits (rmsnorm.hip).
+size_t rms_bwd_workspace(int64_t n, int dim);
+hipError_t launch_rms_fwd(int64_t n, int dim, bool half, const void* x, int64_t xs, const void* residual, int64_t rs,
+                          const void* weight, float eps, void* sum, int64_t ss, void* y, int64_t ys, float* rstd,
+                          hipStream_t stream);
+hipError_t launch_rms_bwd(int64_t n, int dim, bool half, const void* h, int64_t hs, const void* weight,
+                          const float* rstd, const void* dy, int64_t dys, const void* dsum, int64_t dss, void* dx,
+                          int64_t dxs, void* dweight, float* part, hipStream_t stream);
+hipError_t launch_rms_q8(int64_t n, int dim, bool half, const void* x, int64_t xs, const void* residual, int64_t rs,
+                         const void* weight, float eps, void* sum, int64_t ss, uint8_t* q, int64_t qs,
+                         uint8_t* scales, int64_t scs, hipStream_t stream);
+hipError_t launch_quantize_q8(int64_t n, int dim, bool half, const void* x, int64_t xs, uint8_t* q, int64_t qs,
+                              uint8_t* scales, int64_t scs, hipStream_t stream);
+
+// Products of rows in 8 bits (scores.hip): out[n][vocab] float32 or (half) bfloat16.
+struct ScoreArgs {
+    int64_t n, vocab;
+    int cols;  // of both operands, a multiple of 128
+    bool half;
+    const uint8_t *q, *qscales, *w, *wscales;
+    int64_t qs, qss, ws, wss;  // row strides
+    void* out;
+    int64_t os;
+};
+hipError_t launch_label_scores(const ScoreArgs& a, hipStream_t stream);
+
+// Clipping by the global norm (clip.hip). grads, outs (null: norm only), numels, half: arrays on the host.
+size_t clip_workspace(int64_t tensors);
+hipError_t launch_clip_grads(int tensors, const void* const* grads, void* const* outs, const int64_t* numels,
+                             const int32_t* half, float max_norm, float* norm, char* ws, hipStream_t stream);
+
 // One call of the vocabulary loss (device pointers; strides in elements). The backward reads
 // lse and writes dx and dw (either may be null); the forward writes loss, lse, mean and count.
 struct LabelLossArgs {

@@ -305,19 +305,20 @@ __global__ __launch_bounds__(NB) void k_norm_bwd_long(int64_t n, int dim, const 
     }
 }
 
-// Adds the blocks' column sums: RED_COLS columns per block, the rows of part
-// over RED_T / RED_COLS threads, joined in LDS in a fixed order.
+// Adds the blocks' column sums (rows of `width`): RED_COLS columns per block, the
+// rows of part over RED_T / RED_COLS threads, joined in LDS in a fixed order. The
+// first dim columns go to a, the others to b.
 template <class T>
-__global__ __launch_bounds__(RED_T) void k_norm_cols(int nblk, int dim, const float* __restrict__ part,
-                                                     T* __restrict__ dweight, T* __restrict__ dbias) {
+__global__ __launch_bounds__(RED_T) void k_norm_cols(int nblk, int width, int dim, const float* __restrict__ part,
+                                                     T* __restrict__ a_out, T* __restrict__ b_out) {
     constexpr int G = RED_T / RED_COLS;
     __shared__ float s[G][RED_COLS];
     const int j = threadIdx.x % RED_COLS, g = threadIdx.x / RED_COLS;
-    const int c = blockIdx.x * RED_COLS + j;  // over the 2 dim columns of part
+    const int c = blockIdx.x * RED_COLS + j;
     float a = 0.f;
-    if (c < 2 * dim) {
+    if (c < width) {
 #pragma unroll 8
-        for (int b = g; b < nblk; b += G) a += part[(size_t)b * 2 * dim + c];
+        for (int b = g; b < nblk; b += G) a += part[(size_t)b * width + c];
     }
     s[g][j] = a;
     __syncthreads();
@@ -325,11 +326,11 @@ __global__ __launch_bounds__(RED_T) void k_norm_cols(int nblk, int dim, const fl
         if (g < h) s[g][j] += s[g + h][j];
         __syncthreads();
     }
-    if (g == 0 && c < 2 * dim) {
+    if (g == 0 && c < width) {
         if (c < dim) {
-            if (dweight) dweight[c] = (T)s[0][j];
-        } else if (dbias) {
-            dbias[c - dim] = (T)s[0][j];
+            if (a_out) a_out[c] = (T)s[0][j];
+        } else if (b_out) {
+            b_out[c - dim] = (T)s[0][j];
         }
     }
 }
@@ -405,12 +406,20 @@ hipError_t norm_bwd(NormArgs a, void* dweight, void* dbias, hipStream_t s) {
     if (a.n > 0 && (a.dx || a.part)) e = norm_launch<T>(a, s);
     if (e != hipSuccess || (!dweight && !dbias)) return e;
     const int nblk = a.n > 0 ? a.blocks : 0;
-    k_norm_cols<T><<<(2 * a.dim + RED_COLS - 1) / RED_COLS, RED_T, 0, s>>>(nblk, a.dim, a.part, (T*)dweight,
-                                                                          (T*)dbias);
-    return hipGetLastError();
+    return launch_column_sums(sizeof(T) == 2, nblk, 2 * a.dim, a.dim, a.part, dweight, dbias, s);
 }
 
 }  // namespace
+
+hipError_t launch_column_sums(bool half, int nblk, int width, int dim, const float* part, void* a, void* b,
+                              hipStream_t stream) {
+    const int grid = (width + RED_COLS - 1) / RED_COLS;
+    if (half)
+        k_norm_cols<bf16><<<grid, RED_T, 0, stream>>>(nblk, width, dim, part, (bf16*)a, (bf16*)b);
+    else
+        k_norm_cols<float><<<grid, RED_T, 0, stream>>>(nblk, width, dim, part, (float*)a, (float*)b);
+    return hipGetLastError();
+}
 
 size_t norm_bwd_workspace(int64_t n, int dim) {
     const int64_t rows = n < NORM_BLOCKS_BWD ? n : NORM_BLOCKS_BWD;

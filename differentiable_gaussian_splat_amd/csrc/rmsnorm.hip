@@ -1,0 +1,450 @@
+// Root-mean-square normalisation of feature rows after a residual's addition,
+// forward and backward, and with the result in 8 bits (rows8.hpp).
+//
+//   h = x + residual (rounded to the rows' type, as it is handed on)
+//   rstd = (sum_j h_j^2 / D + eps)^-1/2,  y = h rstd w
+//   g = dy w,  dx = rstd (g - h rstd^2 mean_j(g h)) + dh      (dh: h's own gradient)
+//   dw_j = sum_i dy_ij h_ij rstd_i
+//
+// Bound by memory: the forward reads x and the residual and writes h and y once,
+// the backward reads h, dy and dh and writes dx once. A row lies in the registers
+// of LPR lanes (from one lane to a block of 1024 threads for the longest rows), so
+// that its statistic costs no second read. Blocks walk over the rows. The column
+// sums of dw go to the workspace, one row per block, and a second launch adds them
+// in a fixed order.
+#include "elem.hpp"
+#include "launch.hpp"
+#include "rows8.hpp"
+
+// Products are rounded before they are added (fused only where fmaf says so).
+#pragma clang fp contract(off)
+
+namespace gs {
+
+namespace {
+
+// Sum over the LPR lanes that share a row (all of them get it). s: NT / 64 floats, for rows of a whole block.
+template <int NT, int LPR>
+__device__ __forceinline__ float rms_row_sum(float v, float* s) {
+    constexpr int W = LPR < 64 ? LPR : 64;
+#pragma unroll
+    for (int off = W / 2; off > 0; off >>= 1) v += __shfl_xor(v, off);
+    if constexpr (LPR > 64) {
+        static_assert(LPR == NT, "a row of more than a wave is the block's");
+        __syncthreads();  // earlier readers of s are done
+        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int k = 0; k < LPR / 64; ++k) v += s[k];
+    }
+    return v;
+}
+
+struct RmsArgs {
+    int64_t n;
+    int dim;
+    const void *x, *residual, *weight;  // x: h in the backward
+    int64_t xs, rs;
+    float eps;
+    void *sum, *y;
+    int64_t ss, ys;
+    float* rstd;  // written by the forward, read by the backward
+    uint8_t *q, *scales;
+    int64_t qs, scs;
+    const void *dy, *dsum;
+    int64_t dys, dss;
+    void* dx;
+    int64_t dxs;
+    float* part;  // [blocks][dim]
+};
+
+// The accesses of a row whose weights stay in registers over the block's rows.
+constexpr int KEPT = 4;
+
+template <class T, int NT, int LPR, int EPL, bool FULL, bool Q8>
+__global__ __launch_bounds__(NT) void k_rms_fwd(RmsArgs a) {
+    __shared__ float s_red[NT / 64];
+    constexpr int RPB = NT / LPR, VEC = WIDE<T>;
+    constexpr bool KEEP = EPL <= KEPT;
+    const int l = threadIdx.x % LPR, dim = a.dim;
+    const T *x = (const T*)a.x, *residual = (const T*)a.residual, *weight = (const T*)a.weight;
+    wide_t<T> w[KEEP ? EPL : 1];
+    if (KEEP && weight) {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            const int c = (e * LPR + l) * VEC;
+            w[KEEP ? e : 0] = (T)0.f;
+            if (c < dim) w[KEEP ? e : 0] = load_row<FULL>(weight + c, dim - c, dim - c);
+        }
+    }
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.n; r0 += (int64_t)gridDim.x * RPB) {
+        const int64_t r = r0 + threadIdx.x / LPR;
+        const bool live = r < a.n;  // a row past the end is computed from zeros and not stored
+        wide_t<T> raw[EPL];
+        float sq = 0.f;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            const int c = (e * LPR + l) * VEC;
+            raw[e] = (T)0.f;
+            if (live && c < dim) raw[e] = load_row<FULL>(x + r * a.xs + c, dim - c, (a.n - 1 - r) * a.xs + dim - c);
+        }
+        if (residual) {
+            wide_t<T> more[EPL];
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) {
+                const int c = (e * LPR + l) * VEC;
+                more[e] = (T)0.f;
+                if (live && c < dim)
+                    more[e] = load_row<FULL>(residual + r * a.rs + c, dim - c, (a.n - 1 - r) * a.rs + dim - c);
+            }
+#pragma unroll
+            for (int e = 0; e < EPL; ++e)
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) raw[e][k] = (T)((float)raw[e][k] + (float)more[e][k]);
+        }
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            const int left = dim - (e * LPR + l) * VEC;
+            float v[VEC];
+            widen<FULL, T>(raw[e], left, v);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) sq = (FULL ? left > 0 : k < left) ? fmaf(v[k], v[k], sq) : sq;
+        }
+        const float rstd = 1.0f / sqrtf(rms_row_sum<NT, LPR>(sq, s_red) / (float)dim + a.eps);
+        if (a.rstd && live && l == 0) a.rstd[r] = rstd;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            const int c = (e * LPR + l) * VEC, left = dim - c;
+            float v[VEC];
+            widen<FULL, T>(raw[e], left, v);
+            if (a.sum && live && left > 0) store_row<FULL>((T*)a.sum + r * a.ss + c, left, v);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) v[k] *= rstd;
+            if (weight) {
+                float f[VEC];
+                wide_t<T> wr = (T)0.f;
+                if (KEEP)
+                    wr = w[KEEP ? e : 0];
+                else if (left > 0)
+                    wr = load_row<FULL>(weight + c, left, left);
+                widen<FULL, T>(wr, left, f);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) v[k] *= f[k];
+            }
+            if constexpr (Q8) {
+                static_assert(LPR >= Q8_LANES<T>, "a block's lanes stand in one row");
+                float top = 0.f;
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    v[k] = FULL ? (left > 0 ? v[k] : 0.f) : k < left ? v[k] : 0.f;
+                    top = fmaxf(top, finite_abs(v[k]));
+                }
+#pragma unroll
+                for (int off = Q8_LANES<T> / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+                const int ex = scale_exponent(top);
+                if (live && c < q8_cols(dim)) {
+                    store_q8(a.q + r * a.qs + c, v, scale_inverse(ex));
+                    if (l % Q8_LANES<T> == 0) a.scales[r * a.scs + c / Q8_BLOCK] = (uint8_t)ex;
+                }
+            } else if (live && left > 0) {
+                store_row<FULL>((T*)a.y + r * a.ys + c, left, v);
+            }
+        }
+        if constexpr (Q8) {
+            const int at = q8_cols(dim) / Q8_BLOCK + l;
+            if (live && at < q8_groups(dim)) a.scales[r * a.scs + at] = 127;
+        }
+    }
+}
+
+// AGAIN: a row's second use reads it from memory (the cache) again, where registers hold no two rows.
+template <class T, int NT, int LPR, int EPL, bool FULL>
+__global__ __launch_bounds__(NT) void k_rms_bwd(RmsArgs a) {
+    constexpr int RPB = NT / LPR, VEC = WIDE<T>;
+    constexpr bool AGAIN = EPL * VEC > 32;
+    __shared__ float s_red[NT / 64];
+    __shared__ float s_acc[LPR < NT ? LPR * EPL * VEC : 1];
+    const int l = threadIdx.x % LPR, dim = a.dim;
+    const T *h = (const T*)a.x, *weight = (const T*)a.weight, *dy = (const T*)a.dy, *dsum = (const T*)a.dsum;
+    float aw[EPL][VEC];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) aw[e][k] = 0.f;
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.n; r0 += (int64_t)gridDim.x * RPB) {
+        const int64_t r = r0 + threadIdx.x / LPR;
+        const bool live = r < a.n;
+        const float rstd = live ? a.rstd[r] : 0.f;
+        wide_t<T> rh[AGAIN ? 1 : EPL], rg[AGAIN ? 1 : EPL];
+        auto load = [&](int e, wide_t<T>& vh, wide_t<T>& vg) {
+            const int c = (e * LPR + l) * VEC;
+            vh = vg = (T)0.f;
+            if (live && c < dim) {
+                vh = load_row<FULL>(h + r * a.xs + c, dim - c, (a.n - 1 - r) * a.xs + dim - c);
+                vg = load_row<FULL>(dy + r * a.dys + c, dim - c, (a.n - 1 - r) * a.dys + dim - c);
+            }
+        };
+        // hh: h rstd; g: dy w; d: dy
+        auto values = [&](int e, wide_t<T> vh, wide_t<T> vg, float (&hh)[VEC], float (&g)[VEC], float (&d)[VEC]) {
+            const int left = dim - (e * LPR + l) * VEC;
+            widen<FULL, T>(vh, left, hh);
+            widen<FULL, T>(vg, left, d);
+            float f[VEC];
+            if (weight) {
+                wide_t<T> wr = (T)0.f;
+                if (left > 0) wr = load_row<FULL>(weight + (dim - left), left, left);
+                widen<FULL, T>(wr, left, f);
+            }
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                hh[k] *= rstd;
+                g[k] = weight ? d[k] * f[k] : d[k];
+            }
+        };
+        if (!AGAIN) {
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) load(e, rh[AGAIN ? 0 : e], rg[AGAIN ? 0 : e]);
+        }
+        float sx = 0.f;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            if (AGAIN) load(e, rh[0], rg[0]);
+            float hh[VEC], g[VEC], d[VEC];
+            values(e, rh[AGAIN ? 0 : e], rg[AGAIN ? 0 : e], hh, g, d);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {  // a column past the row has d = 0
+                aw[e][k] = fmaf(d[k], hh[k], aw[e][k]);
+                sx = fmaf(g[k], hh[k], sx);
+            }
+        }
+        if (!a.dx) continue;  // the same for the whole launch
+        const float mx = rms_row_sum<NT, LPR>(sx, s_red) / (float)dim;
+        if (!live) continue;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            if (AGAIN) load(e, rh[0], rg[0]);
+            const int c = (e * LPR + l) * VEC, left = dim - c;
+            float hh[VEC], g[VEC], d[VEC];
+            values(e, rh[AGAIN ? 0 : e], rg[AGAIN ? 0 : e], hh, g, d);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) g[k] = rstd * (g[k] - hh[k] * mx);
+            if (left <= 0) continue;
+            if (dsum) {
+                widen<FULL, T>(load_row<FULL>(dsum + r * a.dss + c, left, (a.n - 1 - r) * a.dss + left), left, d);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) g[k] += d[k];
+            }
+            store_row<FULL>((T*)a.dx + r * a.dxs + c, left, g);
+        }
+    }
+    if (!a.part) return;
+    // the block's column sums: over the row groups of a wave, then over the waves in turn
+#pragma unroll
+    for (int e = 0; e < EPL; ++e)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+#pragma unroll
+            for (int off = LPR; off < 64; off <<= 1) aw[e][k] += __shfl_xor(aw[e][k], off);
+    float* pw = a.part + (size_t)blockIdx.x * dim;
+    if constexpr (LPR < NT) {
+        const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        for (int turn = 0; turn < NT / 64; ++turn) {
+            if (wv == turn && lane < LPR) {
+#pragma unroll
+                for (int e = 0; e < EPL; ++e)
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) {
+                        const int c = (e * LPR + l) * VEC + k;
+                        s_acc[c] = turn ? s_acc[c] + aw[e][k] : aw[e][k];
+                    }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < dim; c += NT) pw[c] = s_acc[c];
+    } else {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const int c = (e * LPR + l) * VEC + k;
+                if (c < dim) pw[c] = aw[e][k];
+            }
+    }
+}
+
+// Rows in 8 bits as they are: a lane's access after access, the block's lanes side by side.
+template <class T, bool FULL>
+__global__ __launch_bounds__(256) void k_quantize(int64_t first, int64_t units, int per_row, RmsArgs a) {
+    constexpr int VEC = WIDE<T>, G = Q8_LANES<T>;
+    const int64_t u = first + (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+    if (u >= units) return;  // whole groups of lanes
+    const int64_t r = u / per_row;
+    const int b = (int)(u - r * per_row), l = threadIdx.x % G, c = b * Q8_BLOCK + l * VEC, left = a.dim - c;
+    wide_t<T> raw = (T)0.f;
+    if (left > 0) raw = load_row<FULL>((const T*)a.x + r * a.xs + c, left, (a.n - 1 - r) * a.xs + left);
+    float v[VEC], top = 0.f;
+    widen<FULL, T>(raw, left, v);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) top = fmaxf(top, finite_abs(v[k]));
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    const int ex = scale_exponent(top);
+    if (c < q8_cols(a.dim)) store_q8(a.q + r * a.qs + c, v, scale_inverse(ex));
+    if (l == 0) a.scales[r * a.scs + b] = (uint8_t)(c < q8_cols(a.dim) ? ex : 127);
+}
+
+enum RmsCall { RMS_FWD, RMS_BWD, RMS_Q8 };
+
+constexpr int RMS_BLOCKS_FWD = 2048, RMS_BLOCKS_BWD = 1024;  // of 256 threads; the latter are rows of the column sums
+
+template <class T, int CALL, int NT, int LPR, int EPL, bool FULL>
+hipError_t rms_rows(const RmsArgs& a, int& blocks, hipStream_t s) {
+    const int64_t want = (a.n + NT / LPR - 1) / (NT / LPR);
+    const int cap = (CALL == RMS_BWD ? RMS_BLOCKS_BWD : RMS_BLOCKS_FWD) * 256 / NT;
+    blocks = (int)(want < cap ? want : cap);
+    if constexpr (CALL == RMS_BWD)
+        k_rms_bwd<T, NT, LPR, EPL, FULL><<<blocks, NT, 0, s>>>(a);
+    else
+        k_rms_fwd<T, NT, LPR, EPL, FULL, CALL == RMS_Q8><<<blocks, NT, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+// The lanes of a row and their accesses: the fewest lanes that hold it with one access each up to a wave (in 8 bits, a
+// block of columns at least), then more accesses, then a block of four waves, then of sixteen.
+template <class T, int CALL, bool FULL>
+hipError_t rms_pick(const RmsArgs& a, int& blocks, hipStream_t s) {
+    const int v = (a.dim + WIDE<T> - 1) / WIDE<T>;
+    if constexpr (CALL != RMS_Q8) {
+        if (v <= 1) return rms_rows<T, CALL, 256, 1, 1, FULL>(a, blocks, s);
+        if (v <= 2) return rms_rows<T, CALL, 256, 2, 1, FULL>(a, blocks, s);
+        if (v <= 4) return rms_rows<T, CALL, 256, 4, 1, FULL>(a, blocks, s);
+        if (v <= 8) return rms_rows<T, CALL, 256, 8, 1, FULL>(a, blocks, s);
+    }
+    if constexpr (CALL != RMS_Q8 || Q8_LANES<T> <= 16)
+        if (v <= 16) return rms_rows<T, CALL, 256, 16, 1, FULL>(a, blocks, s);
+    if (v <= 32) return rms_rows<T, CALL, 256, 32, 1, FULL>(a, blocks, s);
+    if (v <= 64) return rms_rows<T, CALL, 256, 64, 1, FULL>(a, blocks, s);
+    if (v <= 128) return rms_rows<T, CALL, 256, 64, 2, FULL>(a, blocks, s);
+    if (v <= 256) return rms_rows<T, CALL, 256, 64, 4, FULL>(a, blocks, s);
+    if (v <= 512) return rms_rows<T, CALL, 256, 256, 2, FULL>(a, blocks, s);
+    if (v <= 1024) return rms_rows<T, CALL, 256, 256, 4, FULL>(a, blocks, s);
+    if (v <= 2048) return rms_rows<T, CALL, 1024, 1024, 2, FULL>(a, blocks, s);
+    if (v <= 4096) return rms_rows<T, CALL, 1024, 1024, 4, FULL>(a, blocks, s);
+    if (v <= 8192) return rms_rows<T, CALL, 1024, 1024, 8, FULL>(a, blocks, s);
+    if constexpr (sizeof(T) == 4) return rms_rows<T, CALL, 1024, 1024, 16, FULL>(a, blocks, s);
+    return hipErrorInvalidValue;  // 65536 bfloat16 are 8192 accesses
+}
+
+template <int CALL>
+hipError_t rms_launch(bool half, const RmsArgs& a, int& blocks, hipStream_t s) {
+    if (half)
+        return a.dim % WIDE<bf16> == 0 ? rms_pick<bf16, CALL, true>(a, blocks, s)
+                                       : rms_pick<bf16, CALL, false>(a, blocks, s);
+    return a.dim % WIDE<float> == 0 ? rms_pick<float, CALL, true>(a, blocks, s)
+                                    : rms_pick<float, CALL, false>(a, blocks, s);
+}
+
+template <class T, bool FULL>
+hipError_t quantize(const RmsArgs& a, hipStream_t s) {
+    const int per_row = q8_groups(a.dim), per_block = 256 / Q8_LANES<T>;
+    const int64_t units = a.n * per_row;
+    for (int64_t first = 0; first < units; first += MOST_BLOCKS * per_block) {
+        const int64_t blocks = (units - first + per_block - 1) / per_block;
+        k_quantize<T, FULL><<<(unsigned)(blocks < MOST_BLOCKS ? blocks : MOST_BLOCKS), 256, 0, s>>>(first, units,
+                                                                                                  per_row, a);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+size_t rms_bwd_workspace(int64_t n, int dim) {
+    const int64_t rows = n < RMS_BLOCKS_BWD ? n : RMS_BLOCKS_BWD;
+    return ((size_t)rows * dim * sizeof(float) + 255) & ~(size_t)255;
+}
+
+hipError_t launch_rms_fwd(int64_t n, int dim, bool half, const void* x, int64_t xs, const void* residual, int64_t rs,
+                          const void* weight, float eps, void* sum, int64_t ss, void* y, int64_t ys, float* rstd,
+                          hipStream_t stream) {
+    RmsArgs a{};
+    a.n = n;
+    a.dim = dim;
+    a.x = x;
+    a.xs = xs;
+    a.residual = residual;
+    a.rs = rs;
+    a.weight = weight;
+    a.eps = eps;
+    a.sum = sum;
+    a.ss = ss;
+    a.y = y;
+    a.ys = ys;
+    a.rstd = rstd;
+    int blocks;
+    return rms_launch<RMS_FWD>(half, a, blocks, stream);
+}
+
+hipError_t launch_rms_bwd(int64_t n, int dim, bool half, const void* h, int64_t hs, const void* weight,
+                          const float* rstd, const void* dy, int64_t dys, const void* dsum, int64_t dss, void* dx,
+                          int64_t dxs, void* dweight, float* part, hipStream_t stream) {
+    RmsArgs a{};
+    a.n = n;
+    a.dim = dim;
+    a.x = h;
+    a.xs = hs;
+    a.weight = weight;
+    a.rstd = const_cast<float*>(rstd);
+    a.dy = dy;
+    a.dys = dys;
+    a.dsum = dsum;
+    a.dss = dss;
+    a.dx = dx;
+    a.dxs = dxs;
+    a.part = dweight ? part : nullptr;
+    int blocks = 0;
+    if (n > 0 && (dx || dweight))
+        if (hipError_t e = rms_launch<RMS_BWD>(half, a, blocks, stream)) return e;
+    return dweight ? launch_column_sums(half, blocks, dim, dim, part, dweight, nullptr, stream) : hipSuccess;
+}
+
+hipError_t launch_rms_q8(int64_t n, int dim, bool half, const void* x, int64_t xs, const void* residual, int64_t rs,
+                         const void* weight, float eps, void* sum, int64_t ss, uint8_t* q, int64_t qs,
+                         uint8_t* scales, int64_t scs, hipStream_t stream) {
+    RmsArgs a{};
+    a.n = n;
+    a.dim = dim;
+    a.x = x;
+    a.xs = xs;
+    a.residual = residual;
+    a.rs = rs;
+    a.weight = weight;
+    a.eps = eps;
+    a.sum = sum;
+    a.ss = ss;
+    a.q = q;
+    a.qs = qs;
+    a.scales = scales;
+    a.scs = scs;
+    int blocks;
+    return rms_launch<RMS_Q8>(half, a, blocks, stream);
+}
+
+hipError_t launch_quantize_q8(int64_t n, int dim, bool half, const void* x, int64_t xs, uint8_t* q, int64_t qs,
+                              uint8_t* scales, int64_t scs, hipStream_t stream) {
+    RmsArgs a{};
+    a.n = n;
+    a.dim = dim;
+    a.x = x;
+    a.xs = xs;
+    a.q = q;
+    a.qs = qs;
+    a.scales = scales;
+    a.scs = scs;
+    if (half)
+        return dim % WIDE<bf16> == 0 ? quantize<bf16, true>(a, stream) : quantize<bf16, false>(a, stream);
+    return dim % WIDE<float> == 0 ? quantize<float, true>(a, stream) : quantize<float, false>(a, stream);
+}
+
+}  // namespace gs

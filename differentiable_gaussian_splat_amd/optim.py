@@ -1,0 +1,110 @@
+"""Clipping of gradients by their global norm, between the backward and the update.
+
+:func:`clip_grads` clips a list of gradients (a scene's, as
+:func:`.raster.gs_adam_step` takes them, or a label head's) in one call;
+:class:`GradClip` keeps the addresses of gradients that stay in their buffers
+from step to step. Both run two kernels over all tensors together, float32 and
+bfloat16 side by side, and neither waits for the device.
+"""
+from __future__ import annotations
+
+import ctypes as C
+from array import array
+
+import torch
+
+from .labels import _call, _stream
+from .raster import load_library
+
+__all__ = ["gs_clip_grads_workspace_size", "gs_clip_grads", "clip_grads", "GradClip"]
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _addresses(values):
+    """A host array of 64-bit values, as the C call takes it."""
+    a = array("q", values)
+    return (C.c_int64 * len(a)).from_buffer(a) if a else None
+
+
+class _Tensors:
+    """The host arrays of a call: checked once, and usable as long as the tensors keep their memory."""
+
+    def __init__(self, grads, outs):
+        self.grads = list(grads)
+        self.outs = None if outs is None else list(outs)
+        for name, ts in (("gradients", self.grads), ("outs", self.outs)):
+            if ts is None:
+                continue
+            for t in ts:
+                if t.dtype not in _DTYPES:
+                    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+            if not all([t.is_cuda for t in ts]):
+                raise TypeError(f"{name} must be on the GPU")
+            if not all([t.is_contiguous() for t in ts]):
+                raise ValueError(f"{name} must be contiguous")
+        devices = {t.get_device() for t in self.grads + (self.outs or [])}
+        if len(devices) > 1:
+            raise ValueError(f"gradients and outs must be on one device, got {sorted(devices)}")
+        self.device = devices.pop() if devices else None
+        sizes = [t.numel() for t in self.grads]
+        if self.outs is not None and [(t.numel(), t.dtype) for t in self.outs] != \
+                [(k, t.dtype) for k, t in zip(sizes, self.grads)]:
+            raise ValueError("outs must have the gradients' number, sizes and types")
+        self.count = len(sizes)
+        self.g = _addresses([t.data_ptr() for t in self.grads])
+        self.o = None if outs is None else _addresses([t.data_ptr() for t in self.outs]) or C.c_void_p(1)
+        self.n = _addresses(sizes)
+        self.t = (C.c_int32 * self.count)(*[_DTYPES[t.dtype] for t in self.grads]) if self.count else None
+
+    def call(self, max_norm, norm, workspace, stream):
+        dev = norm.get_device()
+        _call("gs_clip_grads", dev, self.count, self.g, self.o, self.n, self.t, max_norm, norm.data_ptr(),
+              workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
+
+
+def gs_clip_grads_workspace_size(tensors) -> int:
+    """Workspace bytes for a number of tensors."""
+    return int(load_library().gs_clip_grads_workspace_size(int(tensors)))
+
+
+def gs_clip_grads(grads, outs, norm, max_norm, workspace, stream=None):
+    """norm[0] = sqrt(sum of all g^2); outs = min(1, max_norm / (norm + 1e-6)) grads (outs: the gradients themselves,
+    tensors like them, or None for the norm only)."""
+    t = _Tensors(grads, outs)
+    if norm.dtype != torch.float32 or norm.numel() != 1 or not norm.is_cuda:
+        raise TypeError(f"norm must be one float32 on the GPU, got {tuple(norm.shape)} {norm.dtype} on {norm.device}")
+    if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise TypeError("the workspace must be a contiguous uint8 buffer on the GPU")
+    if {t.device, norm.get_device(), workspace.get_device()} - {None, norm.get_device()}:
+        raise ValueError("gradients, norm and workspace must be on one device")
+    t.call(max_norm, norm, workspace, stream)
+
+
+class GradClip:
+    """Clips gradients that stay in their buffers: ``clip = GradClip(grads)`` once, ``norm = clip(max_norm)`` per step.
+
+    The tensors are checked, and their addresses kept, when the handle is made; it keeps them alive. A gradient that
+    is replaced (``grad = None`` and a new one) needs a new handle. The norm (float32 [1], before clipping) and the
+    workspace are the handle's own, written again by the next call: a handle is for one stream at a time, and a
+    captured graph needs one of its own. outs: where the clipped gradients go (default: in place).
+    """
+
+    def __init__(self, grads, outs=None):
+        grads = list(grads)
+        if not grads:
+            raise ValueError("there are no gradients to clip")
+        self._t = _Tensors(grads, grads if outs is None else outs)
+        self.norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
+        self._ws = torch.empty(gs_clip_grads_workspace_size(len(grads)), dtype=torch.uint8, device=grads[0].device)
+
+    def __call__(self, max_norm, stream=None):
+        self._t.call(max_norm, self.norm, self._ws, stream)
+        return self.norm
+
+
+def clip_grads(params, max_norm, stream=None):
+    """Clips the gradients of the parameters (those that have one) in place by their global norm; returns it (float32
+    [1], before clipping), or None if there is no gradient. max_norm infinite: only the norm."""
+    grads = [p.grad for p in params if p.grad is not None]
+    return GradClip(grads)(max_norm, stream) if grads else None

@@ -77,7 +77,9 @@ EXPORTS = ["gs_default_options", "gs_version", "gs_last_error", "gs_release_thre
            "gs_surfel_preprocess_bwd", "gs_surfel_render_bwd_workspace_size", "gs_surfel_render_bwd",
            "gs_embed_fwd", "gs_embed_bwd_workspace_size", "gs_embed_bwd", "gs_layer_norm_fwd",
            "gs_layer_norm_bwd_workspace_size", "gs_layer_norm_bwd", "gs_label_loss_workspace_size",
-           "gs_label_loss_fwd", "gs_label_loss_bwd"]
+           "gs_label_loss_fwd", "gs_label_loss_bwd", "gs_rms_norm_fwd", "gs_rms_norm_bwd_workspace_size",
+           "gs_rms_norm_bwd", "gs_rms_norm_q8", "gs_quantize_q8", "gs_label_scores_q8",
+           "gs_clip_grads_workspace_size", "gs_clip_grads"]
 SURFEL_GRAD_STRIDE = 16
 NOALLOC_MAX_N = 1 << 20  # GS_NOALLOC_MAX_N
 MAX_VIEWS = 32
@@ -187,6 +189,22 @@ def load_library(path: str = LIB_PATH):
         L.gs_label_loss_bwd.argtypes = ([i64, i32, i64, i32, P, i64, P, i64, P, i32] + [P] * 3 +
                                         [P, i64, P, i64, P, sz, P])
         L.gs_label_loss_bwd.restype = i32
+        L.gs_rms_norm_fwd.argtypes = [i64, i32, i32, P, i64, P, i64, P, f32, P, i64, P, i64, P, P]
+        L.gs_rms_norm_fwd.restype = i32
+        L.gs_rms_norm_bwd_workspace_size.argtypes = [i64, i32, i32]
+        L.gs_rms_norm_bwd_workspace_size.restype = sz
+        L.gs_rms_norm_bwd.argtypes = [i64, i32, i32, P, i64, P, P, P, i64, P, i64, P, i64, P, P, sz, P]
+        L.gs_rms_norm_bwd.restype = i32
+        L.gs_rms_norm_q8.argtypes = [i64, i32, i32, P, i64, P, i64, P, f32, P, i64, P, i64, P, i64, P]
+        L.gs_rms_norm_q8.restype = i32
+        L.gs_quantize_q8.argtypes = [i64, i32, i32, P, i64, P, i64, P, i64, P]
+        L.gs_quantize_q8.restype = i32
+        L.gs_label_scores_q8.argtypes = [i64, i32, i64, i32] + [P, i64] * 5 + [P]
+        L.gs_label_scores_q8.restype = i32
+        L.gs_clip_grads_workspace_size.argtypes = [i32]
+        L.gs_clip_grads_workspace_size.restype = sz
+        L.gs_clip_grads.argtypes = [i32, P, P, P, P, f32, P, P, sz, P]
+        L.gs_clip_grads.restype = i32
         _lib = L
         return L
 

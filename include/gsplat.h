@@ -694,6 +694,84 @@ gs_status gs_label_loss_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype
                             void *dx, int64_t dx_stride, void *dw, int64_t dw_stride, void *workspace,
                             size_t workspace_bytes, void *stream);
 
+/*
+ * gs_rms_norm_fwd -- root-mean-square normalisation of the sum of two matrices:
+ *     h = x + residual (rounded to the rows' type; h = x without a residual),
+ *     rstd = 1 / sqrt(mean over the row of h^2 + eps),   y = h rstd weight.
+ * x, y[n, dim]; residual[n, dim], weight[dim] nullable (nothing added, 1); eps >= 0.
+ * sum[n, dim] (nullable, only with a residual) receives h, to be handed on and
+ * kept for the backward; rstd[n] is nullable. A row of zeros with eps = 0 gives
+ * no numbers, as the formula does.
+ */
+gs_status gs_rms_norm_fwd(int64_t n, int32_t dim, int32_t dtype, const void *x, int64_t x_stride,
+                          const void *residual, int64_t residual_stride, const void *weight, float eps, void *sum,
+                          int64_t sum_stride, void *y, int64_t y_stride, float *rstd, void *stream);
+
+/*
+ * gs_rms_norm_bwd -- gradients of gs_rms_norm_fwd from dy[n, dim], the forward's h
+ * and rstd, and dsum[n, dim] (nullable), the gradient of h as it was handed on:
+ * dx[n, dim], which is the residual's gradient too, and dweight[dim], each nullable.
+ */
+size_t gs_rms_norm_bwd_workspace_size(int64_t n, int32_t dim, int32_t dtype);
+gs_status gs_rms_norm_bwd(int64_t n, int32_t dim, int32_t dtype, const void *h, int64_t h_stride,
+                          const void *weight, const float *rstd, const void *dy, int64_t dy_stride,
+                          const void *dsum, int64_t dsum_stride, void *dx, int64_t dx_stride, void *dweight,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rows in 8 bits. A row of dim columns is `cols` e4m3 values (the 8-bit format
+ * with 4 exponent and 3 mantissa bits, largest value 448, without infinities),
+ * cols = dim rounded up to a multiple of 128, zero from dim on, and one scale for
+ * each 128 of them, a power of two held as its exponent plus 127 in a byte. The
+ * scales of a row are padded to a multiple of four bytes (with 127). The scale of
+ * a block is the least 2^e with max |v| <= 448 2^e over its finite values, e >=
+ * -126 (1 where all are 0); a value is v / 2^e, to nearest even. Infinite values
+ * and NaN become NaN. Rows of values are 16-byte aligned, rows of scales 4-byte
+ * aligned, either's stride at most 2^22 bytes.
+ *
+ * gs_quantize_q8 -- x[n, dim] as rows in 8 bits: q[n, cols], scales[n, groups].
+ * gs_rms_norm_q8 -- gs_rms_norm_fwd with y as rows in 8 bits (of y before any
+ * rounding to the rows' type).
+ */
+gs_status gs_quantize_q8(int64_t n, int32_t dim, int32_t dtype, const void *x, int64_t x_stride, void *q,
+                         int64_t q_stride, void *scales, int64_t scales_stride, void *stream);
+gs_status gs_rms_norm_q8(int64_t n, int32_t dim, int32_t dtype, const void *x, int64_t x_stride,
+                         const void *residual, int64_t residual_stride, const void *weight, float eps, void *sum,
+                         int64_t sum_stride, void *q, int64_t q_stride, void *scales, int64_t scales_stride,
+                         void *stream);
+
+/*
+ * gs_label_scores_q8 -- out[i][v] = the product of row i of q[n, cols] with row v of
+ * w[vocab, cols], both rows in 8 bits, summed in float32 and rounded once to
+ * `dtype`. cols is a multiple of 128. Which scores a row gets does not depend on
+ * the rows beside it except for the order of its sums.
+ */
+gs_status gs_label_scores_q8(int64_t n, int32_t cols, int64_t vocab, int32_t dtype, const void *q,
+                             int64_t q_stride, const void *q_scales, int64_t q_scales_stride, const void *w,
+                             int64_t w_stride, const void *w_scales, int64_t w_scales_stride, void *out,
+                             int64_t out_stride, void *stream);
+
+/* ------------------------------------------------------------------ gradient clipping */
+
+#define GS_CLIP_MAX_TENSORS 65536
+
+/*
+ * gs_clip_grads -- the global norm of all gradients, and the gradients clipped by it:
+ *     norm[0] = sqrt(sum over all tensors and elements of g^2),
+ *     out = min(1, max_norm / (norm + 1e-6)) g.
+ * grads, outs, numels and dtypes are arrays on the HOST of one entry per tensor
+ * (read before the call returns): device addresses of contiguous tensors, their
+ * sizes, GS_F32 or GS_BF16. outs[i] is grads[i] (in place) or overlaps no gradient;
+ * outs NULL: the norm only. max_norm >= 0 (infinite: nothing is clipped). The sum
+ * is float64, in one order: the same bit for bit from run to run. Where a gradient
+ * is NaN so are all results; where one is infinite the norm is, the infinite ones
+ * become NaN and the others 0.
+ */
+size_t gs_clip_grads_workspace_size(int32_t tensors);
+gs_status gs_clip_grads(int32_t tensors, const void *const *grads, void *const *outs, const int64_t *numels,
+                        const int32_t *dtypes, float max_norm, float *norm, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
