@@ -22,6 +22,7 @@ namespace gs {
 
 namespace {
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -212,8 +213,293 @@ hipError_t scores_direct(const ScoreArgs& a, hipStream_t s) {
     return hipSuccess;
 }
 
+// ------------------------------------------------------------------ tiles through LDS
+
+constexpr int STEP = 64;     // columns of a staged step: one e4m3 product deep, half a block
+constexpr int STAGES = 4;    // steps in LDS: one being read, three on their way
+constexpr int GROUP_X = 4;   // rows of tiles that follow one another along the vocabulary
+
+// How a row's four 16-byte chunks are exchanged, so that the sixteen lanes that read one depth's chunks together find
+// them spread over all banks.
+__device__ __forceinline__ int chunk_turn(int r) { return (r >> 2) & 3; }
+
+// The vocabulary row (of a block's) that stands in row s of its tiles: column c of a wave's tile j is its VT c + j, so
+// that a lane's scores in a row join, and the 32 lanes of a row write without gaps. (Runs of a lane's own, 16 bytes at
+// a time with other lanes' between them, cost four times the requests: 8192 x 128 x 65536 437 us, so 300.)
+template <int VT>
+__device__ __forceinline__ int vocab_row(int s) {
+    return s / (32 * VT) * (32 * VT) + s % 32 * VT + s / 32 % VT;
+}
+
+// Stores C scores side by side (out is aligned to its elements only).
+template <class T, int C>
+__device__ __forceinline__ void store_run(T* out, const float (&v)[C]) {
+    typedef T run __attribute__((ext_vector_type(C)));
+    typedef T run_any __attribute__((ext_vector_type(C), aligned(sizeof(T))));
+    run t;
+#pragma unroll
+    for (int c = 0; c < C; ++c) t[c] = (T)v[c];
+    *reinterpret_cast<run_any*>(out) = t;
+}
+
+// A descriptor of `bytes` bytes from p on; reads beyond them give 0.
+__device__ __forceinline__ i32x4 extent(const uint8_t* p, int64_t bytes) {
+    const uint64_t at = (uint64_t)p;
+    i32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)at);
+    r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32)) & 0xffff;
+    r[2] = __builtin_amdgcn_readfirstlane((int)(bytes > 0x7fffffff ? 0x7fffffff : bytes));
+    r[3] = 0x00020000;
+    return r;
+}
+
+// Loads straight to LDS: lane l's 16 (or 4) bytes at off go to lds + 16 l (4 l). They write no register, so that
+// nothing of them is the compiler's to keep: step_barrier waits for their arrival. The wait states are those that a
+// vector write of the descriptor and the write of m0 need before them.
+__device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t off, i32x4 from) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off),
+                 "s"(from)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t off, i32x4 from) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off),
+                 "s"(from)
+                 : "memory", "m0");
+}
+
+// Waits until all but the last `left` of this wave's memory accesses are done and its LDS reads too, then for the block.
+template <int LEFT>
+__device__ __forceinline__ void step_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+
+// Tiles of 32 XT WX feature rows and 32 VT WV vocabulary rows by WX x WV waves. Blocks stay: each goes through its
+// tiles' steps as one sequence, in which the loads run ahead over the tiles' ends and the scores of one tile are
+// written while the next one's operands arrive.
+//
+// In step s a wave multiplies the operands it holds, reads those of step s + 1 from LDS and loads step s + 4 into the
+// place of step s. A barrier a step both publishes the arrived step and frees the one before it. Loads past the last
+// step are made with an empty extent, which keeps their count per step the same. Memory accesses are counted off in
+// order: LOADS to a step, and behind a whole tile's last step its STORES, which the three steps after it let pass.
+// (The scales' loads, one to four blocks of columns, are counted with nothing: a wait is then for a little more.)
+template <class T, int WX, int WV, int XT, int VT>
+__global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(ScoreArgs a, int tiles_x, int tiles_v) {
+    constexpr int NW = WX * WV, BX = 32 * XT * WX, BV = 32 * VT * WV, ROWS = BX + BV;
+    constexpr int LOADS = ROWS / 16 / NW;          // of 16 rows each, per wave and step
+    constexpr int SLOADS = ROWS / 64 / NW;         // of 64 rows' scales each, per wave and four blocks
+    constexpr int STORES = XT * 16;                // of VT scores, per lane and whole tile
+    static_assert(ROWS % (64 * NW) == 0 && BX % 64 == 0 && 2 * LOADS + STORES < 64, "");
+    __shared__ alignas(1024) uint8_t s_rows[STAGES * ROWS * STEP];
+    __shared__ alignas(1024) int s_scales[4 * ROWS];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+    const uint32_t rows0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_rows;
+    const uint32_t scales0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_scales;
+
+    // Consecutive blocks go to the eight dies in turn: each die takes a run of tiles, in groups of GROUP_X rows of
+    // them, so that its cache serves both operands.
+    const int tiles = tiles_x * tiles_v;
+    const int die = blockIdx.x & 7, slot = blockIdx.x >> 3, slots = gridDim.x >> 3;
+    const int first = (int)((int64_t)tiles * die / 8) + slot, last = (int)((int64_t)tiles * (die + 1) / 8);
+    const int mine = first < last ? (last - first + slots - 1) / slots : 0;
+    const int nk = a.cols / STEP;
+    auto corner = [&](int k, int64_t& x0, int64_t& v0) {  // of this block's k-th tile
+        const int at = first + k * slots;
+        const int grp = at / (GROUP_X * tiles_v), in_grp = at - grp * GROUP_X * tiles_v;
+        const int gx = min(GROUP_X, tiles_x - grp * GROUP_X);
+        x0 = (int64_t)(grp * GROUP_X + in_grp % gx) * BX;
+        v0 = (int64_t)(in_grp / gx) * BV;
+    };
+
+    // what this lane loads: of 16 rows a quarter of a row's step; of 64 rows one's scales
+    uint32_t off[LOADS], soff[SLOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const int r = (i * NW + w) * 16 + l / 4, chunk = (l % 4) ^ chunk_turn(r);
+        const int s = r - BX;
+        off[i] = (uint32_t)(r < BX ? r * a.qs : vocab_row<VT>(s) * a.ws) +
+                 chunk * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < SLOADS; ++i) {
+        const int r = (i * NW + w) * 64 + l, s = r - BX;
+        soff[i] = (uint32_t)(r < BX ? r * a.qss : vocab_row<VT>(s) * a.wss);
+    }
+
+    int load_tile = 0, load_k = 0, load_at = 0, load_four = 0;  // the next step to load
+    int64_t lx0 = 0, lv0 = 0;
+    if (mine > 0) corner(0, lx0, lv0);
+    auto issue = [&]() {
+        const bool live = load_tile < mine;
+        if ((load_k & 7) == 0) {  // four blocks of columns begin: their scales, ahead of the values
+            const int64_t sx = live ? (min((int64_t)BX, a.n - lx0) - 1) * a.qss + load_k / 2 + 4 : 0;
+            const int64_t sv = live ? (min((int64_t)BV, a.vocab - lv0) - 1) * a.wss + load_k / 2 + 4 : 0;
+            const i32x4 dx = extent(a.qscales + lx0 * a.qss, sx), dv = extent(a.wscales + lv0 * a.wss, sv);
+#pragma unroll
+            for (int i = 0; i < SLOADS; ++i)
+                load_lds4(scales0 + (load_four * ROWS + (i * NW + w) * 64) * 4, soff[i] + load_k / 2,
+                          (i * NW + w) * 64 < BX ? dx : dv);
+            load_four = (load_four + 1) & 3;
+        }
+        const int64_t ex = live ? (min((int64_t)BX, a.n - lx0) - 1) * a.qs + STEP : 0;
+        const int64_t ev = live ? (min((int64_t)BV, a.vocab - lv0) - 1) * a.ws + STEP : 0;
+        const i32x4 dx = extent(a.q + lx0 * a.qs + load_k * STEP, ex);
+        const i32x4 dv = extent(a.w + lv0 * a.ws + load_k * STEP, ev);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            load_lds16(rows0 + load_at * (ROWS * STEP) + (i * NW + w) * 1024, off[i],
+                       (i * NW + w) * 16 < BX ? dx : dv);
+        load_at = (load_at + 1) & (STAGES - 1);
+        if (++load_k == nk) {
+            load_k = 0;
+            ++load_tile;
+            if (load_tile < mine) corner(load_tile, lx0, lv0);
+        }
+    };
+
+    const int wx = w % WX * (32 * XT), wv = BX + w / WX * (32 * VT);  // the wave's first rows in LDS
+    int read_at = 0;  // the next step to read
+    auto read = [&](i32x8 (&fx)[XT], i32x8 (&fv)[VT]) {
+        const uint8_t* at = s_rows + read_at * (ROWS * STEP);
+        auto row = [&](int r) {
+            const uint8_t* p = at + r * STEP;
+            const int t = chunk_turn(r), h = l / 32;
+            const i32x4 lo = *reinterpret_cast<const i32x4*>(p + ((2 * h) ^ t) * 16);
+            const i32x4 hi = *reinterpret_cast<const i32x4*>(p + ((2 * h + 1) ^ t) * 16);
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        };
+#pragma unroll
+        for (int j = 0; j < VT; ++j) fv[j] = row(wv + 32 * j + l % 32);
+#pragma unroll
+        for (int i = 0; i < XT; ++i) fx[i] = row(wx + 32 * i + l % 32);
+        read_at = (read_at + 1) & (STAGES - 1);
+    };
+
+    f32x16 acc[XT][VT];
+    auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < XT; ++i)
+#pragma unroll
+            for (int j = 0; j < VT; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    };
+    int sx[XT], sv[VT];  // the scales of four blocks, the current one's lowest
+    auto multiply = [&](const i32x8 (&fx)[XT], const i32x8 (&fv)[VT]) {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < XT; ++i)
+#pragma unroll
+                for (int j = 0; j < VT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fx[i], fv[j], acc[i][j], 0, 0, 0, sx[i],
+                                                                              0, sv[j]);
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                bf16x8 hx[XT], hv[VT];
+#pragma unroll
+                for (int i = 0; i < XT; ++i) hx[i] = widen8(fx[i], s, scale_of<0>(sx[i]));
+#pragma unroll
+                for (int j = 0; j < VT; ++j) hv[j] = widen8(fv[j], s, scale_of<0>(sv[j]));
+#pragma unroll
+                for (int i = 0; i < XT; ++i)
+#pragma unroll
+                    for (int j = 0; j < VT; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hx[i], hv[j], acc[i][j], 0, 0, 0);
+            }
+        }
+    };
+
+    if (mine == 0) return;
+    i32x8 fx[2][XT], fv[2][VT];
+    for (int i = 0; i < STAGES - 1; ++i) issue();
+    step_barrier<2 * LOADS>();
+    issue();
+    read(fx[0], fv[0]);
+    clear();
+    int quiet = 0, four = 0;  // steps that may leave a tile's stores behind them; the four blocks' place
+    for (int k = 0; k < mine; ++k) {
+        for (int kb = 0; kb < nk / 2; ++kb) {
+            if ((kb & 3) == 0) {
+                const int* at = s_scales + four * ROWS;
+#pragma unroll
+                for (int i = 0; i < XT; ++i) sx[i] = at[wx + 32 * i + l % 32];
+#pragma unroll
+                for (int j = 0; j < VT; ++j) sv[j] = at[wv + 32 * j + l % 32];
+                four = (four + 1) & 3;
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                // step s + 1 has arrived: only s + 2 and s + 3 are under way
+                if (quiet > 0) {
+                    step_barrier<2 * LOADS + STORES>();
+                    --quiet;
+                } else {
+                    step_barrier<2 * LOADS>();
+                }
+                issue();
+                read(fx[1 - half], fv[1 - half]);
+                multiply(fx[half], fv[half]);
+            }
+#pragma unroll
+            for (int i = 0; i < XT; ++i) sx[i] = (int)((uint32_t)sx[i] >> 8);
+#pragma unroll
+            for (int j = 0; j < VT; ++j) sv[j] = (int)((uint32_t)sv[j] >> 8);
+        }
+        int64_t x0, v0;
+        corner(k, x0, v0);
+        // element e of acc[i][j]: feature row x + 32 i + 8 (e / 4) + e % 4, score v + j
+        const int64_t x = x0 + wx + 4 * (l / 32), v = v0 + (wv - BX) + l % 32 * VT;
+        T* out = (T*)a.out + x * a.os + v;
+        const bool whole = x0 + BX <= a.n && v0 + BV <= a.vocab;
+        const int rows = (int)min((int64_t)BX, a.n - x), left = (int)min((int64_t)VT, a.vocab - v);
+#pragma unroll
+        for (int i = 0; i < XT; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int r = 32 * i + 8 * (e / 4) + e % 4;
+                float t[VT];
+#pragma unroll
+                for (int j = 0; j < VT; ++j) t[j] = acc[i][j][e];
+                if (whole || (r < rows && left == VT)) {
+                    store_run(out + r * a.os, t);
+                } else if (r < rows) {
+#pragma unroll
+                    for (int j = 0; j < VT - 1; ++j)
+                        if (j < left) out[r * a.os + j] = (T)t[j];
+                }
+            }
+        quiet = whole ? 3 : 0;
+        clear();
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last step
+}
+
+template <class T, int WX, int WV, int XT, int VT>
+hipError_t scores_tiles(const ScoreArgs& a, hipStream_t s) {
+    constexpr int BX = 32 * XT * WX, BV = 32 * VT * WV;
+    const int64_t tv = (a.vocab + BV - 1) / BV;
+    // as many rows at a time as 2^30 tiles hold
+    const int64_t most = ((int64_t)1 << 30) / tv * BX;
+    for (int64_t r = 0; r < a.n; r += most) {
+        ScoreArgs p = a;
+        p.n = a.n - r < most ? a.n - r : most;
+        p.q += r * a.qs;
+        p.qscales += r * a.qss;
+        p.out = (T*)a.out + r * a.os;
+        const int64_t tx = (p.n + BX - 1) / BX, blocks = 256 * (8 / (WX * WV));
+        const int64_t grid = tx * tv < blocks ? (tx * tv + 7) / 8 * 8 : blocks;
+        k_scores_tiles<T, WX, WV, XT, VT><<<(unsigned)grid, 64 * WX * WV, 0, s>>>(p, (int)tx, (int)tv);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    return hipSuccess;
+}
+
 template <class T>
 hipError_t scores(const ScoreArgs& a, hipStream_t s) {
+    auto tiles = [&](int64_t bx, int64_t bv) { return ((a.n + bx - 1) / bx) * ((a.vocab + bv - 1) / bv); };
+    if constexpr (sizeof(T) == 2)
+        if (tiles(256, 256) >= 192) return scores_tiles<T, 4, 2, 2, 4>(a, s);
+    if (tiles(128, 128) >= 64) return scores_tiles<T, 2, 2, 2, 2>(a, s);
     return scores_direct<T, 2, 2, 1>(a, s);
 }
 

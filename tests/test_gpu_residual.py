@@ -265,7 +265,8 @@ def check_scores(rows, vocabulary, dtype, pad=0):
 SCORES = [(1, 128, 1), (1, 128, 16), (1, 1024, 1000), (2, 256, 17), (3, 384, 3), (15, 512, 40), (16, 640, 63),
           (17, 128, 64), (33, 896, 65), (48, 2048, 129), (64, 1024, 1000), (100, 256, 255), (127, 128, 257),
           (128, 512, 128), (257, 1152, 513), (300, 8192, 70), (700, 128, 33), (1000, 256, 1000), (1025, 384, 2049),
-          (5003, 256, 1031), (2, 65_536, 5), (4096, 512, 2048)]
+          (5003, 256, 1031), (2, 65_536, 5), (4096, 512, 2048),
+          (4000, 384, 5000), (9001, 128, 8003)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
