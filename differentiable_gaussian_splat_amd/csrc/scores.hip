@@ -242,29 +242,33 @@ __device__ __forceinline__ void store_run(T* out, const float (&v)[C]) {
     *reinterpret_cast<run_any*>(out) = t;
 }
 
-// A descriptor of `bytes` bytes from p on; reads beyond them give 0.
-__device__ __forceinline__ i32x4 extent(const uint8_t* p, int64_t bytes) {
+// A descriptor of `bytes` bytes from p on; reads beyond them give 0. (A step's offset, which is added to a lane's, stays
+// below `bytes`, and a lane's own lies beyond them for every row past the last.)
+__device__ __forceinline__ i32x4 extent(const uint8_t* p, int bytes) {
     const uint64_t at = (uint64_t)p;
     i32x4 r;
     r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)at);
     r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32)) & 0xffff;
-    r[2] = __builtin_amdgcn_readfirstlane((int)(bytes > 0x7fffffff ? 0x7fffffff : bytes));
+    r[2] = __builtin_amdgcn_readfirstlane(bytes);
     r[3] = 0x00020000;
     return r;
 }
 
-// Loads straight to LDS: lane l's 16 (or 4) bytes at off go to lds + 16 l (4 l). They write no register, so that
-// nothing of them is the compiler's to keep: step_barrier waits for their arrival. The wait states are those that a
-// vector write of the descriptor and the write of m0 need before them.
-__device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t off, i32x4 from) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off),
-                 "s"(from)
+// Loads straight to LDS: lane l's 16 (or 4) bytes at off + step go to lds + 16 l (4 l). They write no register, so that
+// nothing of them is the compiler's to keep: step_barrier waits for their arrival. The wait state is what a write of m0
+// needs before them; those that a vector write of the descriptor needs are settle's.
+__device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t off, i32x4 from, int step) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(off),
+                 "s"(from), "s"(step)
                  : "memory", "m0");
 }
-__device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t off, i32x4 from) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off),
-                 "s"(from)
+__device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t off, i32x4 from, int step) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(off),
+                 "s"(from), "s"(step)
                  : "memory", "m0");
+}
+__device__ __forceinline__ void settle(i32x4& a, i32x4& b, i32x4& c, i32x4& d) {
+    asm volatile("s_nop 4" : "+s"(a), "+s"(b), "+s"(c), "+s"(d));
 }
 
 // Waits until all but the last `left` of this wave's memory accesses are done and its LDS reads too, then for the block.
@@ -279,8 +283,8 @@ __device__ __forceinline__ void step_barrier() {
 //
 // In step s a wave multiplies the operands it holds, reads those of step s + 1 from LDS and loads step s + 4 into the
 // place of step s. A barrier a step both publishes the arrived step and frees the one before it. Loads past the last
-// step are made with an empty extent, which keeps their count per step the same. Memory accesses are counted off in
-// order: LOADS to a step, and behind a whole tile's last step its STORES, which the three steps after it let pass.
+// step are made all the same, which keeps their count per step. Memory accesses are counted off in
+// order: LOADS to a step, and behind a whole tile's last step its STORES, which the two steps after it let pass.
 // (The scales' loads, one to four blocks of columns, are counted with nothing: a wait is then for a little more.)
 template <class T, int WX, int WV, int XT, int VT>
 __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(ScoreArgs a, int tiles_x, int tiles_v) {
@@ -288,7 +292,7 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
     constexpr int LOADS = ROWS / 16 / NW;          // of 16 rows each, per wave and step
     constexpr int SLOADS = ROWS / 64 / NW;         // of 64 rows' scales each, per wave and four blocks
     constexpr int STORES = XT * 16;                // of VT scores, per lane and whole tile
-    static_assert(ROWS % (64 * NW) == 0 && BX % 64 == 0 && 2 * LOADS + STORES < 64, "");
+    static_assert(ROWS % (64 * NW) == 0 && BX % (16 * NW) == 0 && BX % 64 == 0 && 2 * LOADS + STORES < 64, "");
     __shared__ alignas(1024) uint8_t s_rows[STAGES * ROWS * STEP];
     __shared__ alignas(1024) int s_scales[4 * ROWS];
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
@@ -296,82 +300,91 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
     const uint32_t scales0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s_scales;
 
     // Consecutive blocks go to the eight dies in turn: each die takes a run of tiles, in groups of GROUP_X rows of
-    // them, so that its cache serves both operands.
+    // them, so that its cache serves both operands. A block's places in the order are apart by a constant.
     const int tiles = tiles_x * tiles_v;
-    const int die = blockIdx.x & 7, slot = blockIdx.x >> 3, slots = gridDim.x >> 3;
-    const int first = (int)((int64_t)tiles * die / 8) + slot, last = (int)((int64_t)tiles * (die + 1) / 8);
+    const int die = blockIdx.x & 7, slots = gridDim.x >> 3;
+    const int first = (int)((int64_t)tiles * die / 8) + (int)(blockIdx.x >> 3);
+    const int last = (int)((int64_t)tiles * (die + 1) / 8);
     const int mine = first < last ? (last - first + slots - 1) / slots : 0;
-    const int nk = a.cols / STEP;
-    auto corner = [&](int k, int64_t& x0, int64_t& v0) {  // of this block's k-th tile
-        const int at = first + k * slots;
-        const int grp = at / (GROUP_X * tiles_v), in_grp = at - grp * GROUP_X * tiles_v;
-        const int gx = min(GROUP_X, tiles_x - grp * GROUP_X);
-        x0 = (int64_t)(grp * GROUP_X + in_grp % gx) * BX;
-        v0 = (int64_t)(in_grp / gx) * BV;
+    if (mine == 0) return;
+    const int nk = a.cols / STEP, n = (int)a.n, vocab = (int)a.vocab;
+    struct Place {
+        int group, in;
     };
+    auto advance = [&](Place& p) {
+        p.in += slots;
+        while (p.in >= GROUP_X * tiles_v) {
+            p.in -= GROUP_X * tiles_v;
+            ++p.group;
+        }
+    };
+    auto corner = [&](const Place& p, int& x0, int& v0) {
+        const int rows = min(GROUP_X, tiles_x - p.group * GROUP_X);
+        const int v = rows == 4 ? p.in >> 2 : rows == 3 ? (int)__umulhi((uint32_t)p.in, 0x55555556u) : p.in >> (rows - 1);
+        x0 = (p.group * GROUP_X + p.in - v * rows) * BX;
+        v0 = v * BV;
+    };
+    static_assert(GROUP_X == 4, "the divisions by a group's rows");
 
-    // what this lane loads: of 16 rows a quarter of a row's step; of 64 rows one's scales
-    uint32_t off[LOADS], soff[SLOADS];
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        const int r = (i * NW + w) * 16 + l / 4, chunk = (l % 4) ^ chunk_turn(r);
-        const int s = r - BX;
-        off[i] = (uint32_t)(r < BX ? r * a.qs : vocab_row<VT>(s) * a.ws) +
-                 chunk * 16;
-    }
-#pragma unroll
-    for (int i = 0; i < SLOADS; ++i) {
-        const int r = (i * NW + w) * 64 + l, s = r - BX;
-        soff[i] = (uint32_t)(r < BX ? r * a.qss : vocab_row<VT>(s) * a.wss);
-    }
+    // what this lane loads first: a quarter of a row's step of either operand (then of rows NW * 16 on, which turns
+    // neither the chunks nor the order of the vocabulary's rows); one row's scales
+    static_assert(NW * 16 % (32 * VT) == 0 && SLOADS == 1, "");
+    const int row = w * 16 + l / 4, chunk = ((l % 4) ^ chunk_turn(row)) * 16;
+    int off_x = row * (int)a.qs + chunk, off_v = vocab_row<VT>(row) * (int)a.ws + chunk;
+    const int srow = w * 64 + l, soff = srow < BX ? srow * (int)a.qss : vocab_row<VT>(srow - BX) * (int)a.wss;
+    const int gap_x = NW * 16 * (int)a.qs, gap_v = NW * 16 * (int)a.ws;
 
-    int load_tile = 0, load_k = 0, load_at = 0, load_four = 0;  // the next step to load
-    int64_t lx0 = 0, lv0 = 0;
-    if (mine > 0) corner(0, lx0, lv0);
-    auto issue = [&]() {
-        const bool live = load_tile < mine;
-        if ((load_k & 7) == 0) {  // four blocks of columns begin: their scales, ahead of the values
-            const int64_t sx = live ? (min((int64_t)BX, a.n - lx0) - 1) * a.qss + load_k / 2 + 4 : 0;
-            const int64_t sv = live ? (min((int64_t)BV, a.vocab - lv0) - 1) * a.wss + load_k / 2 + 4 : 0;
-            const i32x4 dx = extent(a.qscales + lx0 * a.qss, sx), dv = extent(a.wscales + lv0 * a.wss, sv);
-#pragma unroll
-            for (int i = 0; i < SLOADS; ++i)
-                load_lds4(scales0 + (load_four * ROWS + (i * NW + w) * 64) * 4, soff[i] + load_k / 2,
-                          (i * NW + w) * 64 < BX ? dx : dv);
+    // the tile to load next: its place, its rows and how far they reach; the step in it and its places in LDS
+    Place load_place{first / (GROUP_X * tiles_v), first % (GROUP_X * tiles_v)}, place = load_place;
+    int load_tile = 0, load_k = 0, load_at = 0, load_four = 0;
+    i32x4 from_x, from_v, from_xs, from_vs;
+    auto turn = [&]() {
+        int x0 = 0, v0 = 0;  // past the last tile the first one of all again, which nothing reads
+        if (load_tile < mine) corner(load_place, x0, v0);
+        const int x = min(BX, n - x0) - 1, v = min(BV, vocab - v0) - 1, fours = (nk + 7) / 8 * 4;
+        from_x = extent(a.q + x0 * a.qs, x * (int)a.qs + a.cols);
+        from_v = extent(a.w + v0 * a.ws, v * (int)a.ws + a.cols);
+        from_xs = extent(a.qscales + x0 * a.qss, x * (int)a.qss + fours);
+        from_vs = extent(a.wscales + v0 * a.wss, v * (int)a.wss + fours);
+        settle(from_x, from_v, from_xs, from_vs);
+    };
+    auto issue_scales = [&]() {  // where four blocks of columns begin, ahead of their values
+        if ((load_k & 7) == 0) {
+            load_lds4(scales0 + (load_four * ROWS + w * 64) * 4, soff, w * 64 < BX ? from_xs : from_vs, load_k / 2);
             load_four = (load_four + 1) & 3;
         }
-        const int64_t ex = live ? (min((int64_t)BX, a.n - lx0) - 1) * a.qs + STEP : 0;
-        const int64_t ev = live ? (min((int64_t)BV, a.vocab - lv0) - 1) * a.ws + STEP : 0;
-        const i32x4 dx = extent(a.q + lx0 * a.qs + load_k * STEP, ex);
-        const i32x4 dv = extent(a.w + lv0 * a.ws + load_k * STEP, ev);
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            load_lds16(rows0 + load_at * (ROWS * STEP) + (i * NW + w) * 1024, off[i],
-                       (i * NW + w) * 16 < BX ? dx : dv);
+    };
+    auto issue = [&](int i) {  // the i-th of the step's loads
+        constexpr int LX = BX / 16 / NW;
+        asm volatile("" : "+v"(off_x), "+v"(off_v));  // added anew in each step: the sums would not fit the registers
+        load_lds16(rows0 + load_at * (ROWS * STEP) + (i * NW + w) * 1024,
+                   i < LX ? off_x + i * gap_x : off_v + (i - LX) * gap_v, i < LX ? from_x : from_v, load_k * STEP);
+    };
+    auto issued = [&]() {
         load_at = (load_at + 1) & (STAGES - 1);
-        if (++load_k == nk) {
+        ++load_k;
+    };
+    auto issued_block = [&]() {  // behind every second step
+        if (load_k == nk) {
             load_k = 0;
             ++load_tile;
-            if (load_tile < mine) corner(load_tile, lx0, lv0);
+            advance(load_place);
+            turn();
         }
     };
 
     const int wx = w % WX * (32 * XT), wv = BX + w / WX * (32 * VT);  // the wave's first rows in LDS
+    // where a lane's rows of its first tiles begin (the others are 32 rows on, which their chunks' turn does not change)
+    const int turned = ((l / 32 * 2) ^ chunk_turn(l % 32)) * 16;
+    const int at_x = (wx + l % 32) * STEP + turned, at_v = (wv + l % 32) * STEP + turned;
     int read_at = 0;  // the next step to read
-    auto read = [&](i32x8 (&fx)[XT], i32x8 (&fv)[VT]) {
+    auto read = [&](i32x8 (&fx)[XT], i32x8 (&fv)[VT], int f) {  // the f-th of the step's fragments
         const uint8_t* at = s_rows + read_at * (ROWS * STEP);
-        auto row = [&](int r) {
-            const uint8_t* p = at + r * STEP;
-            const int t = chunk_turn(r), h = l / 32;
-            const i32x4 lo = *reinterpret_cast<const i32x4*>(p + ((2 * h) ^ t) * 16);
-            const i32x4 hi = *reinterpret_cast<const i32x4*>(p + ((2 * h + 1) ^ t) * 16);
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        };
-#pragma unroll
-        for (int j = 0; j < VT; ++j) fv[j] = row(wv + 32 * j + l % 32);
-#pragma unroll
-        for (int i = 0; i < XT; ++i) fx[i] = row(wx + 32 * i + l % 32);
-        read_at = (read_at + 1) & (STAGES - 1);
+        const int lo = f < VT ? at_v : at_x, r = 32 * (f < VT ? f : f - VT);
+        const i32x4 a0 = *reinterpret_cast<const i32x4*>(at + lo + r * STEP);
+        const i32x4 a1 = *reinterpret_cast<const i32x4*>(at + (lo ^ 16) + r * STEP);
+        (f < VT ? fv[f < VT ? f : 0] : fx[f < VT ? 0 : f - VT]) =
+            __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
     };
 
     f32x16 acc[XT][VT];
@@ -384,14 +397,21 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
     };
     int sx[XT], sv[VT];  // the scales of four blocks, the current one's lowest
-    auto multiply = [&](const i32x8 (&fx)[XT], const i32x8 (&fv)[VT]) {
+    // between(part, parts): what is done between the products
+    auto multiply = [&](const i32x8 (&fx)[XT], const i32x8 (&fv)[VT], auto between) {
+        // a product stays in its place: left to the compiler they sink past the next barriers, and the operands of
+        // several steps do not fit the registers
+        auto stay = [&](f32x16& c) { asm volatile("" : "+v"(c)); };
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int i = 0; i < XT; ++i)
 #pragma unroll
-                for (int j = 0; j < VT; ++j)
+                for (int j = 0; j < VT; ++j) {
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fx[i], fv[j], acc[i][j], 0, 0, 0, sx[i],
                                                                               0, sv[j]);
+                    stay(acc[i][j]);
+                    between(i * VT + j, XT * VT);
+                }
         } else {
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
@@ -403,72 +423,104 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
 #pragma unroll
                 for (int i = 0; i < XT; ++i)
 #pragma unroll
-                    for (int j = 0; j < VT; ++j)
+                    for (int j = 0; j < VT; ++j) {
                         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hx[i], hv[j], acc[i][j], 0, 0, 0);
+                        stay(acc[i][j]);
+                    }
+                between(s, 4);
             }
         }
     };
 
-    if (mine == 0) return;
+    turn();
     i32x8 fx[2][XT], fv[2][VT];
-    for (int i = 0; i < STAGES - 1; ++i) issue();
-    step_barrier<2 * LOADS>();
-    issue();
-    read(fx[0], fv[0]);
-    clear();
-    int quiet = 0, four = 0;  // steps that may leave a tile's stores behind them; the four blocks' place
-    for (int k = 0; k < mine; ++k) {
-        for (int kb = 0; kb < nk / 2; ++kb) {
-            if ((kb & 3) == 0) {
-                const int* at = s_scales + four * ROWS;
+    static_assert(STAGES == 4, "");
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        issue_scales();
 #pragma unroll
-                for (int i = 0; i < XT; ++i) sx[i] = at[wx + 32 * i + l % 32];
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                for (int j = 0; j < VT; ++j) sv[j] = at[wv + 32 * j + l % 32];
-                four = (four + 1) & 3;
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                // step s + 1 has arrived: only s + 2 and s + 3 are under way
-                if (quiet > 0) {
-                    step_barrier<2 * LOADS + STORES>();
-                    --quiet;
-                } else {
-                    step_barrier<2 * LOADS>();
-                }
-                issue();
-                read(fx[1 - half], fv[1 - half]);
-                multiply(fx[half], fv[half]);
-            }
-#pragma unroll
-            for (int i = 0; i < XT; ++i) sx[i] = (int)((uint32_t)sx[i] >> 8);
-#pragma unroll
-            for (int j = 0; j < VT; ++j) sv[j] = (int)((uint32_t)sv[j] >> 8);
+            for (int j = 0; j < LOADS; ++j) issue(j);
+            issued();
         }
-        int64_t x0, v0;
-        corner(k, x0, v0);
+        issued_block();
+    }
+    step_barrier<3 * LOADS>();
+#pragma unroll
+    for (int f = 0; f < XT + VT; ++f) read(fx[0], fv[0], f);
+    ++read_at;
+    clear();
+    int four = 0;        // the place of the four blocks' scales
+    bool quiet = false;  // whether a whole tile's stores may still be under way
+    // a block of columns: two steps
+    auto block = [&](int kb, auto stores) {
+        if ((kb & 3) == 0) {
+            const int* at = s_scales + four * ROWS;
+#pragma unroll
+            for (int i = 0; i < XT; ++i) sx[i] = at[wx + 32 * i + l % 32];
+#pragma unroll
+            for (int j = 0; j < VT; ++j) sv[j] = at[wv + 32 * j + l % 32];
+            four = (four + 1) & 3;
+        }
+        issue_scales();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            step_barrier<2 * LOADS + decltype(stores)::value>();  // step s + 1 is here, s + 2 and s + 3 under way
+            // the next operands' reads and the loads spread over the products: all waves' at once would keep each other,
+            // and the products behind them, waiting
+            multiply(fx[half], fv[half], [&](int part, int parts) {
+#pragma unroll
+                for (int f = part * (XT + VT) / parts; f < (part + 1) * (XT + VT) / parts; ++f)
+                    read(fx[1 - half], fv[1 - half], f);
+#pragma unroll
+                for (int i = part * LOADS / parts; i < (part + 1) * LOADS / parts; ++i) issue(i);
+            });
+            read_at = (read_at + 1) & (STAGES - 1);
+            issued();
+        }
+        issued_block();
+#pragma unroll
+        for (int i = 0; i < XT; ++i) sx[i] = (int)((uint32_t)sx[i] >> 8);
+#pragma unroll
+        for (int j = 0; j < VT; ++j) sv[j] = (int)((uint32_t)sv[j] >> 8);
+    };
+    for (int k = 0; k < mine; ++k) {
+        if (quiet)
+            block(0, std::integral_constant<int, STORES>{});
+        else
+            block(0, std::integral_constant<int, 0>{});
+        for (int kb = 1; kb < nk / 2; ++kb) block(kb, std::integral_constant<int, 0>{});
+        int x0, v0;
+        corner(place, x0, v0);
+        advance(place);
         // element e of acc[i][j]: feature row x + 32 i + 8 (e / 4) + e % 4, score v + j
-        const int64_t x = x0 + wx + 4 * (l / 32), v = v0 + (wv - BX) + l % 32 * VT;
-        T* out = (T*)a.out + x * a.os + v;
-        const bool whole = x0 + BX <= a.n && v0 + BV <= a.vocab;
-        const int rows = (int)min((int64_t)BX, a.n - x), left = (int)min((int64_t)VT, a.vocab - v);
+        const int x = x0 + wx + 4 * (l / 32), v = v0 + (wv - BX) + l % 32 * VT;
+        T* out = (T*)a.out + (int64_t)x * a.os + v;
+        const bool whole = n - x0 >= BX && vocab - v0 >= BV;
+        int rows = n - x;  // from out on
+        const int left = vocab - v;
 #pragma unroll
         for (int i = 0; i < XT; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const int r = 32 * i + 8 * (e / 4) + e % 4;
                 float t[VT];
 #pragma unroll
                 for (int j = 0; j < VT; ++j) t[j] = acc[i][j][e];
-                if (whole || (r < rows && left == VT)) {
-                    store_run(out + r * a.os, t);
-                } else if (r < rows) {
+                if (whole || (rows > 0 && left >= VT)) {
+                    store_run(out, t);
+                } else if (rows > 0) {
 #pragma unroll
                     for (int j = 0; j < VT - 1; ++j)
-                        if (j < left) out[r * a.os + j] = (T)t[j];
+                        if (j < left) out[j] = (T)t[j];
                 }
+                // row by row: all rows' places together would not fit the registers
+                const int on = e % 4 == 3 ? 5 : 1;
+                out += on * a.os;
+                rows -= on;
+                asm volatile("" : "+v"(out), "+v"(rows));
             }
-        quiet = whole ? 3 : 0;
+        quiet = whole;
         clear();
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last step
