@@ -235,6 +235,7 @@ struct ScoreArgs {
     int64_t qs, qss, ws, wss;  // row strides
     void* out;
     int64_t os;
+    bool past;  // set by the launch
 };
 hipError_t launch_label_scores(const ScoreArgs& a, hipStream_t stream);
 

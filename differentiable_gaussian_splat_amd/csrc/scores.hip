@@ -89,11 +89,13 @@ __device__ __forceinline__ bf16x8 widen8(const i32x8& q, int s, float scale) {
     return v;
 }
 
+constexpr int DIRECT_WAVES = 8;  // of a block
+
 // Straight from memory to registers: a wave takes 16 XT feature rows and 16 VT vocabulary rows over its share of the
 // depth (every KS-th four blocks); the KS waves of a tile join their sums in LDS.
 template <class T, int XT, int VT, int KS>
-__global__ __launch_bounds__(256) void k_scores_direct(ScoreArgs a) {
-    constexpr int VW = 4 / KS;  // tiles side by side
+__global__ __launch_bounds__(64 * DIRECT_WAVES) void k_scores_direct(ScoreArgs a) {
+    constexpr int VW = DIRECT_WAVES / KS;  // tiles side by side
     __shared__ float s_join[KS > 1 ? VW * (KS - 1) * XT * VT * 256 : 1];
     const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
     const int share = w % KS, side = w / KS;
@@ -196,7 +198,7 @@ __global__ __launch_bounds__(256) void k_scores_direct(ScoreArgs a) {
 
 template <class T, int XT, int VT, int KS>
 hipError_t scores_direct(const ScoreArgs& a, hipStream_t s) {
-    const int64_t per = 16 * VT * (4 / KS);
+    const int64_t per = 16 * VT * (DIRECT_WAVES / KS);
     const int64_t bx = (a.vocab + per - 1) / per;
     // a grid's second axis holds 65535 blocks
     const int64_t most = (int64_t)65535 * 16 * XT;
@@ -207,16 +209,29 @@ hipError_t scores_direct(const ScoreArgs& a, hipStream_t s) {
         p.qscales += r * a.qss;
         p.out = (T*)a.out + r * a.os;
         const dim3 grid((unsigned)bx, (unsigned)((p.n + 16 * XT - 1) / (16 * XT)));
-        k_scores_direct<T, XT, VT, KS><<<grid, 256, 0, s>>>(p);
+        k_scores_direct<T, XT, VT, KS><<<grid, 64 * DIRECT_WAVES, 0, s>>>(p);
         if (hipError_t e = hipGetLastError()) return e;
     }
     return hipSuccess;
 }
 
+// The depth is split over as many of a block's waves as it takes to have two to a SIMD, and as there are four blocks of
+// columns.
+template <class T, int XT, int VT>
+hipError_t scores_split(const ScoreArgs& a, hipStream_t s) {
+    const int64_t tiles = ((a.n + 16 * XT - 1) / (16 * XT)) * ((a.vocab + 16 * VT - 1) / (16 * VT));
+    const int fours = (a.cols / Q8_BLOCK + 3) / 4;
+    int ks = 1;
+    while (ks < DIRECT_WAVES && ks < fours && tiles * ks < 2048) ks *= 2;
+    if (ks == 1) return scores_direct<T, XT, VT, 1>(a, s);
+    if (ks == 2) return scores_direct<T, XT, VT, 2>(a, s);
+    if (ks == 4) return scores_direct<T, XT, VT, 4>(a, s);
+    return scores_direct<T, XT, VT, 8>(a, s);
+}
+
 // ------------------------------------------------------------------ tiles through LDS
 
 constexpr int STEP = 64;     // columns of a staged step: one e4m3 product deep, half a block
-constexpr int STAGES = 4;    // steps in LDS: one being read, three on their way
 constexpr int GROUP_X = 4;   // rows of tiles that follow one another along the vocabulary
 
 // How a row's four 16-byte chunks are exchanged, so that the sixteen lanes that read one depth's chunks together find
@@ -231,15 +246,18 @@ __device__ __forceinline__ int vocab_row(int s) {
     return s / (32 * VT) * (32 * VT) + s % 32 * VT + s / 32 % VT;
 }
 
-// Stores C scores side by side (out is aligned to its elements only).
-template <class T, int C>
+// Stores C scores side by side (out is aligned to its elements only). PAST: past the caches, which the operands need.
+template <bool PAST, class T, int C>
 __device__ __forceinline__ void store_run(T* out, const float (&v)[C]) {
     typedef T run __attribute__((ext_vector_type(C)));
     typedef T run_any __attribute__((ext_vector_type(C), aligned(sizeof(T))));
     run t;
 #pragma unroll
     for (int c = 0; c < C; ++c) t[c] = (T)v[c];
-    *reinterpret_cast<run_any*>(out) = t;
+    if (PAST)
+        __builtin_nontemporal_store(t, reinterpret_cast<run_any*>(out));
+    else
+        *reinterpret_cast<run_any*>(out) = t;
 }
 
 // A descriptor of `bytes` bytes from p on; reads beyond them give 0. (A step's offset, which is added to a lane's, stays
@@ -254,7 +272,7 @@ __device__ __forceinline__ i32x4 extent(const uint8_t* p, int bytes) {
     return r;
 }
 
-// Loads straight to LDS: lane l's 16 (or 4) bytes at off + step go to lds + 16 l (4 l). They write no register, so that
+// Loads straight to LDS: lane l's 16 bytes at off + step (4 bytes at from) go to lds + 16 l (4 l). They write no register, so that
 // nothing of them is the compiler's to keep: step_barrier waits for their arrival. The wait state is what a write of m0
 // needs before them; those that a vector write of the descriptor needs are settle's.
 __device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t off, i32x4 from, int step) {
@@ -262,14 +280,10 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t off, i32x4 fro
                  "s"(from), "s"(step)
                  : "memory", "m0");
 }
-__device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t off, i32x4 from, int step) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(off),
-                 "s"(from), "s"(step)
-                 : "memory", "m0");
+__device__ __forceinline__ void load_lds4(uint32_t lds, const uint8_t* from) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(from) : "memory", "m0");
 }
-__device__ __forceinline__ void settle(i32x4& a, i32x4& b, i32x4& c, i32x4& d) {
-    asm volatile("s_nop 4" : "+s"(a), "+s"(b), "+s"(c), "+s"(d));
-}
+__device__ __forceinline__ void settle(i32x4& a, i32x4& b) { asm volatile("s_nop 4" : "+s"(a), "+s"(b)); }
 
 // Waits until all but the last `left` of this wave's memory accesses are done and its LDS reads too, then for the block.
 template <int LEFT>
@@ -281,18 +295,18 @@ __device__ __forceinline__ void step_barrier() {
 // tiles' steps as one sequence, in which the loads run ahead over the tiles' ends and the scores of one tile are
 // written while the next one's operands arrive.
 //
-// In step s a wave multiplies the operands it holds, reads those of step s + 1 from LDS and loads step s + 4 into the
-// place of step s. A barrier a step both publishes the arrived step and frees the one before it. Loads past the last
+// STAGES steps are in LDS. In step s a wave multiplies the operands it holds, reads those of step s + 1 from LDS and
+// loads step s + STAGES into the place of step s. A barrier a step both publishes the arrived step and frees the one before it. Loads past the last
 // step are made all the same, which keeps their count per step. Memory accesses are counted off in
 // order: LOADS to a step, and behind a whole tile's last step its STORES, which the two steps after it let pass.
 // (The scales' loads, one to four blocks of columns, are counted with nothing: a wait is then for a little more.)
-template <class T, int WX, int WV, int XT, int VT>
+template <class T, int WX, int WV, int XT, int VT, int STAGES>
 __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(ScoreArgs a, int tiles_x, int tiles_v) {
     constexpr int NW = WX * WV, BX = 32 * XT * WX, BV = 32 * VT * WV, ROWS = BX + BV;
     constexpr int LOADS = ROWS / 16 / NW;          // of 16 rows each, per wave and step
-    constexpr int SLOADS = ROWS / 64 / NW;         // of 64 rows' scales each, per wave and four blocks
     constexpr int STORES = XT * 16;                // of VT scores, per lane and whole tile
-    static_assert(ROWS % (64 * NW) == 0 && BX % (16 * NW) == 0 && BX % 64 == 0 && 2 * LOADS + STORES < 64, "");
+    static_assert(ROWS % (16 * NW) == 0 && BX % (16 * NW) == 0 && BX % 64 == 0, "");
+    static_assert((STAGES - 2) * LOADS + STORES < 64 && (STAGES - 1) * LOADS < 64, "what a wait can count");
     __shared__ alignas(1024) uint8_t s_rows[STAGES * ROWS * STEP];
     __shared__ alignas(1024) int s_scales[4 * ROWS];
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
@@ -307,7 +321,13 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
     const int last = (int)((int64_t)tiles * (die + 1) / 8);
     const int mine = first < last ? (last - first + slots - 1) / slots : 0;
     if (mine == 0) return;
-    const int nk = a.cols / STEP, n = (int)a.n, vocab = (int)a.vocab;
+    const int nk = a.cols / STEP;
+    // the arguments read again where they are used once a tile: kept over the steps they would not fit the registers
+    auto again = []() {
+        auto p = (const __attribute__((address_space(4))) ScoreArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+        asm volatile("" : "+s"(p));
+        return p;
+    };
     struct Place {
         int group, in;
     };
@@ -326,31 +346,34 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
     };
     static_assert(GROUP_X == 4, "the divisions by a group's rows");
 
-    // what this lane loads first: a quarter of a row's step of either operand (then of rows NW * 16 on, which turns
-    // neither the chunks nor the order of the vocabulary's rows); one row's scales
-    static_assert(NW * 16 % (32 * VT) == 0 && SLOADS == 1, "");
+    // what this lane loads first: a quarter of a row's step of either operand (then of rows apart by multiples of
+    // NW * 16, which turns no chunks and keeps the order of the vocabulary's rows apart from the lane's)
+    static_assert(NW * 16 % 32 == 0 && (VT % (NW / 2) == 0 || NW / 2 % VT == 0), "");
     const int row = w * 16 + l / 4, chunk = ((l % 4) ^ chunk_turn(row)) * 16;
     int off_x = row * (int)a.qs + chunk, off_v = vocab_row<VT>(row) * (int)a.ws + chunk;
-    const int srow = w * 64 + l, soff = srow < BX ? srow * (int)a.qss : vocab_row<VT>(srow - BX) * (int)a.wss;
-    const int gap_x = NW * 16 * (int)a.qs, gap_v = NW * 16 * (int)a.ws;
 
-    // the tile to load next: its place, its rows and how far they reach; the step in it and its places in LDS
+    // the tile to load next: its place and corner, its rows; the step in it and its places in LDS
     Place load_place{first / (GROUP_X * tiles_v), first % (GROUP_X * tiles_v)}, place = load_place;
-    int load_tile = 0, load_k = 0, load_at = 0, load_four = 0;
-    i32x4 from_x, from_v, from_xs, from_vs;
-    auto turn = [&]() {
-        int x0 = 0, v0 = 0;  // past the last tile the first one of all again, which nothing reads
-        if (load_tile < mine) corner(load_place, x0, v0);
-        const int x = min(BX, n - x0) - 1, v = min(BV, vocab - v0) - 1, fours = (nk + 7) / 8 * 4;
-        from_x = extent(a.q + x0 * a.qs, x * (int)a.qs + a.cols);
-        from_v = extent(a.w + v0 * a.ws, v * (int)a.ws + a.cols);
-        from_xs = extent(a.qscales + x0 * a.qss, x * (int)a.qss + fours);
-        from_vs = extent(a.wscales + v0 * a.wss, v * (int)a.wss + fours);
-        settle(from_x, from_v, from_xs, from_vs);
+    int load_tile = 0, load_k = 0, load_at = 0, load_four = 0, load_x = 0, load_v = 0;
+    i32x4 from_x, from_v;
+    auto turn = [&](i32x4& to_x, i32x4& to_v) {
+        load_x = load_v = 0;  // past the last tile the first one of all again, which nothing reads
+        if (load_tile < mine) corner(load_place, load_x, load_v);
+        const auto* p = again();
+        to_x = extent(p->q + load_x * p->qs, (min(BX, (int)p->n - load_x) - 1) * (int)p->qs + p->cols);
+        to_v = extent(p->w + load_v * p->ws, (min(BV, (int)p->vocab - load_v) - 1) * (int)p->ws + p->cols);
+        settle(to_x, to_v);
     };
-    auto issue_scales = [&]() {  // where four blocks of columns begin, ahead of their values
-        if ((load_k & 7) == 0) {
-            load_lds4(scales0 + (load_four * ROWS + w * 64) * 4, soff, w * 64 < BX ? from_xs : from_vs, load_k / 2);
+    auto issue_scales = [&](int k) {  // where four blocks of columns begin, ahead of their values
+        if ((k & 7) == 0) {
+            const auto* p = again();
+#pragma unroll 1
+            for (int r0 = w * 64; r0 < ROWS; r0 += NW * 64) {  // 64 rows, of one operand
+                const int r = r0 + l;
+                load_lds4(scales0 + (load_four * ROWS + r0) * 4,
+                          k / 2 + (r0 < BX ? p->qscales + min(load_x + r, (int)p->n - 1) * p->qss
+                                           : p->wscales + min(load_v + vocab_row<VT>(r - BX), (int)p->vocab - 1) * p->wss));
+            }
             load_four = (load_four + 1) & 3;
         }
     };
@@ -358,19 +381,17 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
         constexpr int LX = BX / 16 / NW;
         asm volatile("" : "+v"(off_x), "+v"(off_v));  // added anew in each step: the sums would not fit the registers
         load_lds16(rows0 + load_at * (ROWS * STEP) + (i * NW + w) * 1024,
-                   i < LX ? off_x + i * gap_x : off_v + (i - LX) * gap_v, i < LX ? from_x : from_v, load_k * STEP);
+                   i < LX ? off_x + i * NW * 16 * (int)a.qs : off_v + vocab_row<VT>((i - LX) * NW * 16) * (int)a.ws,
+                   i < LX ? from_x : from_v, load_k * STEP);
     };
     auto issued = [&]() {
-        load_at = (load_at + 1) & (STAGES - 1);
+        load_at = load_at == STAGES - 1 ? 0 : load_at + 1;
         ++load_k;
     };
-    auto issued_block = [&]() {  // behind every second step
-        if (load_k == nk) {
-            load_k = 0;
-            ++load_tile;
-            advance(load_place);
-            turn();
-        }
+    auto next_tile = [&](i32x4& to_x, i32x4& to_v) {
+        ++load_tile;
+        advance(load_place);
+        turn(to_x, to_v);
     };
 
     const int wx = w % WX * (32 * XT), wv = BX + w / WX * (32 * VT);  // the wave's first rows in LDS
@@ -432,21 +453,20 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
         }
     };
 
-    turn();
+    turn(from_x, from_v);
     i32x8 fx[2][XT], fv[2][VT];
-    static_assert(STAGES == 4, "");
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-        issue_scales();
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int j = 0; j < LOADS; ++j) issue(j);
-            issued();
+    for (int i = 0; i < STAGES; ++i) {
+        if (load_k == nk) {
+            load_k = 0;
+            next_tile(from_x, from_v);
         }
-        issued_block();
+        issue_scales(load_k);
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) issue(j);
+        issued();
     }
-    step_barrier<3 * LOADS>();
+    step_barrier<(STAGES - 1) * LOADS>();
 #pragma unroll
     for (int f = 0; f < XT + VT; ++f) read(fx[0], fv[0], f);
     ++read_at;
@@ -463,10 +483,21 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
             for (int j = 0; j < VT; ++j) sv[j] = at[wv + 32 * j + l % 32];
             four = (four + 1) & 3;
         }
-        issue_scales();
+        // whichever of the block's two loads begins a tile or four blocks is prepared here, so that nothing branches
+        // between the steps
+        i32x4 to_x = from_x, to_v = from_v;
+        const int ahead = STAGES % 2;  // steps until then
+        int k = load_k + ahead;
+        if (k == nk) {
+            k = 0;
+            next_tile(to_x, to_v);
+        }
+        issue_scales(k);
+        if (ahead == 0) from_x = to_x, from_v = to_v, load_k = k;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            step_barrier<2 * LOADS + decltype(stores)::value>();  // step s + 1 is here, s + 2 and s + 3 under way
+            // step s + 1 is here, the later ones are under way
+            step_barrier<(STAGES - 2) * LOADS + decltype(stores)::value>();
             // the next operands' reads and the loads spread over the products: all waves' at once would keep each other,
             // and the products behind them, waiting
             multiply(fx[half], fv[half], [&](int part, int parts) {
@@ -476,10 +507,10 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
 #pragma unroll
                 for (int i = part * LOADS / parts; i < (part + 1) * LOADS / parts; ++i) issue(i);
             });
-            read_at = (read_at + 1) & (STAGES - 1);
+            read_at = read_at == STAGES - 1 ? 0 : read_at + 1;
             issued();
+            if (ahead == 1 && half == 0) from_x = to_x, from_v = to_v, load_k = k;
         }
-        issued_block();
 #pragma unroll
         for (int i = 0; i < XT; ++i) sx[i] = (int)((uint32_t)sx[i] >> 8);
 #pragma unroll
@@ -495,38 +526,47 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
         corner(place, x0, v0);
         advance(place);
         // element e of acc[i][j]: feature row x + 32 i + 8 (e / 4) + e % 4, score v + j
+        const auto* p = again();
+        const int n = (int)p->n, vocab = (int)p->vocab;
+        const int64_t os = p->os;
         const int x = x0 + wx + 4 * (l / 32), v = v0 + (wv - BX) + l % 32 * VT;
-        T* out = (T*)a.out + (int64_t)x * a.os + v;
+        T* out = (T*)p->out + x * os + v;
         const bool whole = n - x0 >= BX && vocab - v0 >= BV;
         int rows = n - x;  // from out on
         const int left = vocab - v;
+        auto store = [&](auto past) {
 #pragma unroll
-        for (int i = 0; i < XT; ++i)
+            for (int i = 0; i < XT; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float t[VT];
+                for (int e = 0; e < 16; ++e) {
+                    float t[VT];
 #pragma unroll
-                for (int j = 0; j < VT; ++j) t[j] = acc[i][j][e];
-                if (whole || (rows > 0 && left >= VT)) {
-                    store_run(out, t);
-                } else if (rows > 0) {
+                    for (int j = 0; j < VT; ++j) t[j] = acc[i][j][e];
+                    if (whole || (rows > 0 && left >= VT)) {
+                        store_run<decltype(past)::value>(out, t);
+                    } else if (rows > 0) {
 #pragma unroll
-                    for (int j = 0; j < VT - 1; ++j)
-                        if (j < left) out[j] = (T)t[j];
+                        for (int j = 0; j < VT - 1; ++j)
+                            if (j < left) out[j] = (T)t[j];
+                    }
+                    // row by row: all rows' places together would not fit the registers
+                    const int on = e % 4 == 3 ? 5 : 1;
+                    out += on * os;
+                    rows -= on;
+                    asm volatile("" : "+v"(out), "+v"(rows));
                 }
-                // row by row: all rows' places together would not fit the registers
-                const int on = e % 4 == 3 ? 5 : 1;
-                out += on * a.os;
-                rows -= on;
-                asm volatile("" : "+v"(out), "+v"(rows));
-            }
+        };
+        if (whole && p->past)
+            store(std::true_type{});
+        else
+            store(std::false_type{});
         quiet = whole;
         clear();
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last step
 }
 
-template <class T, int WX, int WV, int XT, int VT>
+template <class T, int WX, int WV, int XT, int VT, int STAGES>
 hipError_t scores_tiles(const ScoreArgs& a, hipStream_t s) {
     constexpr int BX = 32 * XT * WX, BV = 32 * VT * WV;
     const int64_t tv = (a.vocab + BV - 1) / BV;
@@ -538,9 +578,11 @@ hipError_t scores_tiles(const ScoreArgs& a, hipStream_t s) {
         p.q += r * a.qs;
         p.qscales += r * a.qss;
         p.out = (T*)a.out + r * a.os;
+        // rows of whole cache lines only: of others past the caches the lines' parts go to memory one by one
+        p.past = (uintptr_t)p.out % 128 == 0 && a.os * sizeof(T) % 128 == 0;
         const int64_t tx = (p.n + BX - 1) / BX, blocks = 256 * (8 / (WX * WV));
         const int64_t grid = tx * tv < blocks ? (tx * tv + 7) / 8 * 8 : blocks;
-        k_scores_tiles<T, WX, WV, XT, VT><<<(unsigned)grid, 64 * WX * WV, 0, s>>>(p, (int)tx, (int)tv);
+        k_scores_tiles<T, WX, WV, XT, VT, STAGES><<<(unsigned)grid, 64 * WX * WV, 0, s>>>(p, (int)tx, (int)tv);
         if (hipError_t e = hipGetLastError()) return e;
     }
     return hipSuccess;
@@ -549,10 +591,12 @@ hipError_t scores_tiles(const ScoreArgs& a, hipStream_t s) {
 template <class T>
 hipError_t scores(const ScoreArgs& a, hipStream_t s) {
     auto tiles = [&](int64_t bx, int64_t bv) { return ((a.n + bx - 1) / bx) * ((a.vocab + bv - 1) / bv); };
-    if constexpr (sizeof(T) == 2)
-        if (tiles(256, 256) >= 192) return scores_tiles<T, 4, 2, 2, 4>(a, s);
-    if (tiles(128, 128) >= 64) return scores_tiles<T, 2, 2, 2, 2>(a, s);
-    return scores_direct<T, 2, 2, 1>(a, s);
+    if constexpr (sizeof(T) == 2) {
+        if (a.cols <= 384 && tiles(128, 256) >= 256) return scores_tiles<T, 2, 2, 2, 4, 3>(a, s);
+        if (tiles(256, 256) >= 192) return scores_tiles<T, 4, 2, 2, 4, 4>(a, s);
+    }
+    if (tiles(128, 128) >= 64) return scores_tiles<T, 2, 2, 2, 2, 4>(a, s);
+    return a.n <= 16 ? scores_split<T, 1, 1>(a, s) : scores_split<T, 2, 2>(a, s);
 }
 
 }  // namespace
