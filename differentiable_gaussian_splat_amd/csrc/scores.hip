@@ -588,9 +588,17 @@ hipError_t scores_tiles(const ScoreArgs& a, hipStream_t s) {
     return hipSuccess;
 }
 
+// Few rows read the vocabulary straight to registers; more go through LDS where that gives blocks enough. us, direct
+// and by tiles of 128 x 128: 4 x 1024 x 65536 13, 14 (float32 13, 18), 16 x 1024 x 65536 17, 15 (17, 18),
+// 32 x 1024 x 65536 18, 15 (18.5, 19.5), 64 x 1024 x 65536 32, 16 (34, 21). Tiles of 256 x 256 have the operands' bytes
+// from LDS for half the products of 128 x 128; with few columns to a tile two blocks to a unit hide each other's
+// stores: by tiles of 256 x 256 and two blocks of 128 x 256, 8192 x 256 x 65536 282, 242; x 384 331, 292; x 512 353,
+// 353; x 1024 650, 769.
 template <class T>
 hipError_t scores(const ScoreArgs& a, hipStream_t s) {
     auto tiles = [&](int64_t bx, int64_t bv) { return ((a.n + bx - 1) / bx) * ((a.vocab + bv - 1) / bv); };
+    if (a.n <= (sizeof(T) == 2 ? 8 : 32))
+        return a.n <= 16 ? scores_split<T, 1, 1>(a, s) : scores_split<T, 2, 2>(a, s);
     if constexpr (sizeof(T) == 2) {
         if (a.cols <= 384 && tiles(128, 256) >= 256) return scores_tiles<T, 2, 2, 2, 4, 3>(a, s);
         if (tiles(256, 256) >= 192) return scores_tiles<T, 4, 2, 2, 4, 4>(a, s);
