@@ -38,17 +38,15 @@ struct ClipTable {
 template <class T>
 constexpr int CHUNK = CHUNK_BYTES / (int)sizeof(T);
 
-// The tensor that holds chunk c.
+// The tensor that holds chunk c: how many begin at or before it, counted by the wave's lanes together (a search by
+// halves waits for one load after another).
 __device__ __forceinline__ int tensor_of(const ClipTensor* t, int count, int64_t c) {
-    int lo = 0, hi = count;  // t[lo].first <= c < t[hi].first
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (t[mid].first <= c)
-            lo = mid;
-        else
-            hi = mid;
+    int k = -1;
+    for (int i = 0; i < count; i += 64) {
+        const int at = i + (threadIdx.x & 63);
+        k += __popcll(__ballot(at < count && t[at].first <= c));
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(k);
 }
 
 __device__ __forceinline__ double block_sum(double v, double* s) {
@@ -63,63 +61,80 @@ __device__ __forceinline__ double block_sum(double v, double* s) {
     return v;
 }
 
+// A thread's accesses of a chunk of `left` elements, all under way together; those past its end are zeros.
 template <class T>
-__device__ __forceinline__ double chunk_squares(const T* g, int64_t left) {
-    constexpr int V = WIDE<T>, STEPS = CHUNK<T> / (CB * V);
-    double s0 = 0., s1 = 0.;
-    if (left >= CHUNK<T>) {
-        wide_t<T> raw[STEPS];
+constexpr int STEPS = CHUNK<T> / (CB * WIDE<T>);
+template <bool FULL, class T>
+__device__ __forceinline__ void load_chunk(const T* g, int left, wide_t<T> (&raw)[STEPS<T>]) {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-            raw[i] = *reinterpret_cast<const wide_any<T>*>(g + (i * CB + threadIdx.x) * V);
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-            for (int k = 0; k < V; k += 2) {
-                const double a = (double)(float)raw[i][k], b = (double)(float)raw[i][k + 1];
-                s0 = fma(a, a, s0);
-                s1 = fma(b, b, s1);
-            }
-    } else {
-        for (int i = threadIdx.x * V; i < left; i += CB * V) {
-            if (i + V <= left) {
-                const wide_t<T> r = *reinterpret_cast<const wide_any<T>*>(g + i);
-#pragma unroll
-                for (int k = 0; k < V; ++k) s0 = fma((double)(float)r[k], (double)(float)r[k], s0);
-            } else {
-                for (int k = i; k < left; ++k) s1 = fma((double)(float)g[k], (double)(float)g[k], s1);
-            }
-        }
+    for (int i = 0; i < STEPS<T>; ++i) {
+        const int at = (i * CB + (int)threadIdx.x) * WIDE<T>;
+        raw[i] = (T)0.f;
+        if (FULL || at + WIDE<T> <= left) raw[i] = *reinterpret_cast<const wide_any<T>*>(g + at);
     }
+}
+
+// This thread's element of those behind a chunk's last whole access, or -1.
+template <class T>
+__device__ __forceinline__ int behind(int left) {
+    const int at = left / WIDE<T> * WIDE<T> + (int)threadIdx.x;
+    return at < left ? at : -1;
+}
+
+template <bool FULL, class T>
+__device__ __forceinline__ double chunk_squares(const T* g, int left) {
+    double s0 = 0., s1 = 0.;
+    wide_t<T> raw[STEPS<T>];
+    load_chunk<FULL>(g, left, raw);
+    if (!FULL) {
+        const int at = behind<T>(left);
+        const double a = at < 0 ? 0. : (double)(float)g[at];
+        s0 = a * a;
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS<T>; ++i)
+#pragma unroll
+        for (int k = 0; k < WIDE<T>; k += 2) {
+            const double a = (double)(float)raw[i][k], b = (double)(float)raw[i][k + 1];
+            s0 = fma(a, a, s0);
+            s1 = fma(b, b, s1);
+        }
     return s0 + s1;
 }
 
-template <class T>
-__device__ __forceinline__ void chunk_scale(const T* g, T* o, int64_t left, float c) {
-    constexpr int V = WIDE<T>, STEPS = CHUNK<T> / (CB * V);
-    if (left >= CHUNK<T>) {
-        wide_t<T> raw[STEPS];
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-            raw[i] = *reinterpret_cast<const wide_any<T>*>(g + (i * CB + threadIdx.x) * V);
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-#pragma unroll
-            for (int k = 0; k < V; ++k) raw[i][k] = (T)((float)raw[i][k] * c);
-            *reinterpret_cast<wide_any<T>*>(o + (i * CB + threadIdx.x) * V) = raw[i];
-        }
-    } else {
-        for (int i = threadIdx.x * V; i < left; i += CB * V) {
-            if (i + V <= left) {
-                wide_t<T> r = *reinterpret_cast<const wide_any<T>*>(g + i);
-#pragma unroll
-                for (int k = 0; k < V; ++k) r[k] = (T)((float)r[k] * c);
-                *reinterpret_cast<wide_any<T>*>(o + i) = r;
-            } else {
-                for (int k = i; k < left; ++k) o[k] = (T)((float)g[k] * c);
-            }
-        }
+template <bool FULL, class T>
+__device__ __forceinline__ void chunk_scale(const T* g, T* o, int left, float c) {
+    wide_t<T> raw[STEPS<T>];
+    load_chunk<FULL>(g, left, raw);
+    if (!FULL) {
+        const int at = behind<T>(left);
+        if (at >= 0) o[at] = (T)((float)g[at] * c);
     }
+#pragma unroll
+    for (int i = 0; i < STEPS<T>; ++i) {
+        const int at = (i * CB + (int)threadIdx.x) * WIDE<T>;
+#pragma unroll
+        for (int k = 0; k < WIDE<T>; ++k) raw[i][k] = (T)((float)raw[i][k] * c);
+        if (FULL || at + WIDE<T> <= left) *reinterpret_cast<wide_any<T>*>(o + at) = raw[i];
+    }
+}
+
+template <class T>
+__device__ __forceinline__ double squares(const ClipTensor& e, int64_t n, int64_t chunk) {
+    const T* g = (const T*)e.g + (chunk - e.first) * CHUNK<T>;
+    const int64_t left = n - (chunk - e.first) * CHUNK<T>;
+    return left >= CHUNK<T> ? chunk_squares<true>(g, 0) : chunk_squares<false>(g, (int)left);
+}
+
+template <class T>
+__device__ __forceinline__ void scale(const ClipTensor& e, int64_t n, int64_t chunk, float c) {
+    const int64_t at = (chunk - e.first) * CHUNK<T>, left = n - at;
+    const T* g = (const T*)e.g + at;
+    T* o = (T*)e.out + at;
+    if (left >= CHUNK<T>)
+        chunk_scale<true>(g, o, 0, c);
+    else
+        chunk_scale<false>(g, o, (int)left, c);
 }
 
 // A block's run of chunks: as many for each block, one more for the first ones.
@@ -138,43 +153,34 @@ __device__ __forceinline__ void clip_norm(const ClipTensor* t, int count, int64_
     for (int64_t c = first; c < end; ++c) {
         while (k + 1 < count && t[k + 1].first <= c) ++k;
         const ClipTensor e = t[k];
-        if (e.n < 0) {
-            const int64_t at = (c - e.first) * CHUNK<bf16>;
-            sum += chunk_squares((const bf16*)e.g + at, ~e.n - at);
-        } else {
-            const int64_t at = (c - e.first) * CHUNK<float>;
-            sum += chunk_squares((const float*)e.g + at, e.n - at);
-        }
+        sum += e.n < 0 ? squares<bf16>(e, ~e.n, c) : squares<float>(e, e.n, c);
     }
     sum = block_sum(sum, s);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-// parts: how many sums the first launch left. scale: whether the tensors are wanted, beside the norm.
+// parts: how many sums the first launch left. wanted: whether the tensors are, beside the norm.
 __device__ __forceinline__ void clip_scale(const ClipTensor* t, int count, int64_t chunks, const double* part,
-                                           int parts, float max_norm, float* norm, bool scale) {
+                                           int parts, float max_norm, float* norm, bool wanted) {
     __shared__ double s[CB / 64];
+    int64_t first, end;
+    block_chunks(chunks, first, end);
+    int k = wanted && first < end ? tensor_of(t, count, end - 1) : 0;
     double sum = 0.;
     for (int i = threadIdx.x; i < parts; i += CB) sum += part[i];
     const double whole = sqrt(block_sum(sum, s));
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)whole;
-    if (!scale) return;
+    if (!wanted) return;
     const double f = (double)max_norm / (whole + 1e-6);
     const float c = f >= 1. || max_norm == INFINITY ? 1.f : (float)f;  // no number where the norm is none
-    int64_t first, end;
-    block_chunks(chunks, first, end);
-    int k = first < end ? tensor_of(t, count, end - 1) : 0;
     for (int64_t j = end - 1; j >= first; --j) {
         while (t[k].first > j) --k;
         const ClipTensor e = t[k];
         if (c == 1.f && e.g == e.out) continue;  // in place, and nothing to change
-        if (e.n < 0) {
-            const int64_t at = (j - e.first) * CHUNK<bf16>;
-            chunk_scale((const bf16*)e.g + at, (bf16*)e.out + at, ~e.n - at, c);
-        } else {
-            const int64_t at = (j - e.first) * CHUNK<float>;
-            chunk_scale((const float*)e.g + at, (float*)e.out + at, e.n - at, c);
-        }
+        if (e.n < 0)
+            scale<bf16>(e, ~e.n, j, c);
+        else
+            scale<float>(e, e.n, j, c);
     }
 }
 
@@ -188,14 +194,14 @@ __global__ __launch_bounds__(CB) void k_clip_norm_many(const ClipTensor* __restr
 }
 
 __global__ __launch_bounds__(CB) void k_clip_scale(ClipTable t, int count, int64_t chunks, const double* part,
-                                                   int parts, float max_norm, float* norm, bool scale) {
-    clip_scale(t.t, count, chunks, part, parts, max_norm, norm, scale);
+                                                   int parts, float max_norm, float* norm, bool wanted) {
+    clip_scale(t.t, count, chunks, part, parts, max_norm, norm, wanted);
 }
 
 __global__ __launch_bounds__(CB) void k_clip_scale_many(const ClipTensor* __restrict__ t, int count, int64_t chunks,
                                                         const double* part, int parts, float max_norm, float* norm,
-                                                        bool scale) {
-    clip_scale(t, count, chunks, part, parts, max_norm, norm, scale);
+                                                        bool wanted) {
+    clip_scale(t, count, chunks, part, parts, max_norm, norm, wanted);
 }
 
 __global__ __launch_bounds__(128) void k_clip_table(ClipTable t, int count, ClipTensor* __restrict__ to) {

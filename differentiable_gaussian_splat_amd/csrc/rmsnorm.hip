@@ -158,11 +158,12 @@ __global__ __launch_bounds__(NT) void k_rms_fwd(RmsArgs a) {
     }
 }
 
-// AGAIN: a row's second use reads it from memory (the cache) again, where registers hold no two rows.
+// A row's h, dy and dh are loaded together, before the row's sum, where registers hold them (and the weights) all;
+// longer rows are read again from the cache for their second use.
 template <class T, int NT, int LPR, int EPL, bool FULL>
 __global__ __launch_bounds__(NT) void k_rms_bwd(RmsArgs a) {
     constexpr int RPB = NT / LPR, VEC = WIDE<T>;
-    constexpr bool AGAIN = EPL * VEC > 32;
+    constexpr bool AGAIN = EPL > KEPT;
     __shared__ float s_red[NT / 64];
     __shared__ float s_acc[LPR < NT ? LPR * EPL * VEC : 1];
     const int l = threadIdx.x % LPR, dim = a.dim;
@@ -172,46 +173,55 @@ __global__ __launch_bounds__(NT) void k_rms_bwd(RmsArgs a) {
     for (int e = 0; e < EPL; ++e)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) aw[e][k] = 0.f;
+    wide_t<T> w[AGAIN ? 1 : EPL];
+    auto load_weight = [&](int e) {
+        const int left = dim - (e * LPR + l) * VEC;
+        wide_t<T> v = (T)0.f;
+        if (weight && left > 0) v = load_row<FULL>(weight + (dim - left), left, left);
+        return v;
+    };
+    if (!AGAIN) {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) w[AGAIN ? 0 : e] = load_weight(e);
+    }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.n; r0 += (int64_t)gridDim.x * RPB) {
         const int64_t r = r0 + threadIdx.x / LPR;
         const bool live = r < a.n;
-        const float rstd = live ? a.rstd[r] : 0.f;
-        wide_t<T> rh[AGAIN ? 1 : EPL], rg[AGAIN ? 1 : EPL];
-        auto load = [&](int e, wide_t<T>& vh, wide_t<T>& vg) {
+        wide_t<T> rh[AGAIN ? 1 : EPL], rg[AGAIN ? 1 : EPL], rs[AGAIN ? 1 : EPL];
+        auto load = [&](const T* p, int64_t stride, int e) {
             const int c = (e * LPR + l) * VEC;
-            vh = vg = (T)0.f;
-            if (live && c < dim) {
-                vh = load_row<FULL>(h + r * a.xs + c, dim - c, (a.n - 1 - r) * a.xs + dim - c);
-                vg = load_row<FULL>(dy + r * a.dys + c, dim - c, (a.n - 1 - r) * a.dys + dim - c);
-            }
+            wide_t<T> v = (T)0.f;
+            if (p && live && c < dim) v = load_row<FULL>(p + r * stride + c, dim - c, (a.n - 1 - r) * stride + dim - c);
+            return v;
         };
+        if (!AGAIN) {
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) rh[AGAIN ? 0 : e] = load(h, a.xs, e);
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) rg[AGAIN ? 0 : e] = load(dy, a.dys, e);
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) rs[AGAIN ? 0 : e] = load(dsum, a.dss, e);
+        }
+        const float rstd = live ? a.rstd[r] : 0.f;
         // hh: h rstd; g: dy w; d: dy
-        auto values = [&](int e, wide_t<T> vh, wide_t<T> vg, float (&hh)[VEC], float (&g)[VEC], float (&d)[VEC]) {
+        auto values = [&](int e, float (&hh)[VEC], float (&g)[VEC], float (&d)[VEC]) {
             const int left = dim - (e * LPR + l) * VEC;
-            widen<FULL, T>(vh, left, hh);
-            widen<FULL, T>(vg, left, d);
+            widen<FULL, T>(rh[AGAIN ? 0 : e], left, hh);
+            widen<FULL, T>(rg[AGAIN ? 0 : e], left, d);
             float f[VEC];
-            if (weight) {
-                wide_t<T> wr = (T)0.f;
-                if (left > 0) wr = load_row<FULL>(weight + (dim - left), left, left);
-                widen<FULL, T>(wr, left, f);
-            }
+            widen<FULL, T>(AGAIN ? load_weight(e) : w[AGAIN ? 0 : e], left, f);
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
                 hh[k] *= rstd;
                 g[k] = weight ? d[k] * f[k] : d[k];
             }
         };
-        if (!AGAIN) {
-#pragma unroll
-            for (int e = 0; e < EPL; ++e) load(e, rh[AGAIN ? 0 : e], rg[AGAIN ? 0 : e]);
-        }
         float sx = 0.f;
 #pragma unroll
         for (int e = 0; e < EPL; ++e) {
-            if (AGAIN) load(e, rh[0], rg[0]);
+            if (AGAIN) rh[0] = load(h, a.xs, e), rg[0] = load(dy, a.dys, e);
             float hh[VEC], g[VEC], d[VEC];
-            values(e, rh[AGAIN ? 0 : e], rg[AGAIN ? 0 : e], hh, g, d);
+            values(e, hh, g, d);
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {  // a column past the row has d = 0
                 aw[e][k] = fmaf(d[k], hh[k], aw[e][k]);
@@ -223,19 +233,14 @@ __global__ __launch_bounds__(NT) void k_rms_bwd(RmsArgs a) {
         if (!live) continue;
 #pragma unroll
         for (int e = 0; e < EPL; ++e) {
-            if (AGAIN) load(e, rh[0], rg[0]);
+            if (AGAIN) rh[0] = load(h, a.xs, e), rg[0] = load(dy, a.dys, e), rs[0] = load(dsum, a.dss, e);
             const int c = (e * LPR + l) * VEC, left = dim - c;
             float hh[VEC], g[VEC], d[VEC];
-            values(e, rh[AGAIN ? 0 : e], rg[AGAIN ? 0 : e], hh, g, d);
+            values(e, hh, g, d);
+            widen<FULL, T>(rs[AGAIN ? 0 : e], left, d);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) g[k] = rstd * (g[k] - hh[k] * mx);
-            if (left <= 0) continue;
-            if (dsum) {
-                widen<FULL, T>(load_row<FULL>(dsum + r * a.dss + c, left, (a.n - 1 - r) * a.dss + left), left, d);
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) g[k] += d[k];
-            }
-            store_row<FULL>((T*)a.dx + r * a.dxs + c, left, g);
+            for (int k = 0; k < VEC; ++k) g[k] = rstd * (g[k] - hh[k] * mx) + d[k];  // d: dh, zeros without one
+            if (left > 0) store_row<FULL>((T*)a.dx + r * a.dxs + c, left, g);
         }
     }
     if (!a.part) return;
