@@ -92,6 +92,16 @@ def test_rms_norm_plain(n, dim, dtype):
     check_rms(randn(g, n, dim, dtype=dtype, pad=1, offset=1), None, None, randn(g, n, dim, dtype=dtype), None, 1e-5)
 
 
+@pytest.mark.parametrize("dtype,n,dim", [(F32, 300_000, 128), (BF16, 600_001, 128), (F32, 9_000, 4096), (BF16, 9_000, 8192)],
+                         ids=str)
+def test_rms_norm_larger_than_the_cache(n, dim, dtype):
+    """Calls that go past the caches: more than 256 MB in all."""
+    g = gen(n + dim)
+    x, res, dy = (randn(g, n, dim, dtype=dtype) for _ in range(3))
+    check_rms(x, randn(g, 1, dim, dtype=dtype)[0], res, dy, dy, 1e-6)
+    check_rms(x, None, None, dy, None, 1e-6)
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 def test_rms_norm_broadcast_rows(dtype):
     """One row for all (a stride of 0), as the residual, as x and as the upstream gradient."""
