@@ -597,13 +597,13 @@ hipError_t scores_tiles(const ScoreArgs& a, hipStream_t s) {
 template <class T>
 hipError_t scores(const ScoreArgs& a, hipStream_t s) {
     auto tiles = [&](int64_t bx, int64_t bv) { return ((a.n + bx - 1) / bx) * ((a.vocab + bv - 1) / bv); };
-    if (a.n <= (sizeof(T) == 2 ? 8 : 32))
-        return a.n <= 16 ? scores_split<T, 1, 1>(a, s) : scores_split<T, 2, 2>(a, s);
-    if constexpr (sizeof(T) == 2) {
-        if (a.cols <= 384 && tiles(128, 256) >= 256) return scores_tiles<T, 2, 2, 2, 4, 3>(a, s);
-        if (tiles(256, 256) >= 192) return scores_tiles<T, 4, 2, 2, 4, 4>(a, s);
+    if (a.n > (sizeof(T) == 2 ? 8 : 32)) {
+        if constexpr (sizeof(T) == 2) {
+            if (a.cols <= 384 && tiles(128, 256) >= 256) return scores_tiles<T, 2, 2, 2, 4, 3>(a, s);
+            if (tiles(256, 256) >= 192) return scores_tiles<T, 4, 2, 2, 4, 4>(a, s);
+        }
+        if (tiles(128, 128) >= 64) return scores_tiles<T, 2, 2, 2, 2, 4>(a, s);
     }
-    if (tiles(128, 128) >= 64) return scores_tiles<T, 2, 2, 2, 2, 4>(a, s);
     return a.n <= 16 ? scores_split<T, 1, 1>(a, s) : scores_split<T, 2, 2>(a, s);
 }
 

@@ -551,6 +551,17 @@ class LabelHead(torch.nn.Module):
         """The loss of labels [n] for the Gaussians with the given codes [n]."""
         return label_loss(self.features(codes), self.vocabulary, labels, reduction)
 
+    @torch.no_grad()
+    def vocabulary_q8(self):
+        """The vocabulary in 8 bits, for :meth:`scores`: made once after training."""
+        return quantize_q8(self.vocabulary)
+
+    @torch.no_grad()
+    def scores(self, codes, vocabulary=None, dtype=torch.float32):
+        """Scores [n, labels] of codes [n], features and vocabulary in 8 bits."""
+        return label_scores(quantize_q8(self.features(codes)),
+                            self.vocabulary_q8() if vocabulary is None else vocabulary, dtype)
+
 
 class ResidualLabelHead(torch.nn.Module):
     """Labels from several codes a row (residual quantisation): each stage's codebook row is added to the sum of the

@@ -27,6 +27,20 @@ def _addresses(values):
     return (C.c_int64 * len(a)).from_buffer(a) if a else None
 
 
+def _dense(t):
+    """Whether the tensor's elements fill one piece of memory, in any order of the dimensions."""
+    if t.is_contiguous():
+        return True
+    if t.layout is not torch.strided:
+        return False
+    step = 1
+    for stride, size in sorted((st, k) for st, k in zip(t.stride(), t.shape) if k != 1):
+        if stride != step:
+            return False
+        step *= size
+    return True
+
+
 class _Tensors:
     """The host arrays of a call: checked once, and usable as long as the tensors keep their memory."""
 
@@ -41,19 +55,22 @@ class _Tensors:
                     raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
             if not all([t.is_cuda for t in ts]):
                 raise TypeError(f"{name} must be on the GPU")
-            if not all([t.is_contiguous() for t in ts]):
-                raise ValueError(f"{name} must be contiguous")
+            if not all([_dense(t) for t in ts]):
+                raise ValueError(f"{name} must each fill one piece of memory")
         devices = {t.get_device() for t in self.grads + (self.outs or [])}
         if len(devices) > 1:
             raise ValueError(f"gradients and outs must be on one device, got {sorted(devices)}")
         self.device = devices.pop() if devices else None
         sizes = [t.numel() for t in self.grads]
-        if self.outs is not None and [(t.numel(), t.dtype) for t in self.outs] != \
-                [(k, t.dtype) for k, t in zip(sizes, self.grads)]:
-            raise ValueError("outs must have the gradients' number, sizes and types")
+        if outs is not None and outs is not grads and [(t.shape, t.stride(), t.dtype) for t in self.outs] != \
+                [(t.shape, t.stride(), t.dtype) for t in self.grads]:
+            raise ValueError("outs must have the gradients' number, shapes, strides and types")
         self.count = len(sizes)
         self.g = _addresses([t.data_ptr() for t in self.grads])
-        self.o = None if outs is None else _addresses([t.data_ptr() for t in self.outs]) or C.c_void_p(1)
+        places = None if outs is None else [t.data_ptr() for t in self.outs]
+        if places is not None and len({p for p, k in zip(places, sizes) if k}) != sum([k > 0 for k in sizes]):
+            raise ValueError("each tensor of outs must be there once")
+        self.o = None if outs is None else _addresses(places) or C.c_void_p(1)
         self.n = _addresses(sizes)
         self.t = (C.c_int32 * self.count)(*[_DTYPES[t.dtype] for t in self.grads]) if self.count else None
 
@@ -106,5 +123,5 @@ class GradClip:
 def clip_grads(params, max_norm, stream=None):
     """Clips the gradients of the parameters (those that have one) in place by their global norm; returns it (float32
     [1], before clipping), or None if there is no gradient. max_norm infinite: only the norm."""
-    grads = [p.grad for p in params if p.grad is not None]
+    grads = list({id(p): p.grad for p in params if p.grad is not None}.values())  # a parameter named twice counts once
     return GradClip(grads)(max_norm, stream) if grads else None

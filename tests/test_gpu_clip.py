@@ -111,9 +111,32 @@ def test_refuses_what_does_not_match():
     with pytest.raises(ValueError):
         O.GradClip([a, b], [a])
     with pytest.raises(ValueError):
-        O.GradClip([torch.ones((4, 4), device=DEV).t()])
+        O.GradClip([a], [torch.ones(10, device=DEV)[::2]])
+    with pytest.raises(ValueError):
+        O.GradClip([torch.ones((4, 4), device=DEV)[:, :2]])
+    with pytest.raises(ValueError):
+        O.GradClip([torch.ones((1, 4), device=DEV).expand(4, 4)])
+    with pytest.raises(ValueError):
+        O.GradClip([a, a])  # would be clipped twice
+    with pytest.raises(ValueError):
+        O.GradClip([torch.ones((3, 4), device=DEV)], [torch.ones((4, 3), device=DEV).t()])
     with pytest.raises(raster.GsError):
         O.GradClip([a])(-1.0)
+
+
+def test_any_order_of_dimensions_and_shared_parameters():
+    """Gradients follow their parameters' strides; a parameter that two modules share counts once."""
+    g = gen(7)
+    w = torch.nn.Parameter(torch.randn((30, 50), generator=g, device=DEV).t())
+    v = torch.nn.Parameter(torch.randn(7, generator=g, device=DEV))
+    w.grad = torch.randn((30, 50), generator=g, device=DEV).t()
+    v.grad = torch.randn(7, generator=g, device=DEV)
+    before = w.grad.clone()
+    norm, c = expected([w.grad, v.grad], 3.0)
+    assert not w.grad.is_contiguous()
+    got = O.clip_grads([w, v, w], 3.0)
+    assert abs(float(got) - norm) <= norm * U * 2
+    within("grad", w.grad, before.double() * c, before.double().abs() * 3 * U)
 
 
 def test_same_results_every_time_and_on_a_side_stream():

@@ -405,6 +405,18 @@ def test_head_scores(dtype):
         within("scores", out, y @ w.t(), mag * (2 * 2.0 ** -4 + 2.0 ** -8 + half_step(dtype) * 2) + floor * 2 + 1e-12)
 
 
+def test_label_head_scores():
+    """The head of one codebook names labels by 8-bit scores too."""
+    torch.manual_seed(6)
+    head = L.LabelHead(60, 100, 90)
+    codes = torch.randint(-1, 60, (300,), generator=gen(38), device=DEV)
+    y, w = head.features(codes).detach().double(), head.vocabulary.detach().double()
+    floor = 2.0 ** -17 * (y.abs().amax(1)[:, None] * w.abs().sum(1) + y.abs().sum(1)[:, None] * w.abs().amax(1))
+    out = head.scores(codes)
+    within("scores", out, y @ w.t(), y.abs() @ w.abs().t() * (2 * 2.0 ** -4 + 2.0 ** -8) + floor * 2 + 1e-12)
+    assert torch.equal(out, head.scores(codes, head.vocabulary_q8()))
+
+
 def test_autograd_forms():
     """The sum alone used, the result alone used, frozen inputs, a broadcast residual."""
     g = gen(34)
