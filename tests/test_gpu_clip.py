@@ -95,6 +95,18 @@ def test_not_finite(value):
         assert float(ts[1].nan_to_num().abs().sum()) == 0
 
 
+def test_past_32_bits():
+    """A tensor of more than 2^32 bytes and 2^31 elements."""
+    n = (1 << 31) + 12_345
+    g = torch.full((n,), 0.5, dtype=BF16, device=DEV)
+    g[-3:] = 64.0
+    norm = math.sqrt(0.25 * (n - 3) + 3 * 4096)
+    got = O.GradClip([g])(norm / 2)
+    assert abs(float(got) - norm) <= norm * 2 * U
+    assert (g[-3:] == 32).all() and (g[:5] == 0.25).all() and (g[n // 2:n // 2 + 100_000] == 0.25).all()
+    assert (g[:-3].view(torch.int16) == g[0].view(torch.int16)).all()
+
+
 def test_neighbours_stay():
     buf = torch.full((50_000,), 2.0, device=DEV)
     O.GradClip([buf[101:33_001], buf[40_000:40_001]])(1.0)

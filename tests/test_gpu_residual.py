@@ -332,6 +332,94 @@ def test_scores_one_row_for_all():
     check_scores((q.expand(40, -1), s.expand(40, -1)), vocabulary, BF16)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_scores_one_row_for_all_in_tiles(dtype):
+    """Strides of 0 and the largest ones, in numbers of rows that go through LDS."""
+    g = gen(12)
+    (q, s), (w, ws) = random_rows(g, 1, 256), random_rows(g, 9000, 256)
+    check_scores((q.expand(700, -1), s.expand(700, -1)), (w, ws), dtype)
+    check_scores((w, ws), (q.expand(700, -1), s.expand(700, -1)), dtype)
+    far = [torch.zeros((130, 1 << 22), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    far[0][:, :256], far[1][:, :4] = w[:130].view(torch.uint8), ws[:130].view(torch.uint8)
+    rows = far[0].view(Q8)[:, :256], far[1].view(E8)[:, :4]
+    assert torch.equal(check_scores(rows, (w, ws), dtype), check_scores((w[:130], ws[:130]), (w, ws), dtype))
+    assert torch.equal(check_scores((w, ws), rows, dtype), check_scores((w, ws), (w[:130], ws[:130]), dtype))
+
+
+def some_rows(n):
+    """A few rows from the beginning, the middle and the end of n."""
+    return torch.tensor([0, 1, 255, n // 2 - 1, n // 2, n - 258, n - 2, n - 1], device=DEV)
+
+
+@pytest.mark.parametrize("n,cols,vocab,dtype", [(1_100_000, 4096, 64, BF16), (70_001, 128, 65_536, BF16),
+                                                (40_000, 256, 60_001, F32), (3, 8192, 600_000, F32)], ids=str)
+def test_scores_past_32_bits(n, cols, vocab, dtype):
+    """Operands and results of more than 2^32 bytes, and of more than 2^31 elements."""
+    g = gen(n)
+    rows, vocabulary = random_rows(g, n, cols), random_rows(g, vocab, cols)
+    out = empty(n, vocab, dtype=dtype)
+    L.gs_label_scores_q8(*rows, *vocabulary, out)
+    some = some_rows(n) if n > 1000 else torch.arange(n, device=DEV)
+    few = [t.view(torch.uint8)[some].view(k) for t, k in zip(rows, (Q8, E8))]
+    want = empty(len(some), vocab, dtype=dtype)
+    L.gs_label_scores_q8(*few, *vocabulary, want)
+    a = dequantize(*few)
+    for v0 in range(0, vocab, 65_536):
+        b = dequantize(*(t[v0:v0 + 65_536] for t in vocabulary))
+        mag = a.abs() @ b.abs().t()
+        tol = mag * (2 * cols * U) + (a @ b.t()).abs() * half_step(dtype)
+        if dtype is BF16:
+            tol = tol + 2.0 ** -10 * (a.abs().reshape(len(a), -1, 8).amax(2) @ b.abs().reshape(len(b), -1, 8).amax(2).t())
+        within("scores", out[some, v0:v0 + 65_536], a @ b.t(), tol)
+
+
+def test_norm_past_32_bits():
+    """Matrices of more than 2^32 elements."""
+    n, dim = 34_000_001, 128
+    g = gen(13)
+    x = torch.randint(-100, 100, (n, dim), generator=g, device=DEV, dtype=torch.int8).to(BF16)
+    w = randn(g, 1, dim, dtype=BF16)[0]
+    some = some_rows(n)
+    y, dx, rstd, dw = torch.empty_like(x), torch.empty_like(x), empty(n), empty(dim, dtype=BF16)
+    L.gs_rms_norm_fwd(x, w, y, None, None, rstd)
+    ws = ws_of(L.gs_rms_norm_bwd_workspace_size(n, dim, BF16))
+    L.gs_rms_norm_bwd(x, w, rstd, x, dx, dw, ws)
+    few = run_rms(x[some], w, None, x[some], None, 1e-6)
+    assert torch.equal(y[some], few["y"]) and torch.equal(dx[some], few["dx"])
+    del y, dx
+    q, s = L.rows_q8(n, dim)
+    L.gs_rms_norm_q8(x, w, q, s)
+    q1, s1 = L.rows_q8(len(some), dim)
+    L.gs_rms_norm_q8(x[some], w, q1, s1)
+    assert torch.equal(q.view(torch.uint8)[some], q1.view(torch.uint8)) and torch.equal(s.view(torch.uint8)[some],
+                                                                                       s1.view(torch.uint8))
+    L.gs_quantize_q8(x, q, s)
+    same_q8((q.view(torch.uint8)[some].view(Q8), s.view(torch.uint8)[some].view(E8)), quantize_ref(x[some].float()))
+
+
+def test_two_streams_at_once():
+    g = gen(14)
+    jobs = [(random_rows(g, 3000, 512), random_rows(g, 5000, 512)) for _ in range(2)]
+    x, r = randn(g, 30_000, 256), randn(g, 30_000, 256)
+    want = [empty(3000, 5000, dtype=BF16) for _ in jobs]
+    for job, o in zip(jobs, want):
+        L.gs_label_scores_q8(*job[0], *job[1], o)
+    ref = run_rms(x, None, r, r, x, 1e-6)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [empty(3000, 5000, dtype=BF16) for _ in jobs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for job, o, s in zip(jobs, got, streams):
+            L.gs_label_scores_q8(*job[0], *job[1], o, stream=s)
+        with torch.cuda.stream(streams[2]):
+            again = run_rms(x, None, r, r, x, 1e-6)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(again[k], ref[k]) for k in ref)
+
+
 def test_scores_leave_other_columns_alone():
     g = gen(11)
     wide = torch.full((50, 100), 7.0, dtype=BF16, device=DEV)
