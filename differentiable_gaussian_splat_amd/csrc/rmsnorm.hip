@@ -77,7 +77,36 @@ struct RmsArgs {
     void* dx;
     int64_t dxs;
     float* part;  // [blocks][dim]
+    bool plain;   // into 8 bits without the norm
 };
+
+// Stores a wave's 64 / LPR rows of a block or less in 8 bits, of which a lane has VEC columns: 16 bytes to a lane, side
+// by side over the rows, zeros behind the columns. first: the wave's first row.
+template <int LPR, int VEC>
+__device__ __forceinline__ void store_short(const RmsArgs& a, int64_t first, const float (&v)[VEC], float inverse) {
+    constexpr int ROWS = 64 / LPR, PER = VEC / 4, WORDS = LPR * PER;  // words of a row, PER to a lane
+    const int lane = threadIdx.x & 63;
+    uint32_t have[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) have[p] = pack_q8(v + 4 * p, inverse);
+#pragma unroll
+    for (int i = 0; i < (ROWS * 8 + 63) / 64; ++i) {
+        const int row = (i * 64 + lane) / 8, chunk = lane % 8;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int word = 4 * chunk + k, from = row * LPR + word / PER;
+            uint32_t got = __shfl(have[0], from & 63);
+            if (PER == 2) {
+                const uint32_t odd = __shfl(have[PER - 1], from & 63);
+                got = word % 2 ? odd : got;
+            }
+            w[k] = word < WORDS ? got : 0u;
+        }
+        if (row < ROWS && first + row < a.n)
+            *reinterpret_cast<uint4*>(a.q + (first + row) * a.qs + chunk * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
 
 // The accesses of a row whose weights stay in registers over the block's rows.
 constexpr int KEPT = 4;
@@ -131,7 +160,8 @@ __global__ __launch_bounds__(NT) void k_rms_fwd(RmsArgs a) {
 #pragma unroll
             for (int k = 0; k < VEC; ++k) sq = (FULL ? left > 0 : k < left) ? fmaf(v[k], v[k], sq) : sq;
         }
-        const float rstd = 1.0f / sqrtf(rms_row_sum<NT, LPR>(sq, s_red) / (float)dim + a.eps);
+        // of rows as they are nothing is asked
+        const float rstd = Q8 && a.plain ? 1.f : 1.0f / sqrtf(rms_row_sum<NT, LPR>(sq, s_red) / (float)dim + a.eps);
         if (a.rstd && live && l == 0) a.rstd[r] = rstd;
 #pragma unroll
         for (int e = 0; e < EPL; ++e) {
@@ -153,25 +183,30 @@ __global__ __launch_bounds__(NT) void k_rms_fwd(RmsArgs a) {
                 for (int k = 0; k < VEC; ++k) v[k] *= f[k];
             }
             if constexpr (Q8) {
-                static_assert(LPR >= Q8_LANES<T>, "a block's lanes stand in one row");
+                constexpr int LANES = LPR < Q8_LANES<T> ? LPR : Q8_LANES<T>;
                 float top = 0.f;
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) {
-                    v[k] = FULL ? (left > 0 ? v[k] : 0.f) : k < left ? v[k] : 0.f;
+                    v[k] = (FULL ? left > 0 : k < left) ? v[k] : 0.f;
                     top = fmaxf(top, finite_abs(v[k]));
                 }
 #pragma unroll
-                for (int off = Q8_LANES<T> / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+                for (int off = LANES / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
                 const int ex = scale_exponent(top);
-                if (live && c < q8_cols(dim)) {
-                    store_q8(a.q + r * a.qs + c, v, scale_inverse(ex));
-                    if (l % Q8_LANES<T> == 0) a.scales[r * a.scs + c / Q8_BLOCK] = (uint8_t)ex;
+                if constexpr (LPR >= Q8_LANES<T>) {
+                    if (live && c < q8_cols(dim)) {
+                        store_q8(a.q + r * a.qs + c, v, scale_inverse(ex));
+                        if (l % LANES == 0) a.scales[r * a.scs + c / Q8_BLOCK] = (uint8_t)ex;
+                    }
+                } else {
+                    store_short<LPR>(a, r0 + (threadIdx.x >> 6) * (64 / LPR), v, scale_inverse(ex));
+                    if (live && l == 0) *reinterpret_cast<uint32_t*>(a.scales + r * a.scs) = 0x7f7f7f00u | ex;
                 }
             } else if (live && left > 0) {
                 store_part<FULL, PAST>((T*)a.y + r * a.ys + c, left, v);
             }
         }
-        if constexpr (Q8) {
+        if constexpr (Q8 && LPR >= Q8_LANES<T>) {
             const int at = q8_cols(dim) / Q8_BLOCK + l;
             if (live && at < q8_groups(dim)) a.scales[r * a.scs + at] = 127;
         }
@@ -299,27 +334,6 @@ __global__ __launch_bounds__(NT) void k_rms_bwd(RmsArgs a) {
     }
 }
 
-// Rows in 8 bits as they are: a lane's access after access, the block's lanes side by side.
-template <class T, bool FULL>
-__global__ __launch_bounds__(256) void k_quantize(int64_t first, int64_t units, int per_row, RmsArgs a) {
-    constexpr int VEC = WIDE<T>, G = Q8_LANES<T>;
-    const int64_t u = first + (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
-    if (u >= units) return;  // whole groups of lanes
-    const int64_t r = u / per_row;
-    const int b = (int)(u - r * per_row), l = threadIdx.x % G, c = b * Q8_BLOCK + l * VEC, left = a.dim - c;
-    wide_t<T> raw = (T)0.f;
-    if (left > 0) raw = load_row<FULL>((const T*)a.x + r * a.xs + c, left, (a.n - 1 - r) * a.xs + left);
-    float v[VEC], top = 0.f;
-    widen<FULL, T>(raw, left, v);
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) top = fmaxf(top, finite_abs(v[k]));
-#pragma unroll
-    for (int off = G / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-    const int ex = scale_exponent(top);
-    if (c < q8_cols(a.dim)) store_q8(a.q + r * a.qs + c, v, scale_inverse(ex));
-    if (l == 0) a.scales[r * a.scs + b] = (uint8_t)(c < q8_cols(a.dim) ? ex : 127);
-}
-
 enum RmsCall { RMS_FWD, RMS_BWD, RMS_Q8 };
 
 constexpr int RMS_BLOCKS_FWD = 2048, RMS_BLOCKS_BWD = 1024;  // of 256 threads; the latter are rows of the column sums
@@ -351,19 +365,15 @@ hipError_t rms_rows(const RmsArgs& a, int& blocks, hipStream_t s) {
     return hipGetLastError();
 }
 
-// The lanes of a row and their accesses: the fewest lanes that hold it with one access each up to a wave (in 8 bits, a
-// block of columns at least), then more accesses, then a block of four waves, then of sixteen.
+// The lanes of a row and their accesses: the fewest lanes that hold it with one access each up to a wave, then more accesses, then a block of four waves, then of sixteen.
 template <class T, int CALL, bool FULL>
 hipError_t rms_pick(const RmsArgs& a, int& blocks, hipStream_t s) {
     const int v = (a.dim + WIDE<T> - 1) / WIDE<T>;
-    if constexpr (CALL != RMS_Q8) {
-        if (v <= 1) return rms_rows<T, CALL, 256, 1, 1, FULL>(a, blocks, s);
-        if (v <= 2) return rms_rows<T, CALL, 256, 2, 1, FULL>(a, blocks, s);
-        if (v <= 4) return rms_rows<T, CALL, 256, 4, 1, FULL>(a, blocks, s);
-        if (v <= 8) return rms_rows<T, CALL, 256, 8, 1, FULL>(a, blocks, s);
-    }
-    if constexpr (CALL != RMS_Q8 || Q8_LANES<T> <= 16)
-        if (v <= 16) return rms_rows<T, CALL, 256, 16, 1, FULL>(a, blocks, s);
+    if (v <= 1) return rms_rows<T, CALL, 256, 1, 1, FULL>(a, blocks, s);
+    if (v <= 2) return rms_rows<T, CALL, 256, 2, 1, FULL>(a, blocks, s);
+    if (v <= 4) return rms_rows<T, CALL, 256, 4, 1, FULL>(a, blocks, s);
+    if (v <= 8) return rms_rows<T, CALL, 256, 8, 1, FULL>(a, blocks, s);
+    if (v <= 16) return rms_rows<T, CALL, 256, 16, 1, FULL>(a, blocks, s);
     if (v <= 32) return rms_rows<T, CALL, 256, 32, 1, FULL>(a, blocks, s);
     if (v <= 64) return rms_rows<T, CALL, 256, 64, 1, FULL>(a, blocks, s);
     if (v <= 128) return rms_rows<T, CALL, 256, 64, 2, FULL>(a, blocks, s);
@@ -384,19 +394,6 @@ hipError_t rms_launch(bool half, const RmsArgs& a, int& blocks, hipStream_t s) {
                                        : rms_pick<bf16, CALL, false>(a, blocks, s);
     return a.dim % WIDE<float> == 0 ? rms_pick<float, CALL, true>(a, blocks, s)
                                     : rms_pick<float, CALL, false>(a, blocks, s);
-}
-
-template <class T, bool FULL>
-hipError_t quantize(const RmsArgs& a, hipStream_t s) {
-    const int per_row = q8_groups(a.dim), per_block = 256 / Q8_LANES<T>;
-    const int64_t units = a.n * per_row;
-    for (int64_t first = 0; first < units; first += MOST_BLOCKS * per_block) {
-        const int64_t blocks = (units - first + per_block - 1) / per_block;
-        k_quantize<T, FULL><<<(unsigned)(blocks < MOST_BLOCKS ? blocks : MOST_BLOCKS), 256, 0, s>>>(first, units,
-                                                                                                  per_row, a);
-        if (hipError_t e = hipGetLastError()) return e;
-    }
-    return hipSuccess;
 }
 
 }  // namespace
@@ -483,9 +480,9 @@ hipError_t launch_quantize_q8(int64_t n, int dim, bool half, const void* x, int6
     a.qs = qs;
     a.scales = scales;
     a.scs = scs;
-    if (half)
-        return dim % WIDE<bf16> == 0 ? quantize<bf16, true>(a, stream) : quantize<bf16, false>(a, stream);
-    return dim % WIDE<float> == 0 ? quantize<float, true>(a, stream) : quantize<float, false>(a, stream);
+    a.plain = true;
+    int blocks;
+    return rms_launch<RMS_Q8>(half, a, blocks, stream);
 }
 
 }  // namespace gs
