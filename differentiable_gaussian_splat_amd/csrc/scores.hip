@@ -174,7 +174,7 @@ __global__ __launch_bounds__(64 * DIRECT_WAVES) void k_scores_direct(ScoreArgs a
         }
         __syncthreads();
         if (share > 0) return;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < KS - 1; ++k)
 #pragma unroll
             for (int i = 0; i < XT; ++i)
@@ -216,15 +216,17 @@ hipError_t scores_direct(const ScoreArgs& a, hipStream_t s) {
 }
 
 // The depth is split over as many of a block's waves as it takes to have two to a SIMD, and as there are four blocks of
-// columns.
-template <class T, int XT, int VT>
+// columns (LEAST: so many at least, as the caller has seen).
+template <class T, int XT, int VT, int LEAST>
 hipError_t scores_split(const ScoreArgs& a, hipStream_t s) {
     const int64_t tiles = ((a.n + 16 * XT - 1) / (16 * XT)) * ((a.vocab + 16 * VT - 1) / (16 * VT));
     const int fours = (a.cols / Q8_BLOCK + 3) / 4;
-    int ks = 1;
+    int ks = LEAST;
     while (ks < DIRECT_WAVES && ks < fours && tiles * ks < 2048) ks *= 2;
-    if (ks == 1) return scores_direct<T, XT, VT, 1>(a, s);
-    if (ks == 2) return scores_direct<T, XT, VT, 2>(a, s);
+    if constexpr (LEAST == 1) {
+        if (ks == 1) return scores_direct<T, XT, VT, 1>(a, s);
+        if (ks == 2) return scores_direct<T, XT, VT, 2>(a, s);
+    }
     if (ks == 4) return scores_direct<T, XT, VT, 4>(a, s);
     return scores_direct<T, XT, VT, 8>(a, s);
 }
@@ -260,8 +262,8 @@ __device__ __forceinline__ void store_run(T* out, const float (&v)[C]) {
         *reinterpret_cast<run_any*>(out) = t;
 }
 
-// A descriptor of `bytes` bytes from p on; reads beyond them give 0. (A step's offset, which is added to a lane's, stays
-// below `bytes`, and a lane's own lies beyond them for every row past the last.)
+// A descriptor of `bytes` bytes from p on; reads beyond them give 0. (A step's offset, which is added to a lane's,
+// stays below `bytes`, and a lane's own lies beyond them for every row past the last.)
 __device__ __forceinline__ i32x4 extent(const uint8_t* p, int bytes) {
     const uint64_t at = (uint64_t)p;
     i32x4 r;
@@ -272,9 +274,9 @@ __device__ __forceinline__ i32x4 extent(const uint8_t* p, int bytes) {
     return r;
 }
 
-// Loads straight to LDS: lane l's 16 bytes at off + step (4 bytes at from) go to lds + 16 l (4 l). They write no register, so that
-// nothing of them is the compiler's to keep: step_barrier waits for their arrival. The wait state is what a write of m0
-// needs before them; those that a vector write of the descriptor needs are settle's.
+// Loads straight to LDS: lane l's 16 bytes at off + step (4 bytes at from) go to lds + 16 l (4 l). They write no
+// register, so that nothing of them is the compiler's to keep: step_barrier waits for their arrival. The wait state is
+// what a write of m0 needs before them; those that a vector write of the descriptor needs are settle's.
 __device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t off, i32x4 from, int step) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(off),
                  "s"(from), "s"(step)
@@ -285,7 +287,7 @@ __device__ __forceinline__ void load_lds4(uint32_t lds, const uint8_t* from) {
 }
 __device__ __forceinline__ void settle(i32x4& a, i32x4& b) { asm volatile("s_nop 4" : "+s"(a), "+s"(b)); }
 
-// Waits until all but the last `left` of this wave's memory accesses are done and its LDS reads too, then for the block.
+// Waits until all but the last LEFT of this wave's memory accesses are done and its LDS reads too, then for the block.
 template <int LEFT>
 __device__ __forceinline__ void step_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
@@ -296,10 +298,19 @@ __device__ __forceinline__ void step_barrier() {
 // written while the next one's operands arrive.
 //
 // STAGES steps are in LDS. In step s a wave multiplies the operands it holds, reads those of step s + 1 from LDS and
-// loads step s + STAGES into the place of step s. A barrier a step both publishes the arrived step and frees the one before it. Loads past the last
-// step are made all the same, which keeps their count per step. Memory accesses are counted off in
-// order: LOADS to a step, and behind a whole tile's last step its STORES, which the two steps after it let pass.
-// (The scales' loads, one to four blocks of columns, are counted with nothing: a wait is then for a little more.)
+// loads step s + STAGES into the place of step s. A barrier a step both publishes the arrived step and frees the one
+// before it. Loads past the last step are made all the same, which keeps their count per step. Memory accesses are
+// counted off in order: LOADS to a step, and behind a whole tile's last step its STORES, which the two steps after it
+// let pass. (The scales' loads, one to four blocks of columns, are counted with nothing: a wait is then for a little
+// more, never for less.)
+//
+// 8192 x 8192 x 8192 bfloat16 430 to 490 us (2.3 to 2.55 PFLOP/s): the units are busy 72 % of the cycles, at 1.7 GHz
+// of 2.4: it is power that bounds them (products alone, from registers, reach 3.8). LDS is read without bank
+// conflicts. With the step's reads and loads all behind its barrier 524; with a descriptor formed for each load
+// 30 % more. Four waves of 128 x 128 with a third less to read from LDS 458 where eight had 441.
+// 8192 x 1024 x 65536 bfloat16 540 to 650 us: a gigabyte of scores beside it, which alone takes 225. The stores stand
+// in the same queue as the loads and hold them up (units busy 54 %); past the caches they take 90 us less than
+// through them. Blocks that start a part of a tile's time apart gain 3 % of it, and lose 10 % where tiles are deep.
 template <class T, int WX, int WV, int XT, int VT, int STAGES>
 __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(ScoreArgs a, int tiles_x, int tiles_v) {
     constexpr int NW = WX * WV, BX = 32 * XT * WX, BV = 32 * VT * WV, ROWS = BX + BV;
@@ -340,7 +351,8 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
     };
     auto corner = [&](const Place& p, int& x0, int& v0) {
         const int rows = min(GROUP_X, tiles_x - p.group * GROUP_X);
-        const int v = rows == 4 ? p.in >> 2 : rows == 3 ? (int)__umulhi((uint32_t)p.in, 0x55555556u) : p.in >> (rows - 1);
+        const int third = (int)__umulhi((uint32_t)p.in, 0x55555556u);
+        const int v = rows == 4 ? p.in >> 2 : rows == 3 ? third : p.in >> (rows - 1);
         x0 = (p.group * GROUP_X + p.in - v * rows) * BX;
         v0 = v * BV;
     };
@@ -370,9 +382,10 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
 #pragma unroll 1
             for (int r0 = w * 64; r0 < ROWS; r0 += NW * 64) {  // 64 rows, of one operand
                 const int r = r0 + l;
+                const int64_t x = min(load_x + r, (int)p->n - 1);
+                const int64_t v = min(load_v + vocab_row<VT>(r - BX), (int)p->vocab - 1);
                 load_lds4(scales0 + (load_four * ROWS + r0) * 4,
-                          k / 2 + (r0 < BX ? p->qscales + min(load_x + r, (int)p->n - 1) * p->qss
-                                           : p->wscales + min(load_v + vocab_row<VT>(r - BX), (int)p->vocab - 1) * p->wss));
+                          k / 2 + (r0 < BX ? p->qscales + x * p->qss : p->wscales + v * p->wss));
             }
             load_four = (load_four + 1) & 3;
         }
@@ -395,7 +408,7 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
     };
 
     const int wx = w % WX * (32 * XT), wv = BX + w / WX * (32 * VT);  // the wave's first rows in LDS
-    // where a lane's rows of its first tiles begin (the others are 32 rows on, which their chunks' turn does not change)
+    // where a lane's rows of its first tiles begin (the others are 32 rows on, where the chunks' turn is the same)
     const int turned = ((l / 32 * 2) ^ chunk_turn(l % 32)) * 16;
     const int at_x = (wx + l % 32) * STEP + turned, at_v = (wv + l % 32) * STEP + turned;
     int read_at = 0;  // the next step to read
@@ -498,8 +511,8 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
         for (int half = 0; half < 2; ++half) {
             // step s + 1 is here, the later ones are under way
             step_barrier<(STAGES - 2) * LOADS + decltype(stores)::value>();
-            // the next operands' reads and the loads spread over the products: all waves' at once would keep each other,
-            // and the products behind them, waiting
+            // the next operands' reads and the loads spread over the products: all waves' at once would keep each
+            // other, and the products behind them, waiting
             multiply(fx[half], fv[half], [&](int part, int parts) {
 #pragma unroll
                 for (int f = part * (XT + VT) / parts; f < (part + 1) * (XT + VT) / parts; ++f)
@@ -588,23 +601,36 @@ hipError_t scores_tiles(const ScoreArgs& a, hipStream_t s) {
     return hipSuccess;
 }
 
-// Few rows read the vocabulary straight to registers; more go through LDS where that gives blocks enough. us, direct
-// and by tiles of 128 x 128: 4 x 1024 x 65536 13, 14 (float32 13, 18), 16 x 1024 x 65536 17, 15 (17, 18),
-// 32 x 1024 x 65536 18, 15 (18.5, 19.5), 64 x 1024 x 65536 32, 16 (34, 21). Tiles of 256 x 256 have the operands' bytes
-// from LDS for half the products of 128 x 128; with few columns to a tile two blocks to a unit hide each other's
-// stores: by tiles of 256 x 256 and two blocks of 128 x 256, 8192 x 256 x 65536 282, 242; x 384 331, 292; x 512 353,
-// 353; x 1024 650, 769.
+// Which way a product takes. Straight to registers where there are few rows, or too few tiles for the units; through
+// LDS otherwise. us, straight and by tiles of 128 x 128 (float32 in brackets):
+//   4 x 1024 x 65536     13, 14 (13, 18)        16 x 1024 x 65536   17, 15 (17, 18)
+//   16 x 1024 x 8192     7, 8 (7, 12)           32 x 1024 x 65536   18, 15 (18.5, 19.5)
+//   64 x 1024 x 65536    32, 16 (34, 21)        300 x 1024 x 300    10, 9 (10, 13)
+//   1024 x 1024 x 1024   10, 8 (11, 12)         1280 x 6528 x 576   42, 32 (43, 50)
+//   512 x 8192 x 1000    28, 33 (29, 59)        2048 x 4096 x 512   27, 16 (29, 33)
+//   4000 x 512 x 400     10, 8 (11, 11)         128 x 65536 x 128   125, 211 (126, 431)
+// Straight, 64 x 32 to a wave reads a quarter less than 32 x 32, and fills the units where the depth can be split over
+// eight waves: 512 x 8192 x 1000 28, with 32 x 32 34; 1024 x 1024 x 1024 14, 10.
+// Tiles of 256 x 256 have the operands' bytes from LDS for half the products of 128 x 128; with few columns to a tile
+// two blocks to a unit hide each other's stores: 256 x 256 and two blocks of 128 x 256, 8192 x 256 x 65536 282, 242;
+// x 384 331, 292; x 512 353, 353; x 1024 650, 769; 8192 x 8192 x 8192 493, 621 (128 x 128 702).
 template <class T>
 hipError_t scores(const ScoreArgs& a, hipStream_t s) {
     auto tiles = [&](int64_t bx, int64_t bv) { return ((a.n + bx - 1) / bx) * ((a.vocab + bv - 1) / bv); };
-    if (a.n > (sizeof(T) == 2 ? 8 : 32)) {
-        if constexpr (sizeof(T) == 2) {
+    const bool deep = a.cols >= 4096;
+    if constexpr (sizeof(T) == 2) {
+        if (a.n > 8) {
             if (a.cols <= 384 && tiles(128, 256) >= 256) return scores_tiles<T, 2, 2, 2, 4, 3>(a, s);
             if (tiles(256, 256) >= 192) return scores_tiles<T, 4, 2, 2, 4, 4>(a, s);
+            if (tiles(128, 128) >= (a.n <= 16 ? 256 : deep ? 48 : 8)) return scores_tiles<T, 2, 2, 2, 2, 4>(a, s);
         }
-        if (tiles(128, 128) >= 64) return scores_tiles<T, 2, 2, 2, 2, 4>(a, s);
+    } else if (a.n > 32 && tiles(128, 128) >= 96) {
+        return scores_tiles<T, 2, 2, 2, 2, 4>(a, s);
     }
-    return a.n <= 16 ? scores_split<T, 1, 1>(a, s) : scores_split<T, 2, 2>(a, s);
+    if (a.n <= 16) return scores_split<T, 1, 1, 1>(a, s);
+    // here less than 96 tiles of 128 x 128 are at most 760 of these: 4 waves to each at least
+    if (deep && a.n > 32 && tiles(64, 32) >= 128) return scores_split<T, 4, 2, 4>(a, s);
+    return scores_split<T, 2, 2, 1>(a, s);
 }
 
 }  // namespace

@@ -92,8 +92,8 @@ def test_rms_norm_plain(n, dim, dtype):
     check_rms(randn(g, n, dim, dtype=dtype, pad=1, offset=1), None, None, randn(g, n, dim, dtype=dtype), None, 1e-5)
 
 
-@pytest.mark.parametrize("dtype,n,dim", [(F32, 300_000, 128), (BF16, 600_001, 128), (F32, 9_000, 4096), (BF16, 9_000, 8192)],
-                         ids=str)
+@pytest.mark.parametrize("dtype,n,dim", [(F32, 300_000, 128), (BF16, 600_001, 128), (F32, 9_000, 4096),
+                                         (BF16, 9_000, 8192)], ids=str)
 def test_rms_norm_larger_than_the_cache(n, dim, dtype):
     """Calls that go past the caches: more than 256 MB in all."""
     g = gen(n + dim)
@@ -221,8 +221,8 @@ def test_quantize_every_e4m3_value():
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
-@pytest.mark.parametrize("n,dim", [(1, 1), (1, 1024), (200, 64), (33, 128), (300, 129), (77, 771), (40, 1024), (50, 2050),
-                                   (9, 4096), (7, 8192), (5, 8200), (3, 20_001), (2, 65_536)])
+@pytest.mark.parametrize("n,dim", [(1, 1), (1, 1024), (200, 64), (33, 128), (300, 129), (77, 771), (40, 1024),
+                                   (50, 2050), (9, 4096), (7, 8192), (5, 8200), (3, 20_001), (2, 65_536)])
 def test_rms_norm_q8(n, dim, dtype):
     g = gen(n + dim)
     eps = 1e-6
@@ -276,7 +276,7 @@ SCORES = [(1, 128, 1), (1, 128, 16), (1, 1024, 1000), (2, 256, 17), (3, 384, 3),
           (17, 128, 64), (33, 896, 65), (48, 2048, 129), (64, 1024, 1000), (100, 256, 255), (127, 128, 257),
           (128, 512, 128), (257, 1152, 513), (300, 8192, 70), (700, 128, 33), (1000, 256, 1000), (1025, 384, 2049),
           (5003, 256, 1031), (2, 65_536, 5), (4096, 512, 2048),
-          (4000, 384, 5000), (9001, 128, 8003)]
+          (4000, 384, 5000), (9001, 128, 8003), (517, 4224, 1003), (12, 384, 33_000)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
@@ -369,7 +369,8 @@ def test_scores_past_32_bits(n, cols, vocab, dtype):
         mag = a.abs() @ b.abs().t()
         tol = mag * (2 * cols * U) + (a @ b.t()).abs() * half_step(dtype)
         if dtype is BF16:
-            tol = tol + 2.0 ** -10 * (a.abs().reshape(len(a), -1, 8).amax(2) @ b.abs().reshape(len(b), -1, 8).amax(2).t())
+            tol = tol + 2.0 ** -10 * (a.abs().reshape(len(a), -1, 8).amax(2) @
+                                      b.abs().reshape(len(b), -1, 8).amax(2).t())
         within("scores", out[some, v0:v0 + 65_536], a @ b.t(), tol)
 
 
@@ -488,7 +489,8 @@ def test_head_scores(dtype):
         assert torch.equal(out, head.scores(codes[:stages])) and not out.requires_grad
         y, w = every[stages - 1].double(), head.vocabulary.detach().double()
         mag = y.abs() @ w.abs().t()
-        # both operands' roundings (and, in bfloat16, the products' cut, and, beside small values, the smallest step: 2^-10 of 2^-8 of a block's largest)
+        # both operands' roundings (and, in bfloat16, the products' cut, and, beside small values, the smallest step:
+        # 2^-10 of 2^-8 of a block's largest)
         floor = 2.0 ** -17 * (y.abs().amax(1)[:, None] * w.abs().sum(1) + y.abs().sum(1)[:, None] * w.abs().amax(1))
         within("scores", out, y @ w.t(), mag * (2 * 2.0 ** -4 + 2.0 ** -8 + half_step(dtype) * 2) + floor * 2 + 1e-12)
 
