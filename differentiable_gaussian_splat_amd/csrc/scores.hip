@@ -535,6 +535,8 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
         else
             block(0, std::integral_constant<int, 0>{});
         for (int kb = 1; kb < nk / 2; ++kb) block(kb, std::integral_constant<int, 0>{});
+        // the last products' wait states before their results are read: behind `stay` the compiler need not see them
+        asm volatile("s_nop 15\n\ts_nop 3");
         int x0, v0;
         corner(place, x0, v0);
         advance(place);

@@ -607,6 +607,8 @@ class ResidualLabelHead(torch.nn.Module):
     @torch.no_grad()
     def scores(self, codes, vocabulary=None, dtype=torch.float32):
         """Scores [n, labels] after the last of the given stages (codes [stages, n], as many stages as wanted)."""
+        if not 0 < len(codes) <= len(self.codebooks):
+            raise ValueError(f"codes must be of 1 to {len(self.codebooks)} stages, got {len(codes)}")
         h, rows, last = None, None, len(codes) - 1
         for k, code in enumerate(codes):
             x = embed(self.codebooks[k], code, self.scales[k])

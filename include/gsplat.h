@@ -701,7 +701,8 @@ gs_status gs_label_loss_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype
  * x, y[n, dim]; residual[n, dim], weight[dim] nullable (nothing added, 1); eps >= 0.
  * sum[n, dim] (nullable, only with a residual) receives h, to be handed on and
  * kept for the backward; rstd[n] is nullable. A row of zeros with eps = 0 gives
- * no numbers, as the formula does.
+ * no numbers, as the formula does; one whose squares add up beyond float32 (values
+ * of 1e19) gives zeros.
  */
 gs_status gs_rms_norm_fwd(int64_t n, int32_t dim, int32_t dtype, const void *x, int64_t x_stride,
                           const void *residual, int64_t residual_stride, const void *weight, float eps, void *sum,
@@ -722,8 +723,8 @@ gs_status gs_rms_norm_bwd(int64_t n, int32_t dim, int32_t dtype, const void *h, 
  * Rows in 8 bits. A row of dim columns is `cols` e4m3 values (the 8-bit format
  * with 4 exponent and 3 mantissa bits, largest value 448, without infinities),
  * cols = dim rounded up to a multiple of 128, zero from dim on, and one scale for
- * each 128 of them, a power of two held as its exponent plus 127 in a byte. The
- * scales of a row are padded to a multiple of four bytes (with 127). The scale of
+ * each 128 of them, a power of two held as its exponent plus 127 in a byte (1 to
+ * 254; what a product gives for other bytes is not said). The scales of a row are padded to a multiple of four bytes (with 127). The scale of
  * a block is the least 2^e with max |v| <= 448 2^e over its finite values, e >=
  * -126 (1 where all are 0); a value is v / 2^e, to nearest even. Infinite values
  * and NaN become NaN. Rows of values are 16-byte aligned, rows of scales 4-byte
@@ -763,7 +764,8 @@ gs_status gs_label_scores_q8(int64_t n, int32_t cols, int64_t vocab, int32_t dty
  * (read before the call returns): device addresses of contiguous tensors, their
  * sizes, GS_F32 or GS_BF16. outs[i] is grads[i] (in place) or overlaps no gradient,
  * and no two of outs overlap; outs NULL: the norm only. max_norm >= 0 (infinite: nothing is clipped). The sum
- * is float64, in one order: the same bit for bit from run to run. Where a gradient
+ * is float64, in one order: the same bit for bit from run to run. The workspace is
+ * 256-byte aligned. Where a gradient
  * is NaN so are all results; where one is infinite the norm is, the infinite ones
  * become NaN and the others 0.
  */

@@ -312,6 +312,16 @@ def test_scores_small_terms_beside_large_ones():
     check_scores((a.to(Q8), one), (b.to(Q8), one), F32)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("n,vocab", [(3, 5), (300, 3000)])
+def test_scores_of_far_scales(n, vocab, dtype):
+    """Tiny features against huge words: the scales' ends, products of ordinary size."""
+    g = gen(15)
+    x, w = randn(g, n, 300) * 2.0 ** -110, randn(g, vocab, 300) * 2.0 ** 110
+    check_scores(L.quantize_q8(x), L.quantize_q8(w), dtype)
+    check_scores(L.quantize_q8(randn(g, n, 300) * 2.0 ** 110), L.quantize_q8(randn(g, vocab, 300) * 2.0 ** -110), dtype)
+
+
 def test_scores_nan_stays_in_its_row():
     g = gen(9)
     rows, vocabulary = random_rows(g, 70, 256), random_rows(g, 90, 256)

@@ -65,6 +65,41 @@ def test_descriptors_are_settled(kernels):
         assert loads >= 8, name
 
 
+def vectors(operand):
+    """The vector registers that v7 or v[4:7] names."""
+    m = re.fullmatch(r"v\[(\d+):(\d+)\]", operand)
+    if m:
+        return set(range(int(m.group(1)), int(m.group(2)) + 1))
+    m = re.fullmatch(r"v(\d+)", operand)
+    return {int(m.group(1))} if m else set()
+
+
+def test_products_are_done_before_their_results_are_read(kernels):
+    """Nineteen wait states between a product of sixteen passes and what reads its result, other than as the sum that
+    another product adds to. Empty assembly stands between them, behind which the compiler need not see it."""
+    for name, lines in kernels.items():
+        since, products = {}, 0  # wait states since a product wrote the register
+        for line in lines:
+            op, _, rest = line.partition(" ")
+            operands = [o.strip() for o in re.split(r",\s*(?![^\[]*\])", rest)]
+            product = op.startswith("v_mfma")
+            if op.startswith(("v_", "ds_", "global_", "buffer_")):
+                first = 0 if "store" in op or "write" in op else 1
+                read = [o for k, o in enumerate(operands) if k >= first and not (product and k == 3)]
+                for o in read:
+                    for r in vectors(o.split()[0] if o else ""):
+                        assert since.get(r, 99) >= 19, (name, line)
+            states = int(rest) + 1 if op == "s_nop" else 1
+            since = {r: k + states for r, k in since.items() if k < 40}
+            if product:
+                products += 1
+                since.update({r: 0 for r in vectors(operands[0])})
+            elif op.startswith("v_"):
+                for r in vectors(operands[0]):
+                    since.pop(r, None)
+        assert products >= 8, name
+
+
 def test_steps_stay_in_registers(kernels):
     """Spilled operands would be memory accesses that every step waits for."""
     for name, lines in kernels.items():
