@@ -1490,6 +1490,7 @@ gs_status gs_clip_grads(int32_t tensors, const void* const* grads, void* const* 
                 GS_CLIP_MAX_TENSORS, tensors);
         REQUIRE(max_norm >= 0.f, "%s: max_norm must be >= 0", fn);
         REQUIRE(tensors == 0 || (grads && numels && dtypes), "%s: grads, numels and dtypes must not be NULL", fn);
+        int64_t all = 0;
         for (int i = 0; i < tensors; ++i) {
             REQUIRE(numels[i] >= 0 && numels[i] <= (int64_t)1 << 40, "%s: tensor %d's size must be in [0, 2^40], got %lld",
                     fn, i, (long long)numels[i]);
@@ -1497,6 +1498,8 @@ gs_status gs_clip_grads(int32_t tensors, const void* const* grads, void* const* 
                 return fail(GS_ERR_UNSUPPORTED, "%s: tensor %d's dtype must be GS_F32 or GS_BF16, got %d", fn, i,
                             dtypes[i]);
             if (numels[i] == 0) continue;
+            all += numels[i];
+            REQUIRE(all <= (int64_t)1 << 40, "%s: more than 2^40 elements in all", fn);
             REQUIRE(grads[i] && (!outs || outs[i]), "%s: tensor %d is NULL", fn, i);
             const int size = dtypes[i] == GS_F32 ? 4 : 2;
             REQUIRE(aligned(grads[i], size) && (!outs || aligned(outs[i], size)), "%s: tensor %d is misaligned", fn, i);

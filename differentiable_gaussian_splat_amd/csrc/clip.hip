@@ -12,8 +12,8 @@
 // reverse of the order in which it read them, so that the last ones come from
 // the caches. 59M float32 in five tensors 142 us (3 x 236 MB: 5.0 TB/s, a large copy
 // has 4.8); chunks of 16 or 64 KB and up to 4096 blocks are within 3 % of it. 300
-// bfloat16 tensors of 40M elements 60 us, 45 of it the two launches; the others put
-// the tensors' table in memory, 96 of them to a launch's arguments. Small calls are
+// bfloat16 tensors of 40M elements 57 us, 45 of it the two launches; two others put
+// the tensors' table in memory, 160 of them to a launch's arguments. Small calls are
 // one launch of one block: 1000 elements 4.6 us, by two launches 7.9.
 #include "elem.hpp"
 #include "launch.hpp"
@@ -25,14 +25,15 @@ namespace {
 constexpr int CB = 256;                // threads per block
 constexpr int CHUNK_BYTES = 32768;     // of one tensor
 constexpr int CLIP_BLOCKS = 1024;      // at most; a partial sum each
-constexpr int TABLE = 96;              // tensors in a launch's arguments
+constexpr int TABLE = 160;             // tensors in a launch's arguments, which hold 4 KB
 
 struct ClipTensor {
     const void* g;
     void* out;        // null: norm only
-    int64_t n;        // elements; bfloat16: ~elements
-    int64_t first;    // its first chunk
+    uint32_t first;   // its first chunk
+    uint32_t last;    // elements of its last chunk, and HALF for bfloat16
 };
+constexpr uint32_t HALF = 0x80000000u;
 
 // The tensors by value (in the launch's arguments) if they fit, otherwise in memory.
 struct ClipTable {
@@ -44,7 +45,7 @@ constexpr int CHUNK = CHUNK_BYTES / (int)sizeof(T);
 
 // The tensor that holds chunk c: how many begin at or before it, counted by the wave's lanes together (a search by
 // halves waits for one load after another).
-__device__ __forceinline__ int tensor_of(const ClipTensor* t, int count, int64_t c) {
+__device__ __forceinline__ int tensor_of(const ClipTensor* t, int count, uint32_t c) {
     int k = -1;
     for (int i = 0; i < count; i += 64) {
         const int at = i + (threadIdx.x & 63);
@@ -123,22 +124,24 @@ __device__ __forceinline__ void chunk_scale(const T* g, T* o, int left, float c)
     }
 }
 
+// chunk: of the tensor; last: whether it is the tensor's last.
 template <class T>
-__device__ __forceinline__ double squares(const ClipTensor& e, int64_t n, int64_t chunk) {
-    const T* g = (const T*)e.g + (chunk - e.first) * CHUNK<T>;
-    const int64_t left = n - (chunk - e.first) * CHUNK<T>;
-    return left >= CHUNK<T> ? chunk_squares<true>(g, 0) : chunk_squares<false>(g, (int)left);
+__device__ __forceinline__ double squares(const ClipTensor& e, uint32_t chunk, bool last) {
+    const T* g = (const T*)e.g + (int64_t)chunk * CHUNK<T>;
+    const int left = last ? (int)(e.last & ~HALF) : CHUNK<T>;
+    return left == CHUNK<T> ? chunk_squares<true>(g, 0) : chunk_squares<false>(g, left);
 }
 
 template <class T>
-__device__ __forceinline__ void scale(const ClipTensor& e, int64_t n, int64_t chunk, float c) {
-    const int64_t at = (chunk - e.first) * CHUNK<T>, left = n - at;
+__device__ __forceinline__ void scale(const ClipTensor& e, uint32_t chunk, bool last, float c) {
+    const int64_t at = (int64_t)chunk * CHUNK<T>;
+    const int left = last ? (int)(e.last & ~HALF) : CHUNK<T>;
     const T* g = (const T*)e.g + at;
     T* o = (T*)e.out + at;
-    if (left >= CHUNK<T>)
+    if (left == CHUNK<T>)
         chunk_scale<true>(g, o, 0, c);
     else
-        chunk_scale<false>(g, o, (int)left, c);
+        chunk_scale<false>(g, o, left, c);
 }
 
 // What the gradients are multiplied by: no number where the norm is none.
@@ -148,66 +151,74 @@ __device__ __forceinline__ float factor(float max_norm, double norm) {
 }
 
 // A block's run of chunks: as many for each block, one more for the first ones.
-__device__ __forceinline__ void block_chunks(int64_t chunks, int64_t& first, int64_t& end) {
-    const int64_t b = blockIdx.x, each = chunks / gridDim.x, more = chunks % gridDim.x;
-    first = b * each + (b < more ? b : more);
+__device__ __forceinline__ void block_chunks(uint32_t chunks, uint32_t& first, uint32_t& end) {
+    const uint32_t b = blockIdx.x, each = chunks / gridDim.x, more = chunks % gridDim.x;
+    first = b * each + min(b, more);
     end = first + each + (b < more ? 1 : 0);
 }
 
-__device__ __forceinline__ void clip_norm(const ClipTensor* t, int count, int64_t chunks, double* part) {
+// Where the tensor behind tensor k begins.
+__device__ __forceinline__ uint32_t end_of(const ClipTensor* t, int count, int k, uint32_t chunks) {
+    return k + 1 < count ? t[k + 1].first : chunks;
+}
+
+__device__ __forceinline__ void clip_norm(const ClipTensor* t, int count, uint32_t chunks, double* part) {
     __shared__ double s[CB / 64];
-    int64_t first, end;
+    uint32_t first, end;
     block_chunks(chunks, first, end);
     double sum = 0.;
     int k = first < end ? tensor_of(t, count, first) : 0;
-    for (int64_t c = first; c < end; ++c) {
-        while (k + 1 < count && t[k + 1].first <= c) ++k;
+    uint32_t next = end_of(t, count, k, chunks);
+    for (uint32_t c = first; c < end; ++c) {
+        if (c == next) next = end_of(t, count, ++k, chunks);  // no tensor is without chunks
         const ClipTensor e = t[k];
-        sum += e.n < 0 ? squares<bf16>(e, ~e.n, c) : squares<float>(e, e.n, c);
+        const bool last = c + 1 == next;
+        sum += e.last & HALF ? squares<bf16>(e, c - e.first, last) : squares<float>(e, c - e.first, last);
     }
     sum = block_sum(sum, s);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
 // parts: how many sums the first launch left. wanted: whether the tensors are, beside the norm.
-__device__ __forceinline__ void clip_scale(const ClipTensor* t, int count, int64_t chunks, const double* part,
+__device__ __forceinline__ void clip_scale(const ClipTensor* t, int count, uint32_t chunks, const double* part,
                                            int parts, float max_norm, float* norm, bool wanted) {
     __shared__ double s[CB / 64];
-    int64_t first, end;
+    uint32_t first, end;
     block_chunks(chunks, first, end);
     int k = wanted && first < end ? tensor_of(t, count, end - 1) : 0;
+    uint32_t next = end_of(t, count, k, chunks);
     double sum = 0.;
     for (int i = threadIdx.x; i < parts; i += CB) sum += part[i];
     const double whole = sqrt(block_sum(sum, s));
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)whole;
     if (!wanted) return;
     const float c = factor(max_norm, whole);
-    for (int64_t j = end - 1; j >= first; --j) {
-        while (t[k].first > j) --k;
+    for (uint32_t j = end; j-- > first;) {
+        if (j < t[k].first) next = t[k--].first;
         const ClipTensor e = t[k];
         if (c == 1.f && e.g == e.out) continue;  // in place, and nothing to change
-        if (e.n < 0)
-            scale<bf16>(e, ~e.n, j, c);
+        if (e.last & HALF)
+            scale<bf16>(e, j - e.first, j + 1 == next, c);
         else
-            scale<float>(e, e.n, j, c);
+            scale<float>(e, j - e.first, j + 1 == next, c);
     }
 }
 
-__global__ __launch_bounds__(CB) void k_clip_norm(ClipTable t, int count, int64_t chunks, double* part) {
+__global__ __launch_bounds__(CB) void k_clip_norm(ClipTable t, int count, uint32_t chunks, double* part) {
     clip_norm(t.t, count, chunks, part);
 }
 
-__global__ __launch_bounds__(CB) void k_clip_norm_many(const ClipTensor* __restrict__ t, int count, int64_t chunks,
+__global__ __launch_bounds__(CB) void k_clip_norm_many(const ClipTensor* __restrict__ t, int count, uint32_t chunks,
                                                        double* part) {
     clip_norm(t, count, chunks, part);
 }
 
-__global__ __launch_bounds__(CB) void k_clip_scale(ClipTable t, int count, int64_t chunks, const double* part,
+__global__ __launch_bounds__(CB) void k_clip_scale(ClipTable t, int count, uint32_t chunks, const double* part,
                                                    int parts, float max_norm, float* norm, bool wanted) {
     clip_scale(t.t, count, chunks, part, parts, max_norm, norm, wanted);
 }
 
-__global__ __launch_bounds__(CB) void k_clip_scale_many(const ClipTensor* __restrict__ t, int count, int64_t chunks,
+__global__ __launch_bounds__(CB) void k_clip_scale_many(const ClipTensor* __restrict__ t, int count, uint32_t chunks,
                                                         const double* part, int parts, float max_norm, float* norm,
                                                         bool wanted) {
     clip_scale(t, count, chunks, part, parts, max_norm, norm, wanted);
@@ -222,18 +233,19 @@ __global__ __launch_bounds__(64 * SMALL_WAVES) void k_clip_small(ClipTable t, in
                                                                  float* norm, bool wanted) {
     __shared__ double s[SMALL_WAVES];
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int first = lane < count ? (int)t.t[lane].first : units;
+    const uint32_t first = lane < count ? t.t[lane].first : (uint32_t)units;
     uint32_t raw[SMALL_UNITS][4];
     double sum = 0.;
-    // what(element, at most, tensor, bfloat16) of this lane in the wave's i-th unit
+    // what(element, left from there on, tensor, bfloat16) of this lane in the wave's i-th unit
     auto each = [&](int i, auto what) {
-        const int u = w + i * SMALL_WAVES;
-        if (u >= units) return;
+        const uint32_t u = w + i * SMALL_WAVES;
+        if (u >= (uint32_t)units) return;
         const int k = __builtin_amdgcn_readfirstlane(__popcll(__ballot(first <= u)) - 1);
         const ClipTensor& e = t.t[k];
-        const bool half = e.n < 0;
-        const int at = (u - (int)e.first) * (UNIT_BYTES / (half ? 2 : 4)) + lane * (half ? 8 : 4);
-        what(at, (int)(half ? ~e.n : e.n) - at, e, half);
+        const bool half = e.last & HALF;
+        const int whole = UNIT_BYTES / (half ? 2 : 4), in = lane * (half ? 8 : 4);
+        const int here = u + 1 == end_of(t.t, count, k, units) ? (int)(e.last & ~HALF) : whole;
+        what((int)(u - e.first) * whole + in, here - in, e, half);
     };
 #pragma unroll
     for (int i = 0; i < SMALL_UNITS; ++i) {
@@ -297,7 +309,7 @@ __global__ __launch_bounds__(64 * SMALL_WAVES) void k_clip_small(ClipTable t, in
         });
 }
 
-__global__ __launch_bounds__(128) void k_clip_table(ClipTable t, int count, ClipTensor* __restrict__ to) {
+__global__ __launch_bounds__(TABLE) void k_clip_table(ClipTable t, int count, ClipTensor* __restrict__ to) {
     if ((int)threadIdx.x < count) to[threadIdx.x] = t.t[threadIdx.x];
 }
 
@@ -321,17 +333,17 @@ hipError_t launch_clip_grads(int tensors, const void* const* grads, void* const*
         units += (numels[i] * (half[i] ? 2 : 4) + UNIT_BYTES - 1) / UNIT_BYTES;
     }
     const bool many = full > TABLE, small = full <= 64 && units <= SMALL_WAVES * SMALL_UNITS;
-    const int64_t bytes = small ? UNIT_BYTES : CHUNK_BYTES;
     for (int i = 0; i < tensors; ++i) {
         if (numels[i] == 0) continue;
+        const int64_t per = (small ? UNIT_BYTES : CHUNK_BYTES) / (half[i] ? 2 : 4), mine = (numels[i] + per - 1) / per;
         ClipTensor& e = t.t[held++];
         e.g = grads[i];
         e.out = outs ? outs[i] : nullptr;
-        e.n = half[i] ? ~numels[i] : numels[i];
-        e.first = chunks;
-        chunks += (numels[i] * (half[i] ? 2 : 4) + bytes - 1) / bytes;
+        e.first = (uint32_t)chunks;
+        e.last = (uint32_t)(numels[i] - (mine - 1) * per) | (half[i] ? HALF : 0u);
+        chunks += mine;
         if (many && (held == TABLE || count + held == full)) {
-            k_clip_table<<<1, 128, 0, stream>>>(t, held, table + count);
+            k_clip_table<<<1, TABLE, 0, stream>>>(t, held, table + count);
             if (hipError_t e2 = hipGetLastError()) return e2;
             count += held;
             held = 0;
@@ -345,9 +357,9 @@ hipError_t launch_clip_grads(int tensors, const void* const* grads, void* const*
     const int blocks = (int)(chunks < CLIP_BLOCKS ? chunks : CLIP_BLOCKS);
     if (blocks > 0) {
         if (many)
-            k_clip_norm_many<<<blocks, CB, 0, stream>>>(table, count, chunks, part);
+            k_clip_norm_many<<<blocks, CB, 0, stream>>>(table, count, (uint32_t)chunks, part);
         else
-            k_clip_norm<<<blocks, CB, 0, stream>>>(t, count, chunks, part);
+            k_clip_norm<<<blocks, CB, 0, stream>>>(t, count, (uint32_t)chunks, part);
         if (hipError_t e = hipGetLastError()) return e;
     }
     const int scale_blocks = outs && blocks > 0 ? blocks : 1;

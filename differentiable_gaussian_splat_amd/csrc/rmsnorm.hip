@@ -11,7 +11,8 @@
 // of LPR lanes (from one lane to a block of 1024 threads for the longest rows), so
 // that its statistic costs no second read. Blocks walk over the rows. The column
 // sums of dw go to the workspace, one row per block, and a second launch adds them
-// in a fixed order (norm.hip).
+// in a fixed order (norm.hip); a single block writes dw itself (64 x 6 float32 with
+// gradients 14 us, 19 with the second launch).
 //
 // 1M x 64 float32 with residual and gradients 332 us (1.79 GB read or written once:
 // 5.4 TB/s; a large copy has 4.8); 32771 rows of 771 bfloat16 in a wider matrix 87
@@ -84,7 +85,8 @@ struct RmsArgs {
     int64_t dys, dss;
     void* dx;
     int64_t dxs;
-    float* part;  // [blocks][dim]
+    float* part;    // [blocks][dim]: the blocks' column sums
+    void* dweight;  // they themselves, of one block
     bool plain;   // into 8 bits without the norm
 };
 
@@ -308,7 +310,7 @@ __global__ __launch_bounds__(NT) void k_rms_bwd(RmsArgs a) {
             if (left > 0) store_part<FULL, PAST>((T*)a.dx + r * a.dxs + c, left, g);
         }
     }
-    if (!a.part) return;
+    if (!a.part && !a.dweight) return;
     // the block's column sums: over the row groups of a wave, then over the waves in turn
 #pragma unroll
     for (int e = 0; e < EPL; ++e)
@@ -316,7 +318,12 @@ __global__ __launch_bounds__(NT) void k_rms_bwd(RmsArgs a) {
         for (int k = 0; k < VEC; ++k)
 #pragma unroll
             for (int off = LPR; off < 64; off <<= 1) aw[e][k] += __shfl_xor(aw[e][k], off);
-    float* pw = a.part + (size_t)blockIdx.x * dim;
+    auto store = [&](int c, float v) {
+        if (a.dweight)
+            ((T*)a.dweight)[c] = (T)v;
+        else
+            a.part[(size_t)blockIdx.x * dim + c] = v;
+    };
     if constexpr (LPR < NT) {
         const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
         for (int turn = 0; turn < NT / 64; ++turn) {
@@ -331,14 +338,14 @@ __global__ __launch_bounds__(NT) void k_rms_bwd(RmsArgs a) {
             }
             __syncthreads();
         }
-        for (int c = threadIdx.x; c < dim; c += NT) pw[c] = s_acc[c];
+        for (int c = threadIdx.x; c < dim; c += NT) store(c, s_acc[c]);
     } else {
 #pragma unroll
         for (int e = 0; e < EPL; ++e)
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
                 const int c = (e * LPR + l) * VEC + k;
-                if (c < dim) pw[c] = aw[e][k];
+                if (c < dim) store(c, aw[e][k]);
             }
     }
 }
@@ -354,7 +361,7 @@ constexpr int RMS_BLOCKS_FWD = 2048, RMS_BLOCKS_BWD = 1024;  // of 256 threads; 
 constexpr int64_t CACHED = (int64_t)256 << 20;
 
 template <class T, int CALL, int NT, int LPR, int EPL, bool FULL>
-hipError_t rms_rows(const RmsArgs& a, int& blocks, hipStream_t s) {
+hipError_t rms_rows(RmsArgs a, int& blocks, hipStream_t s) {
     const int64_t want = (a.n + NT / LPR - 1) / (NT / LPR);
     const int cap = (CALL == RMS_BWD ? RMS_BLOCKS_BWD : RMS_BLOCKS_FWD) * 256 / NT;
     blocks = (int)(want < cap ? want : cap);
@@ -362,6 +369,7 @@ hipError_t rms_rows(const RmsArgs& a, int& blocks, hipStream_t s) {
     const bool past = FULL && CALL != RMS_Q8 && a.n * a.dim * (int64_t)sizeof(T) * matrices > CACHED;
     constexpr bool CAN = FULL && CALL != RMS_Q8;
     if constexpr (CALL == RMS_BWD) {
+        if (blocks > 1) a.dweight = nullptr;
         if (past)
             k_rms_bwd<T, NT, LPR, EPL, FULL, CAN><<<blocks, NT, 0, s>>>(a);
         else
@@ -452,10 +460,11 @@ hipError_t launch_rms_bwd(int64_t n, int dim, bool half, const void* h, int64_t 
     a.dx = dx;
     a.dxs = dxs;
     a.part = dweight ? part : nullptr;
+    a.dweight = dweight;
     int blocks = 0;
     if (n > 0 && (dx || dweight))
         if (hipError_t e = rms_launch<RMS_BWD>(half, a, blocks, stream)) return e;
-    return dweight ? launch_column_sums(half, blocks, dim, dim, part, dweight, nullptr, stream) : hipSuccess;
+    return dweight && blocks != 1 ? launch_column_sums(half, blocks, dim, dim, part, dweight, nullptr, stream) : hipSuccess;
 }
 
 hipError_t launch_rms_q8(int64_t n, int dim, bool half, const void* x, int64_t xs, const void* residual, int64_t rs,

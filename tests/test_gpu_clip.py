@@ -48,7 +48,8 @@ KINDS = {"f32": [F32], "bf16": [BF16], "both": [F32, BF16]}
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("sizes", [[1], [0, 1, 0], [3, 5], [8191, 8192, 8193, 16_383, 16_384, 16_385], [113_280],
-                                   [1000] * 96, [777] * 97, [7] * 64, [130] * 64, [5] * 65, [16_384, 1], [33, 0] * 150, [5_000_001, 3, 70_000]],
+                                   [1000] * 96, [777] * 97, [7] * 64, [130] * 64, [5] * 65, [16_384, 1],
+                                   [40_000] * 160, [99] * 161, [20_000, 1] * 170, [33, 0] * 150, [5_000_001, 3, 70_000]],
                          ids=lambda s: f"{len(s)}x{max(s)}")
 def test_clip(sizes, kind):
     kinds = [KINDS[kind][i % len(KINDS[kind])] for i in range(len(sizes))]

@@ -96,6 +96,7 @@ def clip(n=2, grads=(4096, 8192), outs=(4096, 8192), numels=(5, 7), dtypes=(0, 1
     (dict(dtypes=None), INVALID, "NULL"),
     (dict(numels=(5, -1)), INVALID, "tensor 1's size"),
     (dict(numels=(1 << 41, 1)), INVALID, "tensor 0's size"),
+    (dict(numels=(1 << 40, 1)), INVALID, "2^40 elements"),
     (dict(dtypes=(0, 2)), UNSUPPORTED, "tensor 1's dtype"),
     (dict(grads=(0, 8192)), INVALID, "tensor 0 is NULL"),
     (dict(outs=(4096, 0)), INVALID, "tensor 1 is NULL"),
