@@ -10,9 +10,6 @@
 //             score's size on normal data: nothing beside the result's own rounding.
 //   float32   the operands widened to bfloat16 with their scale, which is exact, and
 //             bfloat16 products, at less than a third of the rate: 1.4e-8 to 2e-7.
-// The vocabulary's rows stand for the rows of a unit's tile and the features for its
-// columns, so that a lane holds runs of one feature row's scores; which vocabulary
-// row stands in which row of the tile is chosen so that a lane's runs join.
 #include <type_traits>
 
 #include "launch.hpp"
@@ -92,7 +89,9 @@ __device__ __forceinline__ bf16x8 widen8(const i32x8& q, int s, float scale) {
 constexpr int DIRECT_WAVES = 8;  // of a block
 
 // Straight from memory to registers: a wave takes 16 XT feature rows and 16 VT vocabulary rows over its share of the
-// depth (every KS-th four blocks); the KS waves of a tile join their sums in LDS.
+// depth (every KS-th four blocks); the KS waves of a tile join their sums in LDS. The vocabulary's rows stand for the
+// rows of a unit's tile and the features for its columns, so that a lane holds runs of one feature row's scores; which
+// vocabulary row stands in which row of the tile is chosen so that a lane's runs join.
 template <class T, int XT, int VT, int KS>
 __global__ __launch_bounds__(64 * DIRECT_WAVES) void k_scores_direct(ScoreArgs a) {
     constexpr int VW = DIRECT_WAVES / KS;  // tiles side by side
@@ -242,7 +241,7 @@ __device__ __forceinline__ int chunk_turn(int r) { return (r >> 2) & 3; }
 
 // The vocabulary row (of a block's) that stands in row s of its tiles: column c of a wave's tile j is its VT c + j, so
 // that a lane's scores in a row join, and the 32 lanes of a row write without gaps. (Runs of a lane's own, 16 bytes at
-// a time with other lanes' between them, cost four times the requests: 8192 x 128 x 65536 437 us, so 300.)
+// a time with other lanes' between them, cost four times the requests: 8192 x 128 x 65536 437 us, so 287.)
 template <int VT>
 __device__ __forceinline__ int vocab_row(int s) {
     return s / (32 * VT) * (32 * VT) + s % 32 * VT + s / 32 % VT;
@@ -309,7 +308,7 @@ __device__ __forceinline__ void step_barrier() {
 // conflicts. With the step's reads and loads all behind its barrier 524; with a descriptor formed for each load
 // 30 % more. Four waves of 128 x 128 with a third less to read from LDS 458 where eight had 441.
 // 8192 x 1024 x 65536 bfloat16 540 to 650 us: a gigabyte of scores beside it, which alone takes 225. The stores stand
-// in the same queue as the loads and hold them up (units busy 54 %); past the caches they take 90 us less than
+// in the same queue as the loads and hold them up (units busy 56 %); past the caches they take 90 us less than
 // through them. Blocks that start a part of a tile's time apart gain 3 % of it, and lose 10 % where tiles are deep.
 template <class T, int WX, int WV, int XT, int VT, int STAGES>
 __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(ScoreArgs a, int tiles_x, int tiles_v) {
@@ -431,11 +430,11 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
     };
     int sx[XT], sv[VT];  // the scales of four blocks, the current one's lowest
+    // a product stays in its place: left to the compiler they sink past the next barriers, and the operands of several
+    // steps do not fit the registers
+    auto stay = [](f32x16& c) { asm volatile("" : "+v"(c)); };
     // between(part, parts): what is done between the products
     auto multiply = [&](const i32x8 (&fx)[XT], const i32x8 (&fv)[VT], auto between) {
-        // a product stays in its place: left to the compiler they sink past the next barriers, and the operands of
-        // several steps do not fit the registers
-        auto stay = [&](f32x16& c) { asm volatile("" : "+v"(c)); };
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int i = 0; i < XT; ++i)
@@ -537,6 +536,10 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
         for (int kb = 1; kb < nk / 2; ++kb) block(kb, std::integral_constant<int, 0>{});
         // the last products' wait states before their results are read: behind `stay` the compiler need not see them
         asm volatile("s_nop 15\n\ts_nop 3");
+#pragma unroll
+        for (int i = 0; i < XT; ++i)
+#pragma unroll
+            for (int j = 0; j < VT; ++j) stay(acc[i][j]);
         int x0, v0;
         corner(place, x0, v0);
         advance(place);
