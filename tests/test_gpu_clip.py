@@ -208,3 +208,45 @@ def test_label_head_and_scene_clipped(dtype):
     for v in grads.values():
         v.normal_()
     check(list(grads.values()), 5.0, in_place=True)
+
+
+def test_captured_training_step_replays():
+    """Forward, backward and clipping of a residual head recorded into a graph: replayed on changed inputs, against the
+    same step run eagerly on a copy of the head."""
+    torch.manual_seed(2)
+    heads = [L.ResidualLabelHead([50, 20], 32, 30) for _ in range(2)]
+    heads[1].load_state_dict(heads[0].state_dict())
+    codes = torch.stack([torch.randint(0, k, (900,), device=DEV) for k in (50, 20)])
+    labels = torch.randint(-1, 30, (900,), device=DEV)
+    for head in heads:
+        for p in head.parameters():
+            p.grad = torch.zeros_like(p)
+    clips = [O.GradClip([p.grad for p in head.parameters()]) for head in heads]
+
+    def step(k):
+        for p in heads[k].parameters():
+            p.grad.zero_()
+        loss = heads[k](codes, labels)
+        loss.backward()
+        clips[k](1e-2)
+        return loss.detach()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(0)  # no eager graph of this head's parameters lives on when the step is recorded
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss = step(0)
+    for k in range(4):
+        codes.copy_(torch.stack([torch.randint(0, c, (900,), device=DEV) for c in (50, 20)]))
+        labels.copy_(torch.randint(-1, 30, (900,), device=DEV))
+        want = step(1).clone()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(loss, want) and torch.equal(clips[0].norm, clips[1].norm)
+        for a, b in zip(heads[0].parameters(), heads[1].parameters()):
+            assert torch.equal(a.grad, b.grad)

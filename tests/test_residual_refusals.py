@@ -173,3 +173,31 @@ def test_rows_q8_shapes():
     for dim, cols, groups in ((1, 128, 4), (128, 128, 4), (129, 256, 4), (512, 512, 4), (513, 640, 8)):
         q, scales = L.rows_q8(3, dim, "cpu")
         assert q.shape == (3, cols) and scales.shape == (3, groups)
+
+
+def test_calls_switch_to_the_tensors_device(monkeypatch):
+    """The default stream's handle is the same on every device: a call on another one than the current is made there."""
+    seen = []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            seen.append(("enter", self.index))
+
+        def __exit__(self, *_):
+            seen.append(("leave", self.index))
+
+    class Library:
+        @staticmethod
+        def gs_quantize_q8(*args):
+            seen.append(args)
+            return raster.GS_OK
+
+    monkeypatch.setattr(L, "load_library", Library)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    L._call("gs_quantize_q8", 0, 1, 2)
+    L._call("gs_quantize_q8", 1, 3, 4)
+    assert seen == [(1, 2), ("enter", 1), (3, 4), ("leave", 1)]
