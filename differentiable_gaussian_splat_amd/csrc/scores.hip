@@ -315,6 +315,8 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
     constexpr int NW = WX * WV, BX = 32 * XT * WX, BV = 32 * VT * WV, ROWS = BX + BV;
     constexpr int LOADS = ROWS / 16 / NW;          // of 16 rows each, per wave and step
     constexpr int STORES = XT * 16;                // of VT scores, per lane and whole tile
+    // (float32 by 256 x 256 lets none pass: two ways into a tile, and its widened operands, do not fit the registers.)
+    constexpr bool LET = sizeof(T) == 2 || XT * VT < 8;
     static_assert(ROWS % (16 * NW) == 0 && BX % (16 * NW) == 0 && BX % 64 == 0, "");
     static_assert((STAGES - 2) * LOADS + STORES < 64 && (STAGES - 1) * LOADS < 64, "what a wait can count");
     __shared__ alignas(1024) uint8_t s_rows[STAGES * ROWS * STEP];
@@ -448,18 +450,18 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
         } else {
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                bf16x8 hx[XT], hv[VT];
+                bf16x8 hx[XT];
 #pragma unroll
                 for (int i = 0; i < XT; ++i) hx[i] = widen8(fx[i], s, scale_of<0>(sx[i]));
 #pragma unroll
-                for (int j = 0; j < VT; ++j) hv[j] = widen8(fv[j], s, scale_of<0>(sv[j]));
+                for (int j = 0; j < VT; ++j) {
+                    const bf16x8 hv = widen8(fv[j], s, scale_of<0>(sv[j]));
 #pragma unroll
-                for (int i = 0; i < XT; ++i)
-#pragma unroll
-                    for (int j = 0; j < VT; ++j) {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hx[i], hv[j], acc[i][j], 0, 0, 0);
+                    for (int i = 0; i < XT; ++i) {
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hx[i], hv, acc[i][j], 0, 0, 0);
                         stay(acc[i][j]);
                     }
+                }
                 between(s, 4);
             }
         }
@@ -529,7 +531,7 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
         for (int j = 0; j < VT; ++j) sv[j] = (int)((uint32_t)sv[j] >> 8);
     };
     for (int k = 0; k < mine; ++k) {
-        if (quiet)
+        if (LET && quiet)
             block(0, std::integral_constant<int, STORES>{});
         else
             block(0, std::integral_constant<int, 0>{});
@@ -578,7 +580,7 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
             store(std::true_type{});
         else
             store(std::false_type{});
-        quiet = whole;
+        quiet = LET && whole;
         clear();
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last step
@@ -619,6 +621,9 @@ hipError_t scores_tiles(const ScoreArgs& a, hipStream_t s) {
 // Tiles of 256 x 256 have the operands' bytes from LDS for half the products of 128 x 128; with few columns to a tile
 // two blocks to a unit hide each other's stores: 256 x 256 and two blocks of 128 x 256, 8192 x 256 x 65536 282, 242;
 // x 384 331, 292; x 512 353, 353; x 1024 650, 769; 8192 x 8192 x 8192 493, 621 (128 x 128 702).
+// In float32, where the products take four times as long, 256 x 256 gains little and loses where rounds are not full:
+// 128 x 128 and 256 x 256, 8192 x 8192 x 8192 998, 889; 16384 x 512 x 16384 327, 301; 3000 x 4096 x 5000 116, 105;
+// 5000 x 2048 x 5000 103, 108; 45414 x 1280 x 550 71, 101; 5003 x 256 x 8192 36, 44.
 template <class T>
 hipError_t scores(const ScoreArgs& a, hipStream_t s) {
     auto tiles = [&](int64_t bx, int64_t bv) { return ((a.n + bx - 1) / bx) * ((a.vocab + bv - 1) / bv); };
@@ -630,6 +635,10 @@ hipError_t scores(const ScoreArgs& a, hipStream_t s) {
             if (tiles(128, 128) >= (a.n <= 16 ? 256 : deep ? 48 : 8)) return scores_tiles<T, 2, 2, 2, 2, 4>(a, s);
         }
     } else if (a.n > 32 && tiles(128, 128) >= 96) {
+        // three quarters at least of the units' rounds of 256 x 256 are scores
+        const int64_t rounds = (tiles(256, 256) + 255) / 256;
+        if (a.cols >= 512 && a.n * a.vocab / (3 * 256 * 65536 / 4) >= rounds)
+            return scores_tiles<T, 4, 2, 2, 4, 4>(a, s);
         return scores_tiles<T, 2, 2, 2, 2, 4>(a, s);
     }
     if (a.n <= 16) return scores_split<T, 1, 1, 1>(a, s);

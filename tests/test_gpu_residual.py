@@ -276,7 +276,8 @@ SCORES = [(1, 128, 1), (1, 128, 16), (1, 1024, 1000), (2, 256, 17), (3, 384, 3),
           (17, 128, 64), (33, 896, 65), (48, 2048, 129), (64, 1024, 1000), (100, 256, 255), (127, 128, 257),
           (128, 512, 128), (257, 1152, 513), (300, 8192, 70), (700, 128, 33), (1000, 256, 1000), (1025, 384, 2049),
           (5003, 256, 1031), (2, 65_536, 5), (4096, 512, 2048),
-          (4000, 384, 5000), (9001, 128, 8003), (517, 4224, 1003), (12, 384, 33_000)]
+          (4000, 384, 5000), (9001, 128, 8003), (517, 4224, 1003), (12, 384, 33_000),
+          (4000, 640, 4090), (8192, 512, 5120)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
