@@ -247,18 +247,23 @@ __device__ __forceinline__ int vocab_row(int s) {
     return s / (32 * VT) * (32 * VT) + s % 32 * VT + s / 32 % VT;
 }
 
+// Where a tile's scores go, said to be global memory: through a pointer of any memory they would be flat accesses, which
+// LDS waits count too, and which end in no said order with the loads beside them.
+template <class T>
+using scores_at = T __attribute__((address_space(1)))*;
+
 // Stores C scores side by side (out is aligned to its elements only). PAST: past the caches, which the operands need.
 template <bool PAST, class T, int C>
-__device__ __forceinline__ void store_run(T* out, const float (&v)[C]) {
+__device__ __forceinline__ void store_run(scores_at<T> out, const float (&v)[C]) {
     typedef T run __attribute__((ext_vector_type(C)));
     typedef T run_any __attribute__((ext_vector_type(C), aligned(sizeof(T))));
     run t;
 #pragma unroll
     for (int c = 0; c < C; ++c) t[c] = (T)v[c];
     if (PAST)
-        __builtin_nontemporal_store(t, reinterpret_cast<run_any*>(out));
+        __builtin_nontemporal_store(t, (scores_at<run_any>)out);
     else
-        *reinterpret_cast<run_any*>(out) = t;
+        *(scores_at<run_any>)out = t;
 }
 
 // A descriptor of `bytes` bytes from p on; reads beyond them give 0. (A step's offset, which is added to a lane's,
@@ -550,7 +555,7 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
         const int n = (int)p->n, vocab = (int)p->vocab;
         const int64_t os = p->os;
         const int x = x0 + wx + 4 * (l / 32), v = v0 + (wv - BX) + l % 32 * VT;
-        T* out = (T*)p->out + x * os + v;
+        auto out = (scores_at<T>)((T*)p->out + x * os + v);
         const bool whole = n - x0 >= BX && vocab - v0 >= BV;
         int rows = n - x;  // from out on
         const int left = vocab - v;
@@ -563,7 +568,7 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
 #pragma unroll
                     for (int j = 0; j < VT; ++j) t[j] = acc[i][j][e];
                     if (whole || (rows > 0 && left >= VT)) {
-                        store_run<decltype(past)::value>(out, t);
+                        store_run<decltype(past)::value, T>(out, t);
                     } else if (rows > 0) {
 #pragma unroll
                         for (int j = 0; j < VT - 1; ++j)

@@ -104,3 +104,13 @@ def test_steps_stay_in_registers(kernels):
     """Spilled operands would be memory accesses that every step waits for."""
     for name, lines in kernels.items():
         assert not [x for x in lines if x.startswith("scratch_")], name
+
+
+def test_scores_are_stored_to_global_memory(kernels):
+    """A step's wait counts the loads behind a tile's stores in order, and its LDS reads apart from them. A flat access
+    is in neither's order; and of a tile's stores past the caches there are as many as the wait lets pass, 16 for each
+    row of a wave's tiles."""
+    for name, lines in kernels.items():
+        assert not [x for x in lines if x.startswith("flat_")], name
+        rows = int(re.search(r"k_scores_tilesI(?:f|DF16b)Li\d+ELi\d+ELi(\d+)E", name).group(1))
+        assert len([x for x in lines if re.match(r"global_store_\w+ .* nt$", x)]) == 16 * rows, name
