@@ -104,7 +104,9 @@ class GradClip:
     The tensors are checked, and their addresses kept, when the handle is made; it keeps them alive. A gradient that
     is replaced (``grad = None`` and a new one) needs a new handle. The norm (float32 [1], before clipping) and the
     workspace are the handle's own, written again by the next call: a handle is for one stream at a time, and a
-    captured graph needs one of its own. outs: where the clipped gradients go (default: in place).
+    captured graph needs one of its own, which is kept as long as it. The first call on another stream than the one
+    that was current when the handle was made waits for what that one has been given. outs: where the clipped
+    gradients go (default: in place).
     """
 
     def __init__(self, grads, outs=None):
@@ -114,8 +116,27 @@ class GradClip:
         self._t = _Tensors(grads, grads if outs is None else outs)
         self.norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
         self._ws = torch.empty(gs_clip_grads_workspace_size(len(grads)), dtype=torch.uint8, device=grads[0].device)
+        self._made = _stream(None, self._t.device)
+        self._tied = {self._made}
+
+    def _tie(self, stream):
+        """Makes the buffers, which are memory of the stream that was current when the handle was made, fit for use on
+        another: work that had them before is done first, and none gets them before this stream is through."""
+        device = self._t.device
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return  # a graph's calls run when it is replayed, with the handle kept beside it
+        made = torch.cuda.ExternalStream(self._made, device) if self._made else torch.cuda.default_stream(device)
+        stream.wait_stream(made)
+        for t in [self.norm, self._ws] + self._t.grads + self._t.outs:
+            t.record_stream(stream)
+        self._tied.add(stream.cuda_stream)
 
     def __call__(self, max_norm, stream=None):
+        if _stream(stream, self._t.device) not in self._tied:
+            self._tie(stream)
         self._t.call(max_norm, self.norm, self._ws, stream)
         return self.norm
 
@@ -124,4 +145,14 @@ def clip_grads(params, max_norm, stream=None):
     """Clips the gradients of the parameters (those that have one) in place by their global norm; returns it (float32
     [1], before clipping), or None if there is no gradient. max_norm infinite: only the norm."""
     grads = list({id(p): p.grad for p in params if p.grad is not None}.values())  # a parameter named twice counts once
-    return GradClip(grads)(max_norm, stream) if grads else None
+    if not grads:
+        return None
+    if stream is None:
+        return GradClip(grads)(max_norm)
+    # the handle is gone when this returns: its buffers are the stream's own, so that their next user comes after it
+    with torch.cuda.stream(stream):
+        norm = GradClip(grads)(max_norm)
+    norm.record_stream(torch.cuda.current_stream(norm.device))
+    for t in grads:
+        t.record_stream(stream)
+    return norm
