@@ -142,8 +142,11 @@ class GradClip:
 
 
 def clip_grads(params, max_norm, stream=None):
-    """Clips the gradients of the parameters (those that have one) in place by their global norm; returns it (float32
-    [1], before clipping), or None if there is no gradient. max_norm infinite: only the norm."""
+    """Clips the gradients of the parameters (those that have one; a single tensor is one parameter) in place by their
+    global norm; returns it (float32 [1], before clipping), or None if there is no gradient. max_norm infinite: only
+    the norm."""
+    if isinstance(params, torch.Tensor):
+        params = [params]
     grads = list({id(p): p.grad for p in params if p.grad is not None}.values())  # a parameter named twice counts once
     if not grads:
         return None
