@@ -144,7 +144,7 @@ class GradClip:
 def clip_grads(params, max_norm, stream=None):
     """Clips the gradients of the parameters (those that have one; a single tensor is one parameter) in place by their
     global norm; returns it (float32 [1], before clipping), or None if there is no gradient. max_norm infinite: only
-    the norm."""
+    the norm, the gradients stay as they are even where it is no number."""
     if isinstance(params, torch.Tensor):
         params = [params]
     grads = list({id(p): p.grad for p in params if p.grad is not None}.values())  # a parameter named twice counts once

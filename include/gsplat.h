@@ -763,11 +763,12 @@ gs_status gs_label_scores_q8(int64_t n, int32_t cols, int64_t vocab, int32_t dty
  * grads, outs, numels and dtypes are arrays on the HOST of one entry per tensor
  * (read before the call returns): device addresses of contiguous tensors, their
  * sizes, GS_F32 or GS_BF16. outs[i] is grads[i] (in place) or overlaps no gradient,
- * and no two of outs overlap; outs NULL: the norm only. At most 2^40 elements in all. max_norm >= 0 (infinite: nothing is clipped). The sum
- * is float64, in one order: the same bit for bit from run to run. The workspace is
- * 256-byte aligned. Where a gradient
- * is NaN so are all results; where one is infinite the norm is, the infinite ones
- * become NaN and the others 0.
+ * and no two of outs overlap; outs NULL: the norm only. At most 2^40 elements in
+ * all. max_norm >= 0. The sum is float64, in one order: the same bit for bit from
+ * run to run. The workspace is 256-byte aligned. With max_norm finite, where a
+ * gradient is NaN so are all results; where one is infinite the norm is, the
+ * infinite ones become NaN and the others 0. With max_norm infinite nothing is
+ * clipped: every out is its gradient as it is, whatever the norm.
  */
 size_t gs_clip_grads_workspace_size(int32_t tensors);
 gs_status gs_clip_grads(int32_t tensors, const void *const *grads, void *const *outs, const int64_t *numels,
