@@ -1376,7 +1376,7 @@ gs_status gs_rms_norm_fwd(int64_t n, int32_t dim, int32_t dtype, const void* x, 
 }
 
 size_t gs_rms_norm_bwd_workspace_size(int64_t n, int32_t dim, int32_t dtype) {
-    return rows_ok(n, dim, 1, dtype) ? gs::rms_bwd_workspace(n, dim) : 0;
+    return rows_ok(n, dim, 1, dtype) ? gs::rms_bwd_workspace(n, dim, dtype == GS_BF16) : 0;
 }
 
 gs_status gs_rms_norm_bwd(int64_t n, int32_t dim, int32_t dtype, const void* h, int64_t h_stride, const void* weight,

@@ -213,7 +213,7 @@ hipError_t launch_column_sums(bool half, int nblk, int width, int dim, const flo
                               hipStream_t stream);
 
 // Root-mean-square normalisation after a residual's addition, and rows in 8 bits (rmsnorm.hip).
-size_t rms_bwd_workspace(int64_t n, int dim);
+size_t rms_bwd_workspace(int64_t n, int dim, bool half);
 hipError_t launch_rms_fwd(int64_t n, int dim, bool half, const void* x, int64_t xs, const void* residual, int64_t rs,
                           const void* weight, float eps, void* sum, int64_t ss, void* y, int64_t ys, float* rstd,
                           hipStream_t stream);

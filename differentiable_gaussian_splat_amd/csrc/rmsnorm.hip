@@ -352,7 +352,14 @@ __global__ __launch_bounds__(NT) void k_rms_bwd(RmsArgs a) {
 
 enum RmsCall { RMS_FWD, RMS_BWD, RMS_Q8 };
 
-constexpr int RMS_BLOCKS_FWD = 2048, RMS_BLOCKS_BWD = 1024;  // of 256 threads; the latter are rows of the column sums
+// Of 256 threads, and as many fewer of more. The backward's are rows of the column sums.
+constexpr int RMS_BLOCKS_FWD = 2048, RMS_BLOCKS_BWD = 1024;
+template <int CALL>
+constexpr int rms_blocks(int threads) {
+    return (CALL == RMS_BWD ? RMS_BLOCKS_BWD : RMS_BLOCKS_FWD) * 256 / threads;
+}
+// The accesses of the longest rows that blocks of 256 threads take; 1024 threads take longer ones.
+constexpr int LONGEST_256 = 1024;
 
 // What a call reads and writes in all beyond which it goes past the caches, except for the sum, which the backward
 // reads next: nothing else of it would still be there for who comes next, but it would put the sum out. (What the
@@ -363,7 +370,7 @@ constexpr int64_t CACHED = (int64_t)256 << 20;
 template <class T, int CALL, int NT, int LPR, int EPL, bool FULL>
 hipError_t rms_rows(RmsArgs a, int& blocks, hipStream_t s) {
     const int64_t want = (a.n + NT / LPR - 1) / (NT / LPR);
-    const int cap = (CALL == RMS_BWD ? RMS_BLOCKS_BWD : RMS_BLOCKS_FWD) * 256 / NT;
+    const int cap = rms_blocks<CALL>(NT);
     blocks = (int)(want < cap ? want : cap);
     const int matrices = CALL == RMS_BWD ? 3 + (a.dsum != nullptr) : 2 + (a.residual ? 2 : 0);
     const bool past = FULL && CALL != RMS_Q8 && a.n * a.dim * (int64_t)sizeof(T) * matrices > CACHED;
@@ -398,7 +405,7 @@ hipError_t rms_pick(const RmsArgs& a, int& blocks, hipStream_t s) {
     if (v <= 128) return rms_rows<T, CALL, 256, 64, 2, FULL>(a, blocks, s);
     if (v <= 256) return rms_rows<T, CALL, 256, 64, 4, FULL>(a, blocks, s);
     if (v <= 512) return rms_rows<T, CALL, 256, 256, 2, FULL>(a, blocks, s);
-    if (v <= 1024) return rms_rows<T, CALL, 256, 256, 4, FULL>(a, blocks, s);
+    if (v <= LONGEST_256) return rms_rows<T, CALL, 256, 256, 4, FULL>(a, blocks, s);
     if (v <= 2048) return rms_rows<T, CALL, 1024, 1024, 2, FULL>(a, blocks, s);
     if (v <= 4096) return rms_rows<T, CALL, 1024, 1024, 4, FULL>(a, blocks, s);
     if (v <= 8192) return rms_rows<T, CALL, 1024, 1024, 8, FULL>(a, blocks, s);
@@ -417,8 +424,10 @@ hipError_t rms_launch(bool half, const RmsArgs& a, int& blocks, hipStream_t s) {
 
 }  // namespace
 
-size_t rms_bwd_workspace(int64_t n, int dim) {
-    const int64_t rows = n < RMS_BLOCKS_BWD ? n : RMS_BLOCKS_BWD;
+size_t rms_bwd_workspace(int64_t n, int dim, bool half) {
+    const int wide = half ? WIDE<bf16> : WIDE<float>;
+    const int64_t most = rms_blocks<RMS_BWD>((dim + wide - 1) / wide <= LONGEST_256 ? 256 : 1024);
+    const int64_t rows = n < most ? n : most;
     return ((size_t)rows * dim * sizeof(float) + 255) & ~(size_t)255;
 }
 

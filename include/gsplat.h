@@ -746,13 +746,13 @@ gs_status gs_rms_norm_q8(int64_t n, int32_t dim, int32_t dtype, const void *x, i
  * w[vocab, cols], both rows in 8 bits, rounded once to `dtype`. cols is a multiple
  * of 128. dtype is the type of the scores, and says how they are summed:
  *     GS_F32    every product is whole, and the sums are float32.
- *     GS_BF16   the matrix units' 8-bit products, two to three times as fast. Their sums are
- *               float32, but of eight columns beside each other (from a multiple of
- *               eight on) each product is first cut off at 2^-13 of the largest
- *               one's power of two, so that a score is off by at most 2^-10 of the
- *               sum of the eights' largest products. On normal data that is 1.4e-5
- *               of a score's size, where the rounding to bfloat16 is 2^-9 of the
- *               score; but of large products that cancel, small ones among the same
+ *     GS_BF16   the matrix units' 8-bit products, two to three times as fast. Their
+ *               sums are float32, but of eight columns beside each other (from a
+ *               multiple of eight on) each product is first cut off at 2^-13 of the
+ *               largest one's power of two, so that a score is off by at most 2^-10
+ *               of the sum of the eights' largest products. On normal data that is
+ *               1.4e-5 of a score's size, where the rounding to bfloat16 is up to
+ *               2^-8; but of large products that cancel, small ones among the same
  *               eight do not remain (448 * 448 - 448 * 448 + six of 1 * 1 gives 0).
  *               Who needs those takes GS_F32.
  * Which scores a row gets does not depend on the rows beside it except for the order
