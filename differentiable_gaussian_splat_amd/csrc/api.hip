@@ -1454,6 +1454,7 @@ gs_status gs_label_scores_q8(int64_t n, int32_t cols, int64_t vocab, int32_t dty
         TRY(check_rows8(fn, "q", q, q_stride, q_scales, q_scales_stride, n, cols, true));
         TRY(check_rows8(fn, "w", w, w_stride, w_scales, w_scales_stride, vocab, cols, true));
         TRY(check_matrix(fn, "out", out, out_stride, n, vocab, dtype, false, false));
+        REQUIRE(n * vocab <= (int64_t)1 << 40, "%s: more than 2^40 scores in all", fn);
         if (n == 0) return GS_OK;
         gs::ScoreArgs a{};
         a.n = n;

@@ -200,20 +200,10 @@ __global__ __launch_bounds__(64 * DIRECT_WAVES) void k_scores_direct(ScoreArgs a
 template <class T, int XT, int VT, int KS>
 hipError_t scores_direct(const ScoreArgs& a, hipStream_t s) {
     const int64_t per = 16 * VT * (DIRECT_WAVES / KS);
-    const int64_t bx = (a.vocab + per - 1) / per;
-    // a grid's second axis holds 65535 blocks
-    const int64_t most = (int64_t)65535 * 16 * XT;
-    for (int64_t r = 0; r < a.n; r += most) {
-        ScoreArgs p = a;
-        p.n = a.n - r < most ? a.n - r : most;
-        p.q += r * a.qs;
-        p.qscales += r * a.qss;
-        p.out = (T*)a.out + r * a.os;
-        const dim3 grid((unsigned)bx, (unsigned)((p.n + 16 * XT - 1) / (16 * XT)));
-        k_scores_direct<T, XT, VT, KS><<<grid, 64 * DIRECT_WAVES, 0, s>>>(p);
-        if (hipError_t e = hipGetLastError()) return e;
-    }
-    return hipSuccess;
+    // the rules of `scores` send no more than 12160 rows here: a grid's second axis holds 65535 blocks
+    const dim3 grid((unsigned)((a.vocab + per - 1) / per), (unsigned)((a.n + 16 * XT - 1) / (16 * XT)));
+    k_scores_direct<T, XT, VT, KS><<<grid, 64 * DIRECT_WAVES, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 // The depth is split over as many of a block's waves as it takes to have two to a SIMD, and as there are four blocks of
@@ -594,25 +584,15 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
 }
 
 template <class T, int WX, int WV, int XT, int VT, int STAGES>
-hipError_t scores_tiles(const ScoreArgs& a, hipStream_t s) {
+hipError_t scores_tiles(ScoreArgs a, hipStream_t s) {
     constexpr int BX = 32 * XT * WX, BV = 32 * VT * WV;
-    const int64_t tv = (a.vocab + BV - 1) / BV;
-    // as many rows at a time as 2^30 tiles hold
-    const int64_t most = ((int64_t)1 << 30) / tv * BX;
-    for (int64_t r = 0; r < a.n; r += most) {
-        ScoreArgs p = a;
-        p.n = a.n - r < most ? a.n - r : most;
-        p.q += r * a.qs;
-        p.qscales += r * a.qss;
-        p.out = (T*)a.out + r * a.os;
-        // rows of whole cache lines only: of others past the caches the lines' parts go to memory one by one
-        p.past = (uintptr_t)p.out % 128 == 0 && a.os * sizeof(T) % 128 == 0;
-        const int64_t tx = (p.n + BX - 1) / BX, blocks = 256 * (8 / (WX * WV));
-        const int64_t grid = tx * tv < blocks ? (tx * tv + 7) / 8 * 8 : blocks;
-        k_scores_tiles<T, WX, WV, XT, VT, STAGES><<<(unsigned)grid, 64 * WX * WV, 0, s>>>(p, (int)tx, (int)tv);
-        if (hipError_t e = hipGetLastError()) return e;
-    }
-    return hipSuccess;
+    // rows of whole cache lines only: of others past the caches the lines' parts go to memory one by one
+    a.past = (uintptr_t)a.out % 128 == 0 && a.os * sizeof(T) % 128 == 0;
+    // at most 2^27 tiles: there are at most 2^40 scores
+    const int64_t tx = (a.n + BX - 1) / BX, tv = (a.vocab + BV - 1) / BV, blocks = 256 * (8 / (WX * WV));
+    const int64_t grid = tx * tv < blocks ? (tx * tv + 7) / 8 * 8 : blocks;
+    k_scores_tiles<T, WX, WV, XT, VT, STAGES><<<(unsigned)grid, 64 * WX * WV, 0, s>>>(a, (int)tx, (int)tv);
+    return hipGetLastError();
 }
 
 // Which way a product takes. Straight to registers where there are few rows, or too few tiles for the units; through

@@ -744,7 +744,8 @@ gs_status gs_rms_norm_q8(int64_t n, int32_t dim, int32_t dtype, const void *x, i
 /*
  * gs_label_scores_q8 -- out[i][v] = the product of row i of q[n, cols] with row v of
  * w[vocab, cols], both rows in 8 bits, rounded once to `dtype`. cols is a multiple
- * of 128. dtype is the type of the scores, and says how they are summed:
+ * of 128; n * vocab is at most 2^40. dtype is the type of the scores, and says how
+ * they are summed:
  *     GS_F32    every product is whole, and the sums are float32.
  *     GS_BF16   the matrix units' 8-bit products, two to three times as fast. Their
  *               sums are float32, but of eight columns beside each other (from a
