@@ -620,9 +620,12 @@ class ResidualLabelHead(torch.nn.Module):
         h, rows, last = None, None, len(codes) - 1
         for k, code in enumerate(codes):
             x = embed(self.codebooks[k], code, self.scales[k])
-            if k == last:
-                rows = rms_norm_q8(x, self.weights[k], h, self.eps)
-                rows = rows if h is None else rows[0]
-            else:
-                h = x if h is None else h + x
+            if k == 0 < last:
+                h = x
+                continue
+            # the norm's kernel adds; a stage before the last is there for its sum, and its rows are overwritten
+            rows = rows_q8(*x.shape, x.device) if rows is None else rows
+            total = torch.empty_like(x) if k < last else None
+            gs_rms_norm_q8(x, self.weights[k].contiguous(), *rows, h, total, self.eps)
+            h = total
         return label_scores(rows, self.vocabulary_q8() if vocabulary is None else vocabulary, dtype)
