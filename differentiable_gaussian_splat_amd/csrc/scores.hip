@@ -10,8 +10,11 @@
 //             score's size on normal data: nothing beside the result's own rounding.
 //             Of large products that cancel, small ones among the same eight are lost:
 //             a choice for two to three times the rate, which the caller makes with the type.
-//   float32   the operands widened to bfloat16 with their scale, which is exact, and
-//             bfloat16 products, at less than a third of the rate: 1.4e-8 to 2e-7.
+//   float32   the operands widened to bfloat16 with their scale, and bfloat16
+//             products, at less than a third of the rate: 1.4e-8 to 2e-7. The widening
+//             is exact for scales of 2^-111 to 2^112. A wave that meets others takes
+//             the 8-bit products for them, one of each eight columns at a time: there
+//             is nothing beside it then that a product could be cut off by.
 #include <type_traits>
 
 #include "launch.hpp"
@@ -88,6 +91,25 @@ __device__ __forceinline__ bf16x8 widen8(const i32x8& q, int s, float scale) {
     return v;
 }
 
+// Whether one of a lane's four scales, of `used` blocks of columns, is too far from 1 for widen8. With a byte of 16 to
+// 239 the least value times its scale (2^-9 2^-111) and the greatest (448 2^112) are normal bfloat16 numbers.
+__device__ __forceinline__ bool far_scales(int four, int used) {
+    const uint32_t in = used >= 4 ? ~0u : (1u << (8 * used)) - 1;
+    const uint32_t s = ((uint32_t)four & in) | (0x7f7f7f7fu & ~in);
+    // a byte's upper half is 0 or 15: one more, it is 0 but for its lowest bit (and the 16)
+    const uint32_t near = (((s >> 4) & 0x0f0f0f0fu) + 0x01010101u) & 0x0e0e0e0eu;
+    return (near - 0x01010101u) & 0x80808080u;
+}
+
+// Of a lane's values those in place m of each eight, zeros in the others' places.
+__device__ __forceinline__ i32x8 one_of_eight(const i32x8& q, int m) {
+    const int byte = 0xff << (8 * (m & 3)), even = m < 4 ? byte : 0, odd = m < 4 ? 0 : byte;
+    i32x8 v;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = q[k] & (k % 2 ? odd : even);
+    return v;
+}
+
 constexpr int DIRECT_WAVES = 8;  // of a block
 
 // Straight from memory to registers: a wave takes 16 XT feature rows and 16 VT vocabulary rows over its share of the
@@ -127,6 +149,7 @@ __global__ __launch_bounds__(64 * DIRECT_WAVES) void k_scores_direct(ScoreArgs a
         for (int i = 0; i < XT; ++i) sx[i] = *reinterpret_cast<const int*>(xs[i] + 4 * f);
 #pragma unroll
         for (int j = 0; j < VT; ++j) sv[j] = *reinterpret_cast<const int*>(vs[j] + 4 * f);
+        bool far = false;  // float32: whether a scale is, of this wave's and these four blocks
         auto block = [&](auto which) {
             constexpr int B = decltype(which)::value;
             if (4 * f + B >= blocks) return;
@@ -136,14 +159,34 @@ __global__ __launch_bounds__(64 * DIRECT_WAVES) void k_scores_direct(ScoreArgs a
             for (int i = 0; i < XT; ++i) fx[i] = block_of(xp[i] + at);
 #pragma unroll
             for (int j = 0; j < VT; ++j) fv[j] = block_of(vp[j] + at);
+            auto product = [&](const i32x8& x, int i, int j) {
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fv[j], x, acc[i][j], 0, 0, B, sv[j], B,
+                                                                           sx[i]);
+            };
             if constexpr (sizeof(T) == 2) {
 #pragma unroll
                 for (int i = 0; i < XT; ++i)
 #pragma unroll
-                    for (int j = 0; j < VT; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fv[j], fx[i], acc[i][j], 0, 0, B,
-                                                                                   sv[j], B, sx[i]);
+                    for (int j = 0; j < VT; ++j) product(fx[i], i, j);
             } else {
+                if (B == 0) {  // behind the first block's loads, which do not wait for it
+#pragma unroll
+                    for (int i = 0; i < XT; ++i) far |= far_scales(sx[i], blocks - 4 * f);
+#pragma unroll
+                    for (int j = 0; j < VT; ++j) far |= far_scales(sv[j], blocks - 4 * f);
+                    far = __ballot(far) != 0;
+                }
+                if (far) {
+#pragma unroll 1
+                    for (int m = 0; m < 8; ++m)
+#pragma unroll
+                        for (int i = 0; i < XT; ++i) {
+                            const i32x8 one = one_of_eight(fx[i], m);
+#pragma unroll
+                            for (int j = 0; j < VT; ++j) product(one, i, j);
+                        }
+                    return;
+                }
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     bf16x8 hx[XT], hv[VT];
@@ -287,6 +330,45 @@ __device__ __forceinline__ void settle(i32x4& a, i32x4& b) { asm volatile("s_nop
 template <int LEFT>
 __device__ __forceinline__ void step_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+
+// A wave's part of a tile in which a scale is far from 1, again from memory, by one of eight columns at a time: feature
+// rows from x0 on, 32 rows of them each, against the rows of the vocabulary's tile at v0 that stand from s0 on. 32 x 32
+// scores at a time, which need few registers: next to the tile's next operands there are no more. (Every tile so: 8192 x
+// 1024 x 8192 833 us, 5003 x 256 x 8191 127, where the scales are near 129 and 38; straight from memory 5 to 15 % more.)
+template <int VT, class Args>
+__device__ __forceinline__ void far_tile(const Args& a, int x0, int rows, int v0, int s0) {
+    const int l = threadIdx.x & 63;
+    const int cols = a.cols;
+#pragma unroll 1
+    for (int t = 0; t < rows * VT; ++t) {
+        const int x = x0 + t / VT * 32, v = v0 + vocab_row<VT>(s0 + t % VT * 32 + l % 32);
+        const int64_t xr = min(x + l % 32, (int)a.n - 1), vr = min(v, (int)a.vocab - 1);
+        const uint8_t *q = a.q + xr * a.qs + l / 32 * 32, *w = a.w + vr * a.ws + l / 32 * 32;
+        const uint8_t *qs = a.qscales + xr * a.qss, *ws = a.wscales + vr * a.wss;
+        f32x16 c;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) c[e] = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < cols; k += STEP) {
+            const auto at = [&](const uint8_t* p) {
+                const i32x4 lo = *reinterpret_cast<const i32x4*>(p + k), hi = *reinterpret_cast<const i32x4*>(p + k + 16);
+                return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            };
+            const i32x8 fx = at(q), fv = at(w);
+            const int sx = qs[k / Q8_BLOCK], sv = ws[k / Q8_BLOCK];
+#pragma unroll 1
+            for (int m = 0; m < 8; ++m)
+                c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(one_of_eight(fx, m), fv, c, 0, 0, 0, sx, 0, sv);
+        }
+        if (v < a.vocab) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int r = x + 4 * (l / 32) + 8 * (e / 4) + e % 4;
+                if (r < a.n) ((scores_at<float>)a.out)[r * a.os + v] = c[e];
+            }
+        }
+    }
 }
 
 // Tiles of 32 XT WX feature rows and 32 VT WV vocabulary rows by WX x WV waves. Blocks stay: each goes through its
@@ -484,6 +566,7 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
     clear();
     int four = 0;        // the place of the four blocks' scales
     bool quiet = false;  // whether a whole tile's stores may still be under way
+    bool far = false;    // float32: whether a scale of this lane's rows of the tile is
     // a block of columns: two steps
     auto block = [&](int kb, auto stores) {
         if ((kb & 3) == 0) {
@@ -493,6 +576,12 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
 #pragma unroll
             for (int j = 0; j < VT; ++j) sv[j] = at[wv + 32 * j + l % 32];
             four = (four + 1) & 3;
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < XT; ++i) far |= far_scales(sx[i], nk / 2 - kb);
+#pragma unroll
+                for (int j = 0; j < VT; ++j) far |= far_scales(sv[j], nk / 2 - kb);
+            }
         }
         // whichever of the block's two loads begins a tile or four blocks is prepared here, so that nothing branches
         // between the steps
@@ -573,11 +662,16 @@ __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(Sc
                     asm volatile("" : "+v"(out), "+v"(rows));
                 }
         };
-        if (whole && p->past)
-            store(std::true_type{});
-        else
-            store(std::false_type{});
-        quiet = LET && whole;
+        if (sizeof(T) == 4 && __ballot(far)) {
+            far_tile<VT>(*p, x0 + wx, XT, v0, wv - BX);
+            quiet = far = false;
+        } else {
+            if (whole && p->past)
+                store(std::true_type{});
+            else
+                store(std::false_type{});
+            quiet = LET && whole;
+        }
         clear();
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last step
