@@ -1493,8 +1493,8 @@ gs_status gs_clip_grads(int32_t tensors, const void* const* grads, void* const* 
         REQUIRE(tensors == 0 || (grads && numels && dtypes), "%s: grads, numels and dtypes must not be NULL", fn);
         int64_t all = 0;
         for (int i = 0; i < tensors; ++i) {
-            REQUIRE(numels[i] >= 0 && numels[i] <= (int64_t)1 << 40, "%s: tensor %d's size must be in [0, 2^40], got %lld",
-                    fn, i, (long long)numels[i]);
+            REQUIRE(numels[i] >= 0 && numels[i] <= (int64_t)1 << 40,
+                    "%s: tensor %d's size must be in [0, 2^40], got %lld", fn, i, (long long)numels[i]);
             if (dtypes[i] != GS_F32 && dtypes[i] != GS_BF16)
                 return fail(GS_ERR_UNSUPPORTED, "%s: tensor %d's dtype must be GS_F32 or GS_BF16, got %d", fn, i,
                             dtypes[i]);

@@ -144,8 +144,8 @@ __device__ __forceinline__ void scale(const ClipTensor& e, uint32_t chunk, bool 
         chunk_scale<false>(g, o, left, c);
 }
 
-// What the gradients are multiplied by: no number where the norm is none; 1 whatever the norm where max_norm is infinite,
-// which asks for the norm alone.
+// What the gradients are multiplied by: no number where the norm is none; 1 whatever the norm where max_norm is
+// infinite, which asks for the norm alone.
 __device__ __forceinline__ float factor(float max_norm, double norm) {
     const double f = (double)max_norm / (norm + 1e-6);
     return f >= 1. || max_norm == INFINITY ? 1.f : (float)f;

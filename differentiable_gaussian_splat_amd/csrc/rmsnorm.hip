@@ -14,13 +14,14 @@
 // in a fixed order (norm.hip); a single block writes dw itself (64 x 6 float32 with
 // gradients 14 us, 19 with the second launch).
 //
-// 1M x 64 float32 with residual and gradients 332 us (1.79 GB read or written once:
-// 5.4 TB/s; a large copy has 4.8); 32771 rows of 771 bfloat16 in a wider matrix 87
-// (4.1 TB/s: forward 41, backward 41, column sums 5; where the backward loaded the
-// sum's gradient behind its row's sum it took 66). 65536 x 1024 bfloat16 with
-// residual into 8 bits 92 (5.1 TB/s), the rows as they are 36 (5.6). Short rows share
-// a wave: 636224 x 13 float32 into 8 bits 22 us, 31 with residual and norm; with a
-// row to the 32 lanes of a block of columns 250 and 88.
+// With inputs that change from call to call: 1M x 64 float32 with residual and
+// gradients 333 us (1.79 GB read or written once: 5.4 TB/s; a large copy has 4.8);
+// 32771 rows of 771 bfloat16 in a wider matrix 87 (4.1 TB/s: forward 40, backward 39,
+// column sums 5; where the backward loaded the sum's gradient behind its row's sum it
+// took 66). 65536 x 1024 bfloat16 with residual into 8 bits 93 (5.1 TB/s), the rows as
+// they are 42 (4.8). Short rows share a wave: 636224 x 13 float32 into 8 bits 24 us, 40
+// with residual and norm (on one set of buffers 22 and 31; with a row to the 32 lanes of
+// a block of columns 250 and 88).
 #include "elem.hpp"
 #include "launch.hpp"
 #include "rows8.hpp"
@@ -87,7 +88,7 @@ struct RmsArgs {
     int64_t dxs;
     float* part;    // [blocks][dim]: the blocks' column sums
     void* dweight;  // they themselves, of one block
-    bool plain;   // into 8 bits without the norm
+    bool plain;     // into 8 bits without the norm
 };
 
 // Stores a wave's 64 / LPR rows of a block or less in 8 bits, of which a lane has VEC columns: 16 bytes to a lane, side
@@ -473,7 +474,8 @@ hipError_t launch_rms_bwd(int64_t n, int dim, bool half, const void* h, int64_t 
     int blocks = 0;
     if (n > 0 && (dx || dweight))
         if (hipError_t e = rms_launch<RMS_BWD>(half, a, blocks, stream)) return e;
-    return dweight && blocks != 1 ? launch_column_sums(half, blocks, dim, dim, part, dweight, nullptr, stream) : hipSuccess;
+    if (!dweight || blocks == 1) return hipSuccess;
+    return launch_column_sums(half, blocks, dim, dim, part, dweight, nullptr, stream);
 }
 
 hipError_t launch_rms_q8(int64_t n, int dim, bool half, const void* x, int64_t xs, const void* residual, int64_t rs,

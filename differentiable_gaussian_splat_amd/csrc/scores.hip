@@ -9,7 +9,7 @@
 //             (seen by products of single powers of two), which leaves 1.4e-5 of a
 //             score's size on normal data: nothing beside the result's own rounding.
 //             Of large products that cancel, small ones among the same eight are lost:
-//             a choice for two to three times the rate, which the caller makes with the type.
+//             a choice for up to 1.8 times the speed, which the caller makes with the type.
 //   float32   the operands widened to bfloat16 with their scale, and bfloat16
 //             products, at less than a third of the rate: 1.4e-8 to 2e-7. The widening
 //             is exact for scales of 2^-111 to 2^112. A wave that meets others takes
@@ -282,8 +282,8 @@ __device__ __forceinline__ int vocab_row(int s) {
     return s / (32 * VT) * (32 * VT) + s % 32 * VT + s / 32 % VT;
 }
 
-// Where a tile's scores go, said to be global memory: through a pointer of any memory they would be flat accesses, which
-// LDS waits count too, and which end in no said order with the loads beside them.
+// Where a tile's scores go, said to be global memory: through a pointer of any memory they would be flat accesses,
+// which LDS waits count too, and which end in no said order with the loads beside them.
 template <class T>
 using scores_at = T __attribute__((address_space(1)))*;
 
@@ -334,8 +334,8 @@ __device__ __forceinline__ void step_barrier() {
 
 // A wave's part of a tile in which a scale is far from 1, again from memory, by one of eight columns at a time: feature
 // rows from x0 on, 32 rows of them each, against the rows of the vocabulary's tile at v0 that stand from s0 on. 32 x 32
-// scores at a time, which need few registers: next to the tile's next operands there are no more. (Every tile so: 8192 x
-// 1024 x 8192 833 us, 5003 x 256 x 8191 127, where the scales are near 129 and 38; straight from memory 5 to 15 % more.)
+// scores at a time, which need few registers: next to the tile's next operands there are no more. (Every tile so:
+// 8192 x 1024 x 8192 833 us, with near scales 129; 5003 x 256 x 8191 127, 38. Straight from memory 5 to 15 % more.)
 template <int VT, class Args>
 __device__ __forceinline__ void far_tile(const Args& a, int x0, int rows, int v0, int s0) {
     const int l = threadIdx.x & 63;
@@ -352,7 +352,8 @@ __device__ __forceinline__ void far_tile(const Args& a, int x0, int rows, int v0
 #pragma unroll 1
         for (int k = 0; k < cols; k += STEP) {
             const auto at = [&](const uint8_t* p) {
-                const i32x4 lo = *reinterpret_cast<const i32x4*>(p + k), hi = *reinterpret_cast<const i32x4*>(p + k + 16);
+                const i32x4 lo = *reinterpret_cast<const i32x4*>(p + k);
+                const i32x4 hi = *reinterpret_cast<const i32x4*>(p + k + 16);
                 return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
             };
             const i32x8 fx = at(q), fv = at(w);
@@ -382,12 +383,12 @@ __device__ __forceinline__ void far_tile(const Args& a, int x0, int rows, int v0
 // let pass. (The scales' loads, one to four blocks of columns, are counted with nothing: a wait is then for a little
 // more, never for less.)
 //
-// 8192 x 8192 x 8192 bfloat16 430 to 490 us (2.3 to 2.55 PFLOP/s): the units are busy 72 % of the cycles, at 1.7 GHz
+// 8192 x 8192 x 8192 bfloat16 430 to 455 us (2.4 to 2.55 PFLOP/s): the units are busy 73 % of the cycles, at 1.7 GHz
 // of 2.4: it is power that bounds them (products alone, from registers, reach 3.8). LDS is read without bank
 // conflicts. With the step's reads and loads all behind its barrier 524; with a descriptor formed for each load
 // 30 % more. Four waves of 128 x 128 with a third less to read from LDS 458 where eight had 441.
-// 8192 x 1024 x 65536 bfloat16 540 to 650 us: a gigabyte of scores beside it, which alone takes 225. The stores stand
-// in the same queue as the loads and hold them up (units busy 56 %); past the caches they take 90 us less than
+// 8192 x 1024 x 65536 bfloat16 530 to 625 us: a gigabyte of scores beside it, which alone takes 225. The stores stand
+// in the same queue as the loads and hold them up (units busy 59 %); past the caches they take 90 us less than
 // through them. Blocks that start a part of a tile's time apart gain 3 % of it, and lose 10 % where tiles are deep.
 template <class T, int WX, int WV, int XT, int VT, int STAGES>
 __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(ScoreArgs a, int tiles_x, int tiles_v) {
@@ -691,20 +692,20 @@ hipError_t scores_tiles(ScoreArgs a, hipStream_t s) {
 
 // Which way a product takes. Straight to registers where there are few rows, or too few tiles for the units; through
 // LDS otherwise. us, straight and by tiles of 128 x 128 (float32 in brackets):
-//   4 x 1024 x 65536     13, 14 (13, 18)        16 x 1024 x 65536   17, 15 (17, 18)
-//   16 x 1024 x 8192     7, 8 (7, 12)           32 x 1024 x 65536   18, 15 (18.5, 19.5)
-//   64 x 1024 x 65536    32, 16 (34, 21)        300 x 1024 x 300    10, 9 (10, 13)
-//   1024 x 1024 x 1024   10, 8 (11, 12)         1280 x 6528 x 576   42, 32 (43, 50)
-//   512 x 8192 x 1000    28, 33 (29, 59)        2048 x 4096 x 512   27, 16 (29, 33)
-//   4000 x 512 x 400     10, 8 (11, 11)         128 x 65536 x 128   125, 211 (126, 431)
+//   4 x 1024 x 65536     13, 14.5 (13, 17.5)    16 x 1024 x 65536   17, 15 (17, 18)
+//   16 x 1024 x 8192     8, 8 (8, 12)           32 x 1024 x 65536   18, 15 (18.7, 19.1)
+//   64 x 1024 x 65536    32, 16.5 (34, 21)      300 x 1024 x 300    10, 9 (10, 12.5)
+//   1024 x 1024 x 1024   10, 8 (11, 11)         1280 x 6528 x 576   39, 31 (42, 48)
+//   512 x 8192 x 1000    28, 32 (29, 58)        2048 x 4096 x 512   27, 18 (29, 30.5)
+//   4000 x 512 x 400     10, 8 (11, 10)         128 x 65536 x 128   126, 214 (127, 412)
 // Straight, 64 x 32 to a wave reads a quarter less than 32 x 32, and fills the units where the depth can be split over
-// eight waves: 512 x 8192 x 1000 28, with 32 x 32 34; 1024 x 1024 x 1024 14, 10.
+// eight waves: 512 x 8192 x 1000 27, with 32 x 32 34; 512 x 2048 x 1000 15, 11.
 // Tiles of 256 x 256 have the operands' bytes from LDS for half the products of 128 x 128; with few columns to a tile
 // two blocks to a unit hide each other's stores: 256 x 256 and two blocks of 128 x 256, 8192 x 256 x 65536 282, 242;
-// x 384 331, 292; x 512 353, 353; x 1024 650, 769; 8192 x 8192 x 8192 493, 621 (128 x 128 702).
+// x 384 323, 294; x 512 349, 352; x 1024 547, 605; 8192 x 8192 x 8192 438, 533 (128 x 128 633).
 // In float32, where the products take four times as long, 256 x 256 gains little and loses where rounds are not full:
-// 128 x 128 and 256 x 256, 8192 x 8192 x 8192 998, 889; 16384 x 512 x 16384 327, 301; 3000 x 4096 x 5000 116, 105;
-// 5000 x 2048 x 5000 103, 108; 45414 x 1280 x 550 71, 101; 5003 x 256 x 8192 36, 44.
+// 128 x 128 and 256 x 256, 8192 x 8192 x 8192 920, 797; 16384 x 512 x 16384 327, 287; 3000 x 4096 x 5000 116, 102;
+// 8192 x 1024 x 65536 1084, 942; 5000 x 2048 x 5000 100, 101; 45414 x 1280 x 550 75, 100; 5003 x 256 x 8192 37, 43.
 template <class T>
 hipError_t scores(const ScoreArgs& a, hipStream_t s) {
     auto tiles = [&](int64_t bx, int64_t bv) { return ((a.n + bx - 1) / bx) * ((a.vocab + bv - 1) / bv); };

@@ -3,8 +3,10 @@
 :func:`clip_grads` clips a list of gradients (a scene's, as
 :func:`.raster.gs_adam_step` takes them, or a label head's) in one call;
 :class:`GradClip` keeps the addresses of gradients that stay in their buffers
-from step to step. Both run two kernels over all tensors together, float32 and
-bfloat16 side by side, and neither waits for the device.
+from step to step. Both take all tensors together, float32 and bfloat16 side by
+side, and neither waits for the device: one kernel for a small call (up to 64
+tensors, 64 KB), else one for the norm and one for the scaling, and for more than
+160 tensors one more for each 160, which puts their addresses into the workspace.
 """
 from __future__ import annotations
 

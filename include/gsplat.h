@@ -701,8 +701,9 @@ gs_status gs_label_loss_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype
  * x, y[n, dim]; residual[n, dim], weight[dim] nullable (nothing added, 1); eps >= 0.
  * sum[n, dim] (nullable, only with a residual) receives h, to be handed on and
  * kept for the backward; rstd[n] is nullable. A row of zeros with eps = 0 gives
- * no numbers, as the formula does; one whose squares add up beyond float32 (values
- * of 1e19) gives zeros.
+ * no numbers, as the formula does. The squares are float32: a row whose squares add
+ * up beyond it (values of 1e19) gives zeros, and with eps = 0 one whose squares it
+ * does not hold (values of 1e-23 and less) infinities or no numbers.
  */
 gs_status gs_rms_norm_fwd(int64_t n, int32_t dim, int32_t dtype, const void *x, int64_t x_stride,
                           const void *residual, int64_t residual_stride, const void *weight, float eps, void *sum,
@@ -724,11 +725,12 @@ gs_status gs_rms_norm_bwd(int64_t n, int32_t dim, int32_t dtype, const void *h, 
  * with 4 exponent and 3 mantissa bits, largest value 448, without infinities),
  * cols = dim rounded up to a multiple of 128, zero from dim on, and one scale for
  * each 128 of them, a power of two held as its exponent plus 127 in a byte (1 to
- * 254; what a product gives for other bytes is not said). The scales of a row are padded to a multiple of four bytes (with 127). The scale of
- * a block is the least 2^e with max |v| <= 448 2^e over its finite values, e >=
- * -126 (1 where all are 0); a value is v / 2^e, to nearest even. Infinite values
- * and NaN become NaN. Rows of values are 16-byte aligned, rows of scales 4-byte
- * aligned, either's stride at most 2^22 bytes.
+ * 254; what a product gives for other bytes is not said). The scales of a row are
+ * padded to a multiple of four bytes (with 127). The scale of a block is the least
+ * 2^e with max |v| <= 448 2^e over its finite values, e >= -126 (1 where all are 0);
+ * a value is v / 2^e, to nearest even. Infinite values and NaN become NaN. Rows of
+ * values are 16-byte aligned, rows of scales 4-byte aligned, either's stride at most
+ * 2^22 bytes.
  *
  * gs_quantize_q8 -- x[n, dim] as rows in 8 bits: q[n, cols], scales[n, groups].
  * gs_rms_norm_q8 -- gs_rms_norm_fwd with y as rows in 8 bits (of y before any
@@ -747,7 +749,7 @@ gs_status gs_rms_norm_q8(int64_t n, int32_t dim, int32_t dtype, const void *x, i
  * of 128; n * vocab is at most 2^40. dtype is the type of the scores, and says how
  * they are summed:
  *     GS_F32    every product is whole, and the sums are float32.
- *     GS_BF16   the matrix units' 8-bit products, two to three times as fast. Their
+ *     GS_BF16   the matrix units' 8-bit products, up to 1.8 times as fast. Their
  *               sums are float32, but of eight columns beside each other (from a
  *               multiple of eight on) each product is first cut off at 2^-13 of the
  *               largest one's power of two, so that a score is off by at most 2^-10
