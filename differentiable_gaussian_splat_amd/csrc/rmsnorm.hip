@@ -142,7 +142,6 @@ __global__ __launch_bounds__(NT) void k_rms_fwd(RmsArgs a) {
         const int64_t r = r0 + threadIdx.x / LPR;
         const bool live = r < a.n;  // a row past the end is computed from zeros and not stored
         wide_t<T> raw[EPL];
-        float sq = 0.f;
 #pragma unroll
         for (int e = 0; e < EPL; ++e) {
             const int c = (e * LPR + l) * VEC;
@@ -164,17 +163,34 @@ __global__ __launch_bounds__(NT) void k_rms_fwd(RmsArgs a) {
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) raw[e][k] = (T)((float)raw[e][k] + (float)more[e][k]);
         }
+        auto squares = [&](float by) {
+            float sq = 0.f;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) {
-            const int left = dim - (e * LPR + l) * VEC;
-            float v[VEC];
-            widen<FULL, T>(raw[e], left, v);
+            for (int e = 0; e < EPL; ++e) {
+                const int left = dim - (e * LPR + l) * VEC;
+                float v[VEC];
+                widen<FULL, T>(raw[e], left, v);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) sq = (FULL ? left > 0 : k < left) ? fmaf(v[k], v[k], sq) : sq;
+                for (int k = 0; k < VEC; ++k) {
+                    v[k] *= by;
+                    sq = (FULL ? left > 0 : k < left) ? fmaf(v[k], v[k], sq) : sq;
+                }
+            }
+            return rms_row_sum<NT, LPR>(sq, s_red);
+        };
+        // A row whose squares float32 does not hold (values of 1e18 and more, or with an eps below 1e-24 of 1e-12 and
+        // less) is summed again times a power of two, from its registers. All lanes of a row go the same way. (Of rows
+        // as they are nothing is asked.)
+        float by = 1.f, root = 1.f;
+        if (!(Q8 && a.plain)) {
+            float sum = squares(1.f);
+            if (sum > 0x1p120f || (sum < 0x1p-80f && a.eps < 0x1p-80f)) {
+                by = sum > 1.f ? 0x1p-80f : 0x1p100f;
+                sum = squares(by);
+            }
+            root = 1.0f / sqrtf(sum / (float)dim + a.eps * by * by);
         }
-        // of rows as they are nothing is asked
-        const float rstd = Q8 && a.plain ? 1.f : 1.0f / sqrtf(rms_row_sum<NT, LPR>(sq, s_red) / (float)dim + a.eps);
-        if (a.rstd && live && l == 0) a.rstd[r] = rstd;
+        if (a.rstd && live && l == 0) a.rstd[r] = root * by;
 #pragma unroll
         for (int e = 0; e < EPL; ++e) {
             const int c = (e * LPR + l) * VEC, left = dim - c;
@@ -182,7 +198,7 @@ __global__ __launch_bounds__(NT) void k_rms_fwd(RmsArgs a) {
             widen<FULL, T>(raw[e], left, v);
             if (a.sum && live && left > 0) store_row<FULL>((T*)a.sum + r * a.ss + c, left, v);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) v[k] *= rstd;
+            for (int k = 0; k < VEC; ++k) v[k] = v[k] * by * root;
             if (weight) {
                 float f[VEC];
                 wide_t<T> wr = (T)0.f;

@@ -701,9 +701,9 @@ gs_status gs_label_loss_bwd(int64_t n, int32_t dim, int64_t vocab, int32_t dtype
  * x, y[n, dim]; residual[n, dim], weight[dim] nullable (nothing added, 1); eps >= 0.
  * sum[n, dim] (nullable, only with a residual) receives h, to be handed on and
  * kept for the backward; rstd[n] is nullable. A row of zeros with eps = 0 gives
- * no numbers, as the formula does. The squares are float32: a row whose squares add
- * up beyond it (values of 1e19) gives zeros, and with eps = 0 one whose squares it
- * does not hold (values of 1e-23 and less) infinities or no numbers.
+ * no numbers, as the formula does. Rows of any other size are normalised, those whose
+ * squares float32 does not hold too; rstd of a mean square below 2^-256 is infinite
+ * (the backward of such a row gives no numbers).
  */
 gs_status gs_rms_norm_fwd(int64_t n, int32_t dim, int32_t dtype, const void *x, int64_t x_stride,
                           const void *residual, int64_t residual_stride, const void *weight, float eps, void *sum,
