@@ -388,8 +388,9 @@ __device__ __forceinline__ void far_tile(const Args& a, int x0, int rows, int v0
 // conflicts. With the step's reads and loads all behind its barrier 524; with a descriptor formed for each load
 // 30 % more. Four waves of 128 x 128 with a third less to read from LDS 458 where eight had 441.
 // 8192 x 1024 x 65536 bfloat16 530 to 625 us: a gigabyte of scores beside it, which alone takes 225. The stores stand
-// in the same queue as the loads and hold them up (units busy 59 %); past the caches they take 90 us less than
-// through them. Blocks that start a part of a tile's time apart gain 3 % of it, and lose 10 % where tiles are deep.
+// in the same queue as the loads and hold them up (units busy 49 to 59 % of the cycles, at 1.9 to 1.4 GHz); past the
+// caches they take 90 us less than through them. Blocks that start a part of a tile's time apart gain 3 % of it, and
+// lose 10 % where tiles are deep.
 template <class T, int WX, int WV, int XT, int VT, int STAGES>
 __global__ __launch_bounds__(64 * WX * WV, 8 / (WX * WV)) void k_scores_tiles(ScoreArgs a, int tiles_x, int tiles_v) {
     constexpr int NW = WX * WV, BX = 32 * XT * WX, BV = 32 * VT * WV, ROWS = BX + BV;
