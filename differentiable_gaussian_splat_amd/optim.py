@@ -146,7 +146,8 @@ class GradClip:
 def clip_grads(params, max_norm, stream=None):
     """Clips the gradients of the parameters (those that have one; a single tensor is one parameter) in place by their
     global norm; returns it (float32 [1], before clipping), or None if there is no gradient. max_norm infinite: only
-    the norm, the gradients stay as they are even where it is no number."""
+    the norm, the gradients stay as they are even where it is no number. stream: where this runs (default: the current
+    one); its order with what writes and reads the gradients is the caller's."""
     if isinstance(params, torch.Tensor):
         params = [params]
     grads = list({id(p): p.grad for p in params if p.grad is not None}.values())  # a parameter named twice counts once
@@ -156,7 +157,7 @@ def clip_grads(params, max_norm, stream=None):
         return GradClip(grads)(max_norm)
     # the handle is gone when this returns: its buffers are the stream's own, so that their next user comes after it
     with torch.cuda.stream(stream):
-        norm = GradClip(grads)(max_norm)
+        norm = GradClip(grads)(max_norm, stream)  # named, so that another device's is refused
     norm.record_stream(torch.cuda.current_stream(norm.device))
     for t in grads:
         t.record_stream(stream)

@@ -112,3 +112,11 @@ def test_a_captured_call_waits_for_nothing(gpu):
     gpu["capturing"] = False
     clip(1.0, side)
     assert side.waited == [0]
+
+
+def test_a_named_stream_is_the_one_that_is_called(gpu, monkeypatch):
+    """A stream of another device is not the current one of the gradients' device, whatever context it is in: it goes to
+    the call, which refuses it, and nothing runs on that device's own stream instead."""
+    monkeypatch.setattr(O, "_stream", lambda s, _: 0 if s is None else s.cuda_stream)
+    O.clip_grads([Parameter()], 1.0, stream=Stream(7))
+    assert [c[2] for c in gpu["calls"]] == [7]
