@@ -90,3 +90,25 @@ def test_quantised_ends():
     for rows, words in ((big, small), (small, big)):
         check_scores(L.quantize_q8(rows), L.quantize_q8(words), F32)
         check_scores(L.quantize_q8(rows), L.quantize_q8(words), BF16)
+
+
+@pytest.mark.parametrize("share", [0.003, 0.1])
+@pytest.mark.parametrize("side", [0, 1], ids=["rows", "words"])
+@pytest.mark.parametrize("n,cols,vocab", [(40, 640, 3000), (300, 1024, 300), (4000, 640, 4090), (9001, 128, 8003),
+                                          (8192, 512, 6144), (8192, 1024, 8192)])
+def test_far_and_near_tiles_in_turn(n, cols, vocab, side, share):
+    """Some rows (or words) of whole numbers are 2^-115 of the others: tiles with and without them follow one another in
+    a block, and each score is exact."""
+    g = gen(n + cols + vocab + side)
+    sides = []
+    for k, which in ((n, 0), (vocab, 1)):
+        q = torch.randint(-2, 3, (k, cols), generator=g, device=DEV).float().to(Q8)
+        s = torch.randint(127, 130, (k, cols // 128), generator=g, device=DEV)
+        if which == side:
+            s = s - 115 * (torch.rand((k, 1), generator=g, device=DEV) < share)
+        sides.append((q, bytes_of(s, k, cols)))
+    want = dequantize(*sides[0]) @ dequantize(*sides[1]).t()
+    for _ in range(3):
+        out = empty(n, vocab)
+        L.gs_label_scores_q8(*sides[0], *sides[1], out)
+        assert torch.equal(out.double(), want)
